@@ -14,6 +14,7 @@ _c_void_p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _size = ctypes.c_size_t
 _int = ctypes.c_int
+_f32 = ctypes.c_float
 
 # name -> (restype, argtypes); mirrors include/svdq.h
 SIGNATURES = {
@@ -75,6 +76,22 @@ SIGNATURES = {
     "svdq_linear_mxfp4": (_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                  _c_void_p, _c_void_p, _i64, _i64, _i64, _i64, _c_void_p, _c_void_p, _size,
                                  _c_void_p]),
+    "svdq_quantize_int8": (_int, [_c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p, _c_void_p]),
+    "svdq_gemm_int8_workspace_bytes": (_size, [_i64, _i64, _i64]),
+    "svdq_gemm_int8": (_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p,
+                              _c_void_p, _size, _c_void_p]),
+    "svdq_linear_int8_workspace_bytes": (_size, [_i64, _i64, _i64]),
+    "svdq_linear_int8": (_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p,
+                                _c_void_p, _size, _c_void_p]),
+    "svdq_norm_gated": (_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _f32, _c_void_p, _c_void_p, _c_void_p,
+                               _i64, _i64, _i64, _f32, _c_void_p, _c_void_p, _c_void_p]),
+    "svdq_norm_gated_int8": (_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _f32, _c_void_p, _c_void_p, _c_void_p,
+                                    _i64, _i64, _i64, _f32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
+    "svdq_rope_axes": (_int, [_c_void_p, _i64, _i64, _i64, _c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p, _f32,
+                              _c_void_p, ctypes.POINTER(ctypes.c_int32), _int, ctypes.c_double, _int, _i64, _i64,
+                              _c_void_p, _i64, _i64, _c_void_p, _i64, _i64, _c_void_p]),
+    "svdq_attention_packed": (_int, [_c_void_p, _i64, _i64, _c_void_p, _i64, _i64, _c_void_p, _i64, _i64, _c_void_p,
+                                     _i64, _i64, _i64, _i64, _i64, _int, _f32, _c_void_p, _i64, _i64, _c_void_p]),
     "svdq_calib_table_bytes": (_size, []),
     "svdq_calib_flop_per_iteration": (_i64, [_i64]),
     "svdq_calib_mfma": (_int, [_c_void_p, _size, _i64, _i64, _c_void_p, _size, _c_void_p, _size, _c_void_p]),

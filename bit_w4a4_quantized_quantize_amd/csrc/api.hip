@@ -1,5 +1,6 @@
 // C ABI of the library (declared in include/svdq.h): argument validation on
 // the host, workspace layout, and the launch sequence of each entry point.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <stdlib.h>
@@ -1199,6 +1200,427 @@ int svdq_linear_w4a4_noalloc(const void* x, const void* smooth, const void* weig
 }
 
 // ---- measurement helpers (not part of the layer) ----
+
+static int check_int8_mnk(int64_t M, int64_t N, int64_t K) {
+  int st = check_mk(M, K, 0);
+  if (st) return st;
+  if (N < 0) return fail(SVDQ_ERR_SHAPE, "N = %lld is negative", (long long)N);
+  if (N > kMaxDim) return fail(SVDQ_ERR_UNSUPPORTED, "dimension above 2^24 (N=%lld)", (long long)N);
+  if (K > svdq::kInt8MaxK)
+    return fail(SVDQ_ERR_UNSUPPORTED, "K = %lld: the int32 sums of the 8-bit product hold K up to %lld", (long long)K,
+                (long long)svdq::kInt8MaxK);
+  return SVDQ_OK;
+}
+
+int svdq_quantize_int8(const void* x, const void* smooth, int64_t M, int64_t K, void* codes, void* ascales,
+                       void* stream) {
+  int st = check_mk(M, K, 0);
+  if (st) return st;
+  if (M == 0) return ok();
+  const char* names[] = {"x", "codes", "ascales"};
+  const void* ptrs[] = {x, codes, ascales};
+  if ((st = check_ptrs(names, ptrs, 3))) return st;
+  if (smooth != nullptr && !aligned16(smooth)) return fail(SVDQ_ERR_ALIGN, "smooth is not 16-byte aligned");
+  const Range in[] = {range("x", x, (size_t)M * K * 2), range("smooth", smooth, (size_t)K * 2)};
+  const Range out[] = {range("codes", codes, (size_t)M * K), range("ascales", ascales, (size_t)M * 4)};
+  if ((st = check_alias(in, 2, out, 2))) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = svdq::launch_quant_int8(static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(smooth), M, K,
+                                         static_cast<int8_t*>(codes), static_cast<float*>(ascales), s);
+  if (int st_ = launched(e, "int8 quantisation", s)) return st_;
+  return ok();
+}
+
+size_t svdq_gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  return svdq::gemm_int8_workspace_bytes(M, N, K);
+}
+
+// what the two products share: pointers, workspace, overlaps (the outputs and the
+// inputs besides the activations), with the activations' own ranges from the caller
+static int check_int8_gemm(const Range* act, int n_act, const void* weight, const void* wscales, const void* bias,
+                           int64_t M, int64_t N, int64_t K, const void* y, const void* workspace,
+                           size_t workspace_bytes, size_t need) {
+  int st;
+  const char* names[] = {"weight", "wscales", "y"};
+  const void* ptrs[] = {weight, wscales, y};
+  if ((st = check_ptrs(names, ptrs, 3))) return st;
+  if (bias != nullptr && !aligned16(bias)) return fail(SVDQ_ERR_ALIGN, "bias is not 16-byte aligned");
+  if (need > 0) {
+    if (workspace_bytes < need)
+      return fail(SVDQ_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+    const char* wn[] = {"workspace"};
+    const void* wp[] = {workspace};
+    if ((st = check_ptrs(wn, wp, 1))) return st;
+  }
+  Range in[5];
+  for (int i = 0; i < n_act; ++i) in[i] = act[i];
+  in[n_act] = range("weight", weight, (size_t)N * K);
+  in[n_act + 1] = range("wscales", wscales, (size_t)N * 4);
+  in[n_act + 2] = range("bias", bias, (size_t)N * 2);
+  const Range out[] = {range("y", y, (size_t)M * N * 2), range("workspace", need > 0 ? workspace : nullptr, need)};
+  return check_alias(in, n_act + 3, out, 2);
+}
+
+static svdq::Int8GemmArgs int8_args(const void* codes, const void* ascales, const void* weight, const void* wscales,
+                                    const void* bias, int64_t M, int64_t N, int64_t K, void* y) {
+  svdq::Int8GemmArgs a{};
+  a.codes = static_cast<const int8_t*>(codes);
+  a.ascales = static_cast<const float*>(ascales);
+  a.weight = static_cast<const int8_t*>(weight);
+  a.wscales = static_cast<const float*>(wscales);
+  a.bias = static_cast<const uint16_t*>(bias);
+  a.y = static_cast<uint16_t*>(y);
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  return a;
+}
+
+int svdq_gemm_int8(const void* codes, const void* ascales, const void* weight, const void* wscales, const void* bias,
+                   int64_t M, int64_t N, int64_t K, void* y, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_int8_mnk(M, N, K);
+  if (st) return st;
+  if (M == 0 || N == 0) return ok();
+  const char* names[] = {"codes", "ascales"};
+  const void* ptrs[] = {codes, ascales};
+  if ((st = check_ptrs(names, ptrs, 2))) return st;
+  const Range act[] = {range("codes", codes, (size_t)M * K), range("ascales", ascales, (size_t)M * 4)};
+  const size_t need = svdq::gemm_int8_workspace_bytes(M, N, K);
+  if ((st = check_int8_gemm(act, 2, weight, wscales, bias, M, N, K, y, workspace, workspace_bytes, need))) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = svdq::launch_gemm_int8(int8_args(codes, ascales, weight, wscales, bias, M, N, K, y), workspace, s);
+  if (int st_ = launched(e, "int8 gemm", s)) return st_;
+  return ok();
+}
+
+// workspace of the whole layer: codes, scales, then the product's own scratch
+struct Int8Ws {
+  size_t scales, gemm, total;
+};
+static Int8Ws int8_ws(int64_t M, int64_t N, int64_t K) {
+  Int8Ws w;
+  w.scales = align256((size_t)M * (size_t)K);
+  w.gemm = align256(w.scales + (size_t)M * 4);
+  w.total = w.gemm + svdq::gemm_int8_workspace_bytes(M, N, K);
+  return w;
+}
+
+size_t svdq_linear_int8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  return int8_ws(M, N, K).total;
+}
+
+int svdq_linear_int8(const void* x, const void* smooth, const void* weight, const void* wscales, const void* bias,
+                     int64_t M, int64_t N, int64_t K, void* y, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  int st = check_int8_mnk(M, N, K);
+  if (st) return st;
+  if (M == 0 || N == 0) return ok();
+  const char* names[] = {"x"};
+  const void* ptrs[] = {x};
+  if ((st = check_ptrs(names, ptrs, 1))) return st;
+  if (smooth != nullptr && !aligned16(smooth)) return fail(SVDQ_ERR_ALIGN, "smooth is not 16-byte aligned");
+  const Int8Ws ws = int8_ws(M, N, K);
+  const Range act[] = {range("x", x, (size_t)M * K * 2), range("smooth", smooth, (size_t)K * 2)};
+  if ((st = check_int8_gemm(act, 2, weight, wscales, bias, M, N, K, y, workspace, workspace_bytes, ws.total))) return st;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = svdq::launch_quant_int8(static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(smooth), M, K,
+                                         reinterpret_cast<int8_t*>(w), reinterpret_cast<float*>(w + ws.scales), s);
+  if (int st_ = launched(e, "int8 quantisation", s)) return st_;
+  e = svdq::launch_gemm_int8(int8_args(w, w + ws.scales, weight, wscales, bias, M, N, K, y), w + ws.gemm, s);
+  if (int st_ = launched(e, "int8 gemm", s)) return st_;
+  return ok();
+}
+
+// Norms around a block. codes == NULL: the bf16 form.
+static int norm_gated_impl(const void* h, const void* block, const void* post_weight, const void* gate,
+                           float residual_scale, const void* pre_weight, const void* scale, const void* cu_seqlens,
+                           int64_t G, int64_t M, int64_t K, float eps, void* h_out, void* x_out, const void* smooth,
+                           void* codes, void* ascales, bool int8, void* stream) {
+  int st = check_mk(M, K, 0);
+  if (st) return st;
+  if (K > svdq::kNormMaxK)
+    return fail(SVDQ_ERR_UNSUPPORTED, "K = %lld: a row of the norm holds at most %lld elements", (long long)K,
+                (long long)svdq::kNormMaxK);
+  if (G < 1) return fail(SVDQ_ERR_SHAPE, "G = %lld must be positive", (long long)G);
+  if (G > kMaxDim) return fail(SVDQ_ERR_UNSUPPORTED, "G = %lld is above 2^24", (long long)G);
+  if (cu_seqlens == nullptr && G != 1)
+    return fail(SVDQ_ERR_INVALID, "G = %lld groups need cu_seqlens", (long long)G);
+  if (!(eps >= 0.0f && eps <= 3.4e38f)) return fail(SVDQ_ERR_INVALID, "eps = %g must be finite and not negative", eps);
+  if (!(residual_scale >= -3.4e38f && residual_scale <= 3.4e38f))
+    return fail(SVDQ_ERR_INVALID, "residual_scale = %g must be finite", residual_scale);
+  if (M == 0) return ok();
+  if (block == nullptr && h_out != nullptr)
+    return fail(SVDQ_ERR_INVALID, "h_out must be NULL without a block (it would be h)");
+  if (block == nullptr && (post_weight != nullptr || gate != nullptr))
+    return fail(SVDQ_ERR_INVALID, "post_weight and gate belong to a block");
+  if (!int8 && x_out == nullptr && block == nullptr) return fail(SVDQ_ERR_INVALID, "neither a block nor x_out");
+  if (!int8 && x_out == nullptr && (pre_weight != nullptr || scale != nullptr))
+    return fail(SVDQ_ERR_INVALID, "pre_weight and scale belong to x_out");
+  {
+    const char* names[] = {"h", "block", "h_out"};
+    const void* ptrs[] = {h, block, h_out};
+    if ((st = check_ptrs(names, ptrs, block != nullptr ? 3 : 1))) return st;
+  }
+  if (int8) {
+    const char* names[] = {"codes", "ascales"};
+    const void* ptrs[] = {codes, ascales};
+    if ((st = check_ptrs(names, ptrs, 2))) return st;
+  }
+  {
+    const char* names[] = {"post_weight", "gate", "pre_weight", "scale", "cu_seqlens", "x_out", "smooth"};
+    const void* ptrs[] = {post_weight, gate, pre_weight, scale, cu_seqlens, x_out, smooth};
+    for (int i = 0; i < 7; ++i)
+      if (!aligned16(ptrs[i])) return fail(SVDQ_ERR_ALIGN, "%s is not 16-byte aligned", names[i]);
+  }
+  const size_t mk = (size_t)M * (size_t)K, gk = (size_t)G * (size_t)K;
+  const bool in_place = h_out == h;
+  const Range in[] = {range("h", in_place ? nullptr : h, mk * 2), range("block", block, mk * 2),
+                      range("post_weight", post_weight, (size_t)K * 2), range("gate", gate, gk * 2),
+                      range("pre_weight", pre_weight, (size_t)K * 2), range("scale", scale, gk * 2),
+                      range("cu_seqlens", cu_seqlens, (size_t)(G + 1) * 4), range("smooth", smooth, (size_t)K * 2)};
+  const Range out[] = {range("h_out", h_out, mk * 2), range("x_out", x_out, mk * 2), range("codes", codes, mk),
+                       range("ascales", ascales, (size_t)M * 4)};
+  if ((st = check_alias(in, 8, out, 4))) return st;
+  svdq::NormArgs a{};
+  a.h = static_cast<const uint16_t*>(h);
+  a.block = static_cast<const uint16_t*>(block);
+  a.post = static_cast<const uint16_t*>(post_weight);
+  a.gate = static_cast<const uint16_t*>(gate);
+  a.pre = static_cast<const uint16_t*>(pre_weight);
+  a.scale = static_cast<const uint16_t*>(scale);
+  a.cu = static_cast<const int32_t*>(cu_seqlens);
+  a.smooth = static_cast<const uint16_t*>(smooth);
+  a.h_out = static_cast<uint16_t*>(h_out);
+  a.x_out = static_cast<uint16_t*>(x_out);
+  a.codes = static_cast<int8_t*>(codes);
+  a.ascales = static_cast<float*>(ascales);
+  a.M = M;
+  a.K = K;
+  a.G = (int)G;
+  a.eps = eps;
+  a.rs = residual_scale;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = svdq::launch_norm_gated(a, s);
+  if (int st_ = launched(e, "gated norm", s)) return st_;
+  return ok();
+}
+
+int svdq_norm_gated(const void* h, const void* block, const void* post_weight, const void* gate, float residual_scale,
+                    const void* pre_weight, const void* scale, const void* cu_seqlens, int64_t G, int64_t M, int64_t K,
+                    float eps, void* h_out, void* x_out, void* stream) {
+  return norm_gated_impl(h, block, post_weight, gate, residual_scale, pre_weight, scale, cu_seqlens, G, M, K, eps,
+                         h_out, x_out, nullptr, nullptr, nullptr, false, stream);
+}
+
+int svdq_norm_gated_int8(const void* h, const void* block, const void* post_weight, const void* gate,
+                         float residual_scale, const void* pre_weight, const void* scale, const void* cu_seqlens,
+                         int64_t G, int64_t M, int64_t K, float eps, void* h_out, const void* smooth, void* codes,
+                         void* ascales, void* stream) {
+  return norm_gated_impl(h, block, post_weight, gate, residual_scale, pre_weight, scale, cu_seqlens, G, M, K, eps,
+                         h_out, nullptr, smooth, codes, ascales, true, stream);
+}
+
+// A tensor of T tokens x `heads` heads x D contiguous elements with element strides
+// for token and head (the stride of an axis of length one does not matter: it
+// becomes 0). span: elements from the first to one past the last.
+struct Heads {
+  const char* name;
+  const void* p;
+  int64_t st, sh, T, heads, D, span;
+};
+
+static int make_heads(Heads* o, const char* name, const void* p, int64_t st, int64_t sh, int64_t T, int64_t heads,
+                      int64_t D) {
+  if (p == nullptr) return fail(SVDQ_ERR_NULL, "%s is NULL", name);
+  if (!aligned16(p)) return fail(SVDQ_ERR_ALIGN, "%s is not 16-byte aligned", name);
+  if (T == 1) st = 0;
+  if (heads == 1) sh = 0;
+  if (st < 0 || sh < 0) return fail(SVDQ_ERR_SHAPE, "%s has a negative stride", name);
+  if (st >= kMaxDim || sh >= (int64_t(1) << 40))
+    return fail(SVDQ_ERR_UNSUPPORTED, "%s: a token stride must be below 2^24 elements and a head stride below 2^40", name);
+  if (st % 8 != 0 || sh % 8 != 0)
+    return fail(SVDQ_ERR_ALIGN, "%s: strides (%lld, %lld) must be multiples of 8 elements", name, (long long)st,
+                (long long)sh);
+  if (T > 1 && st < D)
+    return fail(SVDQ_ERR_SHAPE, "%s: token stride %lld is below the head size %lld", name, (long long)st, (long long)D);
+  if (heads > 1 && sh < D)
+    return fail(SVDQ_ERR_SHAPE, "%s: head stride %lld is below the head size %lld", name, (long long)sh, (long long)D);
+  *o = Heads{name, p, st, sh, T, heads, D, (T - 1) * st + (heads - 1) * sh + D};
+  return SVDQ_OK;
+}
+
+// elements of different (token, head) never coincide
+static bool heads_distinct(const Heads& a) {
+  const bool token_major = a.T == 1 || a.heads == 1 || a.st >= (a.heads - 1) * a.sh + a.D;
+  const bool head_major = a.T == 1 || a.heads == 1 || a.sh >= (a.T - 1) * a.st + a.D;
+  return token_major || head_major;
+}
+
+// No element in common: disjoint ranges, or (views of one fused buffer) the same
+// token stride with the heads of a token in disjoint spans of it.
+static bool heads_disjoint(const Heads& a, const Heads& b) {
+  if (!overlaps(range("", a.p, (size_t)a.span * 2), range("", b.p, (size_t)b.span * 2))) return true;
+  const int64_t sa = (a.heads - 1) * a.sh + a.D, sb = (b.heads - 1) * b.sh + b.D;
+  if (a.T == 1 || a.st != b.st || sa > a.st || sb > b.st) return false;
+  const int64_t bytes = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
+  int64_t off = bytes % (2 * a.st);
+  if (off < 0) off += 2 * a.st;
+  return off >= 2 * sa && off + 2 * sb <= 2 * a.st;
+}
+
+static Range heads_range(const Heads& h) { return range(h.name, h.p, (size_t)h.span * 2); }
+
+static svdq::HeadView view_of(const Heads& h) {
+  return svdq::HeadView{static_cast<const uint16_t*>(h.p), h.st, h.sh};
+}
+
+static int check_heads_shape(int64_t T, int64_t D) {
+  if (T < 0) return fail(SVDQ_ERR_SHAPE, "T = %lld is negative", (long long)T);
+  if (T >= kMaxDim) return fail(SVDQ_ERR_UNSUPPORTED, "T = %lld must be below 2^24", (long long)T);
+  if (D != 64 && D != 128) return fail(SVDQ_ERR_UNSUPPORTED, "head size D = %lld is not 64 or 128", (long long)D);
+  return SVDQ_OK;
+}
+
+int svdq_rope_axes(const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t H, const void* k,
+                   int64_t k_stride_t, int64_t k_stride_h, int64_t Hk, const void* q_weight, const void* k_weight,
+                   float eps, const void* positions, const int32_t* axis_dims, int axes, double theta,
+                   int interleaved, int64_t T, int64_t D, void* q_out, int64_t qo_stride_t, int64_t qo_stride_h,
+                   void* k_out, int64_t ko_stride_t, int64_t ko_stride_h, void* stream) {
+  int st = check_heads_shape(T, D);
+  if (st) return st;
+  if (H < 0 || Hk < 0 || H + Hk == 0)
+    return fail(SVDQ_ERR_SHAPE, "H = %lld and Hk = %lld: at least one head, none negative", (long long)H, (long long)Hk);
+  if (H > 65535 || Hk > 65535) return fail(SVDQ_ERR_UNSUPPORTED, "more than 65535 heads");
+  if (T * (H + Hk) >= (int64_t(1) << 31)) return fail(SVDQ_ERR_UNSUPPORTED, "T * (H + Hk) must be below 2^31");
+  if (axes < 1 || axes > 4) return fail(SVDQ_ERR_SHAPE, "axes = %d is not 1..4", axes);
+  if (axis_dims == nullptr) return fail(SVDQ_ERR_NULL, "axis_dims is NULL");
+  int64_t sum = 0;
+  for (int i = 0; i < axes; ++i) {
+    if (axis_dims[i] <= 0 || axis_dims[i] % 2 != 0)
+      return fail(SVDQ_ERR_SHAPE, "axis_dims[%d] = %d must be positive and even", i, axis_dims[i]);
+    sum += axis_dims[i];
+  }
+  if (sum != D) return fail(SVDQ_ERR_SHAPE, "axis_dims sum to %lld, not D = %lld", (long long)sum, (long long)D);
+  if (!(theta >= 1.0 && theta <= 1e9)) return fail(SVDQ_ERR_INVALID, "theta = %g is not in [1, 1e9]", theta);
+  if (!(eps >= 0.0f && eps <= 3.4e38f)) return fail(SVDQ_ERR_INVALID, "eps = %g must be finite and not negative", eps);
+  if (T == 0) return ok();
+  {
+    const char* names[] = {"positions"};
+    const void* ptrs[] = {positions};
+    if ((st = check_ptrs(names, ptrs, 1))) return st;
+  }
+  if (!aligned16(q_weight)) return fail(SVDQ_ERR_ALIGN, "q_weight is not 16-byte aligned");
+  if (!aligned16(k_weight)) return fail(SVDQ_ERR_ALIGN, "k_weight is not 16-byte aligned");
+  Heads in[2], out[2];
+  const int64_t n[2] = {H, Hk};
+  const void* ip[2] = {q, k};
+  void* op[2] = {q_out, k_out};
+  const int64_t is[2][2] = {{q_stride_t, q_stride_h}, {k_stride_t, k_stride_h}};
+  const int64_t os[2][2] = {{qo_stride_t, qo_stride_h}, {ko_stride_t, ko_stride_h}};
+  const void* wt[2] = {q_weight, k_weight};
+  static const char* const in_name[2] = {"q", "k"};
+  static const char* const out_name[2] = {"q_out", "k_out"};
+  for (int i = 0; i < 2; ++i) {
+    if (n[i] == 0) {
+      if (ip[i] != nullptr || op[i] != nullptr || wt[i] != nullptr)
+        return fail(SVDQ_ERR_INVALID, "%s has no heads, so its tensors must be NULL", in_name[i]);
+      continue;
+    }
+    if ((st = make_heads(&in[i], in_name[i], ip[i], is[i][0], is[i][1], T, n[i], D))) return st;
+    if ((st = make_heads(&out[i], out_name[i], op[i], os[i][0], os[i][1], T, n[i], D))) return st;
+    if (!heads_distinct(out[i])) return fail(SVDQ_ERR_SHAPE, "%s: heads overlap under its strides", out_name[i]);
+  }
+  const Range pos = range("positions", positions, (size_t)T * axes * 4);
+  for (int o = 0; o < 2; ++o) {
+    if (n[o] == 0) continue;
+    for (int i = 0; i < 2; ++i) {
+      if (n[i] == 0) continue;
+      const bool in_place = i == o && in[i].p == out[o].p && in[i].st == out[o].st && in[i].sh == out[o].sh;
+      if (!in_place && !heads_disjoint(in[i], out[o]))
+        return fail(SVDQ_ERR_ALIAS, "output %s overlaps input %s", out[o].name, in[i].name);
+    }
+    const Range rest[] = {pos, range("q_weight", q_weight, (size_t)D * 2), range("k_weight", k_weight, (size_t)D * 2)};
+    for (const Range& r : rest)
+      if (r.lo != 0 && overlaps(heads_range(out[o]), r))
+        return fail(SVDQ_ERR_ALIAS, "output %s overlaps input %s", out[o].name, r.name);
+  }
+  if (H > 0 && Hk > 0 && !heads_disjoint(out[0], out[1]))
+    return fail(SVDQ_ERR_ALIAS, "output q_out overlaps output k_out");
+  svdq::RopeArgs a{};
+  for (int i = 0; i < 2; ++i) {
+    a.H[i] = (int)n[i];
+    if (n[i] == 0) continue;
+    a.in[i] = view_of(in[i]);
+    a.out[i] = static_cast<uint16_t*>(op[i]);
+    a.out_st[i] = out[i].st;
+    a.out_sh[i] = out[i].sh;
+    a.weight[i] = static_cast<const uint16_t*>(wt[i]);
+  }
+  a.positions = static_cast<const int32_t*>(positions);
+  a.axes = axes;
+  a.T = T;
+  a.eps = eps;
+  int p = 0;
+  for (int i = 0; i < axes; ++i)
+    for (int j = 0; j < axis_dims[i] / 2; ++j, ++p) {
+      a.axis[p] = (uint8_t)i;
+      a.turns[p] = pow(theta, -2.0 * j / axis_dims[i]) / 6.283185307179586476925;
+    }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = svdq::launch_rope(a, (int)D, interleaved != 0, s);
+  if (int st_ = launched(e, "rotary positions", s)) return st_;
+  return ok();
+}
+
+int svdq_attention_packed(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k, int64_t k_stride_t,
+                          int64_t k_stride_h, const void* v, int64_t v_stride_t, int64_t v_stride_h,
+                          const void* cu_seqlens, int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t D, int causal,
+                          float scale, void* o, int64_t o_stride_t, int64_t o_stride_h, void* stream) {
+  int st = check_heads_shape(T, D);
+  if (st) return st;
+  if (H < 1 || Hk < 1) return fail(SVDQ_ERR_SHAPE, "H = %lld and Hk = %lld must be positive", (long long)H, (long long)Hk);
+  if (H % Hk != 0)
+    return fail(SVDQ_ERR_SHAPE, "H = %lld is not a multiple of Hk = %lld", (long long)H, (long long)Hk);
+  if (B < 0) return fail(SVDQ_ERR_SHAPE, "B = %lld is negative", (long long)B);
+  if (H > 65535 || B > 65535) return fail(SVDQ_ERR_UNSUPPORTED, "H = %lld and B = %lld may be at most 65535", (long long)H,
+                                          (long long)B);
+  if (cu_seqlens == nullptr && B != 1)
+    return fail(SVDQ_ERR_INVALID, "B = %lld sequences need cu_seqlens", (long long)B);
+  if (!(scale > 0.0f && scale <= 3.4e38f)) return fail(SVDQ_ERR_INVALID, "scale = %g must be positive and finite", scale);
+  if (T == 0 || B == 0) return ok();
+  Heads hq, hk, hv, ho;
+  if ((st = make_heads(&hq, "q", q, q_stride_t, q_stride_h, T, H, D))) return st;
+  if ((st = make_heads(&hk, "k", k, k_stride_t, k_stride_h, T, Hk, D))) return st;
+  if ((st = make_heads(&hv, "v", v, v_stride_t, v_stride_h, T, Hk, D))) return st;
+  if ((st = make_heads(&ho, "o", o, o_stride_t, o_stride_h, T, H, D))) return st;
+  if (!aligned16(cu_seqlens)) return fail(SVDQ_ERR_ALIGN, "cu_seqlens is not 16-byte aligned");
+  if (!heads_distinct(ho)) return fail(SVDQ_ERR_SHAPE, "o: heads overlap under its strides");
+  for (const Heads* i : {&hq, &hk, &hv})
+    if (!heads_disjoint(*i, ho)) return fail(SVDQ_ERR_ALIAS, "output o overlaps input %s", i->name);
+  if (cu_seqlens != nullptr && overlaps(heads_range(ho), range("cu_seqlens", cu_seqlens, (size_t)(B + 1) * 4)))
+    return fail(SVDQ_ERR_ALIAS, "output o overlaps input cu_seqlens");
+  svdq::AttnArgs a{};
+  a.q = view_of(hq);
+  a.k = view_of(hk);
+  a.v = view_of(hv);
+  a.o = static_cast<uint16_t*>(o);
+  a.o_st = ho.st;
+  a.o_sh = ho.sh;
+  a.cu = static_cast<const int32_t*>(cu_seqlens);
+  a.B = (int)B;
+  a.H = (int)H;
+  a.Hk = (int)Hk;
+  a.causal = causal != 0;
+  a.T = T;
+  a.scale = scale;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = svdq::launch_attention(a, (int)D, s);
+  if (int st_ = launched(e, "attention", s)) return st_;
+  return ok();
+}
 
 size_t svdq_calib_table_bytes(void) { return svdq::calib_table_bytes(); }
 

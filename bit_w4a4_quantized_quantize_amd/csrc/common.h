@@ -126,6 +126,32 @@ __device__ __forceinline__ f16x8 dequant8_f16(uint32_t codes, _Float16 s) {
   return r;
 }
 
+// Scale of an 8-bit integer row with maximum magnitude amax: codes = rne(v * inv),
+// scale = amax / 127, both quotients correctly rounded. A zero row, and one whose
+// 127 / amax overflows (amax below 2^-120), has zero codes and scale.
+struct Int8Scale {
+  float inv, scale;
+};
+__device__ __forceinline__ Int8Scale int8_scale(float amax) {
+  Int8Scale q;
+  q.inv = __fdiv_rn(127.0f, amax);
+  q.scale = __fdiv_rn(amax, 127.0f);
+  if (!(q.inv <= 3.4028234663852886e38f)) q.inv = q.scale = 0.0f;
+  return q;
+}
+// 8 codes of v * inv, |v * inv| <= 127 (1 + 2^-23), packed in order
+__device__ __forceinline__ u32x2 int8_codes8(const float (&v)[8], float inv) {
+  u32x2 r;
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w |= ((uint32_t)(int)__builtin_rintf(v[4 * d + i] * inv) & 0xFFu) << (8 * i);
+    r[d] = w;
+  }
+  return r;
+}
+
 __device__ __forceinline__ u32x4 zero4() { u32x4 z = {0u, 0u, 0u, 0u}; return z; }
 
 // Raw buffer resource over [base, base + bytes): loads at an offset at or past

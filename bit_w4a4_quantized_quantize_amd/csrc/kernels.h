@@ -154,6 +154,80 @@ hipError_t launch_repack(const uint8_t* qweight, const uint8_t* wscales, uint8_t
 hipError_t launch_unpack(const uint8_t* packed, uint8_t* qweight, uint8_t* wscales,
                          int64_t N, int64_t K, hipStream_t stream);
 
+// Linear in 8-bit integers: codes and per-row scales of x * smooth (smooth NULL =
+// 1), and y = bf16(codes @ weight^T * ascales * wscales + bias). K % 16 == 0,
+// K <= kInt8MaxK for the product (exact int32 sums).
+constexpr int64_t kInt8MaxK = 131072;
+hipError_t launch_quant_int8(const uint16_t* x, const uint16_t* smooth, int64_t M, int64_t K, int8_t* codes,
+                             float* ascales, hipStream_t stream);
+struct Int8GemmArgs {
+  const int8_t* codes;     // [M, K]
+  const float* ascales;    // [M]
+  const int8_t* weight;    // [N, K]
+  const float* wscales;    // [N]
+  const uint16_t* bias;    // [N] or NULL
+  uint16_t* y;             // [M, N]
+  int64_t M, N, K;
+};
+hipError_t launch_gemm_int8(const Int8GemmArgs& a, void* workspace, hipStream_t stream);
+size_t gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+// Norms around a block: h_out = h + rs * gate[g] * rms(block, post), and
+// x_out = rms(h_out, pre) * (1 + scale[g]) in bf16 or, with codes, in int8 with
+// a scale per row. Optional pointers may be NULL (svdq.h, svdq_norm_gated).
+struct NormArgs {
+  const uint16_t* h;
+  const uint16_t* block;
+  const uint16_t* post;
+  const uint16_t* gate;
+  const uint16_t* pre;
+  const uint16_t* scale;
+  const int32_t* cu;
+  const uint16_t* smooth;
+  uint16_t* h_out;
+  uint16_t* x_out;
+  int8_t* codes;
+  float* ascales;
+  int64_t M, K;
+  int G;
+  float eps, rs;
+};
+constexpr int64_t kNormMaxK = 32768;
+hipError_t launch_norm_gated(const NormArgs& a, hipStream_t stream);
+
+// Rotary positions with several axes and the per-head norm, q and k in one launch.
+struct HeadView {   // [T, H, D], strides in elements
+  const uint16_t* p;
+  int64_t st, sh;
+};
+struct RopeArgs {
+  HeadView in[2];          // q, k
+  uint16_t* out[2];
+  int64_t out_st[2], out_sh[2];
+  const uint16_t* weight[2];
+  int H[2];
+  const int32_t* positions;  // [T, axes]
+  int axes;
+  int64_t T;
+  float eps;
+  // per pair: its frequency in turns (theta^(-2i/d) / 2 pi), and its axis
+  double turns[64];
+  uint8_t axis[64];
+};
+hipError_t launch_rope(const RopeArgs& a, int D, bool interleaved, hipStream_t stream);
+
+// Attention over packed sequences.
+struct AttnArgs {
+  HeadView q, k, v;
+  uint16_t* o;
+  int64_t o_st, o_sh;
+  const int32_t* cu;   // [B + 1] or NULL (one sequence)
+  int B, H, Hk, causal;
+  int64_t T;
+  float scale;
+};
+hipError_t launch_attention(const AttnArgs& a, int D, hipStream_t stream);
+
 // Measurement helpers (not part of the layer): sustained f16 matrix-instruction
 // rate on a caller-filled operand table of calib_table_bytes() bytes, with the
 // core-clock and constant-rate counters of each workgroup's start and end in

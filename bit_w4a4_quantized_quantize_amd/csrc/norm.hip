@@ -1,0 +1,182 @@
+// Norms before and after a transformer block, fused with its gate, the residual
+// scale and the next block's modulation:
+//
+//   h_out = h + rs * gate[g] * (block / sqrt(mean block^2 + eps)) * post
+//   x_out = (h_out / sqrt(mean h_out^2 + eps)) * pre * (1 + scale[g])
+//
+// One workgroup per row; the row stays in registers between the two sums, so h
+// and block are read once and h_out and x_out (or x's int8 codes) written once.
+// Sums in fp32; x_out comes from h_out before its rounding to bf16.
+#include "common.h"
+#include "kernels.h"
+
+namespace svdq {
+
+namespace {
+
+__device__ __forceinline__ void unpack8(const u32x4 w, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16lo_to_f32(w[i]);
+    v[2 * i + 1] = bf16hi_to_f32(w[i]);
+  }
+}
+__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+  return w;
+}
+
+// Group of `row`: the last g with cu[g] <= row, if row < cu[g + 1]; -1 outside.
+__device__ __forceinline__ int row_group(const int32_t* cu, int G, int64_t row) {
+  int lo = 0, hi = G;                       // cu[lo] <= row < cu[hi] if any group has the row
+  if (row < cu[0] || row >= cu[G]) return -1;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= row) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// sum (or maximum) over the workgroup's NW waves, the same value in every lane
+template <int NW, bool MAX>
+__device__ __forceinline__ float reduce_wg(float v, float* part) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) {
+    const float o = __shfl_xor(v, d);
+    v = MAX ? fmaxf(v, o) : v + o;
+  }
+  if (NW == 1) return v;
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = part[0];
+#pragma unroll
+  for (int w = 1; w < NW; ++w) v = MAX ? fmaxf(v, part[w]) : v + part[w];
+  return v;
+}
+
+// NW waves hold NV 8-element pieces per lane: K <= NW * 64 * NV * 8.
+template <int NW, int NV, bool BLOCK>
+__global__ __launch_bounds__(64 * NW) void norm_gated_kernel(NormArgs a) {
+  constexpr int kThreads = 64 * NW;
+  __shared__ float part[3][NW];
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.x;
+  const int g = a.cu != nullptr ? row_group(a.cu, a.G, row) : 0;
+  if (g < 0) return;
+  const int np = (int)(a.K / 8);
+  const size_t base = (size_t)row * (size_t)a.K;
+  const size_t gbase = (size_t)g * (size_t)a.K;
+  const float rk = 1.0f / (float)a.K;
+  auto piece = [](const uint16_t* p, size_t off, int i) {
+    return *reinterpret_cast<const u32x4*>(p + off + 8 * (size_t)i);
+  };
+
+  float h[NV][8];
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const int i = tid + kThreads * u;
+    unpack8(i < np ? piece(a.h, base, i) : zero4(), h[u]);
+  }
+  if (BLOCK) {
+    float b[NV][8];
+    float ss = 0.0f;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int i = tid + kThreads * u;
+      unpack8(i < np ? piece(a.block, base, i) : zero4(), b[u]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(b[u][e], b[u][e], ss);
+    }
+    ss = reduce_wg<NW, false>(ss, part[0]);
+    const float r = a.rs / __builtin_sqrtf(ss * rk + a.eps);
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int i = tid + kThreads * u;
+      if (i < np) {
+        float w[8], gt[8];
+        if (a.post != nullptr) unpack8(piece(a.post, 0, i), w);
+        if (a.gate != nullptr) unpack8(piece(a.gate, gbase, i), gt);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float f = r;
+          if (a.post != nullptr) f *= w[e];
+          if (a.gate != nullptr) f *= gt[e];
+          h[u][e] = __builtin_fmaf(b[u][e], f, h[u][e]);
+        }
+        *reinterpret_cast<u32x4*>(a.h_out + base + 8 * (size_t)i) = pack8(h[u]);
+      }
+    }
+  }
+  if (a.x_out == nullptr && a.codes == nullptr) return;
+
+  float ss = 0.0f;
+#pragma unroll
+  for (int u = 0; u < NV; ++u)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(h[u][e], h[u][e], ss);
+  ss = reduce_wg<NW, false>(ss, part[1]);
+  const float r = 1.0f / __builtin_sqrtf(ss * rk + a.eps);
+  float amax = 0.0f;
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const int i = tid + kThreads * u;
+    if (i < np) {
+      float w[8], sc[8];
+      if (a.pre != nullptr) unpack8(piece(a.pre, 0, i), w);
+      if (a.scale != nullptr) unpack8(piece(a.scale, gbase, i), sc);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float f = r;
+        if (a.pre != nullptr) f *= w[e];
+        if (a.scale != nullptr) f *= 1.0f + sc[e];
+        h[u][e] *= f;
+      }
+      const u32x4 x = pack8(h[u]);
+      if (a.codes == nullptr) {
+        *reinterpret_cast<u32x4*>(a.x_out + base + 8 * (size_t)i) = x;
+      } else {   // the codes are those of the bf16 x
+        unpack8(x, h[u]);
+        if (a.smooth != nullptr) {
+          float sm[8];
+          unpack8(piece(a.smooth, 0, i), sm);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[u][e] *= sm[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(h[u][e]));
+      }
+    }
+  }
+  if (a.codes == nullptr) return;
+  amax = reduce_wg<NW, true>(amax, part[2]);
+  const Int8Scale q = int8_scale(amax);
+  if (tid == 0) a.ascales[row] = q.scale;
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const int i = tid + kThreads * u;
+    if (i < np) *reinterpret_cast<u32x2*>(a.codes + base + 8 * (size_t)i) = int8_codes8(h[u], q.inv);
+  }
+}
+
+template <int NW, int NV>
+void launch_norm_cfg(const NormArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)a.M), block(64 * NW);
+  if (a.block != nullptr)
+    hipLaunchKernelGGL((norm_gated_kernel<NW, NV, true>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((norm_gated_kernel<NW, NV, false>), grid, block, 0, s, a);
+}
+
+}  // namespace
+
+hipError_t launch_norm_gated(const NormArgs& a, hipStream_t stream) {
+  if (a.K <= 2048) launch_norm_cfg<4, 1>(a, stream);
+  else if (a.K <= 4096) launch_norm_cfg<4, 2>(a, stream);
+  else if (a.K <= 16384) launch_norm_cfg<16, 2>(a, stream);
+  else launch_norm_cfg<16, 4>(a, stream);
+  return hipGetLastError();
+}
+
+}  // namespace svdq

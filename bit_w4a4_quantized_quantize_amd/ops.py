@@ -677,3 +677,254 @@ def linear_mxfp4(x, w: "SVDQLinearWeights", w_codes, w_scales, y=None, workspace
         _p(w.proj_down) if w.R > 0 else None, _p(w.proj_up) if w.R > 0 else None, _p(w.bias),
         M, w.N, K, w.R, _p(y), _p(workspace), workspace.numel(), _stream(x.device)))
     return y
+
+
+def _launch(name, dev, *args):
+    """Call the C entry point `name` on dev's current stream, with dev the current HIP device."""
+    fn = getattr(_lib.lib(), name)
+    if dev.index == torch.cuda.current_device():
+        _lib.check(name, fn(*args, _stream(dev)))
+    else:
+        with torch.cuda.device(dev):
+            _lib.check(name, fn(*args, _stream(dev)))
+
+
+def _workspace(workspace, need, dev):
+    """The given workspace, checked, or a new one (None when no bytes are needed); and its size."""
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    return workspace, _need(workspace, "workspace", torch.uint8, 1, min_numel=need).numel()
+
+
+def quantize_int8(x, smooth=None, codes=None, scales=None):
+    """8-bit codes with one scale per row: v = x * smooth, scales = max |v| / 127 (float32
+    [M]), codes = round(v * (127 / max |v|)) (int8 [M, K]). x [M, K] bf16, smooth [K] bf16 or
+    None. The same rule quantises activations (rows = tokens) and weights (rows = output
+    channels, smooth = 1 / the layer's smooth). Returns (codes, scales)."""
+    _need(x, "x", torch.bfloat16, 2)
+    M, K = x.shape
+    _k_ok(K)
+    if smooth is not None:
+        _need(smooth, "smooth", torch.bfloat16, shape=(K,))
+    dev = x.device
+    if codes is None:
+        codes = torch.empty((M, K), dtype=torch.int8, device=dev)
+    if scales is None:
+        scales = torch.empty(M, dtype=torch.float32, device=dev)
+    _need(codes, "codes", torch.int8, shape=(M, K))
+    _need(scales, "scales", torch.float32, shape=(M,))
+    _devices(x=x, smooth=smooth, codes=codes, scales=scales)
+    _launch("svdq_quantize_int8", dev, _p(x), _p(smooth), M, K, _p(codes), _p(scales))
+    return codes, scales
+
+
+def _check_int8_weight(weight, wscales, bias, K):
+    _need(weight, "weight", torch.int8, 2)
+    N = weight.shape[0]
+    if weight.shape[1] != K:
+        raise ValueError(f"the activations have K={K}, weight has K={weight.shape[1]}")
+    _need(weight, "weight", torch.int8, shape=(N, K))
+    _need(wscales, "wscales", torch.float32, shape=(N,))
+    if bias is not None:
+        _need(bias, "bias", torch.bfloat16, shape=(N,))
+    return N
+
+
+def gemm_int8_workspace_bytes(M, N, K):
+    """Scratch bytes gemm_int8 needs."""
+    return int(_lib.lib().svdq_gemm_int8_workspace_bytes(M, N, K))
+
+
+def linear_int8_workspace_bytes(M, N, K):
+    """Scratch bytes linear_int8 needs."""
+    return int(_lib.lib().svdq_linear_int8_workspace_bytes(M, N, K))
+
+
+def gemm_int8(codes, ascales, weight, wscales, bias=None, y=None, workspace=None):
+    """y [M, N] bf16 = (codes @ weight^T) * ascales[m] * wscales[n] + bias from 8-bit codes:
+    codes int8 [M, K], ascales float32 [M] (quantize_int8 or norm_gated_int8), weight int8
+    [N, K], wscales float32 [N], bias bf16 [N] or None. K <= 131072."""
+    _need(codes, "codes", torch.int8, 2)
+    M, K = codes.shape
+    _k_ok(K)
+    _need(ascales, "ascales", torch.float32, shape=(M,))
+    N = _check_int8_weight(weight, wscales, bias, K)
+    dev = codes.device
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    _need(y, "y", torch.bfloat16, shape=(M, N))
+    workspace, ws_bytes = _workspace(workspace, gemm_int8_workspace_bytes(M, N, K), dev)
+    _devices(codes=codes, ascales=ascales, weight=weight, wscales=wscales, bias=bias, y=y, workspace=workspace)
+    _launch("svdq_gemm_int8", dev, _p(codes), _p(ascales), _p(weight), _p(wscales), _p(bias), M, N, K, _p(y),
+            _p(workspace), ws_bytes)
+    return y
+
+
+def linear_int8(x, weight, wscales, bias=None, smooth=None, y=None, workspace=None):
+    """The whole linear in 8-bit integers: quantize_int8(x, smooth), then gemm_int8. x [M, K]
+    bf16, weight int8 [N, K], wscales float32 [N]; returns y [M, N] bf16."""
+    _need(x, "x", torch.bfloat16, 2)
+    M, K = x.shape
+    _k_ok(K)
+    N = _check_int8_weight(weight, wscales, bias, K)
+    if smooth is not None:
+        _need(smooth, "smooth", torch.bfloat16, shape=(K,))
+    dev = x.device
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    _need(y, "y", torch.bfloat16, shape=(M, N))
+    workspace, ws_bytes = _workspace(workspace, linear_int8_workspace_bytes(M, N, K), dev)
+    _devices(x=x, smooth=smooth, weight=weight, wscales=wscales, bias=bias, y=y, workspace=workspace)
+    _launch("svdq_linear_int8", dev, _p(x), _p(smooth), _p(weight), _p(wscales), _p(bias), M, N, K, _p(y),
+            _p(workspace), ws_bytes)
+    return y
+
+
+def _check_norm(h, block, post_weight, gate, pre_weight, scale, cu_seqlens, h_out):
+    """Arguments common to the two norms; returns (M, K, G, h_out)."""
+    _need(h, "h", torch.bfloat16, 2)
+    M, K = h.shape
+    _k_ok(K)
+    G = 1
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, 1, min_numel=2)
+        G = cu_seqlens.numel() - 1
+    if block is not None:
+        _need(block, "block", torch.bfloat16, shape=(M, K))
+        if h_out is None:
+            h_out = torch.empty_like(h)
+        _need(h_out, "h_out", torch.bfloat16, shape=(M, K))
+    for name, t, shape in (("post_weight", post_weight, (K,)), ("gate", gate, (G, K)),
+                           ("pre_weight", pre_weight, (K,)), ("scale", scale, (G, K))):
+        if t is not None:
+            _need(t, name, torch.bfloat16, shape=shape)
+    return M, K, G, h_out
+
+
+def norm_gated(h, block=None, post_weight=None, gate=None, residual_scale=1.0, pre_weight=None, scale=None,
+               cu_seqlens=None, eps=1e-6, h_out=None, x_out=None, pre=True):
+    """The norms between two transformer blocks, in one pass:
+
+        h_out = h + residual_scale * gate[g] * rms(block) * post_weight
+        x_out = rms(h_out) * pre_weight * (1 + scale[g])
+
+    h, block [M, K] bf16 (block None before the first block: x_out from h, and h_out None);
+    weights [K] or None (1); gate, scale [G, K] or None (1 and 0); cu_seqlens int32 [G + 1] row
+    offsets of the groups, or None for one group. Rows outside cu_seqlens are not written. h_out
+    may be h (in place). pre=False leaves x_out out (after the last block). Returns (h_out, x_out)."""
+    M, K, G, h_out = _check_norm(h, block, post_weight, gate, pre_weight, scale, cu_seqlens, h_out)
+    if pre:
+        if x_out is None:
+            x_out = torch.empty_like(h)
+        _need(x_out, "x_out", torch.bfloat16, shape=(M, K))
+    elif x_out is not None:
+        raise ValueError("x_out must be None with pre=False")
+    _devices(h=h, block=block, post_weight=post_weight, gate=gate, pre_weight=pre_weight, scale=scale,
+             cu_seqlens=cu_seqlens, h_out=h_out, x_out=x_out)
+    _launch("svdq_norm_gated", h.device, _p(h), _p(block), _p(post_weight), _p(gate), residual_scale, _p(pre_weight),
+            _p(scale), _p(cu_seqlens), G, M, K, eps, _p(h_out), _p(x_out))
+    return h_out, x_out
+
+
+def norm_gated_int8(h, block=None, post_weight=None, gate=None, residual_scale=1.0, pre_weight=None, scale=None,
+                    cu_seqlens=None, eps=1e-6, h_out=None, smooth=None, codes=None, scales=None):
+    """norm_gated whose x_out leaves as 8-bit codes for gemm_int8, those of
+    quantize_int8(x_out, smooth) bit for bit. Returns (h_out, codes int8 [M, K], scales float32 [M])."""
+    M, K, G, h_out = _check_norm(h, block, post_weight, gate, pre_weight, scale, cu_seqlens, h_out)
+    if smooth is not None:
+        _need(smooth, "smooth", torch.bfloat16, shape=(K,))
+    if codes is None:
+        codes = torch.empty((M, K), dtype=torch.int8, device=h.device)
+    if scales is None:
+        scales = torch.empty(M, dtype=torch.float32, device=h.device)
+    _need(codes, "codes", torch.int8, shape=(M, K))
+    _need(scales, "scales", torch.float32, shape=(M,))
+    _devices(h=h, block=block, post_weight=post_weight, gate=gate, pre_weight=pre_weight, scale=scale,
+             cu_seqlens=cu_seqlens, h_out=h_out, smooth=smooth, codes=codes, scales=scales)
+    _launch("svdq_norm_gated_int8", h.device, _p(h), _p(block), _p(post_weight), _p(gate), residual_scale,
+            _p(pre_weight), _p(scale), _p(cu_seqlens), G, M, K, eps, _p(h_out), _p(smooth), _p(codes), _p(scales))
+    return h_out, codes, scales
+
+
+def _need_heads(t, name, shape=None):
+    """A [tokens, heads, D] bf16 tensor, a view with any token and head strides; the D elements
+    of a head are contiguous."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims [tokens, heads, D], got shape {tuple(t.shape)}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if t.numel() > 0 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    return t
+
+
+def _heads_args(t):
+    return (None, 0, 0) if t is None else (t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def rope_axes(q, k, positions, axis_dims, theta=10000.0, interleaved=True, q_weight=None, k_weight=None, eps=1e-6,
+              q_out=None, k_out=None):
+    """Rotary positions with several axes, after the per-head norm when a weight is given, for
+    q [T, H, D] and k [T, Hk, D] (bf16 views with any token and head strides, as out of a fused
+    qkv buffer; either may be None). positions int32 [T, A]; axis_dims: A even sizes of sum
+    D: the i-th pair of axis a turns by positions[t, a] * theta^(-2i / axis_dims[a]). interleaved: pairs
+    are neighbours, else halves of the head. q_weight, k_weight [D] bf16. q_out / k_out may be q / k
+    themselves (in place). Returns (q_out, k_out)."""
+    if q is None and k is None:
+        raise ValueError("q or k is required")
+    given = q if q is not None else k
+    _need_heads(given, "q" if q is not None else "k")
+    T, _, D = given.shape
+    axis_dims = tuple(int(d) for d in axis_dims)
+    _need(positions, "positions", torch.int32, shape=(T, len(axis_dims)))
+    dev = given.device
+    outs = []
+    for name, t, w, out in (("q", q, q_weight, q_out), ("k", k, k_weight, k_out)):
+        if t is None:
+            if w is not None or out is not None:
+                raise ValueError(f"{name}_weight and {name}_out need {name}")
+            outs.append(None)
+            continue
+        _need_heads(t, name, (T, t.shape[1] if t.dim() == 3 else 0, D))
+        if w is not None:
+            _need(w, f"{name}_weight", torch.bfloat16, shape=(D,))
+        if out is None:
+            out = torch.empty(t.shape, dtype=torch.bfloat16, device=dev)
+        outs.append(_need_heads(out, f"{name}_out", t.shape))
+    _devices(q=q, k=k, positions=positions, q_weight=q_weight, k_weight=k_weight, q_out=outs[0], k_out=outs[1])
+    _launch("svdq_rope_axes", dev, *_heads_args(q), 0 if q is None else q.shape[1], *_heads_args(k),
+            0 if k is None else k.shape[1], _p(q_weight), _p(k_weight), eps, _p(positions),
+            (ctypes.c_int32 * len(axis_dims))(*axis_dims), len(axis_dims), theta, int(bool(interleaved)), T, D,
+            *_heads_args(outs[0]), *_heads_args(outs[1]))
+    return outs[0], outs[1]
+
+
+def attention_packed(q, k, v, cu_seqlens=None, causal=False, scale=None, out=None):
+    """softmax(scale * q k^T) v over whole packed sequences. q [T, H, D], k, v [T, Hk, D] bf16 (views
+    with any token and head strides; H a multiple of Hk, D 64 or 128); cu_seqlens int32 [B + 1] token
+    offsets of the sequences (None: one sequence); causal: a token sees itself and those before it
+    in its sequence. scale defaults to D ** -0.5. Rows of a given `out` outside cu_seqlens are left as
+    they were (a new one is not initialised there). Returns out [T, H, D]."""
+    _need_heads(q, "q")
+    T, H, D = q.shape
+    _need_heads(k, "k")
+    Hk = k.shape[1]
+    _need_heads(k, "k", (T, Hk, D))
+    _need_heads(v, "v", (T, Hk, D))
+    B = 1
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, 1, min_numel=1)
+        B = cu_seqlens.numel() - 1
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
+    _need_heads(out, "out", (T, H, D))
+    _devices(q=q, k=k, v=v, cu_seqlens=cu_seqlens, out=out)
+    _launch("svdq_attention_packed", q.device, *_heads_args(q), *_heads_args(k), *_heads_args(v), _p(cu_seqlens), B,
+            T, H, Hk, D, int(bool(causal)), D ** -0.5 if scale is None else scale, *_heads_args(out))
+    return out

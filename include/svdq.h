@@ -422,6 +422,131 @@ int svdq_linear_mxfp4(const void* x, const void* smooth, const void* w_codes, co
                       size_t workspace_bytes, void* stream);
 
 /*
+ * Linear in 8-bit integers with one scale per token and one per output channel:
+ * the step between the NVFP4 layer and svdq_linear_bf16 for the linears a
+ * mixed-precision model finds too sensitive for 4 bits.
+ *
+ *   v = x * smooth (fp32, exact; smooth NULL = 1), a[m] = max_k |v|,
+ *   codes = rne(v * (127 / a[m])), ascales[m] = a[m] / 127   (fp32 steps; the
+ *     quotients correctly rounded; a zero row gives zero codes and scale 0, and a
+ *     row whose maximum is so small that 127 / a[m] overflows is taken as zero)
+ *   y = bf16( (sum_k codes[m, k] * weight[n, k]) * ascales[m] * wscales[n] + bias[n] )
+ *
+ *   x [M, K] bf16, smooth [K] bf16 or NULL, codes [M, K] int8, ascales [M] fp32,
+ *   weight [N, K] int8, wscales [N] fp32, bias [N] bf16 or NULL, y [M, N] bf16.
+ * The sum over k is exact (int32); the epilogue rounds in fp32 and once to bf16.
+ * svdq_quantize_int8 with a bf16 weight [N, K] as x (and smooth = 1 / the
+ *   layer's smooth) gives weight and wscales: the rule is the same for both.
+ *   Its codes and scales are bit-exact functions of x and smooth.
+ * svdq_gemm_int8: from codes; svdq_linear_int8: the whole layer from x.
+ * K: a positive multiple of 16, at most 131072 (the int32 sum) for the products.
+ * codes, weight: below 2^24 rows and columns; weight codes of -128 are allowed.
+ * workspace: svdq_gemm_int8_workspace_bytes(M, N, K) and
+ *   svdq_linear_int8_workspace_bytes(M, N, K) bytes (0 for some sizes: then it may
+ *   be NULL); no initialisation needed, contents unspecified afterwards.
+ */
+int svdq_quantize_int8(const void* x, const void* smooth, int64_t M, int64_t K, void* codes, void* ascales,
+                       void* stream);
+size_t svdq_gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int svdq_gemm_int8(const void* codes, const void* ascales, const void* weight, const void* wscales,
+                   const void* bias, int64_t M, int64_t N, int64_t K, void* y, void* workspace,
+                   size_t workspace_bytes, void* stream);
+size_t svdq_linear_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int svdq_linear_int8(const void* x, const void* smooth, const void* weight, const void* wscales, const void* bias,
+                     int64_t M, int64_t N, int64_t K, void* y, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/*
+ * The norms before and after a transformer block, fused with the block's gate,
+ * the residual scale and the next block's modulation:
+ *
+ *   rms(z, w)[k] = z[k] / sqrt(mean_k z[k]^2 + eps) * w[k]
+ *   h_out = h + residual_scale * gate[g] * rms(block, post_weight)
+ *   x_out = rms(h_out, pre_weight) * (1 + scale[g])
+ *
+ *   h [M, K] bf16: the residual stream; block [M, K] bf16: the block's output, or
+ *     NULL before the first block (then h_out = h, and h_out must be NULL);
+ *   post_weight, pre_weight [K] bf16 or NULL (= 1); gate, scale [G, K] bf16 or
+ *     NULL (gate = 1, scale = 0);
+ *   cu_seqlens: G + 1 int32 row offsets on the device (row m belongs to group g when
+ *     cu_seqlens[g] <= m < cu_seqlens[g + 1]; not decreasing), or NULL: every row
+ *     is in group 0 and G must be 1. Rows outside [cu_seqlens[0], cu_seqlens[G])
+ *     are left as they were in every output. Offsets outside 0..M cause no access
+ *     outside the tensors.
+ *   h_out [M, K] bf16: required with a block; may be h itself (in place).
+ *   x_out [M, K] bf16, or NULL with a block (after the last one).
+ * The sums run in fp32; x_out is computed from h_out before its rounding to bf16.
+ * K: a positive multiple of 16, at most 32768. eps >= 0, finite; residual_scale finite.
+ * svdq_norm_gated_int8: the same, with x_out rounded to bf16 and quantised as
+ *   svdq_quantize_int8(x_out, smooth) does, bit for bit: codes [M, K] int8 and
+ *   ascales [M] fp32 for svdq_gemm_int8; x itself is not written.
+ */
+int svdq_norm_gated(const void* h, const void* block, const void* post_weight, const void* gate,
+                    float residual_scale, const void* pre_weight, const void* scale, const void* cu_seqlens,
+                    int64_t G, int64_t M, int64_t K, float eps, void* h_out, void* x_out, void* stream);
+int svdq_norm_gated_int8(const void* h, const void* block, const void* post_weight, const void* gate,
+                         float residual_scale, const void* pre_weight, const void* scale, const void* cu_seqlens,
+                         int64_t G, int64_t M, int64_t K, float eps, void* h_out, const void* smooth, void* codes,
+                         void* ascales, void* stream);
+
+/*
+ * Rotary positions with several axes (time, height, width), with the per-head
+ * q/k norm in front of them, for q and k in one call.
+ *
+ *   z = head of q or k; with a weight, z = z / sqrt(mean z^2 + eps) * weight;
+ *   the D/2 pairs are dealt to the axes in order, axis_dims[a] / 2 pairs each; the
+ *   i-th pair (u, w) of axis a turns by angle = positions[t, a] * theta^(-2 i / axis_dims[a]):
+ *     u' = u cos - w sin,  w' = w cos + u sin.
+ *   interleaved != 0: pair p is (z[2p], z[2p+1]); 0: (z[p], z[p + D/2]).
+ *
+ *   q [T, H, D], k [T, Hk, D] bf16 with element strides for token and head, so
+ *     that both can be views of a fused qkv buffer (either may be NULL with 0
+ *     heads); the D elements of a head are contiguous. Strides and pointers
+ *     keep 16-byte alignment (multiples of 8 elements, SVDQ_ERR_ALIGN); heads
+ *     of different tokens must not overlap.
+ *   q_weight, k_weight [D] bf16 or NULL (no norm).
+ *   positions [T, axes] int32 on the device (negative ones are allowed);
+ *   axis_dims: a HOST array of `axes` (1..4) positive even numbers of sum D.
+ *   q_out, k_out: same shapes with their own strides; either may be exactly its
+ *     input (same pointer and strides: in place). Any other overlap with an input or
+ *     the other output is SVDQ_ERR_ALIAS.
+ * Angles are reduced in fp64; norm and rotation run in fp32 with one rounding to
+ * bf16. D: 64 or 128 (SVDQ_ERR_UNSUPPORTED); theta in [1, 1e9]; T * (H + Hk) < 2^31.
+ */
+int svdq_rope_axes(const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t H, const void* k,
+                   int64_t k_stride_t, int64_t k_stride_h, int64_t Hk, const void* q_weight, const void* k_weight,
+                   float eps, const void* positions, const int32_t* axis_dims, int axes, double theta,
+                   int interleaved, int64_t T, int64_t D, void* q_out, int64_t qo_stride_t, int64_t qo_stride_h,
+                   void* k_out, int64_t ko_stride_t, int64_t ko_stride_h, void* stream);
+
+/*
+ * Attention over whole packed sequences, full or causal, with grouped heads:
+ *
+ *   o[t, h] = sum_j softmax_j( scale * q[t, h] . k[j, h / (H / Hk)] ) v[j, h / (H / Hk)]
+ *
+ * over the tokens j of t's own sequence (causal: only j <= t).
+ *   q, o [T, H, D], k, v [T, Hk, D] bf16 with element strides for token and head as
+ *     in svdq_rope_axes (views of a fused qkv buffer are taken as they are).
+ *   cu_seqlens: B + 1 int32 token offsets on the device (sequence b is
+ *     cu_seqlens[b] .. cu_seqlens[b + 1] - 1; not decreasing; empty sequences are
+ *     allowed), or NULL: one sequence of T tokens and B must be 1. Rows of o
+ *     outside [cu_seqlens[0], cu_seqlens[B]) are left as they were. Offsets outside
+ *     0..T cause no access outside the tensors.
+ *   scale: positive and finite. o must not overlap q, k or v.
+ * Scores and softmax statistics are fp32; the probabilities are rounded to bf16
+ * for the second product (relative to a running maximum), their sum is taken of
+ * the rounded values, and o is rounded once to bf16. A non-finite value
+ * reaches no other sequence's rows.
+ * D: 64 or 128; H a multiple of Hk; T below 2^24; H, B at most 65535; token strides below
+ * 2^24 elements. No workspace.
+ */
+int svdq_attention_packed(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
+                          int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                          int64_t v_stride_h, const void* cu_seqlens, int64_t B, int64_t T, int64_t H, int64_t Hk,
+                          int64_t D, int causal, float scale, void* o, int64_t o_stride_t, int64_t o_stride_h,
+                          void* stream);
+
+/*
  * Measurement helpers. Not part of the layer and not from the pages: they
  * calibrate the roofline figures reported beside AMD's published MI355X peaks.
  *

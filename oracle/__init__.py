@@ -27,6 +27,10 @@ in NumPy with float64 / int64 arithmetic:
                  written independently from its definition, so the GPU repack
                  can be compared byte for byte.
 
+* ``block``    - what stands between the linears: the linear in 8-bit integers, the
+                 gated norms around a block, rotary positions with several axes, and
+                 attention over packed sequences.
+
 Parity pins (tests/test_oracle_*.py) tie every function to something other
 than itself: the E2M1 grid and bit structure, the e4m3fn range, exhaustive
 decode tables, torch's float8_e4m3fn cast, exact rational brute force on tiny
@@ -39,4 +43,4 @@ output or test vector, so the activation quantiser is pinned only to the
 readings stated in svdq.py, not to any published artifact.
 """
 
-from . import formats, svdq, repack, prep, mx  # noqa: F401
+from . import formats, svdq, repack, prep, mx, block  # noqa: F401

@@ -1,0 +1,178 @@
+"""GPU: attention over packed sequences against the oracle in float64, element by element within the bound
+that oracle/block.py derives (fp32 scores, probabilities rounded to bf16, fp32 sums), plus the output's own
+bf16 rounding (2^-8)."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import block as B
+
+pytestmark = pytest.mark.gpu
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def make(T, H, Hk, D, seed, sharp=1.0):
+    g = torch.Generator().manual_seed(seed)
+    q = (torch.randn(T, H, D, generator=g) * sharp).bfloat16().cuda()
+    k = torch.randn(T, Hk, D, generator=g).bfloat16().cuda()
+    v = torch.randn(T, Hk, D, generator=g).bfloat16().cuda()
+    return q, k, v
+
+
+def offsets(lens, start=0):
+    return [int(c) for c in np.cumsum([start] + list(lens))]
+
+
+def dev(cu):
+    return torch.tensor(cu, dtype=torch.int32, device="cuda")
+
+
+def check(o, q, k, v, cu=None, causal=False, scale=None):
+    ref, tol, rows = B.attention_packed(f64(q), f64(k), f64(v), cu, causal, scale)
+    tol = (1 + 2.0 ** -8) * tol + 2.0 ** -8 * np.abs(ref)
+    err = np.abs(f64(o) - ref)[rows]
+    assert (err <= tol[rows]).all(), float((err / tol[rows]).max())
+    return torch.from_numpy(rows).cuda()
+
+
+LENGTHS = [[1], [2], [31, 33], [64], [65], [5, 0, 64, 1, 200], [127, 129], [256], [257], [300, 513], [1000], [0, 0, 3, 0],
+           [1] * 70, [17] * 150 + [0] * 20 + [400]]
+
+
+@pytest.mark.parametrize("lens", LENGTHS, ids=lambda x: "-".join(map(str, x[:6])))
+@pytest.mark.parametrize("H,Hk,D", [(4, 2, 128), (3, 3, 64), (5, 1, 128)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_against_oracle(gpu_lib, lens, H, Hk, D, causal):
+    print(f"[attention] {lens[:6]} H={H} Hk={Hk} D={D} causal={causal}", flush=True)
+    T = sum(lens)
+    q, k, v = make(T, H, Hk, D, T + D)
+    cu = offsets(lens)
+    o = gpu_lib.attention_packed(q, k, v, dev(cu), causal=causal)
+    check(o, q, k, v, cu, causal)
+    if len(lens) == 1:
+        assert torch.equal(gpu_lib.attention_packed(q, k, v, causal=causal), o)
+
+
+@pytest.mark.parametrize("T,H,Hk,D,causal", [(2500, 2, 1, 128, False), (2500, 2, 2, 64, True), (4100, 1, 1, 128, True)])
+def test_long(gpu_lib, T, H, Hk, D, causal):
+    print(f"[attention] long {T}", flush=True)
+    q, k, v = make(T, H, Hk, D, 3)
+    check(gpu_lib.attention_packed(q, k, v, causal=causal), q, k, v, None, causal)
+
+
+@pytest.mark.parametrize("sharp", [8.0, 60.0])
+@pytest.mark.parametrize("causal", [False, True])
+def test_peaked_and_growing_scores(gpu_lib, sharp, causal):
+    """Scores up to hundreds: the running maximum moves by more than any fixed step, in every tile."""
+    T, D = 700, 128
+    q, k, v = make(T, 2, 2, D, 5, sharp)
+    ramp = torch.linspace(0.1, 3.0, T, device="cuda")[:, None, None]
+    k = (k * ramp).bfloat16()
+    check(gpu_lib.attention_packed(q, k, v, causal=causal), q, k, v, None, causal)
+    k2 = torch.flip(k, [0])
+    check(gpu_lib.attention_packed(q, k2, v, causal=causal), q, k2, v, None, causal)
+
+
+@pytest.mark.parametrize("scale", [1e-6, 0.02, 1.0])
+def test_scales_and_equal_scores(gpu_lib, scale):
+    q, k, v = make(200, 2, 1, 64, 6)
+    check(gpu_lib.attention_packed(q, k, v, scale=scale), q, k, v, None, False, scale)
+    z = torch.zeros_like(q)
+    check(gpu_lib.attention_packed(z, k, v, scale=scale, causal=True), z, k, v, None, True, scale)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_strided_views(gpu_lib, D):
+    """A fused qkv buffer, head-major storage, and a padded output."""
+    T, H, Hk = 333, 6, 2
+    g = torch.Generator().manual_seed(7)
+    qkv = torch.randn(T, (H + 2 * Hk) * D, generator=g).bfloat16().cuda()
+    q = qkv[:, : H * D].view(T, H, D)
+    k = qkv[:, H * D: (H + Hk) * D].view(T, Hk, D)
+    v = qkv[:, (H + Hk) * D:].view(T, Hk, D)
+    cu = offsets([100, 233])
+    want = gpu_lib.attention_packed(q.contiguous(), k.contiguous(), v.contiguous(), dev(cu))
+    out = torch.full((T, H + 1, D + 8), 3.0, dtype=torch.bfloat16, device="cuda")
+    gpu_lib.attention_packed(q, k, v, dev(cu), out=out[:, :H, :D])
+    assert torch.equal(out[:, :H, :D], want)
+    assert (out[:, H] == 3).all() and (out[:, :, D:] == 3).all()
+    qh, kh, vh = (t.transpose(0, 1).contiguous().transpose(0, 1) for t in (q, k, v))
+    oh = torch.empty(H, T, D, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    gpu_lib.attention_packed(qh, kh, vh, dev(cu), out=oh)
+    assert torch.equal(oh, want)
+    check(want, q, k, v, cu)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_rows_outside_the_sequences_are_left(gpu_lib, causal):
+    T = 500
+    q, k, v = make(T, 3, 1, 128, 8)
+    for cu in ([0, 100, 400], [37, 37, 300], [500, 500, 500], [0, 0, 0], [130, 131, 131, 490]):
+        o = torch.full_like(q, 7.0)
+        gpu_lib.attention_packed(q, k, v, dev(cu), causal=causal, out=o)
+        rows = check(o, q, k, v, cu, causal)
+        assert (o[~rows] == 7).all()
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_other_sequences_values_do_not_leak(gpu_lib, causal):
+    """Infinities and NaN in the neighbours, and behind the last sequence."""
+    q, k, v = make(400, 2, 2, 128, 9)
+    cu = offsets([90, 110, 130])
+    want = gpu_lib.attention_packed(q, k, v, dev(cu), causal=causal)
+    bad = torch.tensor([float("nan"), float("inf"), -float("inf")], device="cuda").bfloat16()
+    for t in (q, k, v):
+        t[:90] = bad[0]
+        t[200:] = bad[1]
+        t[250:] = bad[2]
+        t[330:] = bad[0]
+    got = gpu_lib.attention_packed(q, k, v, dev(cu), causal=causal)
+    assert torch.equal(got[90:200], want[90:200])
+
+
+@pytest.mark.parametrize("cu", [[-9, 50, 1 << 30], [300, 20, 200], [200, 0, 200], [0, 5000, 100], [-1, -1, -1]])
+def test_bad_offsets_stay_inside(gpu_lib, cu):
+    """Offsets outside 0..T or decreasing: results are unspecified, nothing outside is touched."""
+    T = 200
+    q, k, v = make(T, 2, 1, 64, 10)
+    buf = torch.full((3, T, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    gpu_lib.attention_packed(q, k, v, dev(cu), out=buf[1])
+    torch.cuda.synchronize()
+    assert (buf[0] == 7).all() and (buf[2] == 7).all()
+
+
+def test_repeats_streams_and_graph(gpu_lib):
+    q, k, v = make(600, 4, 2, 128, 11)
+    cu = dev(offsets([250, 1, 349]))
+    want = gpu_lib.attention_packed(q, k, v, cu, causal=True)
+    assert torch.equal(gpu_lib.attention_packed(q, k, v, cu, causal=True), want)
+    o = torch.empty_like(want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        o.zero_()
+        gpu_lib.attention_packed(q, k, v, cu, causal=True, out=o)
+    s.synchronize()
+    assert torch.equal(o, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        gpu_lib.attention_packed(q, k, v, cu, causal=True, out=o)
+    for _ in range(4):
+        o.zero_()
+        gpu_lib.attention_packed(q, k, v, cu)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want)
+
+
+def test_empty(gpu_lib):
+    q, k, v = make(4, 2, 1, 64, 12)
+    assert gpu_lib.attention_packed(q[:0], k[:0], v[:0]).shape == (0, 2, 64)
+    o = torch.full_like(q, 2.0)
+    gpu_lib.attention_packed(q, k, v, dev([2]), out=o)
+    assert (o == 2).all()
