@@ -1300,8 +1300,8 @@ struct Int8Ws {
 };
 static Int8Ws int8_ws(int64_t M, int64_t N, int64_t K) {
   Int8Ws w;
-  w.scales = align256((size_t)M * (size_t)K);
-  w.gemm = align256(w.scales + (size_t)M * 4);
+  w.scales = align256(svdq::linear_int8_codes_bytes(M, K));
+  w.gemm = w.scales > 0 ? align256(w.scales + (size_t)M * 4) : 0;
   w.total = w.gemm + svdq::gemm_int8_workspace_bytes(M, N, K);
   return w;
 }
@@ -1324,13 +1324,13 @@ int svdq_linear_int8(const void* x, const void* smooth, const void* weight, cons
   const Int8Ws ws = int8_ws(M, N, K);
   const Range act[] = {range("x", x, (size_t)M * K * 2), range("smooth", smooth, (size_t)K * 2)};
   if ((st = check_int8_gemm(act, 2, weight, wscales, bias, M, N, K, y, workspace, workspace_bytes, ws.total))) return st;
-  uint8_t* w = static_cast<uint8_t*>(workspace);
+  uint8_t* w = static_cast<uint8_t*>(ws.total > 0 ? workspace : nullptr);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t e = svdq::launch_quant_int8(static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(smooth), M, K,
-                                         reinterpret_cast<int8_t*>(w), reinterpret_cast<float*>(w + ws.scales), s);
-  if (int st_ = launched(e, "int8 quantisation", s)) return st_;
-  e = svdq::launch_gemm_int8(int8_args(w, w + ws.scales, weight, wscales, bias, M, N, K, y), w + ws.gemm, s);
-  if (int st_ = launched(e, "int8 gemm", s)) return st_;
+  hipError_t e = svdq::launch_linear_int8(
+      int8_args(nullptr, nullptr, weight, wscales, bias, M, N, K, y), static_cast<const uint16_t*>(x),
+      static_cast<const uint16_t*>(smooth), reinterpret_cast<int8_t*>(w), reinterpret_cast<float*>(w + ws.scales),
+      w + ws.gemm, s);
+  if (int st_ = launched(e, "int8 linear", s)) return st_;
   return ok();
 }
 

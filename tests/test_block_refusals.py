@@ -198,7 +198,7 @@ def test_binding_int8():
     refused("bias must have shape", ops.linear_int8, x, w, ws, bias=z(7))
     refused("smooth must have shape", ops.linear_int8, x, w, ws, smooth=z(16))
     refused("y must have shape", ops.linear_int8, x, w, ws, y=z(4, 9))
-    refused("workspace has", ops.linear_int8, x, w, ws, workspace=z(8, dtype=torch.uint8))
+    refused("workspace has", ops.linear_int8, z(64, 32), w, ws, workspace=z(8, dtype=torch.uint8))
     refused("contiguous", ops.linear_int8, z(32, 4).t(), w, ws)
     refused("ascales must have shape", ops.gemm_int8, z(4, 32, dtype=i8), z(3, dtype=f32), w, ws)
     refused("codes must be", ops.gemm_int8, x, z(4, dtype=f32), w, ws)
