@@ -154,6 +154,23 @@ __device__ __forceinline__ u32x2 int8_codes8(const float (&v)[8], float inv) {
 
 __device__ __forceinline__ u32x4 zero4() { u32x4 z = {0u, 0u, 0u, 0u}; return z; }
 
+// Position of `x` among not decreasing device offsets cu[0 .. n - 1]: the number of them
+// that are <= x. The wave's 64 lanes probe together, so up to 64 offsets cost one load.
+// Offsets out of order give some number in 0..n.
+__device__ __forceinline__ int wave_count_le(const int32_t* cu, int n, int64_t x) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = n;                  // the answer is in [lo, hi]
+  while (hi > lo) {
+    const int step = (hi - lo + 63) / 64;
+    const int idx = lo + (lane + 1) * step - 1;   // the last of this lane's `step` offsets
+    const int count = __popcll(__ballot(idx < hi && cu[idx < hi ? idx : hi - 1] <= x));
+    lo += count * step;
+    if (step == 1) break;
+    hi = hi < lo + step - 1 ? hi : lo + step - 1;
+  }
+  return lo < n ? lo : n;
+}
+
 // Raw buffer resource over [base, base + bytes): loads at an offset at or past
 // `bytes` return zero and stores there are dropped, so bounds checks become
 // offset selects instead of branches. Every access in this library is either

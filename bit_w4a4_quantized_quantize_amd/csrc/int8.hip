@@ -38,11 +38,12 @@ __device__ __forceinline__ void scaled8(const u32x4 x, const u32x4 s, float (&v)
 // row comes from the caches).
 template <bool SMOOTH>
 __global__ __launch_bounds__(256) void quant_int8_kernel(const uint16_t* __restrict__ x,
-                                                         const uint16_t* __restrict__ smooth, int K,
-                                                         int8_t* __restrict__ codes, float* __restrict__ ascales) {
+                                                         const uint16_t* __restrict__ smooth, int64_t M,
+                                                         int K, int8_t* __restrict__ codes, float* __restrict__ ascales) {
   __shared__ float part[4];
   const int tid = threadIdx.x;
-  const size_t row = blockIdx.x;
+  const size_t row = (size_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (row >= (size_t)M) return;
   const u32x4* xr = reinterpret_cast<const u32x4*>(x + row * (size_t)K);
   const u32x4* sm = reinterpret_cast<const u32x4*>(smooth);
   const int nv = K / 8;
@@ -539,11 +540,12 @@ bool few_from_x(int64_t M, int64_t K) {
 
 hipError_t launch_quant_int8(const uint16_t* x, const uint16_t* smooth, int64_t M, int64_t K, int8_t* codes,
                              float* ascales, hipStream_t stream) {
-  const dim3 grid((unsigned)M);
+  const int64_t gx = M < (1 << 20) ? M : (1 << 20);   // gridDim.x * 256 stays below 2^32
+  const dim3 grid((unsigned)gx, (unsigned)((M + gx - 1) / gx));
   if (smooth != nullptr)
-    hipLaunchKernelGGL(quant_int8_kernel<true>, grid, dim3(256), 0, stream, x, smooth, (int)K, codes, ascales);
+    hipLaunchKernelGGL(quant_int8_kernel<true>, grid, dim3(256), 0, stream, x, smooth, M, (int)K, codes, ascales);
   else
-    hipLaunchKernelGGL(quant_int8_kernel<false>, grid, dim3(256), 0, stream, x, smooth, (int)K, codes, ascales);
+    hipLaunchKernelGGL(quant_int8_kernel<false>, grid, dim3(256), 0, stream, x, smooth, M, (int)K, codes, ascales);
   return hipGetLastError();
 }
 

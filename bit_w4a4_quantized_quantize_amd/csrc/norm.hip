@@ -28,17 +28,6 @@ __device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
   return w;
 }
 
-// Group of `row`: the last g with cu[g] <= row, if row < cu[g + 1]; -1 outside.
-__device__ __forceinline__ int row_group(const int32_t* cu, int G, int64_t row) {
-  int lo = 0, hi = G;                       // cu[lo] <= row < cu[hi] if any group has the row
-  if (row < cu[0] || row >= cu[G]) return -1;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cu[mid] <= row) lo = mid; else hi = mid;
-  }
-  return lo;
-}
-
 // sum (or maximum) over the workgroup's NW waves, the same value in every lane
 template <int NW, bool MAX>
 __device__ __forceinline__ float reduce_wg(float v, float* part) {
@@ -56,36 +45,47 @@ __device__ __forceinline__ float reduce_wg(float v, float* part) {
   return v;
 }
 
-// NW waves hold NV 8-element pieces per lane: K <= NW * 64 * NV * 8.
+// A row is held by NW waves of NV 8-element pieces per lane, K <= NW * 64 * NV * 8; with NW = 1
+// a workgroup's four waves take a row each.
 template <int NW, int NV, bool BLOCK>
-__global__ __launch_bounds__(64 * NW) void norm_gated_kernel(NormArgs a) {
+__global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_gated_kernel(NormArgs a) {
   constexpr int kThreads = 64 * NW;
+  constexpr int kRows = NW == 1 ? 4 : 1;
   __shared__ float part[3][NW];
-  const int tid = threadIdx.x;
-  const int64_t row = blockIdx.x;
-  const int g = a.cu != nullptr ? row_group(a.cu, a.G, row) : 0;
-  if (g < 0) return;
+  const int tid = NW == 1 ? threadIdx.x & 63 : threadIdx.x;
+  const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kRows +
+                      (NW == 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) : 0);
+  if (row >= a.M) return;
   const int np = (int)(a.K / 8);
   const size_t base = (size_t)row * (size_t)a.K;
-  const size_t gbase = (size_t)g * (size_t)a.K;
   const float rk = 1.0f / (float)a.K;
   auto piece = [](const uint16_t* p, size_t off, int i) {
     return *reinterpret_cast<const u32x4*>(p + off + 8 * (size_t)i);
   };
 
-  float h[NV][8];
+  // the row's loads go out before its group is looked up
+  u32x4 hw[NV], bw[NV];
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
     const int i = tid + kThreads * u;
-    unpack8(i < np ? piece(a.h, base, i) : zero4(), h[u]);
+    hw[u] = i < np ? piece(a.h, base, i) : zero4();
+    if (BLOCK) bw[u] = i < np ? piece(a.block, base, i) : zero4();
   }
+  int g = 0;
+  if (a.cu != nullptr) {   // the group of the row: one less than the offsets up to it
+    g = wave_count_le(a.cu, a.G + 1, row) - 1;
+    if (g < 0 || g >= a.G) return;
+  }
+  const size_t gbase = (size_t)g * (size_t)a.K;
+  float h[NV][8];
+#pragma unroll
+  for (int u = 0; u < NV; ++u) unpack8(hw[u], h[u]);
   if (BLOCK) {
     float b[NV][8];
     float ss = 0.0f;
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
-      const int i = tid + kThreads * u;
-      unpack8(i < np ? piece(a.block, base, i) : zero4(), b[u]);
+      unpack8(bw[u], b[u]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(b[u][e], b[u][e], ss);
     }
@@ -162,7 +162,9 @@ __global__ __launch_bounds__(64 * NW) void norm_gated_kernel(NormArgs a) {
 
 template <int NW, int NV>
 void launch_norm_cfg(const NormArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)a.M), block(64 * NW);
+  const int64_t wgs = NW == 1 ? (a.M + 3) / 4 : a.M;
+  const int64_t gx = wgs < (1 << 20) ? wgs : (1 << 20);   // gridDim.x * threads stays below 2^32
+  const dim3 grid((unsigned)gx, (unsigned)((wgs + gx - 1) / gx)), block(NW == 1 ? 256 : 64 * NW);
   if (a.block != nullptr)
     hipLaunchKernelGGL((norm_gated_kernel<NW, NV, true>), grid, block, 0, s, a);
   else
@@ -172,8 +174,11 @@ void launch_norm_cfg(const NormArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_norm_gated(const NormArgs& a, hipStream_t stream) {
-  if (a.K <= 2048) launch_norm_cfg<4, 1>(a, stream);
+  if (a.K <= 512) launch_norm_cfg<1, 1>(a, stream);
+  else if (a.K <= 1024) launch_norm_cfg<1, 2>(a, stream);
+  else if (a.K <= 2048) launch_norm_cfg<4, 1>(a, stream);
   else if (a.K <= 4096) launch_norm_cfg<4, 2>(a, stream);
+  else if (a.K <= 8192) launch_norm_cfg<8, 2>(a, stream);
   else if (a.K <= 16384) launch_norm_cfg<16, 2>(a, stream);
   else launch_norm_cfg<16, 4>(a, stream);
   return hipGetLastError();
