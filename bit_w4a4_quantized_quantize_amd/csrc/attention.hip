@@ -24,10 +24,8 @@ namespace {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kWavesA = 8;          // waves of a workgroup, 32 queries each
-constexpr int kBM = 32 * kWavesA;   // queries of a workgroup
 constexpr int kBN = 64;             // keys of a tile
-constexpr int kAhead = 3;           // operand reads in flight ahead of a product
+constexpr int kAhead = 2;           // operand reads in flight ahead of a product
 constexpr float kSlack = 8.0f;      // powers of two that a score may pass the running maximum by
 
 // copies into LDS stay outside template-dependent code (see gemm_mx.hip)
@@ -37,44 +35,56 @@ __device__ __forceinline__ void att_to_lds(__amdgpu_buffer_rsrc_t r, void* lds, 
 __device__ __forceinline__ s16x4 att_read_tr(const uint8_t* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16(ATT_LDS(s16x4, p));
 }
-
-// Tiles are numbered so that sequence b starts at floor(cu[b] / kBM) + b, which needs
-// no prefix sum and leaves at most one unused number per sequence. Returns the
-// sequence of tile `t` (-1: none); the wave's lanes probe 64 offsets at a time.
-__device__ __forceinline__ int tile_sequence(const int32_t* cu, int B, int64_t T, int t) {
-  const int lane = threadIdx.x & 63;
-  int lo = 0, hi = B;
-  while (true) {
-    const int step = (hi - lo + 63) / 64;
-    const int idx = lo + lane * step;
-    bool below = false;
-    if (idx < hi) {
-      const int64_t c = min(max((int64_t)cu[idx], (int64_t)0), T);
-      below = (int)(c / kBM) + idx <= t;
-    }
-    const int n = __popcll(__ballot(below));
-    if (n == 0) return -1;
-    lo = lo + (n - 1) * step;
-    if (step == 1) return lo;
-    hi = min(hi, lo + step);
-  }
-}
-
 __device__ __forceinline__ void att_barrier() {   // as in gemm_bf16.hip: the waits are explicit
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
+template <int N>
+__device__ __forceinline__ void att_wait_copies() {   // vmcnt(N)
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+}
 
-template <int D, bool CAUSAL>
-__global__ __launch_bounds__(64 * kWavesA) void attention_kernel(AttnArgs a) {
+// Tiles of 2^lg queries are numbered so that sequence b starts at floor(cu[b] / 2^lg) + b, which needs
+// no prefix sum and leaves at most one unused number per sequence. Finds the sequence of
+// tile t and its bounds (clamped to 0..T); false where there is none. The wave's lanes probe
+// 64 offsets at a time, so up to 64 sequences cost one load.
+__device__ __forceinline__ bool tile_sequence(const int32_t* cu, int B, int64_t T, int lg, int t, int& b, int& beg,
+                                              int& end) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = B;
+  while (true) {
+    const int step = (hi - lo + 63) / 64;
+    const int idx = lo + lane * step;
+    const int c0 = min(max(cu[min(idx, B)], 0), (int)T), c1 = min(max(cu[min(idx + 1, B)], 0), (int)T);
+    const int n = __popcll(__ballot(idx < hi && (c0 >> lg) + idx <= t));
+    if (n == 0) return false;
+    if (step == 1) {
+      b = lo + n - 1;
+      beg = __builtin_amdgcn_readlane(c0, n - 1);
+      end = __builtin_amdgcn_readlane(c1, n - 1);
+      return true;
+    }
+    lo += (n - 1) * step;
+    hi = min(hi, lo + step);
+  }
+}
+
+// A workgroup of NW waves, each with 32 queries of one head. The waves are dealt to 2^lg_heads
+// query heads of one group first (they share K and V, and short or causal sequences waste less
+// in few rows of many heads), then to rows: 2^lg_rows queries per head.
+template <int D, bool CAUSAL, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a, int lg_heads) {
   constexpr int kRowBytes = 2 * D;
   constexpr int kTileBytes = kBN * kRowBytes;
   constexpr int kPieces = D / 8;                    // 16-byte pieces of a row
   constexpr int kRowsPerCopy = 64 / kPieces;
-  constexpr int kCopies = kTileBytes / 1024 / kWavesA;
+  constexpr int kCopies = kTileBytes / 1024 / NW;
   constexpr int KD = D / 16;                        // 16-element steps of the first product
   constexpr int JD = D / 32;                        // 32-column blocks of the output
+  constexpr int kLgWaves = NW == 8 ? 3 : 2;
+  static_assert(NW == 1 << kLgWaves, "waves");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * kTileBytes];
 
   const int tid = threadIdx.x;
@@ -83,71 +93,63 @@ __global__ __launch_bounds__(64 * kWavesA) void attention_kernel(AttnArgs a) {
   const int h = lane >> 5, l32 = lane & 31;
 
   // heads of one group and the tiles of one head stay on one XCD (its L2 holds their keys)
-  const int tiles = (int)(a.T / kBM) + a.B;
+  const int lg_rows = 5 + kLgWaves - lg_heads;
+  const int tiles = (int)(a.T >> lg_rows) + a.B;
   const int per_xcd = (int)(gridDim.x / 8);
   const int id = (int)(blockIdx.x % 8) * per_xcd + (int)(blockIdx.x / 8);
-  if (id >= tiles * a.H) return;
-  const int head = id / tiles;
+  if (id >= tiles * (a.H >> lg_heads)) return;
+  const int head0 = (id / tiles) << lg_heads;
   const int tile = id % tiles;
-  int b = 0;
-  int64_t beg = 0, end = a.T;
-  if (a.cu != nullptr) {
-    b = tile_sequence(a.cu, a.B, a.T, tile);
-    if (b < 0) return;
-    beg = min(max((int64_t)a.cu[b], (int64_t)0), a.T);
-    end = min(max((int64_t)a.cu[b + 1], (int64_t)0), a.T);
-  }
-  const int len = (int)(end - beg);
-  int local = tile - (int)(beg / kBM) - b;               // tile within the sequence
-  if (local * kBM >= len) return;
-  if (CAUSAL) local = (len - 1) / kBM - local;           // those with the most keys first
-  const int q0 = local * kBM;
-  const int hk = head / (a.H / a.Hk);
-  const int q = q0 + 32 * wave + l32;                    // this lane's query
-  const bool wave_live = q0 + 32 * wave < len;
+  int b = 0, beg = 0, end = (int)a.T;
+  if (a.cu != nullptr && !tile_sequence(a.cu, a.B, a.T, lg_rows, tile, b, beg, end)) return;
+  const int len = end - beg;
+  int local = tile - (beg >> lg_rows) - b;               // tile within the sequence
+  if (len <= 0 || local > (len - 1) >> lg_rows) return;
+  if (CAUSAL) local = ((len - 1) >> lg_rows) - local;    // those with the most keys first
+  const int q0 = local << lg_rows;
+  const int hk = head0 / (a.H / a.Hk);
 
-  // Q^T operand: this lane's query, elements 16 t + 8 h .. + 7
+  // this wave's first row and head, and Q^T's operand (this lane's query, elements
+  // 16 t + 8 h .. + 7)
+  const int row0 = q0 + 32 * (wave >> lg_heads);
+  const int head = head0 + (wave & ((1 << lg_heads) - 1));
   bf16x8 fq[KD];
   {
-    const uint16_t* qp = a.q.p + (beg + min(q, len - 1)) * a.q.st + head * a.q.sh + 8 * h;
+    const uint16_t* qp = a.q.p + (int64_t)(beg + min(row0 + l32, len - 1)) * a.q.st + head * a.q.sh + 8 * h;
 #pragma unroll
     for (int t = 0; t < KD; ++t) fq[t] = *reinterpret_cast<const bf16x8*>(qp + 16 * t);
   }
-
-  const int last_q = min(q0 + kBM, len) - 1;
-  const int nt = (CAUSAL ? last_q : len - 1) / kBN + 1;
+  const int nt = (CAUSAL ? min(q0 + (1 << lg_rows), len) - 1 : len - 1) / kBN + 1;
 
   // Tile copies: row r of K (V) at r * kRowBytes, its 16-byte pieces permuted by
   // piece ^ swz(r) so that the operand reads hit distinct banks: 16 rows at one
-  // piece for K, 4 rows x 4 pieces for V.
+  // piece for K, 4 rows x 4 pieces for V. Rows past the sequence read as zero.
   auto swz_k = [](int r) { return D == 128 ? (r & 15) : ((r >> 1) & 7); };
   auto swz_v = [](int r) { return D == 128 ? ((r & 3) << 2) : (((r >> 1) & 1) << 2); };
-  const uint16_t* kp = a.k.p + beg * a.k.st + hk * a.k.sh;
-  const uint16_t* vp = a.v.p + beg * a.v.st + hk * a.v.sh;
+  const uint16_t* kp = a.k.p + (int64_t)beg * a.k.st + hk * a.k.sh;
+  const uint16_t* vp = a.v.p + (int64_t)beg * a.v.st + hk * a.v.sh;
+  const int kst = (int)a.k.st, vst = (int)a.v.st;
   int koff[kCopies], voff[kCopies];
 #pragma unroll
   for (int c = 0; c < kCopies; ++c) {
-    const int r = (wave + kWavesA * c) * kRowsPerCopy + lane / kPieces;
+    const int r = (wave + NW * c) * kRowsPerCopy + lane / kPieces;
     const int slot = lane % kPieces;
-    koff[c] = r * (int)a.k.st * 2 + (slot ^ swz_k(r)) * 16;
-    voff[c] = r * (int)a.v.st * 2 + (slot ^ swz_v(r)) * 16;
+    koff[c] = r * kst * 2 + (slot ^ swz_k(r)) * 16;
+    voff[c] = r * vst * 2 + (slot ^ swz_v(r)) * 16;
   }
-  // K in two stages, then V in two
   auto load_k = [&](int kt) {
-    const int row0 = kt * kBN;
-    const int rows = min(kBN, len - row0);   // rows past the sequence read as zero
-    const __amdgpu_buffer_rsrc_t r = make_rsrc(kp + row0 * a.k.st, (uint32_t)(((rows - 1) * (int)a.k.st + D) * 2));
-    uint8_t* st = smem + (kt & 1) * kTileBytes;
+    const int rows = min(kBN, len - kt * kBN);
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(kp + (int64_t)kt * kBN * kst, (uint32_t)(((rows - 1) * kst + D) * 2));
+    uint8_t* st = smem + (kt & 1) * (2 * kTileBytes);
 #pragma unroll
-    for (int c = 0; c < kCopies; ++c) att_to_lds(r, st + (wave + kWavesA * c) * 1024, koff[c]);
+    for (int c = 0; c < kCopies; ++c) att_to_lds(r, st + (wave + NW * c) * 1024, koff[c]);
   };
   auto load_v = [&](int kt) {
-    const int row0 = kt * kBN;
-    const int rows = min(kBN, len - row0);
-    const __amdgpu_buffer_rsrc_t r = make_rsrc(vp + row0 * a.v.st, (uint32_t)(((rows - 1) * (int)a.v.st + D) * 2));
-    uint8_t* st = smem + (2 + (kt & 1)) * kTileBytes;
+    const int rows = min(kBN, len - kt * kBN);
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(vp + (int64_t)kt * kBN * vst, (uint32_t)(((rows - 1) * vst + D) * 2));
+    uint8_t* st = smem + (kt & 1) * (2 * kTileBytes) + kTileBytes;
 #pragma unroll
-    for (int c = 0; c < kCopies; ++c) att_to_lds(r, st + (wave + kWavesA * c) * 1024, voff[c]);
+    for (int c = 0; c < kCopies; ++c) att_to_lds(r, st + (wave + NW * c) * 1024, voff[c]);
   };
 
   // operand addresses within a tile
@@ -161,16 +163,6 @@ __global__ __launch_bounds__(64 * kWavesA) void attention_kernel(AttnArgs a) {
     const int piece = 4 * j + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
     vfrag[j] = vrow * kRowBytes + ((piece ^ swz_v(vrow)) * 16) + 8 * (lane & 1);
   }
-
-  f32x16 acc[JD];
-#pragma unroll
-  for (int j = 0; j < JD; ++j)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) acc[j][r] = 0.0f;
-  float m = -1e30f, l = 0.0f, mc = 0.0f;
-  const float c = a.scale * 1.4426950408889634f;   // exponents in base 2
-  const float slack = kSlack / c;
-
   // Operand u of the first product (rows 32 (u % 2) of the tile, elements 16 (u / 2) of the
   // head), and of the second (keys 16 (u / JD), columns 32 (u % JD))
   auto read_k = [&](const uint8_t* sk, int u) {
@@ -182,49 +174,50 @@ __global__ __launch_bounds__(64 * kWavesA) void attention_kernel(AttnArgs a) {
     return __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
   };
   constexpr int NK = 2 * KD, NV = 4 * JD;   // products of a tile
-  const bf16x2_t ones = {(__bf16)1.0f, (__bf16)1.0f};
-  // probabilities of score pair r (0..15) of a tile
-  auto pair = [&](const f32x16 (&s)[2], uint32_t (&p)[16], int r) {
-    const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r >> 3][2 * (r & 7)], c, -mc));
-    const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r >> 3][2 * (r & 7) + 1], c, -mc));
+
+  f32x16 acc[JD];
+#pragma unroll
+  for (int j = 0; j < JD; ++j) acc[j] = f32x16{};
+  float m = -1e30f, l = 0.0f, mc = 0.0f;
+  const float c = a.scale * 1.4426950408889634f;   // exponents in base 2
+  const float slack = kSlack / c;
+
+  // probabilities of score pair r (0..15) of a tile; their sum is taken before they are
+  // rounded to bf16 (v_dot2 on the rounded pairs holds up the matrix unit)
+  auto pair = [&](const f32x16 (&x)[2], uint32_t (&p)[16], int r) {
+    const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r >> 3][2 * (r & 7)], c, -mc));
+    const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r >> 3][2 * (r & 7) + 1], c, -mc));
     p[r] = pack_bf16x2(p0, p1);
-    l = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, p[r]), ones, l, false);
+    l += p0 + p1;
+    asm volatile("" : "+v"(p[r]), "+v"(l));   // made here: not moved to their use
   };
   auto prob_operand = [&](const uint32_t (&p)[16], int t) {
     return __builtin_bit_cast(bf16x8, u32x4{p[4 * t], p[4 * t + 1], p[4 * t + 2], p[4 * t + 3]});
   };
-  auto zero_scores = [&](f32x16 (&s)[2]) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) s[i][r] = 0.0f;
-  };
   // keys past the sequence, or past the query
-  auto mask = [&](f32x16 (&s)[2], int kt) {
-    if (kt * kBN + kBN > len || (CAUSAL && kt * kBN + kBN - 1 > q0 + 32 * wave)) {
-      const int lim = (CAUSAL ? min(q, len - 1) : len - 1) - kt * kBN - 4 * h;
+  auto mask = [&](f32x16 (&x)[2], int kt) {
+    if (kt * kBN + kBN > len || (CAUSAL && kt * kBN + kBN - 1 > row0)) {
+      const int lim = (CAUSAL ? min(row0 + l32, len - 1) : len - 1) - kt * kBN - 4 * h;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (32 * i + 8 * (r >> 2) + (r & 3) > lim) s[i][r] = -__builtin_inff();
+      for (int r = 0; r < 32; ++r) {
+        if (32 * (r >> 4) + 8 * ((r & 15) >> 2) + (r & 3) > lim) x[r >> 4][r & 15] = -__builtin_inff();
+        if (r % 8 == 7) __builtin_amdgcn_sched_barrier(0);   // few condition registers at a time
+      }
     }
   };
-  // the running maximum moves only when a score passes it by more than kSlack powers of
-  // two: until then the probabilities are at most 2^kSlack, with the same relative rounding
-  auto rescale = [&](float mx) {
-    if (__ballot(mx > m + slack) == 0) return;
+  // The running maximum moves only when a score passes it by more than kSlack powers of
+  // two: until then the probabilities are at most 2^kSlack, with the same relative rounding.
+  // Returns the factor for what was accumulated so far (l has it already).
+  auto raise = [&](float mx) {
     mx = fmaxf(mx, __shfl_xor(mx, 32));
     const float mn = fmaxf(m, mx);
     const float alpha = __builtin_amdgcn_exp2f((m - mn) * c);
     m = mn;
-    mc = m * c;
+    mc = mn * c;
     l *= alpha;
-#pragma unroll
-    for (int j = 0; j < JD; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[j][r] *= alpha;
+    return alpha;
   };
+
   // Start of step kt: one barrier frees K(kt) and V(kt - 1) for the copies of K(kt + 2) and
   // V(kt + 1), and publishes K(kt + 1) and V(kt), which were requested a step ago.
   auto next_tiles = [&](int kt) {
@@ -233,103 +226,149 @@ __global__ __launch_bounds__(64 * kWavesA) void attention_kernel(AttnArgs a) {
     if (kt + 2 < nt) load_k(kt + 2);
     if (kt + 1 < nt) load_v(kt + 1);
   };
-  // A step: the next tile's scores on the matrix unit while this tile's probabilities are
-  // made, then the product with V while the maximum of the next scores is found. Each
-  // product is issued with its share of the other work and the operand reads of kAhead
-  // products later.
-  auto step = [&](f32x16 (&cur)[2], f32x16 (&nxt)[2], int kt) {
+  // A step: the next tile's scores on the matrix unit while the second half of this tile's
+  // probabilities is made, then the product with V while the next scores' maximum is found
+  // and the first half of their probabilities is made. The exponentials cost about as
+  // much issue time as the products: spread over both, they hide behind them.
+  auto step = [&](f32x16 (&cur)[2], uint32_t (&pc)[16], f32x16 (&nxt)[2], uint32_t (&pn)[16], int kt) {
     next_tiles(kt);
-    const uint8_t* sk = smem + ((kt + 1) & 1) * kTileBytes;
-    const uint8_t* sv = smem + (2 + (kt & 1)) * kTileBytes;
-    uint32_t p[16];
+    const uint8_t* sk = smem + ((kt + 1) & 1) * (2 * kTileBytes);
+    const uint8_t* sv = smem + (kt & 1) * (2 * kTileBytes) + kTileBytes;
     bf16x8 fk[NK], fv[NV];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) fk[u] = read_k(sk, u);
-    zero_scores(nxt);
+    __builtin_amdgcn_s_setprio(1);   // of the two waves of a SIMD, one runs ahead into the other product
 #pragma unroll
     for (int u = 0; u < NK; ++u) {
       if (u + kAhead < NK) fk[u + kAhead] = read_k(sk, u + kAhead);
       else fv[u + kAhead - NK] = read_v(sv, u + kAhead - NK);
-      nxt[u & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fk[u], fq[u >> 1], nxt[u & 1], 0, 0, 0);
+      nxt[u & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fk[u], fq[u >> 1], u < 2 ? f32x16{} : nxt[u & 1], 0, 0, 0);
 #pragma unroll
-      for (int r = 16 / NK * u; r < 16 / NK * (u + 1); ++r) {
-        pair(cur, p, r);
-        asm volatile("" : "+v"(p[r]));   // made here: not moved down to its use
-      }
+      for (int r = 8 + 8 * u / NK; r < 8 + 8 * (u + 1) / NK; ++r) pair(cur, pc, r);
       __builtin_amdgcn_sched_barrier(0);
     }
+    __builtin_amdgcn_s_setprio(0);
     mask(nxt, kt + 1);
-    float mx = -__builtin_inff();
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
+    constexpr int kMax = NV / 4;   // products that cover the maximum
+    auto value = [&](int u) {
       if (u + kAhead < NV) fv[u + kAhead] = read_v(sv, u + kAhead);
-      acc[u % JD] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fv[u], prob_operand(p, u / JD), acc[u % JD], 0, 0, 0);
+      acc[u % JD] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fv[u], prob_operand(pc, u / JD), acc[u % JD], 0, 0, 0);
+    };
+    float mx = -__builtin_inff(), alpha = 1.0f;
 #pragma unroll
-      for (int r = 32 / NV * u; r < 32 / NV * (u + 1); ++r) mx = fmaxf(mx, nxt[r >> 4][r & 15]);
+    for (int u = 0; u < kMax; ++u) {
+      value(u);
+#pragma unroll
+      for (int r = 32 * u / kMax; r < 32 * (u + 1) / kMax; ++r) mx = fmaxf(mx, nxt[r >> 4][r & 15]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    rescale(mx);
+    const bool up = __ballot(mx > m + slack) != 0;
+    if (up) alpha = raise(mx);
+#pragma unroll
+    for (int u = kMax; u < NV; ++u) {
+      value(u);
+#pragma unroll
+      for (int r = 8 * (u - kMax) / (NV - kMax); r < 8 * (u + 1 - kMax) / (NV - kMax); ++r) pair(nxt, pn, r);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (up) {
+#pragma unroll
+      for (int j = 0; j < JD; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[j][r] *= alpha;
+    }
   };
 
   // tiles this wave needs; the others it only helps to load
-  const int ntw = !wave_live ? 0 : CAUSAL ? min(nt, (q0 + 32 * wave + 31) / kBN + 1) : nt;
+  const int ntw = row0 >= len ? 0 : CAUSAL ? min(nt, (row0 + 31) / kBN + 1) : nt;
   load_k(0);
-  __builtin_amdgcn_s_waitcnt(0x0F70);
-  att_barrier();
   load_v(0);
-  if (nt > 1) load_k(1);
+  if (nt > 1) {
+    load_k(1);
+    att_wait_copies<2 * kCopies>();   // K(0), and Q before it
+  } else {
+    att_wait_copies<kCopies>();
+  }
+  att_barrier();
   int kt = 0;
   if (ntw > 0) {
     f32x16 s0[2], s1[2];
-    zero_scores(s0);
+    uint32_t p0[16], p1[16];
 #pragma unroll
     for (int u = 0; u < NK; ++u)
-      s0[u & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_k(smem, u), fq[u >> 1], s0[u & 1], 0, 0, 0);
+      s0[u & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_k(smem, u), fq[u >> 1], u < 2 ? f32x16{} : s0[u & 1], 0, 0, 0);
     mask(s0, 0);
     float mx = s0[0][0];
 #pragma unroll
     for (int r = 1; r < 32; ++r) mx = fmaxf(mx, s0[r >> 4][r & 15]);
-    rescale(mx);
+    raise(mx);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) pair(s0, p0, r);
     for (; kt + 2 < ntw; kt += 2) {
-      step(s0, s1, kt);
-      step(s1, s0, kt + 1);
+      step(s0, p0, s1, p1, kt);
+      step(s1, p1, s0, p0, kt + 1);
     }
     if (kt + 1 < ntw) {
-      step(s0, s1, kt);
-      s0[0] = s1[0];
+      step(s0, p0, s1, p1, kt);
       s0[1] = s1[1];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) p0[r] = p1[r];
       ++kt;
     }
     next_tiles(kt);   // the last tile
-    const uint8_t* sv = smem + (2 + (kt & 1)) * kTileBytes;
+    const uint8_t* sv = smem + (kt & 1) * (2 * kTileBytes) + kTileBytes;
     ++kt;
-    uint32_t p[16];
 #pragma unroll
-    for (int r = 0; r < 16; ++r) pair(s0, p, r);
+    for (int r = 8; r < 16; ++r) pair(s0, p0, r);
 #pragma unroll
     for (int u = 0; u < NV; ++u)
-      acc[u % JD] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_v(sv, u), prob_operand(p, u / JD), acc[u % JD], 0, 0, 0);
+      acc[u % JD] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_v(sv, u), prob_operand(p0, u / JD), acc[u % JD], 0, 0, 0);
   }
   for (; kt < nt; ++kt) next_tiles(kt);
 
+  // O^T through LDS (the tiles' space): each wave turns its block into rows and stores whole
+  // 16-byte pieces. Row r's pieces are permuted by piece ^ (r % kPieces).
+  __syncthreads();
+  uint8_t* out = smem + wave * (32 * kRowBytes);
+  static_assert(NW * 32 * kRowBytes <= 4 * kTileBytes, "output staging");
   l += __shfl_xor(l, 32);
-  if (q >= len) return;
   const float inv = 1.0f / l;
-  uint16_t* op = a.o + (beg + q) * a.o_st + head * a.o_sh;
 #pragma unroll
   for (int j = 0; j < JD; ++j)
 #pragma unroll
     for (int r = 0; r < 16; r += 4)
-      *reinterpret_cast<u32x2*>(op + 32 * j + 2 * r + 4 * h) =
+      *reinterpret_cast<u32x2*>(out + l32 * kRowBytes + (((4 * j + r / 4) ^ (l32 & (kPieces - 1))) * 16) + 8 * h) =
           u32x2{pack_bf16x2(acc[j][r] * inv, acc[j][r + 1] * inv), pack_bf16x2(acc[j][r + 2] * inv, acc[j][r + 3] * inv)};
+  __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the wave's own writes
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int u = 0; u < 32 / kRowsPerCopy; ++u) {
+    const int r = u * kRowsPerCopy + lane / kPieces, piece = lane % kPieces;
+    const u32x4 w = *reinterpret_cast<const u32x4*>(out + r * kRowBytes + ((piece ^ (r & (kPieces - 1))) * 16));
+    if (row0 + r < len) *reinterpret_cast<u32x4*>(a.o + (int64_t)(beg + row0 + r) * a.o_st + head * a.o_sh + 8 * piece) = w;
+  }
 }
 
+template <int D, int NW>
+void launch_attention_cfg(const AttnArgs& a, hipStream_t s) {
+  // as many heads of a group as divide it, up to the workgroup's waves
+  int lg_heads = 0;
+  while ((2 << lg_heads) <= NW && (a.H / a.Hk) % (2 << lg_heads) == 0) ++lg_heads;
+  const int rows = 32 * NW >> lg_heads;
+  const int64_t total = (a.T / rows + a.B) * (a.H >> lg_heads);
+  const dim3 grid((unsigned)((total + 7) / 8 * 8)), block(64 * NW);
+  if (a.causal) hipLaunchKernelGGL((attention_kernel<D, true, NW>), grid, block, 0, s, a, lg_heads);
+  else hipLaunchKernelGGL((attention_kernel<D, false, NW>), grid, block, 0, s, a, lg_heads);
+}
+
+// Four waves or eight: eight load each tile half as often, four leave two workgroups on a CU,
+// whose starts and ends overlap, and waste less at the ends of short sequences. Measured, 4
+// and 8 waves: 30 heads of 128, one sequence of 16896: 3900 and 3710 us; of 4096: 267 and
+// 270 us; 13 causal prompts of 315 on average, 32 heads on 8: 34.5 and 39.0 us.
 template <int D>
 void launch_attention_d(const AttnArgs& a, hipStream_t s) {
-  const int64_t total = (a.T / kBM + a.B) * a.H;
-  const dim3 grid((unsigned)((total + 7) / 8 * 8)), block(64 * kWavesA);
-  if (a.causal) hipLaunchKernelGGL((attention_kernel<D, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((attention_kernel<D, false>), grid, block, 0, s, a);
+  if (a.T >= 8192 * (int64_t)a.B) launch_attention_cfg<D, 8>(a, s);
+  else launch_attention_cfg<D, 4>(a, s);
 }
 
 }  // namespace

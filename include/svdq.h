@@ -534,9 +534,9 @@ int svdq_rope_axes(const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_
  *     0..T cause no access outside the tensors.
  *   scale: positive and finite. o must not overlap q, k or v.
  * Scores and softmax statistics are fp32; the probabilities are rounded to bf16
- * for the second product (relative to a running maximum), their sum is taken of
- * the rounded values, and o is rounded once to bf16. A non-finite value
- * reaches no other sequence's rows.
+ * for the second product (relative to a running maximum), their sum is taken
+ * before that, and o is rounded once to bf16. A non-finite value reaches no
+ * other sequence's rows.
  * D: 64 or 128; H a multiple of Hk; T below 2^24; H, B at most 65535; token strides below
  * 2^24 elements. No workspace.
  */

@@ -101,10 +101,10 @@ def attention_packed(q, k, v, cu=None, causal=False, scale=None):
     rounding, and the rows that belong to a sequence.
 
     The bound: the device's score is off by at most e_j = scale * (D + 8) * 2^-24 * sum |q| |k_j| (fp32
-    sums, and the exponent's own roundings 2^-21 on its argument), each probability is rounded to
-    bf16 (2^-8) and the sum is taken of the rounded ones, so o is off by at most
-    sum_j p_j (2^-8 + e_j) |v_j - o| (to first order; 5 % on top for the rest), plus the fp32 sum of the
-    second product, (L + 8) * 2^-24 * sum_j p_j |v_j|."""
+    sums) + 2^-21 (the exponent's own roundings), which moves o by at most sum_j p_j e_j |v_j - o|. Each
+    probability is rounded to bf16 (2^-8) for the product with v, the sum that divides it is taken before
+    that: sum_j p_j 2^-8 |v_j|. First order; 5 % on top for the rest, plus the fp32 sums of the second product
+    and of the probabilities, (L + 8) * 2^-24 * sum_j p_j (|v_j| + |o|)."""
     T, H, D = q.shape
     Hk = k.shape[1]
     scale = D ** -0.5 if scale is None else scale
@@ -128,9 +128,8 @@ def attention_packed(q, k, v, cu=None, causal=False, scale=None):
             p = p / p.sum(1, keepdims=True)
             out = p @ vv
             o[r, hd] = out
-            w = p * (2.0 ** -8 + e)
-            # sum_j w_j |v_j - o| <= sqrt(sum w_j) * sqrt(sum_j w_j (v_j - o)^2)
-            sw = w.sum(1, keepdims=True)
-            sq = np.maximum(w @ vv ** 2 - 2 * out * (w @ vv) + sw * out ** 2, 0.0)
-            tol[r, hd] = 1.05 * np.sqrt(sw * sq) + (L + 8) * 2.0 ** -24 * (p @ np.abs(vv)) + 1e-30
+            pe = p * e
+            pv = p @ np.abs(vv)
+            tol[r, hd] = (1.05 * (2.0 ** -8 * pv + pe @ np.abs(vv) + pe.sum(1, keepdims=True) * np.abs(out))
+                          + (L + 8) * 2.0 ** -24 * (pv + np.abs(out)) + 1e-30)
     return o, tol, rows

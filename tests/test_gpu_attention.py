@@ -1,5 +1,5 @@
 """GPU: attention over packed sequences against the oracle in float64, element by element within the bound
-that oracle/block.py derives (fp32 scores, probabilities rounded to bf16, fp32 sums), plus the output's own
+that oracle/block.py derives (fp32 scores and sums, probabilities rounded to bf16), plus the output's own
 bf16 rounding (2^-8)."""
 
 import numpy as np
