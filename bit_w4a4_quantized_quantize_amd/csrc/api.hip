@@ -1563,12 +1563,17 @@ int svdq_rope_axes(const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_
   a.axes = axes;
   a.T = T;
   a.eps = eps;
+  // theta^(-2 j / d) / 2 pi by products of the axis' ratio: the long double's 64 bits leave 63
+  // of them below half a unit of a double
   int p = 0;
-  for (int i = 0; i < axes; ++i)
-    for (int j = 0; j < axis_dims[i] / 2; ++j, ++p) {
+  for (int i = 0; i < axes; ++i) {
+    const long double ratio = powl((long double)theta, -2.0L / axis_dims[i]);
+    long double f = 0.159154943091895335768883763372514362L;
+    for (int j = 0; j < axis_dims[i] / 2; ++j, ++p, f *= ratio) {
       a.axis[p] = (uint8_t)i;
-      a.turns[p] = pow(theta, -2.0 * j / axis_dims[i]) / 6.283185307179586476925;
+      a.turns[p] = (double)f;
     }
+  }
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = svdq::launch_rope(a, (int)D, interleaved != 0, s);
   if (int st_ = launched(e, "rotary positions", s)) return st_;

@@ -34,39 +34,85 @@ __device__ __forceinline__ void scaled8(const u32x4 x, const u32x4 s, float (&v)
   }
 }
 
-// One workgroup per row: the row's maximum, then its codes (the second read of the
-// row comes from the caches).
-template <bool SMOOTH>
-__global__ __launch_bounds__(256) void quant_int8_kernel(const uint16_t* __restrict__ x,
-                                                         const uint16_t* __restrict__ smooth, int64_t M,
-                                                         int K, int8_t* __restrict__ codes, float* __restrict__ ascales) {
-  __shared__ float part[4];
-  const int tid = threadIdx.x;
-  const size_t row = (size_t)blockIdx.y * gridDim.x + blockIdx.x;
-  if (row >= (size_t)M) return;
-  const u32x4* xr = reinterpret_cast<const u32x4*>(x + row * (size_t)K);
+// The row's maximum, then its codes. A row is held in registers by NW waves of NV 8-element
+// pieces per lane (K <= NW * 64 * NV * 8), with NW = 1 a workgroup's four waves take a row each;
+// NV = 0: rows of any length, read twice (the second time from the caches). Memory bound:
+// 4096 x 3840 moves 47 MB.
+template <int NW, int NV, bool SMOOTH>
+__global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void quant_int8_kernel(const uint16_t* __restrict__ x,
+                                                                             const uint16_t* __restrict__ smooth,
+                                                                             int64_t M, int K,
+                                                                             int8_t* __restrict__ codes,
+                                                                             float* __restrict__ ascales) {
+  constexpr int kThreads = 64 * NW;
+  constexpr int kRows = NW == 1 ? 4 : 1;
+  constexpr int kHeld = NV > 0 ? NV : 1;
+  __shared__ float part[NW];
+  const int tid = NW == 1 ? threadIdx.x & 63 : threadIdx.x;
+  const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kRows +
+                      (NW == 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) : 0);
+  if (row >= M) return;
+  const u32x4* xr = reinterpret_cast<const u32x4*>(x + (size_t)row * (size_t)K);
   const u32x4* sm = reinterpret_cast<const u32x4*>(smooth);
   const int nv = K / 8;
   float amax = 0.0f;
-  for (int i = tid; i < nv; i += 256) {
-    float v[8];
-    scaled8<SMOOTH>(xr[i], SMOOTH ? sm[i] : zero4(), v);
+  float v[kHeld][8];
+  if constexpr (NV > 0) {
+    u32x4 w[kHeld], f[kHeld];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+    for (int u = 0; u < NV; ++u) {
+      const int i = tid + kThreads * u;
+      w[u] = i < nv ? xr[i] : zero4();
+      f[u] = SMOOTH && i < nv ? sm[i] : zero4();
+    }
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      scaled8<SMOOTH>(w[u], f[u], v[u]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[u][e]));
+    }
+  } else {
+    for (int i = tid; i < nv; i += kThreads) {
+      scaled8<SMOOTH>(xr[i], SMOOTH ? sm[i] : zero4(), v[0]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[0][e]));
+    }
   }
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor(amax, d));
-  if ((tid & 63) == 0) part[tid >> 6] = amax;
-  __syncthreads();
-  amax = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+  if constexpr (NW > 1) {
+    if ((tid & 63) == 0) part[tid >> 6] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NW; ++w) amax = fmaxf(amax, part[w]);
+  }
   const Int8Scale q = int8_scale(amax);
   if (tid == 0) ascales[row] = q.scale;
-  u32x2* out = reinterpret_cast<u32x2*>(codes + row * (size_t)K);
-  for (int i = tid; i < nv; i += 256) {
-    float v[8];
-    scaled8<SMOOTH>(xr[i], SMOOTH ? sm[i] : zero4(), v);
-    out[i] = int8_codes8(v, q.inv);
+  u32x2* out = reinterpret_cast<u32x2*>(codes + (size_t)row * (size_t)K);
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int i = tid + kThreads * u;
+      if (i < nv) out[i] = int8_codes8(v[u], q.inv);
+    }
+  } else {
+    for (int i = tid; i < nv; i += kThreads) {
+      scaled8<SMOOTH>(xr[i], SMOOTH ? sm[i] : zero4(), v[0]);
+      out[i] = int8_codes8(v[0], q.inv);
+    }
   }
+}
+
+template <int NW, int NV>
+void launch_quant_cfg(const uint16_t* x, const uint16_t* smooth, int64_t M, int64_t K, int8_t* codes, float* ascales,
+                      hipStream_t s) {
+  const int64_t wgs = NW == 1 ? (M + 3) / 4 : M;
+  const int64_t gx = wgs < (1 << 20) ? wgs : (1 << 20);   // gridDim.x * threads stays below 2^32
+  const dim3 grid((unsigned)gx, (unsigned)((wgs + gx - 1) / gx)), block(NW == 1 ? 256 : 64 * NW);
+  if (smooth != nullptr)
+    hipLaunchKernelGGL((quant_int8_kernel<NW, NV, true>), grid, block, 0, s, x, smooth, M, (int)K, codes, ascales);
+  else
+    hipLaunchKernelGGL((quant_int8_kernel<NW, NV, false>), grid, block, 0, s, x, smooth, M, (int)K, codes, ascales);
 }
 
 // (copies into LDS stay outside template-dependent code, see gemm_mx.hip)
@@ -540,12 +586,12 @@ bool few_from_x(int64_t M, int64_t K) {
 
 hipError_t launch_quant_int8(const uint16_t* x, const uint16_t* smooth, int64_t M, int64_t K, int8_t* codes,
                              float* ascales, hipStream_t stream) {
-  const int64_t gx = M < (1 << 20) ? M : (1 << 20);   // gridDim.x * 256 stays below 2^32
-  const dim3 grid((unsigned)gx, (unsigned)((M + gx - 1) / gx));
-  if (smooth != nullptr)
-    hipLaunchKernelGGL(quant_int8_kernel<true>, grid, dim3(256), 0, stream, x, smooth, M, (int)K, codes, ascales);
-  else
-    hipLaunchKernelGGL(quant_int8_kernel<false>, grid, dim3(256), 0, stream, x, smooth, M, (int)K, codes, ascales);
+  if (K <= 1024) launch_quant_cfg<1, 2>(x, smooth, M, K, codes, ascales, stream);
+  else if (K <= 2048) launch_quant_cfg<4, 1>(x, smooth, M, K, codes, ascales, stream);
+  else if (K <= 4096) launch_quant_cfg<4, 2>(x, smooth, M, K, codes, ascales, stream);
+  else if (K <= 8192) launch_quant_cfg<8, 2>(x, smooth, M, K, codes, ascales, stream);
+  else if (K <= 12288) launch_quant_cfg<8, 3>(x, smooth, M, K, codes, ascales, stream);
+  else launch_quant_cfg<8, 0>(x, smooth, M, K, codes, ascales, stream);
   return hipGetLastError();
 }
 

@@ -680,13 +680,14 @@ def linear_mxfp4(x, w: "SVDQLinearWeights", w_codes, w_scales, y=None, workspace
 
 # the current stream's handle without the Stream object around it (1.6 us less per call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _stream
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _launch(name, dev, *args):
     """Call the C entry point `name` on dev's current stream, with dev the current HIP device."""
     fn = getattr(_lib.lib(), name)
     index = dev.index
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -716,7 +717,7 @@ def quantize_int8(x, smooth=None, codes=None, scales=None):
         _need(smooth, "smooth", torch.bfloat16, shape=(K,))
     dev = x.device
     if codes is None:
-        codes = torch.empty((M, K), dtype=torch.int8, device=dev)
+        codes = torch.empty_like(x, dtype=torch.int8)
     if scales is None:
         scales = torch.empty(M, dtype=torch.float32, device=dev)
     _need(codes, "codes", torch.int8, shape=(M, K))
@@ -842,7 +843,7 @@ def norm_gated_int8(h, block=None, post_weight=None, gate=None, residual_scale=1
     if smooth is not None:
         _need(smooth, "smooth", torch.bfloat16, shape=(K,))
     if codes is None:
-        codes = torch.empty((M, K), dtype=torch.int8, device=h.device)
+        codes = torch.empty_like(h, dtype=torch.int8)
     if scales is None:
         scales = torch.empty(M, dtype=torch.float32, device=h.device)
     _need(codes, "codes", torch.int8, shape=(M, K))
@@ -855,23 +856,23 @@ def norm_gated_int8(h, block=None, post_weight=None, gate=None, residual_scale=1
 
 
 def _need_heads(t, name, shape=None):
-    """A [tokens, heads, D] bf16 tensor, a view with any token and head strides; the D elements
-    of a head are contiguous."""
+    """Check a [tokens, heads, D] bf16 tensor, a view with any token and head strides (the D
+    elements of a head are contiguous), and return it as the C ABI takes it: pointer, strides."""
     if t is None:
         raise ValueError(f"{name} is required")
     if t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must have 3 dims [tokens, heads, D], got shape {tuple(t.shape)}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    if t.numel() > 0 and t.stride(2) != 1:
+    have, strides = t.shape, t.stride()
+    if len(have) != 3:
+        raise ValueError(f"{name} must have 3 dims [tokens, heads, D], got shape {tuple(have)}")
+    if shape is not None and have != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(have)}")
+    if strides[2] != 1 and t.numel() > 0:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
-    return t
+    return t.data_ptr(), strides[0], strides[1]
 
 
-def _heads_args(t):
-    return (None, 0, 0) if t is None else (t.data_ptr(), t.stride(0), t.stride(1))
+_NO_HEADS = (None, 0, 0)
 
 
 def rope_axes(q, k, positions, axis_dims, theta=10000.0, interleaved=True, q_weight=None, k_weight=None, eps=1e-6,
@@ -881,34 +882,41 @@ def rope_axes(q, k, positions, axis_dims, theta=10000.0, interleaved=True, q_wei
     qkv buffer; either may be None). positions int32 [T, A]; axis_dims: A even sizes of sum
     D: the i-th pair of axis a turns by positions[t, a] * theta^(-2i / axis_dims[a]). interleaved: pairs
     are neighbours, else halves of the head. q_weight, k_weight [D] bf16. q_out / k_out may be q / k
-    themselves (in place). Returns (q_out, k_out)."""
+    themselves (in place); new ones are laid out like their input. Returns (q_out, k_out)."""
     if q is None and k is None:
         raise ValueError("q or k is required")
     given = q if q is not None else k
-    _need_heads(given, "q" if q is not None else "k")
+    qa, ka, qoa, koa, H, Hk = _NO_HEADS, _NO_HEADS, _NO_HEADS, _NO_HEADS, 0, 0
+    if q is not None:
+        qa = _need_heads(q, "q")
+        H = q.shape[1]
+    if k is not None:
+        ka = _need_heads(k, "k")
+        Hk = k.shape[1]
     T, _, D = given.shape
-    axis_dims = tuple(int(d) for d in axis_dims)
+    if q is not None and k is not None and (k.shape[0] != T or k.shape[2] != D):
+        raise ValueError(f"k must have shape {[T, Hk, D]}, got {list(k.shape)}")
+    axis_dims = tuple(axis_dims)
     _need(positions, "positions", torch.int32, shape=(T, len(axis_dims)))
-    dev = given.device
-    outs = []
-    for name, t, w, out in (("q", q, q_weight, q_out), ("k", k, k_weight, k_out)):
-        if t is None:
-            if w is not None or out is not None:
-                raise ValueError(f"{name}_weight and {name}_out need {name}")
-            outs.append(None)
-            continue
-        _need_heads(t, name, (T, t.shape[1] if t.dim() == 3 else 0, D))
-        if w is not None:
-            _need(w, f"{name}_weight", torch.bfloat16, shape=(D,))
-        if out is None:
-            out = torch.empty(t.shape, dtype=torch.bfloat16, device=dev)
-        outs.append(_need_heads(out, f"{name}_out", t.shape))
-    _devices(q=q, k=k, positions=positions, q_weight=q_weight, k_weight=k_weight, q_out=outs[0], k_out=outs[1])
-    _launch("svdq_rope_axes", dev, *_heads_args(q), 0 if q is None else q.shape[1], *_heads_args(k),
-            0 if k is None else k.shape[1], _p(q_weight), _p(k_weight), eps, _p(positions),
-            (ctypes.c_int32 * len(axis_dims))(*axis_dims), len(axis_dims), theta, int(bool(interleaved)), T, D,
-            *_heads_args(outs[0]), *_heads_args(outs[1]))
-    return outs[0], outs[1]
+    if q_weight is not None:
+        _need(q_weight, "q_weight", torch.bfloat16, shape=(D,))
+    if k_weight is not None:
+        _need(k_weight, "k_weight", torch.bfloat16, shape=(D,))
+    if q is not None:
+        q_out = torch.empty_like(q) if q_out is None else q_out
+        qoa = _need_heads(q_out, "q_out", q.shape)
+    elif q_weight is not None or q_out is not None:
+        raise ValueError("q_weight and q_out need q")
+    if k is not None:
+        k_out = torch.empty_like(k) if k_out is None else k_out
+        koa = _need_heads(k_out, "k_out", k.shape)
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("k_weight and k_out need k")
+    _devices(q=q, k=k, positions=positions, q_weight=q_weight, k_weight=k_weight, q_out=q_out, k_out=k_out)
+    _launch("svdq_rope_axes", given.device, *qa, H, *ka, Hk, _p(q_weight), _p(k_weight), eps, positions.data_ptr(),
+            (ctypes.c_int32 * len(axis_dims))(*axis_dims), len(axis_dims), theta, 1 if interleaved else 0, T, D, *qoa,
+            *koa)
+    return q_out, k_out
 
 
 def attention_packed(q, k, v, cu_seqlens=None, causal=False, scale=None, out=None):
@@ -916,21 +924,22 @@ def attention_packed(q, k, v, cu_seqlens=None, causal=False, scale=None, out=Non
     with any token and head strides; H a multiple of Hk, D 64 or 128); cu_seqlens int32 [B + 1] token
     offsets of the sequences (None: one sequence); causal: a token sees itself and those before it
     in its sequence. scale defaults to D ** -0.5. Rows of a given `out` outside cu_seqlens are left as
-    they were (a new one is not initialised there). Returns out [T, H, D]."""
-    _need_heads(q, "q")
+    they were (a new one, laid out like q, is not initialised there). Returns out [T, H, D]."""
+    qa = _need_heads(q, "q")
     T, H, D = q.shape
-    _need_heads(k, "k")
+    ka = _need_heads(k, "k")
     Hk = k.shape[1]
-    _need_heads(k, "k", (T, Hk, D))
-    _need_heads(v, "v", (T, Hk, D))
+    if k.shape[0] != T or k.shape[2] != D:
+        raise ValueError(f"k must have shape {[T, Hk, D]}, got {list(k.shape)}")
+    va = _need_heads(v, "v", k.shape)
     B = 1
     if cu_seqlens is not None:
         _need(cu_seqlens, "cu_seqlens", torch.int32, 1, min_numel=1)
         B = cu_seqlens.numel() - 1
     if out is None:
-        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
-    _need_heads(out, "out", (T, H, D))
+        out = torch.empty_like(q)
+    oa = _need_heads(out, "out", q.shape)
     _devices(q=q, k=k, v=v, cu_seqlens=cu_seqlens, out=out)
-    _launch("svdq_attention_packed", q.device, *_heads_args(q), *_heads_args(k), *_heads_args(v), _p(cu_seqlens), B,
-            T, H, Hk, D, int(bool(causal)), D ** -0.5 if scale is None else scale, *_heads_args(out))
+    _launch("svdq_attention_packed", q.device, *qa, *ka, *va, _p(cu_seqlens), B, T, H, Hk, D, 1 if causal else 0,
+            D ** -0.5 if scale is None else scale, *oa)
     return out
