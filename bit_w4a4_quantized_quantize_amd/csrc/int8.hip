@@ -274,9 +274,12 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_int8_kernel(Int8GemmArgs a,
       for (int kp = p0; kp < p1; ++kp) {
         const uint8_t* cur = smem + ((kp - p0) % S) * C::kStageBytes;
         const uint8_t* nxt = smem + ((kp + 1 - p0) % S) * C::kStageBytes;
+        // a SIMD's waves run out of step by priority (128 x 128 tiles at 2048 x 3840: 39 -> 35 us)
+        __builtin_amdgcn_s_setprio(1);
         step(fr[0], fr[1], cur, 1, true);
         step(fr[1], fr[0], cur, 2, true);
         step(fr[0], fr[1], cur, 3, true);
+        __builtin_amdgcn_s_setprio(0);
         // this stage has been read to the end and panel kp + 1 has landed: publish it, then
         // refill this stage while the last step multiplies
         wait_panel(min(S - 2, p1 - 2 - kp));
@@ -539,7 +542,7 @@ struct I8Plan {
 
 I8Plan plan_int8(int64_t M, int64_t N, int64_t K) {
   static const struct { int bm, bn; double share, least; } shapes[] = {
-      {256, 320, 2.2, 2.2}, {256, 256, 1.85, 1.85}, {128, 128, 0.54, 0.75}, {128, 64, 0.37, 0.37}, {64, 64, 0.23, 0.29}};
+      {256, 320, 2.2, 2.2}, {256, 256, 1.85, 1.85}, {128, 128, 0.5, 0.72}, {128, 64, 0.33, 0.39}, {64, 64, 0.23, 0.29}};
   const int64_t panels = (K + 127) / 128;
   I8Plan best{0, 1, (int)panels};
   double best_t = 1e300;
