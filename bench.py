@@ -66,6 +66,14 @@ FFN_BLOCKS = {
 }
 
 
+# the attention half of a DiT block between two norms: tokens, width, heads, text tokens
+ATTN_BLOCKS = {
+    "attn_block_1024": (dict(M=4096, K=3840, H=30, text=0), "DiT attention half-block at 1024^2"),
+    "attn_block_2048": (dict(M=16384 + 512, K=3840, H=30, text=512),
+                        "DiT attention half-block at 2048px (16384 image + 512 text tokens)"),
+}
+
+
 # the mixed-precision linear sweep of a whole DiT forward (bf16 and W4A4 layers)
 SWEEPS = {
     "dit_sweep_1024": "DiT mixed-precision linear sweep at 1024^2: 30 blocks x {qkv, out, w1, w3, w2}, "
@@ -308,7 +316,7 @@ def parse():
     p = argparse.ArgumentParser()
     p.add_argument("--workload",
                    choices=sorted(WORKLOADS) + sorted(FFN_BLOCKS) + sorted(SWEEPS) + sorted(PREPS) + sorted(MX_VARIANTS)
-                   + sorted(CALIBS) + sorted(ORACLE_TIMES) + sorted(STATIC_VARIANTS),
+                   + sorted(CALIBS) + sorted(ORACLE_TIMES) + sorted(STATIC_VARIANTS) + sorted(ATTN_BLOCKS),
                    default=DEFAULT_WORKLOAD,
                    help="layer shape (the default is the headline workload; the rest are for comparison)")
     p.add_argument("--gpus", type=int, default=1)
@@ -877,6 +885,104 @@ def run_ffn_block(args):
     print(json.dumps(result), flush=True)
 
 
+def run_attn_block(args):
+    """The attention half of a block with its linears in 8 bits: the norm that makes qkv's codes,
+    qkv, rotary positions with the q/k norm (in place), attention, the out projection, and the
+    gated norm that ends the half and starts the next."""
+    import torch
+
+    from bit_w4a4_quantized_quantize_amd import ops
+
+    dev = torch.device("cuda:0")
+    torch.cuda.set_device(dev)
+    stream = torch.cuda.current_stream(dev)
+    cfg, desc = ATTN_BLOCKS[args.workload]
+    M, K, H, text = cfg["M"], cfg["K"], cfg["H"], cfg["text"]
+    D = K // H
+    axes = (D // 4, 3 * D // 8, 3 * D // 8)   # text index (or frame), row, column
+    bf = torch.bfloat16
+    n_sets = 1 if args.warm else min(args.sets, 3)
+    side = math.isqrt(M - text)
+    j = torch.arange(M, device=dev)
+    i = (j - text).clamp_min(0)
+    pos = torch.stack([torch.where(j < text, j, text), i // side, i % side], 1).to(torch.int32)
+    cu = torch.tensor([0, M], dtype=torch.int32, device=dev)
+    sets = []
+    for seed in range(n_sets):
+        g = torch.Generator(device=dev).manual_seed(8100 + seed)
+        rnd = lambda *shape: torch.randn(*shape, generator=g, device=dev)  # noqa: E731
+        h = rnd(M, K)
+        h[:, torch.randperm(K, generator=g, device=dev)[: K // 100]] *= 20.0
+        qkv = torch.empty(M, 3 * K, dtype=bf, device=dev)
+        q, k, v = (t.view(M, H, D) for t in qkv.split(K, 1))
+        wqkv, wout = (rnd(3 * K, K) * 0.02).to(bf), (rnd(K, K) * 0.02).to(bf)
+        e = dict(h=h.to(bf), qkv=qkv, q=q, k=k, v=v, wqkv=wqkv, wout=wout, qkv8=ops.quantize_int8(wqkv),
+                 out8=ops.quantize_int8(wout), bias=(rnd(K) * 0.01).to(bf), pre=(1 + 0.1 * rnd(K)).to(bf),
+                 post=(1 + 0.1 * rnd(K)).to(bf), pre2=(1 + 0.1 * rnd(K)).to(bf), gate=rnd(1, K).tanh().to(bf),
+                 scale=(0.3 * rnd(1, K)).to(bf), scale2=(0.3 * rnd(1, K)).to(bf), qw=(1 + 0.1 * rnd(D)).to(bf),
+                 kw=(1 + 0.1 * rnd(D)).to(bf), codes=torch.empty(M, K, dtype=torch.int8, device=dev),
+                 cs=torch.empty(M, device=dev), o=torch.empty(M, H, D, dtype=bf, device=dev),
+                 y=torch.empty(M, K, dtype=bf, device=dev), h2=torch.empty(M, K, dtype=bf, device=dev),
+                 x2=torch.empty(M, K, dtype=bf, device=dev))
+        e["ws"] = torch.empty(max(1, ops.gemm_int8_workspace_bytes(M, 3 * K, K),
+                                  ops.linear_int8_workspace_bytes(M, K, K)), dtype=torch.uint8, device=dev)
+        sets.append(e)
+
+    parts = {
+        "norm_to_codes": lambda e: ops.norm_gated_int8(e["h"], pre_weight=e["pre"], scale=e["scale"], codes=e["codes"],
+                                                       scales=e["cs"]),
+        "qkv_int8": lambda e: ops.gemm_int8(e["codes"], e["cs"], *e["qkv8"], y=e["qkv"], workspace=e["ws"]),
+        "rope": lambda e: ops.rope_axes(e["q"], e["k"], pos, axes, theta=256.0, q_weight=e["qw"], k_weight=e["kw"],
+                                        q_out=e["q"], k_out=e["k"]),
+        "attention": lambda e: ops.attention_packed(e["q"], e["k"], e["v"], cu, out=e["o"]),
+        "out_int8": lambda e: ops.linear_int8(e["o"].view(M, K), *e["out8"], bias=e["bias"], y=e["y"],
+                                              workspace=e["ws"]),
+        "norm_gated": lambda e: ops.norm_gated(e["h"], e["y"], post_weight=e["post"], gate=e["gate"],
+                                               pre_weight=e["pre2"], scale=e["scale2"], h_out=e["h2"], x_out=e["x2"]),
+    }
+
+    def step(n):
+        for part in parts.values():
+            part(sets[n])
+
+    flops = 2 * M * K * 4 * K + 4 * M * M * K
+    ms_per_step, cond = timed(step, n_sets, args.steps, stream, warmup=args.warmup, min_ms=args.condition_ms)
+    tflops = flops / (ms_per_step * 1e-3) / 1e12
+    kw = max(1, args.warmup // 2)
+    iters = max(10, args.kernel_iters // 4)
+    part_us = {name: round(time_loop(lambda n, f=f: f(sets[n]), n_sets, iters, kw, stream) * 1e3, 2)
+               for name, f in parts.items()}
+    # the same two linears kept in bf16, from the bf16 norm output
+    x = ops.norm_gated(sets[0]["h"], pre_weight=sets[0]["pre"], scale=sets[0]["scale"])[1]
+    part_us["qkv_bf16"] = round(time_loop(lambda n: ops.linear_bf16(x, sets[n]["wqkv"], y=sets[n]["qkv"]), n_sets,
+                                          iters, kw, stream) * 1e3, 2)
+    part_us["out_bf16"] = round(time_loop(lambda n: ops.linear_bf16(sets[n]["o"].view(M, K), sets[n]["wout"],
+                                                                    y=sets[n]["y"]), n_sets, iters, kw, stream) * 1e3, 2)
+    print(f"[bench] attention half-block: {ms_per_step * 1e3:.1f} us/step, {tflops:.1f} TFLOP/s "
+          f"(conditioned {cond['conditioning_ms']:.1f} ms); parts in us: {part_us}", file=sys.stderr, flush=True)
+    att = 4 * M * M * K / (part_us["attention"] * 1e-6) / 1e12
+    print(json.dumps({
+        "metric": f"attention half-block (norms, 8-bit qkv/out, rotary, attention) TFLOP/s at M={M},K={K},H={H}, 1 GPU",
+        "value": round(tflops, 2),
+        "unit": "TFLOP/s",
+        "n_gpus": 1,
+        "steps": args.steps,
+        "warmup": args.warmup,
+        "ms_per_step": round(ms_per_step, 5),
+        "higher_is_better": True,
+        "scaling": "weak",
+        "vs_baseline": None,
+        "dtype": "int8 linears, bf16 attention",
+        "data": "synthetic",
+        "config": {"workload": f"{desc}: M={M} K={K} heads={H} of {D}, rotary axes {list(axes)}, full attention",
+                   "cache": "warm" if args.warm else f"cold (rotating {n_sets} sets)", "flop_per_step": flops},
+        "roofline": {"kernel": "attention_kernel", "bound": "mfma", "achieved": round(att, 2),
+                     "peak": PEAK_F16_MFMA_TFLOPS, "unit": "TFLOP/s", "frac": round(att / PEAK_F16_MFMA_TFLOPS, 4),
+                     "traffic": None, "flop_per_launch": 4 * M * M * K, "avg_launch_us": part_us["attention"]},
+        "part_us": part_us,
+    }), flush=True)
+
+
 def sweep_build(dev, n_fwd, keep_prequant=False):
     """Weights of the sweep's 150 linears and fresh activations for n_fwd forwards, drawn on
     the device (torch's generator, seeded per layer / per (forward, layer)) with the
@@ -1389,6 +1495,11 @@ def main():
             print("bench.py: --gpus must be 1 (single-GPU build)", file=sys.stderr)
             sys.exit(2)
         return run_sweep(args)
+    if args.workload in ATTN_BLOCKS:
+        if args.gpus != 1 or int(os.environ.get("WORLD_SIZE", "1")) > 1:
+            print("bench.py: --gpus must be 1 (single-GPU build)", file=sys.stderr)
+            sys.exit(2)
+        return run_attn_block(args)
     if args.workload in FFN_BLOCKS:
         if args.gpus != 1 or int(os.environ.get("WORLD_SIZE", "1")) > 1:
             print("bench.py: --gpus must be 1 (single-GPU build)", file=sys.stderr)

@@ -1206,6 +1206,8 @@ static int check_int8_mnk(int64_t M, int64_t N, int64_t K) {
   if (st) return st;
   if (N < 0) return fail(SVDQ_ERR_SHAPE, "N = %lld is negative", (long long)N);
   if (N > kMaxDim) return fail(SVDQ_ERR_UNSUPPORTED, "dimension above 2^24 (N=%lld)", (long long)N);
+  if (M * N > (int64_t(1) << 38))
+    return fail(SVDQ_ERR_UNSUPPORTED, "more than 2^38 outputs (M=%lld N=%lld)", (long long)M, (long long)N);
   if (K > svdq::kInt8MaxK)
     return fail(SVDQ_ERR_UNSUPPORTED, "K = %lld: the int32 sums of the 8-bit product hold K up to %lld", (long long)K,
                 (long long)svdq::kInt8MaxK);
@@ -1594,7 +1596,10 @@ int svdq_attention_packed(const void* q, int64_t q_stride_t, int64_t q_stride_h,
                                           (long long)B);
   if (cu_seqlens == nullptr && B != 1)
     return fail(SVDQ_ERR_INVALID, "B = %lld sequences need cu_seqlens", (long long)B);
-  if (!(scale > 0.0f && scale <= 3.4e38f)) return fail(SVDQ_ERR_INVALID, "scale = %g must be positive and finite", scale);
+  if (!(scale > 0.0f && scale <= 1048576.0f)) return fail(SVDQ_ERR_INVALID, "scale = %g is not in (0, 2^20]", scale);
+  if (2 * T * H + 512 * B * H >= (int64_t(1) << 32))   // work items of the grid
+    return fail(SVDQ_ERR_UNSUPPORTED, "2 T H + 512 B H must be below 2^32 (T=%lld B=%lld H=%lld)", (long long)T,
+                (long long)B, (long long)H);
   if (T == 0 || B == 0) return ok();
   Heads hq, hk, hv, ho;
   if ((st = make_heads(&hq, "q", q, q_stride_t, q_stride_h, T, H, D))) return st;

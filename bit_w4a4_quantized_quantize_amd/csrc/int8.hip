@@ -582,7 +582,8 @@ constexpr int kFewTokens = 32;
 // 8 x 3840, 12.3 and 9.5 us for 12 x 3840 on the device alone; one launch saves another 3 us
 // of the caller's time where the calls are not in a graph.
 bool few_from_x(int64_t M, int64_t K) {
-  return M <= kFewTokens && M * K <= 40960 && M * few_pitch((int)K) <= 56 * 1024;
+  // codes and sums together stay inside 64 KB of LDS
+  return M <= kFewTokens && M * K <= 40960 && M * few_pitch((int)K) <= 46 * 1024;
 }
 
 }  // namespace

@@ -440,7 +440,7 @@ int svdq_linear_mxfp4(const void* x, const void* smooth, const void* w_codes, co
  *   Its codes and scales are bit-exact functions of x and smooth.
  * svdq_gemm_int8: from codes; svdq_linear_int8: the whole layer from x.
  * K: a positive multiple of 16, at most 131072 (the int32 sum) for the products.
- * codes, weight: below 2^24 rows and columns; weight codes of -128 are allowed.
+ * M, N: at most 2^24, M * N at most 2^38; weight codes of -128 are allowed.
  * workspace: svdq_gemm_int8_workspace_bytes(M, N, K) and
  *   svdq_linear_int8_workspace_bytes(M, N, K) bytes (0 for some sizes: then it may
  *   be NULL); no initialisation needed, contents unspecified afterwards.
@@ -476,7 +476,8 @@ int svdq_linear_int8(const void* x, const void* smooth, const void* weight, cons
  *   h_out [M, K] bf16: required with a block; may be h itself (in place).
  *   x_out [M, K] bf16, or NULL with a block (after the last one).
  * The sums run in fp32; x_out is computed from h_out before its rounding to bf16.
- * K: a positive multiple of 16, at most 32768. eps >= 0, finite; residual_scale finite.
+ * K: a positive multiple of 16, at most 32768. eps >= 0, finite; residual_scale finite. The sums of
+ * squares must stay inside fp32 (elements below about 1e17).
  * svdq_norm_gated_int8: the same, with x_out rounded to bf16 and quantised as
  *   svdq_quantize_int8(x_out, smooth) does, bit for bit: codes [M, K] int8 and
  *   ascales [M] fp32 for svdq_gemm_int8; x itself is not written.
@@ -532,13 +533,13 @@ int svdq_rope_axes(const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_
  *     allowed), or NULL: one sequence of T tokens and B must be 1. Rows of o
  *     outside [cu_seqlens[0], cu_seqlens[B]) are left as they were. Offsets outside
  *     0..T cause no access outside the tensors.
- *   scale: positive and finite. o must not overlap q, k or v.
+ *   scale in (0, 2^20]. o must not overlap q, k or v.
  * Scores and softmax statistics are fp32; the probabilities are rounded to bf16
  * for the second product (relative to a running maximum), their sum is taken
  * before that, and o is rounded once to bf16. A non-finite value reaches no
  * other sequence's rows.
- * D: 64 or 128; H a multiple of Hk; T below 2^24; H, B at most 65535; token strides below
- * 2^24 elements. No workspace.
+ * D: 64 or 128; H a multiple of Hk; T below 2^24; H, B at most 65535; 2 T H + 512 B H
+ * below 2^32; token strides below 2^24 elements. No workspace.
  */
 int svdq_attention_packed(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
                           int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,

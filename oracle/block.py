@@ -96,9 +96,10 @@ def rope_axes(z, positions, axis_dims, theta=10000.0, interleaved=True, weight=N
     return out, mag
 
 
-def attention_packed(q, k, v, cu=None, causal=False, scale=None):
+def attention_packed(q, k, v, cu=None, causal=False, scale=None, queries=None):
     """(o, tol, rows): o [T, H, D] in float64, a bound on the device's error before the final
-    rounding, and the rows that belong to a sequence.
+    rounding, and the rows that belong to a sequence (of `queries`, token numbers, if given: the others
+    are left zero).
 
     The bound: the device's score is off by at most e_j = scale * (D + 8) * 2^-24 * sum |q| |k_j| (fp32
     sums) + 2^-21 (the exponent's own roundings), which moves o by at most sum_j p_j e_j |v_j - o|. Each
@@ -117,19 +118,22 @@ def attention_packed(q, k, v, cu=None, causal=False, scale=None):
         L = cu[b + 1] - cu[b]
         if L <= 0:
             continue
-        rows[r] = True
+        at = np.arange(cu[b], cu[b + 1])
+        if queries is not None:
+            at = np.intersect1d(at, queries)
+        rows[at] = True
         for hd in range(H):
-            qq, kk, vv = q[r, hd], k[r, hd // (H // Hk)], v[r, hd // (H // Hk)]
+            qq, kk, vv = q[at, hd], k[r, hd // (H // Hk)], v[r, hd // (H // Hk)]
             s = scale * (qq @ kk.T)
             e = scale * (D + 8) * 2.0 ** -24 * (np.abs(qq) @ np.abs(kk).T) + 2.0 ** -21
             if causal:
-                s = np.where(np.tril(np.ones((L, L), bool)), s, -np.inf)
+                s = np.where(np.arange(L)[None, :] <= (at - cu[b])[:, None], s, -np.inf)
             p = np.exp(s - s.max(1, keepdims=True))
             p = p / p.sum(1, keepdims=True)
             out = p @ vv
-            o[r, hd] = out
+            o[at, hd] = out
             pe = p * e
             pv = p @ np.abs(vv)
-            tol[r, hd] = (1.05 * (2.0 ** -8 * pv + pe @ np.abs(vv) + pe.sum(1, keepdims=True) * np.abs(out))
+            tol[at, hd] = (1.05 * (2.0 ** -8 * pv + pe @ np.abs(vv) + pe.sum(1, keepdims=True) * np.abs(out))
                           + (L + 8) * 2.0 ** -24 * (pv + np.abs(out)) + 1e-30)
     return o, tol, rows

@@ -48,7 +48,7 @@ def gemm(fn="svdq_gemm_int8", **kw):
 @no_gpu_only
 @pytest.mark.parametrize("kw,code", [
     (dict(M=-1), 2), (dict(N=-1), 2), (dict(K=40), 2), (dict(K=131072 + 16), 3), (dict(N=(1 << 24) + 1), 3),
-    (dict(weight=None), 1), (dict(wscales=None), 1), (dict(y=None), 1), (dict(codes=None), 1),
+    (dict(M=1 << 24, N=1 << 15), 3), (dict(weight=None), 1), (dict(wscales=None), 1), (dict(y=None), 1), (dict(codes=None), 1),
     (dict(bias=fake(7) + 2), 4), (dict(y=fake(5) + 2), 4),
     (dict(y=fake(3) + 128), 6), (dict(y=fake(4)), 6), (dict(y=fake(1)), 6), (dict(bias=fake(5)), 6),
 ])
@@ -162,6 +162,7 @@ def attn(**kw):
     (dict(T=-1), 2), (dict(T=1 << 24), 3), (dict(D=80), 3), (dict(H=3), 2), (dict(H=0), 2), (dict(Hk=0), 2),
     (dict(B=-1), 2), (dict(B=65536), 3), (dict(H=65538), 3), (dict(cu=None), 8),
     (dict(scale=0.0), 8), (dict(scale=-1.0), 8), (dict(scale=float("nan")), 8), (dict(scale=float("inf")), 8),
+    (dict(scale=2e6), 8), (dict(T=(1 << 24) - 1, H=256, qst=1 << 15, ost=1 << 15), 3),
     (dict(q=None), 1), (dict(k=None), 1), (dict(v=None), 1), (dict(o=None), 1),
     (dict(k=fake(2) + 8), 4), (dict(vst=260), 4), (dict(cu=fake(4) + 4), 4), (dict(kst=1 << 24), 3), (dict(ksh=64), 2),
     (dict(kst=0), 2), (dict(ost=256), 2),

@@ -31,8 +31,8 @@ def dev(cu):
     return torch.tensor(cu, dtype=torch.int32, device="cuda")
 
 
-def check(o, q, k, v, cu=None, causal=False, scale=None):
-    ref, tol, rows = B.attention_packed(f64(q), f64(k), f64(v), cu, causal, scale)
+def check(o, q, k, v, cu=None, causal=False, scale=None, queries=None):
+    ref, tol, rows = B.attention_packed(f64(q), f64(k), f64(v), cu, causal, scale, queries)
     tol = (1 + 2.0 ** -8) * tol + 2.0 ** -8 * np.abs(ref)
     err = np.abs(f64(o) - ref)[rows]
     assert (err <= tol[rows]).all(), float((err / tol[rows]).max())
@@ -62,6 +62,49 @@ def test_long(gpu_lib, T, H, Hk, D, causal):
     print(f"[attention] long {T}", flush=True)
     q, k, v = make(T, H, Hk, D, 3)
     check(gpu_lib.attention_packed(q, k, v, causal=causal), q, k, v, None, causal)
+
+
+@pytest.mark.parametrize("T,H,Hk,D", [(8192, 1, 1, 128), (8300, 2, 1, 64), (9001, 4, 1, 128), (16700, 3, 3, 64)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_longest_sampled_queries(gpu_lib, T, H, Hk, D, causal):
+    """Mean lengths from 8192 on take eight waves per workgroup; sampled queries, ends and tile borders."""
+    print(f"[attention] longest {T} causal={causal}", flush=True)
+    q, k, v = make(T, H, Hk, D, T)
+    pick = np.unique(np.concatenate([[0, 1, 63, 64, 255, 256, T - 257, T - 65, T - 2, T - 1],
+                                     np.random.default_rng(T).integers(0, T, 40)]))
+    check(gpu_lib.attention_packed(q, k, v, causal=causal), q, k, v, None, causal, None, pick)
+
+
+def test_two_long_sequences_eight_waves(gpu_lib):
+    cu = offsets([9000, 8100], 3)
+    T = cu[-1] + 2
+    q, k, v = make(T, 2, 1, 128, 21)
+    o = torch.full_like(q, 7.0)
+    pick = np.array([3, 4, 9002, 9003, 9004, 9300, T - 3, 5000])
+    gpu_lib.attention_packed(q, k, v, dev(cu), causal=True, out=o)
+    check(o, q, k, v, cu, True, None, pick)
+    assert (o[:3] == 7).all() and (o[-2:] == 7).all()
+
+
+def test_thousands_of_sequences(gpu_lib):
+    """More sequences than 64 * 64 lanes probe in two rounds; lengths 0 to 5."""
+    lens = np.random.default_rng(3).integers(0, 6, 5000).tolist()
+    cu = offsets(lens)
+    q, k, v = make(cu[-1], 2, 2, 64, 22)
+    o = gpu_lib.attention_packed(q, k, v, dev(cu), causal=True)
+    check(o, q, k, v, cu, True)
+
+
+def test_offsets_beyond_32_bits(gpu_lib):
+    """A token stride of 2^20 elements: the last tokens lie more than 2^32 bytes in."""
+    T, H, D, st = 2100, 1, 128, 1 << 20
+    q, k, v = make(T, H, H, D, 23)
+    buf = torch.empty(T * st, dtype=torch.bfloat16, device="cuda")
+    views = [torch.as_strided(buf, (T, H, D), (st, D, 1), 512 * i) for i in range(4)]
+    for dst, src in zip(views, (q, k, v)):
+        dst.copy_(src)
+    gpu_lib.attention_packed(*views[:3], out=views[3])
+    assert torch.equal(views[3], gpu_lib.attention_packed(q, k, v))
 
 
 @pytest.mark.parametrize("sharp", [8.0, 60.0])

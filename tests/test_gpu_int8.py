@@ -65,9 +65,10 @@ def test_quantize_zero_tiny_and_tie_rows(gpu_lib):
     assert codes[4, 1] == 0 and codes[4, 2] == 2 and codes[4, 3] == 2   # to even
 
 
-SHAPES = [(1, 16, 1), (1, 3840, 3840), (2, 272, 107), (5, 48, 33), (7, 10240, 65), (16, 3840, 257), (17, 64, 40),
+SHAPES = [(31, 1312, 70), (29, 1408, 33), (8, 5120, 48), (4, 10240, 40), (32, 1280, 50), (1, 16, 1), (1, 3840, 3840), (2, 272, 107), (5, 48, 33), (7, 10240, 65), (16, 3840, 257), (17, 64, 40),
           (31, 1040, 130), (33, 96, 64), (48, 3840, 1000), (64, 256, 512), (65, 528, 129), (100, 10240, 300),
-          (129, 400, 257), (200, 3840, 1283), (333, 1024, 640), (513, 784, 769), (1000, 272, 96), (1030, 2064, 520)]
+          (129, 400, 257), (200, 3840, 1283), (333, 1024, 640), (513, 784, 769), (1000, 272, 96), (1030, 2064, 520),
+          (333, 10240, 3840)]
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)
@@ -96,6 +97,20 @@ def test_large_sampled_rows(gpu_lib, M, N, rows):
     pick = np.unique(np.concatenate([[0, 1, M - 2, M - 1], np.random.default_rng(0).integers(0, M, rows)]))
     codes, scales = B.quantize_int8(f64(x[torch.from_numpy(pick).cuda()]))
     check_y(y[torch.from_numpy(pick).cuda()], codes, scales, w, ws, b)
+
+
+def test_offsets_beyond_32_bits(gpu_lib):
+    """Codes of more than 2^32 bytes: the last rows as those of a short call."""
+    M, K, N = 530000, 8192, 48
+    c = torch.zeros(M, K, dtype=torch.int8, device="cuda")
+    s = torch.ones(M, device="cuda")
+    w, ws, b = weights(N, K, 14)
+    x = activations(40, K, 15)
+    codes, scales = gpu_lib.quantize_int8(x)
+    c[-40:], s[-40:] = codes, scales
+    y = gpu_lib.gemm_int8(c, s, w, ws, bias=b)
+    check_y(y[-40:], codes.cpu().numpy(), scales.cpu().numpy(), w, ws, b)
+    check_y(y[:40], np.zeros((40, K), np.int8), np.ones(40), w, ws, b)
 
 
 def test_extreme_codes_largest_k(gpu_lib):

@@ -165,6 +165,19 @@ def test_many_groups_and_graph(gpu_lib):
         assert torch.equal(ho, want[0]) and torch.equal(x, want[1])
 
 
+def test_offsets_beyond_32_bits(gpu_lib):
+    """h, block and the outputs of more than 2^32 bytes each: the last rows as those of a short call."""
+    M, K = 140000, 16384
+    h = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    b = torch.zeros_like(h)
+    d = make(8, K, 1, 12)
+    h[-8:], b[-8:] = d["h"], d["block"]
+    want = gpu_lib.norm_gated(**d)
+    ho, x = gpu_lib.norm_gated(**(d | dict(h=h, block=b)))
+    assert torch.equal(ho[-8:], want[0]) and torch.equal(x[-8:], want[1])
+    assert not x[:-8].any()
+
+
 def test_empty(gpu_lib):
     d = make(1, 32, 1, 1, full=False)
     ho, x = gpu_lib.norm_gated(d["h"][:0], d["block"][:0])

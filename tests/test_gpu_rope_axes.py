@@ -34,7 +34,7 @@ def positions(T, A, far, seed):
 
 @pytest.mark.parametrize("T,H,Hk,D,axes", [
     (1, 1, 1, 128, (32, 48, 48)), (77, 30, 30, 128, (32, 48, 48)), (5, 3, 1, 64, (16, 24, 24)), (300, 7, 2, 64, (64,)),
-    (33, 32, 8, 128, (128,)), (64, 5, 5, 128, (2, 6, 118, 2)), (9, 40, 3, 64, (32, 32)), (1025, 4, 4, 128, (16, 56, 56))])
+    (33, 32, 8, 128, (128,)), (64, 5, 5, 128, (2, 6, 118, 2)), (9, 40, 3, 64, (32, 32)), (3, 100, 7, 128, (64, 64)), (1025, 4, 4, 128, (16, 56, 56))])
 @pytest.mark.parametrize("inter", [True, False])
 @pytest.mark.parametrize("norm", [True, False])
 def test_against_oracle(gpu_lib, T, H, Hk, D, axes, inter, norm):
@@ -92,6 +92,36 @@ def test_strides_and_sides(gpu_lib):
     assert torch.equal(only_q, qo) and torch.equal(only_k, ko[:H].transpose(0, 1))
     one = q[:1].expand(1, H, D)
     assert torch.equal(gpu_lib.rope_axes(one, None, pos[:1], axes)[0], qo[:1])
+
+
+def test_norm_on_one_side(gpu_lib):
+    g = torch.Generator().manual_seed(8)
+    q, k = torch.randn(21, 3, 128, generator=g).bfloat16().cuda(), torch.randn(21, 2, 128, generator=g).bfloat16().cuda()
+    w = (1 + 0.1 * torch.randn(128, generator=g)).bfloat16().cuda()
+    pos = positions(21, 1, 50, 9)
+    for qw, kw in ((w, None), (None, w)):
+        qo, ko = gpu_lib.rope_axes(q, k, pos, (128,), q_weight=qw, k_weight=kw, eps=1e-5)
+        check(qo, q, pos, (128,), 10000.0, True, qw, 1e-5)
+        check(ko, k, pos, (128,), 10000.0, True, kw, 1e-5)
+
+
+def test_zero_heads_rows_and_eps(gpu_lib):
+    """A head of zeros stays zero through the norm."""
+    q = torch.zeros(5, 2, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    qo, _ = gpu_lib.rope_axes(q, None, positions(5, 1, 9, 1), (64,), q_weight=w)
+    assert not qo.any()
+
+
+def test_offsets_beyond_32_bits(gpu_lib):
+    T, st, axes = 2100, 1 << 20, (64, 64)
+    q = torch.randn(T, 1, 128, generator=torch.Generator().manual_seed(10)).bfloat16().cuda()
+    pos = positions(T, 2, 300, 11)
+    buf = torch.empty(T * st, dtype=torch.bfloat16, device="cuda")
+    src, dst = (torch.as_strided(buf, (T, 1, 128), (st, 128, 1), 512 * i) for i in range(2))
+    src.copy_(q)
+    gpu_lib.rope_axes(src, None, pos, axes, q_out=dst)
+    assert torch.equal(dst, gpu_lib.rope_axes(q, None, pos, axes)[0])
 
 
 def test_graph_and_empty(gpu_lib):
