@@ -531,7 +531,7 @@ hipError_t launch_few(const Int8GemmArgs& a, const uint16_t* x, const uint16_t* 
 // 40 to 4096, 500 to 11520, 1040 to 10240): a workgroup's panel takes `share` of its CU's time, at
 // least `least` when it has the CU to itself (the panel's loads are then the limit), and a CU
 // works through ceil(workgroups / 256) of them; 5 us start and end a product. A split adds a
-// launch (2.5 us) and the partial sums' traffic. Measured at 4096 x 10240, K = 3840: 148 us in
+// launch (2.5 us on the device, 3 of the caller) and the partial sums' traffic. Measured at 4096 x 10240, K = 3840: 148 us in
 // 256 x 320 tiles, 171 in 256 x 256, 185 in 128 x 128; at 333 x 3840, K = 10240: 36 us in
 // 128 x 64 tiles, 129 in 256 x 320; at 40 x 3840, K = 3840: 9.8 us in 64 x 64 tiles with k
 // split four ways, 12.6 unsplit.
@@ -553,7 +553,7 @@ I8Plan plan_int8(int64_t M, int64_t N, int64_t K) {
       const int64_t per = (panels + sp - 1) / sp;
       const double rounds = (double)((tiles * sp + 255) / 256);
       const double t = 5.0 + (double)per * fmax(shapes[s].least, rounds * shapes[s].share) +
-                       (sp > 1 ? 2.5 + 1e-6 * (double)(M * N) * sp : 0.0);
+                       (sp > 1 ? 4.0 + 1e-6 * (double)(M * N) * sp : 0.0);
       if (t < best_t) {
         best_t = t;
         best = I8Plan{s, (int)((panels + per - 1) / per), (int)per};

@@ -696,6 +696,15 @@ def _launch(name, dev, *args):
         _lib.check(name, status)
 
 
+def _on_one_device(index, **tensors):
+    """Every given tensor (None skipped) is on GPU `index`; the error is _devices'."""
+    for t in tensors.values():
+        if t is not None and t.get_device() != index:
+            _devices(**tensors)
+    if index < 0:
+        _devices(**tensors)
+
+
 def _workspace(workspace, need, dev):
     """The given workspace, checked, or a new one (None when no bytes are needed); and its size."""
     if workspace is None:
@@ -718,11 +727,13 @@ def quantize_int8(x, smooth=None, codes=None, scales=None):
     dev = x.device
     if codes is None:
         codes = torch.empty_like(x, dtype=torch.int8)
+    else:
+        _need(codes, "codes", torch.int8, shape=(M, K))
     if scales is None:
         scales = torch.empty(M, dtype=torch.float32, device=dev)
-    _need(codes, "codes", torch.int8, shape=(M, K))
-    _need(scales, "scales", torch.float32, shape=(M,))
-    _devices(x=x, smooth=smooth, codes=codes, scales=scales)
+    else:
+        _need(scales, "scales", torch.float32, shape=(M,))
+    _on_one_device(x.get_device(), x=x, smooth=smooth, codes=codes, scales=scales)
     _launch("svdq_quantize_int8", dev, _p(x), _p(smooth), M, K, _p(codes), _p(scales))
     return codes, scales
 
@@ -741,12 +752,12 @@ def _check_int8_weight(weight, wscales, bias, K):
 
 def gemm_int8_workspace_bytes(M, N, K):
     """Scratch bytes gemm_int8 needs."""
-    return int(_lib.lib().svdq_gemm_int8_workspace_bytes(M, N, K))
+    return _lib.lib().svdq_gemm_int8_workspace_bytes(M, N, K)
 
 
 def linear_int8_workspace_bytes(M, N, K):
     """Scratch bytes linear_int8 needs."""
-    return int(_lib.lib().svdq_linear_int8_workspace_bytes(M, N, K))
+    return _lib.lib().svdq_linear_int8_workspace_bytes(M, N, K)
 
 
 def gemm_int8(codes, ascales, weight, wscales, bias=None, y=None, workspace=None):
@@ -761,9 +772,11 @@ def gemm_int8(codes, ascales, weight, wscales, bias=None, y=None, workspace=None
     dev = codes.device
     if y is None:
         y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    _need(y, "y", torch.bfloat16, shape=(M, N))
+    else:
+        _need(y, "y", torch.bfloat16, shape=(M, N))
     workspace, ws_bytes = _workspace(workspace, gemm_int8_workspace_bytes(M, N, K), dev)
-    _devices(codes=codes, ascales=ascales, weight=weight, wscales=wscales, bias=bias, y=y, workspace=workspace)
+    _on_one_device(codes.get_device(), codes=codes, ascales=ascales, weight=weight, wscales=wscales, bias=bias, y=y,
+                   workspace=workspace)
     _launch("svdq_gemm_int8", dev, _p(codes), _p(ascales), _p(weight), _p(wscales), _p(bias), M, N, K, _p(y),
             _p(workspace), ws_bytes)
     return y
@@ -781,9 +794,11 @@ def linear_int8(x, weight, wscales, bias=None, smooth=None, y=None, workspace=No
     dev = x.device
     if y is None:
         y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    _need(y, "y", torch.bfloat16, shape=(M, N))
+    else:
+        _need(y, "y", torch.bfloat16, shape=(M, N))
     workspace, ws_bytes = _workspace(workspace, linear_int8_workspace_bytes(M, N, K), dev)
-    _devices(x=x, smooth=smooth, weight=weight, wscales=wscales, bias=bias, y=y, workspace=workspace)
+    _on_one_device(x.get_device(), x=x, smooth=smooth, weight=weight, wscales=wscales, bias=bias, y=y,
+                   workspace=workspace)
     _launch("svdq_linear_int8", dev, _p(x), _p(smooth), _p(weight), _p(wscales), _p(bias), M, N, K, _p(y),
             _p(workspace), ws_bytes)
     return y
@@ -802,11 +817,16 @@ def _check_norm(h, block, post_weight, gate, pre_weight, scale, cu_seqlens, h_ou
         _need(block, "block", torch.bfloat16, shape=(M, K))
         if h_out is None:
             h_out = torch.empty_like(h)
-        _need(h_out, "h_out", torch.bfloat16, shape=(M, K))
-    for name, t, shape in (("post_weight", post_weight, (K,)), ("gate", gate, (G, K)),
-                           ("pre_weight", pre_weight, (K,)), ("scale", scale, (G, K))):
-        if t is not None:
-            _need(t, name, torch.bfloat16, shape=shape)
+        else:
+            _need(h_out, "h_out", torch.bfloat16, shape=(M, K))
+    if post_weight is not None:
+        _need(post_weight, "post_weight", torch.bfloat16, shape=(K,))
+    if gate is not None:
+        _need(gate, "gate", torch.bfloat16, shape=(G, K))
+    if pre_weight is not None:
+        _need(pre_weight, "pre_weight", torch.bfloat16, shape=(K,))
+    if scale is not None:
+        _need(scale, "scale", torch.bfloat16, shape=(G, K))
     return M, K, G, h_out
 
 
@@ -825,11 +845,12 @@ def norm_gated(h, block=None, post_weight=None, gate=None, residual_scale=1.0, p
     if pre:
         if x_out is None:
             x_out = torch.empty_like(h)
-        _need(x_out, "x_out", torch.bfloat16, shape=(M, K))
+        else:
+            _need(x_out, "x_out", torch.bfloat16, shape=(M, K))
     elif x_out is not None:
         raise ValueError("x_out must be None with pre=False")
-    _devices(h=h, block=block, post_weight=post_weight, gate=gate, pre_weight=pre_weight, scale=scale,
-             cu_seqlens=cu_seqlens, h_out=h_out, x_out=x_out)
+    _on_one_device(h.get_device(), h=h, block=block, post_weight=post_weight, gate=gate, pre_weight=pre_weight,
+                   scale=scale, cu_seqlens=cu_seqlens, h_out=h_out, x_out=x_out)
     _launch("svdq_norm_gated", h.device, _p(h), _p(block), _p(post_weight), _p(gate), residual_scale, _p(pre_weight),
             _p(scale), _p(cu_seqlens), G, M, K, eps, _p(h_out), _p(x_out))
     return h_out, x_out
@@ -844,12 +865,14 @@ def norm_gated_int8(h, block=None, post_weight=None, gate=None, residual_scale=1
         _need(smooth, "smooth", torch.bfloat16, shape=(K,))
     if codes is None:
         codes = torch.empty_like(h, dtype=torch.int8)
+    else:
+        _need(codes, "codes", torch.int8, shape=(M, K))
     if scales is None:
         scales = torch.empty(M, dtype=torch.float32, device=h.device)
-    _need(codes, "codes", torch.int8, shape=(M, K))
-    _need(scales, "scales", torch.float32, shape=(M,))
-    _devices(h=h, block=block, post_weight=post_weight, gate=gate, pre_weight=pre_weight, scale=scale,
-             cu_seqlens=cu_seqlens, h_out=h_out, smooth=smooth, codes=codes, scales=scales)
+    else:
+        _need(scales, "scales", torch.float32, shape=(M,))
+    _on_one_device(h.get_device(), h=h, block=block, post_weight=post_weight, gate=gate, pre_weight=pre_weight,
+                   scale=scale, cu_seqlens=cu_seqlens, h_out=h_out, smooth=smooth, codes=codes, scales=scales)
     _launch("svdq_norm_gated_int8", h.device, _p(h), _p(block), _p(post_weight), _p(gate), residual_scale,
             _p(pre_weight), _p(scale), _p(cu_seqlens), G, M, K, eps, _p(h_out), _p(smooth), _p(codes), _p(scales))
     return h_out, codes, scales
@@ -912,7 +935,8 @@ def rope_axes(q, k, positions, axis_dims, theta=10000.0, interleaved=True, q_wei
         koa = _need_heads(k_out, "k_out", k.shape)
     elif k_weight is not None or k_out is not None:
         raise ValueError("k_weight and k_out need k")
-    _devices(q=q, k=k, positions=positions, q_weight=q_weight, k_weight=k_weight, q_out=q_out, k_out=k_out)
+    _on_one_device(given.get_device(), q=q, k=k, positions=positions, q_weight=q_weight, k_weight=k_weight,
+                   q_out=q_out, k_out=k_out)
     _launch("svdq_rope_axes", given.device, *qa, H, *ka, Hk, _p(q_weight), _p(k_weight), eps, positions.data_ptr(),
             (ctypes.c_int32 * len(axis_dims))(*axis_dims), len(axis_dims), theta, 1 if interleaved else 0, T, D, *qoa,
             *koa)
@@ -939,7 +963,7 @@ def attention_packed(q, k, v, cu_seqlens=None, causal=False, scale=None, out=Non
     if out is None:
         out = torch.empty_like(q)
     oa = _need_heads(out, "out", q.shape)
-    _devices(q=q, k=k, v=v, cu_seqlens=cu_seqlens, out=out)
+    _on_one_device(q.get_device(), q=q, k=k, v=v, cu_seqlens=cu_seqlens, out=out)
     _launch("svdq_attention_packed", q.device, *qa, *ka, *va, _p(cu_seqlens), B, T, H, Hk, D, 1 if causal else 0,
             D ** -0.5 if scale is None else scale, *oa)
     return out
