@@ -5,7 +5,8 @@
 //   x_out = (h_out / sqrt(mean h_out^2 + eps)) * pre * (1 + scale[g])
 //
 // One workgroup per row; the row stays in registers between the two sums, so h
-// and block are read once and h_out and x_out (or x's int8 codes) written once.
+// and block are read once and h_out and x_out (or x's int8 codes) written once:
+// 16896 x 3840 moves 519 MB in 100 us (5.2 TB/s; 103 us without streaming stores).
 // Sums in fp32; x_out comes from h_out before its rounding to bf16.
 #include "common.h"
 #include "kernels.h"
@@ -105,7 +106,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_gated_kernel(Nor
           if (a.gate != nullptr) f *= gt[e];
           h[u][e] = __builtin_fmaf(b[u][e], f, h[u][e]);
         }
-        *reinterpret_cast<u32x4*>(a.h_out + base + 8 * (size_t)i) = pack8(h[u]);
+        __builtin_nontemporal_store(pack8(h[u]), reinterpret_cast<u32x4*>(a.h_out + base + 8 * (size_t)i));
       }
     }
   }
@@ -135,7 +136,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_gated_kernel(Nor
       }
       const u32x4 x = pack8(h[u]);
       if (a.codes == nullptr) {
-        *reinterpret_cast<u32x4*>(a.x_out + base + 8 * (size_t)i) = x;
+        __builtin_nontemporal_store(x, reinterpret_cast<u32x4*>(a.x_out + base + 8 * (size_t)i));
       } else {   // the codes are those of the bf16 x
         unpack8(x, h[u]);
         if (a.smooth != nullptr) {
