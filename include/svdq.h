@@ -537,7 +537,8 @@ int svdq_rope_axes(const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_
  * Scores and softmax statistics are fp32; the probabilities are rounded to bf16
  * for the second product (relative to a running maximum), their sum is taken
  * before that, and o is rounded once to bf16. A non-finite value reaches no
- * other sequence's rows.
+ * other sequence's rows; within a causal sequence a non-finite v may reach rows
+ * before it (they multiply it by zero), a non-finite k does not.
  * D: 64 or 128; H a multiple of Hk; T below 2^24; H, B at most 65535; 2 T H + 512 B H
  * below 2^32; token strides below 2^24 elements. No workspace.
  */

@@ -95,6 +95,38 @@ def test_thousands_of_sequences(gpu_lib):
     check(o, q, k, v, cu, True)
 
 
+@pytest.mark.parametrize("H,Hk", [(6, 1), (8, 1), (16, 1), (12, 2), (24, 8)])
+@pytest.mark.parametrize("D,causal", [(128, True), (64, False)])
+def test_head_groups(gpu_lib, H, Hk, D, causal):
+    """Groups that fill a workgroup's waves, do not divide them, or exceed them."""
+    lens = [70, 1, 200, 33]
+    q, k, v = make(sum(lens), H, Hk, D, 24)
+    cu = offsets(lens)
+    check(gpu_lib.attention_packed(q, k, v, dev(cu), causal=causal), q, k, v, cu, causal)
+
+
+@pytest.mark.parametrize("H,Hk", [(8, 1), (12, 2)])
+def test_head_groups_eight_waves(gpu_lib, H, Hk):
+    T = 8200
+    q, k, v = make(T, H, Hk, 64, 25)
+    pick = np.array([0, 31, 32, 63, 100, 4111, T - 33, T - 1])
+    check(gpu_lib.attention_packed(q, k, v, causal=True), q, k, v, None, True, None, pick)
+
+
+def test_most_tokens_and_sequences(gpu_lib):
+    """T = 2^24 - 1 tokens in 65535 sequences: the last ones as those of a call of their own."""
+    T, B, D = (1 << 24) - 1, 65535, 64
+    g = torch.Generator(device="cuda").manual_seed(26)
+    q, k, v = (torch.randn(T, 1, D, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(3))
+    cu = (torch.arange(B + 1, device="cuda") * (T // B)).to(torch.int32)
+    cu[-1] = T
+    o = gpu_lib.attention_packed(q, k, v, cu, causal=True)
+    for b in (0, 1, 63, 64, 40000, B - 1):
+        r = slice(int(cu[b]), int(cu[b + 1]))
+        one = gpu_lib.attention_packed(q[r], k[r], v[r], causal=True)
+        assert torch.equal(o[r], one), b
+
+
 def test_offsets_beyond_32_bits(gpu_lib):
     """A token stride of 2^20 elements: the last tokens lie more than 2^32 bytes in."""
     T, H, D, st = 2100, 1, 128, 1 << 20

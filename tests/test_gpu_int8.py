@@ -68,7 +68,7 @@ def test_quantize_zero_tiny_and_tie_rows(gpu_lib):
 SHAPES = [(31, 1312, 70), (29, 1408, 33), (8, 5120, 48), (4, 10240, 40), (32, 1280, 50), (1, 16, 1), (1, 3840, 3840), (2, 272, 107), (5, 48, 33), (7, 10240, 65), (16, 3840, 257), (17, 64, 40),
           (31, 1040, 130), (33, 96, 64), (48, 3840, 1000), (64, 256, 512), (65, 528, 129), (100, 10240, 300),
           (129, 400, 257), (200, 3840, 1283), (333, 1024, 640), (513, 784, 769), (1000, 272, 96), (1030, 2064, 520),
-          (333, 10240, 3840)]
+          (333, 10240, 3840), (100, 10000, 300), (1, 40960, 40), (40, 4000, 48)]
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)
@@ -97,6 +97,20 @@ def test_large_sampled_rows(gpu_lib, M, N, rows):
     pick = np.unique(np.concatenate([[0, 1, M - 2, M - 1], np.random.default_rng(0).integers(0, M, rows)]))
     codes, scales = B.quantize_int8(f64(x[torch.from_numpy(pick).cuda()]))
     check_y(y[torch.from_numpy(pick).cuda()], codes, scales, w, ws, b)
+
+
+def test_most_rows(gpu_lib):
+    """2^24 rows: quantiser and product, sampled."""
+    M, K, N = 1 << 24, 16, 8
+    g = torch.Generator(device="cuda").manual_seed(16)
+    x = torch.randn(M, K, generator=g, device="cuda", dtype=torch.bfloat16)
+    w, ws, b = weights(N, K, 17)
+    codes, scales = gpu_lib.quantize_int8(x)
+    y = gpu_lib.gemm_int8(codes, scales, w, ws, bias=b)
+    pick = torch.tensor([0, 1, 4095, 1 << 20, (1 << 22) + 3, M - 2, M - 1], device="cuda")
+    rc, rs = B.quantize_int8(f64(x[pick]))
+    assert np.array_equal(codes[pick].cpu().numpy(), rc) and np.array_equal(scales[pick].cpu().numpy(), rs)
+    check_y(y[pick], rc, rs, w, ws, b)
 
 
 def test_offsets_beyond_32_bits(gpu_lib):

@@ -165,6 +165,17 @@ def test_many_groups_and_graph(gpu_lib):
         assert torch.equal(ho, want[0]) and torch.equal(x, want[1])
 
 
+def test_most_rows(gpu_lib):
+    """2^24 rows, sampled."""
+    M, K = 1 << 24, 16
+    g = torch.Generator(device="cuda").manual_seed(18)
+    h, b = (torch.randn(M, K, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    ho, x = gpu_lib.norm_gated(h, b, residual_scale=0.5)
+    pick = torch.tensor([0, 3, 4, 1 << 20, (1 << 22) + 1, M - 1], device="cuda")
+    want = gpu_lib.norm_gated(h[pick], b[pick], residual_scale=0.5)
+    assert torch.equal(ho[pick], want[0]) and torch.equal(x[pick], want[1])
+
+
 def test_offsets_beyond_32_bits(gpu_lib):
     """h, block and the outputs of more than 2^32 bytes each: the last rows as those of a short call."""
     M, K = 140000, 16384

@@ -113,6 +113,15 @@ def test_zero_heads_rows_and_eps(gpu_lib):
     assert not qo.any()
 
 
+def test_most_tokens(gpu_lib):
+    T = (1 << 24) - 1
+    q = torch.randn(T, 1, 64, generator=torch.Generator(device="cuda").manual_seed(12), device="cuda", dtype=torch.bfloat16)
+    pos = torch.arange(T, device="cuda", dtype=torch.int32)[:, None].contiguous()
+    qo, _ = gpu_lib.rope_axes(q, None, pos, (64,))
+    pick = torch.tensor([0, 15, 16, 1 << 20, T - 2, T - 1], device="cuda")
+    assert torch.equal(qo[pick], gpu_lib.rope_axes(q[pick], None, pos[pick], (64,))[0])
+
+
 def test_offsets_beyond_32_bits(gpu_lib):
     T, st, axes = 2100, 1 << 20, (64, 64)
     q = torch.randn(T, 1, 128, generator=torch.Generator().manual_seed(10)).bfloat16().cuda()
