@@ -139,20 +139,45 @@ __device__ __forceinline__ Int8Scale int8_scale(float amax) {
   if (!(q.inv <= 3.4028234663852886e38f)) q.inv = q.scale = 0.0f;
   return q;
 }
-// 8 codes of v * inv, |v * inv| <= 127 (1 + 2^-23), packed in order
+// 8 codes of v * inv, |v * inv| <= 127 (1 + 2^-23), packed in order. The product, rounded to
+// fp32, plus 1.5 * 2^23 is rounded to the nearest even integer, whose low byte is the code.
 __device__ __forceinline__ u32x2 int8_codes8(const float (&v)[8], float inv) {
+#pragma clang fp contract(off)   // two roundings, not one of a fused product
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(v[i] * inv + 12582912.0f);
   u32x2 r;
 #pragma unroll
   for (int d = 0; d < 2; ++d) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w |= ((uint32_t)(int)__builtin_rintf(v[4 * d + i] * inv) & 0xFFu) << (8 * i);
-    r[d] = w;
+    const uint32_t lo = __builtin_amdgcn_perm(b[4 * d + 1], b[4 * d], 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(b[4 * d + 3], b[4 * d + 2], 0x04000C0Cu);
+    r[d] = lo | hi;
   }
   return r;
 }
 
 __device__ __forceinline__ u32x4 zero4() { u32x4 z = {0u, 0u, 0u, 0u}; return z; }
+
+// Sum (or maximum) over the wave's 64 lanes, the same value in each: within rows of 16 lanes by
+// DPP (lane ^ 1, lane ^ 2, mirrors of 8 and 16), the four rows through scalar registers. A
+// shuffle through LDS costs about 100 cycles a step.
+template <bool MAX>
+__device__ __forceinline__ float wave_reduce(float v) {
+  auto both = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+#define SVDQ_DPP(x, ctrl) \
+  __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), ctrl, 0xF, 0xF, true))
+  v = both(v, SVDQ_DPP(v, 0xB1));
+  v = both(v, SVDQ_DPP(v, 0x4E));
+  v = both(v, SVDQ_DPP(v, 0x141));
+  v = both(v, SVDQ_DPP(v, 0x140));
+#undef SVDQ_DPP
+  const int i = __builtin_bit_cast(int, v);
+  const float r0 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(i, 0));
+  const float r1 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(i, 16));
+  const float r2 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(i, 32));
+  const float r3 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(i, 48));
+  return both(both(r0, r1), both(r2, r3));
+}
 
 // Position of `x` among not decreasing device offsets cu[0 .. n - 1]: the number of them
 // that are <= x. The wave's 64 lanes probe together, so up to 64 offsets cost one load.

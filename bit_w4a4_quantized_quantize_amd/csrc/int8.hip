@@ -78,8 +78,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void quant_int8_kernel(con
       for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[0][e]));
     }
   }
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor(amax, d));
+  amax = wave_reduce<true>(amax);
   if constexpr (NW > 1) {
     if ((tid & 63) == 0) part[tid >> 6] = amax;
     __syncthreads();
@@ -451,8 +450,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void gemm_int8_few_kernel(Int8GemmA
 #pragma unroll
         for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
       }
-#pragma unroll
-      for (int d = 32; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor(amax, d));
+      amax = wave_reduce<true>(amax);
       if (lane == 0) row_max[m][wave % wpr] = amax;
     }
     if (wpr > 1) __syncthreads();

@@ -32,11 +32,7 @@ __device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
 // sum (or maximum) over the workgroup's NW waves, the same value in every lane
 template <int NW, bool MAX>
 __device__ __forceinline__ float reduce_wg(float v, float* part) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    const float o = __shfl_xor(v, d);
-    v = MAX ? fmaxf(v, o) : v + o;
-  }
+  v = wave_reduce<MAX>(v);
   if (NW == 1) return v;
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
   __syncthreads();
@@ -64,7 +60,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_gated_kernel(Nor
     return *reinterpret_cast<const u32x4*>(p + off + 8 * (size_t)i);
   };
 
-  // the row's loads go out before its group is looked up
+  // the row's loads go out before its group is looked up, and each norm's weights before its sum
   u32x4 hw[NV], bw[NV];
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
@@ -78,10 +74,19 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_gated_kernel(Nor
     if (g < 0 || g >= a.G) return;
   }
   const size_t gbase = (size_t)g * (size_t)a.K;
-  float h[NV][8];
+  auto weights = [&](const uint16_t* p, size_t off, u32x4 (&w)[NV]) {
+    if (p == nullptr) return;
 #pragma unroll
-  for (int u = 0; u < NV; ++u) unpack8(hw[u], h[u]);
+    for (int u = 0; u < NV; ++u) {
+      const int i = tid + kThreads * u;
+      if (i < np) w[u] = piece(p, off, i);
+    }
+  };
+  u32x4 w1[NV], w2[NV];
+  float h[NV][8];
   if (BLOCK) {
+    weights(a.post, 0, w1);
+    weights(a.gate, gbase, w2);
     float b[NV][8];
     float ss = 0.0f;
 #pragma unroll
@@ -95,10 +100,11 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_gated_kernel(Nor
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       const int i = tid + kThreads * u;
+      unpack8(hw[u], h[u]);
       if (i < np) {
         float w[8], gt[8];
-        if (a.post != nullptr) unpack8(piece(a.post, 0, i), w);
-        if (a.gate != nullptr) unpack8(piece(a.gate, gbase, i), gt);
+        if (a.post != nullptr) unpack8(w1[u], w);
+        if (a.gate != nullptr) unpack8(w2[u], gt);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float f = r;
@@ -109,9 +115,14 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_gated_kernel(Nor
         __builtin_nontemporal_store(pack8(h[u]), reinterpret_cast<u32x4*>(a.h_out + base + 8 * (size_t)i));
       }
     }
+  } else {
+#pragma unroll
+    for (int u = 0; u < NV; ++u) unpack8(hw[u], h[u]);
   }
   if (a.x_out == nullptr && a.codes == nullptr) return;
 
+  weights(a.pre, 0, w1);
+  weights(a.scale, gbase, w2);
   float ss = 0.0f;
 #pragma unroll
   for (int u = 0; u < NV; ++u)
@@ -119,14 +130,16 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_gated_kernel(Nor
     for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(h[u][e], h[u][e], ss);
   ss = reduce_wg<NW, false>(ss, part[1]);
   const float r = 1.0f / __builtin_sqrtf(ss * rk + a.eps);
+  u32x4 sw[NV];
+  weights(a.smooth, 0, sw);
   float amax = 0.0f;
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
     const int i = tid + kThreads * u;
     if (i < np) {
       float w[8], sc[8];
-      if (a.pre != nullptr) unpack8(piece(a.pre, 0, i), w);
-      if (a.scale != nullptr) unpack8(piece(a.scale, gbase, i), sc);
+      if (a.pre != nullptr) unpack8(w1[u], w);
+      if (a.scale != nullptr) unpack8(w2[u], sc);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         float f = r;
@@ -141,7 +154,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_gated_kernel(Nor
         unpack8(x, h[u]);
         if (a.smooth != nullptr) {
           float sm[8];
-          unpack8(piece(a.smooth, 0, i), sm);
+          unpack8(sw[u], sm);
 #pragma unroll
           for (int e = 0; e < 8; ++e) h[u][e] *= sm[e];
         }
@@ -180,7 +193,8 @@ hipError_t launch_norm_gated(const NormArgs& a, hipStream_t stream) {
   else if (a.K <= 2048) launch_norm_cfg<4, 1>(a, stream);
   else if (a.K <= 4096) launch_norm_cfg<4, 2>(a, stream);
   else if (a.K <= 8192) launch_norm_cfg<8, 2>(a, stream);
-  else if (a.K <= 16384) launch_norm_cfg<16, 2>(a, stream);
+  else if (a.K <= 12288) launch_norm_cfg<8, 3>(a, stream);
+  else if (a.K <= 16384) launch_norm_cfg<8, 4>(a, stream);
   else launch_norm_cfg<16, 4>(a, stream);
   return hipGetLastError();
 }
