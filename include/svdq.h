@@ -1,5 +1,6 @@
 /*
- * svdq.h - C ABI of the MI355X (gfx950) SVDQuant W4A4 NVFP4 linear layer.
+ * svdq.h - C ABI of the MI355X (gfx950) SVDQuant W4A4 NVFP4 linear layer, and of
+ * the operators between a transformer block's linears.
  *
  * The layer (model card "nunchaku-z-image-turbo-svdq", section "What's stored
  * on disk", runtime reconstruction formula):
