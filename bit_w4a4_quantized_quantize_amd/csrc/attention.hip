@@ -103,8 +103,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a, int l
   int b = 0, beg = 0, end = (int)a.T;
   if (a.cu != nullptr && !tile_sequence(a.cu, a.B, a.T, lg_rows, tile, b, beg, end)) return;
   const int len = end - beg;
-  int local = tile - (beg >> lg_rows) - b;               // tile within the sequence
-  if (len <= 0 || local > (len - 1) >> lg_rows) return;
+  int local = tile - (beg >> lg_rows) - b;               // tile within the sequence (negative only where
+  if (len <= 0 || local < 0 || local > (len - 1) >> lg_rows) return;   // the offsets decrease)
   if (CAUSAL) local = ((len - 1) >> lg_rows) - local;    // those with the most keys first
   const int q0 = local << lg_rows;
   const int hk = head0 / (a.H / a.Hk);

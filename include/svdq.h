@@ -472,8 +472,8 @@ int svdq_linear_int8(const void* x, const void* smooth, const void* weight, cons
  *   cu_seqlens: G + 1 int32 row offsets on the device (row m belongs to group g when
  *     cu_seqlens[g] <= m < cu_seqlens[g + 1]; not decreasing), or NULL: every row
  *     is in group 0 and G must be 1. Rows outside [cu_seqlens[0], cu_seqlens[G])
- *     are left as they were in every output. Offsets outside 0..M cause no access
- *     outside the tensors.
+ *     are left as they were in every output. Offsets outside 0..M, or decreasing
+ *     ones, cause no access outside the tensors.
  *   h_out [M, K] bf16: required with a block; may be h itself (in place).
  *   x_out [M, K] bf16, or NULL with a block (after the last one).
  * The sums run in fp32; x_out is computed from h_out before its rounding to bf16.
@@ -533,7 +533,7 @@ int svdq_rope_axes(const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_
  *     cu_seqlens[b] .. cu_seqlens[b + 1] - 1; not decreasing; empty sequences are
  *     allowed), or NULL: one sequence of T tokens and B must be 1. Rows of o
  *     outside [cu_seqlens[0], cu_seqlens[B]) are left as they were. Offsets outside
- *     0..T cause no access outside the tensors.
+ *     0..T, or decreasing ones, cause no access outside the tensors.
  *   scale in (0, 2^20]. o must not overlap q, k or v.
  * Scores and softmax statistics are fp32; the probabilities are rounded to bf16
  * for the second product (relative to a running maximum), their sum is taken

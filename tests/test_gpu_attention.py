@@ -220,6 +220,21 @@ def test_bad_offsets_stay_inside(gpu_lib, cu):
     assert (buf[0] == 7).all() and (buf[2] == 7).all()
 
 
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("cu", [[0, 100, 200, 0, 300], [250, 300, 0, 200, 100, 300], [100, 200, 300, 0, 40, 300]])
+def test_decreasing_offsets_stay_inside(gpu_lib, cu, causal):
+    """Tiles are numbered by the offsets: decreasing ones can name a tile before its sequence's start. What
+    stands around the output stays, and every written row is a mean of values of the tensor."""
+    T, H, D, pad = 300, 2, 64, 400
+    q, k, _ = make(T, H, H, D, 21)
+    v = torch.full_like(k, 0.75)
+    buf = torch.full((T + 2 * pad, H, D), 3.0, device="cuda", dtype=torch.bfloat16)
+    gpu_lib.attention_packed(q, k, v, dev(cu), causal=causal, out=buf[pad:pad + T])
+    assert bool((buf[:pad] == 3.0).all()) and bool((buf[pad + T:] == 3.0).all())
+    mid = buf[pad:pad + T]
+    assert bool(((mid == 3.0) | ((mid - 0.75).abs() <= 2.0 ** -7)).all())
+
+
 def test_repeats_streams_and_graph(gpu_lib):
     q, k, v = make(600, 4, 2, 128, 11)
     cu = dev(offsets([250, 1, 349]))
