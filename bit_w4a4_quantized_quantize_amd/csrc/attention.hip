@@ -178,8 +178,12 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a, int l
   f32x16 acc[JD];
 #pragma unroll
   for (int j = 0; j < JD; ++j) acc[j] = f32x16{};
-  float m = -1e30f, l = 0.0f, mc = 0.0f;
   const float c = a.scale * 1.4426950408889634f;   // exponents in base 2
+  // The maximum starts below every finite score whose exponent is finite. Exponents are x c - mc,
+  // mc = m c: its rounding is a factor common to the row, unless it is so large (`far`) that the
+  // factor leaves fp32: then m is taken off the scores first and mc is 0.
+  float m = -3.4028234663852886e38f / fmaxf(c, 1.0f), l = 0.0f, mc = 0.0f;
+  bool far = false;   // the same in every lane
   const float slack = kSlack / c;
 
   // probabilities of score pair r (0..15) of a tile; their sum is taken before they are
@@ -214,8 +218,17 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a, int l
     const float alpha = __builtin_amdgcn_exp2f((m - mn) * c);
     m = mn;
     mc = mn * c;
+    far = __ballot(fabsf(mc) > 1048576.0f) != 0;
+    if (far) mc = 0.0f;
     l *= alpha;
     return alpha;
+  };
+
+  auto from_max = [&](f32x16 (&x)[2]) {
+    if (far) {
+#pragma unroll
+      for (int r = 0; r < 32; ++r) x[r >> 4][r & 15] -= m;
+    }
   };
 
   // Start of step kt: one barrier frees K(kt) and V(kt - 1) for the copies of K(kt + 2) and
@@ -264,6 +277,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a, int l
     }
     const bool up = __ballot(mx > m + slack) != 0;
     if (up) alpha = raise(mx);
+    from_max(nxt);
 #pragma unroll
     for (int u = kMax; u < NV; ++u) {
       value(u);
@@ -302,6 +316,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a, int l
 #pragma unroll
     for (int r = 1; r < 32; ++r) mx = fmaxf(mx, s0[r >> 4][r & 15]);
     raise(mx);
+    from_max(s0);
 #pragma unroll
     for (int r = 0; r < 8; ++r) pair(s0, p0, r);
     for (; kt + 2 < ntw; kt += 2) {

@@ -235,6 +235,18 @@ def test_decreasing_offsets_stay_inside(gpu_lib, cu, causal):
     assert bool(((mid == 3.0) | ((mid - 0.75).abs() <= 2.0 ** -7)).all())
 
 
+@pytest.mark.parametrize("T", [1, 70, 300])
+def test_far_negative_scores(gpu_lib, T):
+    """Equal scores of -1.3e34 (q k^T = -128 * 1e16 * 1e16): the mean of the values, as for any equal scores.
+    Probabilities are exactly 1, so only the fp32 sums (T 2^-24 of the magnitudes) and one rounding remain."""
+    _, _, v = make(T, 2, 2, 128, 22)
+    q = torch.full_like(v, 1e16)
+    o = gpu_lib.attention_packed(q, -q, v)
+    ref = f64(v).mean(0, keepdims=True)
+    tol = 2.0 ** -8 * np.abs(ref) + 2 * T * 2.0 ** -24 * np.abs(f64(v)).mean(0, keepdims=True)
+    assert (np.abs(f64(o) - ref) <= tol).all()
+
+
 def test_repeats_streams_and_graph(gpu_lib):
     q, k, v = make(600, 4, 2, 128, 11)
     cu = dev(offsets([250, 1, 349]))
