@@ -1199,7 +1199,7 @@ int svdq_linear_w4a4_noalloc(const void* x, const void* smooth, const void* weig
                           M, N, K, R, y, ws, kNoallocScratchBytes, stream);
 }
 
-// ---- measurement helpers (not part of the layer) ----
+// ---- operators between the linears ----
 
 static int check_int8_mnk(int64_t M, int64_t N, int64_t K) {
   int st = check_mk(M, K, 0);
@@ -1427,7 +1427,7 @@ int svdq_norm_gated_int8(const void* h, const void* block, const void* post_weig
 
 // A tensor of T tokens x `heads` heads x D contiguous elements with element strides
 // for token and head (the stride of an axis of length one does not matter: it
-// becomes 0). span: elements from the first to one past the last.
+// becomes that of packed elements). span: elements from the first to one past the last.
 struct Heads {
   const char* name;
   const void* p;
@@ -1438,8 +1438,8 @@ static int make_heads(Heads* o, const char* name, const void* p, int64_t st, int
                       int64_t D) {
   if (p == nullptr) return fail(SVDQ_ERR_NULL, "%s is NULL", name);
   if (!aligned16(p)) return fail(SVDQ_ERR_ALIGN, "%s is not 16-byte aligned", name);
-  if (T == 1) st = 0;
-  if (heads == 1) sh = 0;
+  if (T == 1) st = D;
+  if (heads == 1) sh = D;
   if (st < 0 || sh < 0) return fail(SVDQ_ERR_SHAPE, "%s has a negative stride", name);
   if (st >= kMaxDim || sh >= (int64_t(1) << 40))
     return fail(SVDQ_ERR_UNSUPPORTED, "%s: a token stride must be below 2^24 elements and a head stride below 2^40", name);
@@ -1631,6 +1631,8 @@ int svdq_attention_packed(const void* q, int64_t q_stride_t, int64_t q_stride_h,
   if (int st_ = launched(e, "attention", s)) return st_;
   return ok();
 }
+
+// ---- measurement helpers (not part of the layer) ----
 
 size_t svdq_calib_table_bytes(void) { return svdq::calib_table_bytes(); }
 

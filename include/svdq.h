@@ -513,7 +513,8 @@ int svdq_norm_gated_int8(const void* h, const void* block, const void* post_weig
  *     input (same pointer and strides: in place). Any other overlap with an input or
  *     the other output is SVDQ_ERR_ALIAS.
  * Angles are reduced in fp64; norm and rotation run in fp32 with one rounding to
- * bf16. D: 64 or 128 (SVDQ_ERR_UNSUPPORTED); theta in [1, 1e9]; T * (H + Hk) < 2^31.
+ * bf16. D: 64 or 128 (SVDQ_ERR_UNSUPPORTED); theta in [1, 1e9]; T below 2^24; H, Hk at
+ * most 65535; T * (H + Hk) < 2^31.
  */
 int svdq_rope_axes(const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t H, const void* k,
                    int64_t k_stride_t, int64_t k_stride_h, int64_t Hk, const void* q_weight, const void* k_weight,

@@ -247,6 +247,15 @@ def test_far_negative_scores(gpu_lib, T):
     assert (np.abs(f64(o) - ref) <= tol).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_one_token_with_infinite_values(gpu_lib, D):
+    """A sequence of one token answers with that token's values, infinities included."""
+    q, k, v = make(1, 2, 2, D, 23)
+    v[0, 0, 3], v[0, 1, 5] = float("inf"), float("-inf")
+    for cu in (None, dev([0, 1])):
+        assert torch.equal(gpu_lib.attention_packed(q, k, v, cu), v)
+
+
 def test_repeats_streams_and_graph(gpu_lib):
     q, k, v = make(600, 4, 2, 128, 11)
     cu = dev(offsets([250, 1, 349]))
