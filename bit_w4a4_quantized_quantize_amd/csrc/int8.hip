@@ -291,8 +291,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_int8_kernel(Int8GemmArgs a,
   } else {
     if (p0 < p1) load_panel(p0);
     for (int kp = p0; kp < p1; ++kp) {
-      wait_copies<0>();
-      barrier_no_fence();   // panel kp visible to every wave, the other stage is free
+      __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0), lgkmcnt(0)
+      barrier_no_fence();   // panel kp visible to every wave, the other stage is read to its end
       if (kp + 1 < p1) load_panel(kp + 1);
       const uint8_t* cur = smem + ((kp - p0) & 1) * C::kStageBytes;
       i32x4 f[TM + TN], g[TM + TN];
@@ -453,7 +453,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void gemm_int8_few_kernel(Int8GemmA
       amax = wave_reduce<true>(amax);
       if (lane == 0) row_max[m][wave % wpr] = amax;
     }
-    if (wpr > 1) __syncthreads();
+    __syncthreads();
     for (int m = wave / wpr; m < M; m += kFewWaves / wpr) {
       const u32x4* xr = reinterpret_cast<const u32x4*>(x + (size_t)m * K);
       float amax = row_max[m][0];
