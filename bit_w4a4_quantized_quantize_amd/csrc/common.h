@@ -126,9 +126,13 @@ __device__ __forceinline__ f16x8 dequant8_f16(uint32_t codes, _Float16 s) {
   return r;
 }
 
+// the larger, or NaN if either is (v_maximum3_f32; fmaxf would drop the NaN)
+__device__ __forceinline__ float max_or_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // Scale of an 8-bit integer row with maximum magnitude amax: codes = rne(v * inv),
 // scale = amax / 127, both quotients correctly rounded. A zero row, and one whose
-// 127 / amax overflows (amax below 2^-120), has zero codes and scale.
+// 127 / amax overflows (amax below 2^-120), has zero codes and scale. A row with an infinity
+// or NaN keeps it as its scale.
 struct Int8Scale {
   float inv, scale;
 };
@@ -136,7 +140,7 @@ __device__ __forceinline__ Int8Scale int8_scale(float amax) {
   Int8Scale q;
   q.inv = __fdiv_rn(127.0f, amax);
   q.scale = __fdiv_rn(amax, 127.0f);
-  if (!(q.inv <= 3.4028234663852886e38f)) q.inv = q.scale = 0.0f;
+  if (q.inv > 3.4028234663852886e38f) q.inv = q.scale = 0.0f;
   return q;
 }
 // 8 codes of v * inv, |v * inv| <= 127 (1 + 2^-23), packed in order. The product, rounded to
@@ -163,7 +167,7 @@ __device__ __forceinline__ u32x4 zero4() { u32x4 z = {0u, 0u, 0u, 0u}; return z;
 // shuffle through LDS costs about 100 cycles a step.
 template <bool MAX>
 __device__ __forceinline__ float wave_reduce(float v) {
-  auto both = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+  auto both = [](float a, float b) { return MAX ? max_or_nan(a, b) : a + b; };
 #define SVDQ_DPP(x, ctrl) \
   __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), ctrl, 0xF, 0xF, true))
   v = both(v, SVDQ_DPP(v, 0xB1));

@@ -69,13 +69,13 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void quant_int8_kernel(con
     for (int u = 0; u < NV; ++u) {
       scaled8<SMOOTH>(w[u], f[u], v[u]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[u][e]));
+      for (int e = 0; e < 8; ++e) amax = max_or_nan(amax, fabsf(v[u][e]));
     }
   } else {
     for (int i = tid; i < nv; i += kThreads) {
       scaled8<SMOOTH>(xr[i], SMOOTH ? sm[i] : zero4(), v[0]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[0][e]));
+      for (int e = 0; e < 8; ++e) amax = max_or_nan(amax, fabsf(v[0][e]));
     }
   }
   amax = wave_reduce<true>(amax);
@@ -83,7 +83,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void quant_int8_kernel(con
     if ((tid & 63) == 0) part[tid >> 6] = amax;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < NW; ++w) amax = fmaxf(amax, part[w]);
+    for (int w = 0; w < NW; ++w) amax = max_or_nan(amax, part[w]);
   }
   const Int8Scale q = int8_scale(amax);
   if (tid == 0) ascales[row] = q.scale;
@@ -448,7 +448,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void gemm_int8_few_kernel(Int8GemmA
         float v[8];
         scaled8<SMOOTH>(xr[i], SMOOTH ? sm[i] : zero4(), v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+        for (int e = 0; e < 8; ++e) amax = max_or_nan(amax, fabsf(v[e]));
       }
       amax = wave_reduce<true>(amax);
       if (lane == 0) row_max[m][wave % wpr] = amax;
@@ -457,7 +457,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void gemm_int8_few_kernel(Int8GemmA
     for (int m = wave / wpr; m < M; m += kFewWaves / wpr) {
       const u32x4* xr = reinterpret_cast<const u32x4*>(x + (size_t)m * K);
       float amax = row_max[m][0];
-      for (int w = 1; w < wpr; ++w) amax = fmaxf(amax, row_max[m][w]);
+      for (int w = 1; w < wpr; ++w) amax = max_or_nan(amax, row_max[m][w]);
       const Int8Scale qs = int8_scale(amax);
       if (sub == 0) scales[m] = qs.scale;
       for (int i = sub; i < nv; i += step) {

@@ -38,7 +38,7 @@ __device__ __forceinline__ float reduce_wg(float v, float* part) {
   __syncthreads();
   v = part[0];
 #pragma unroll
-  for (int w = 1; w < NW; ++w) v = MAX ? fmaxf(v, part[w]) : v + part[w];
+  for (int w = 1; w < NW; ++w) v = MAX ? max_or_nan(v, part[w]) : v + part[w];
   return v;
 }
 
@@ -159,7 +159,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_gated_kernel(Nor
           for (int e = 0; e < 8; ++e) h[u][e] *= sm[e];
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(h[u][e]));
+        for (int e = 0; e < 8; ++e) amax = max_or_nan(amax, fabsf(h[u][e]));
       }
     }
   }

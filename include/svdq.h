@@ -50,7 +50,8 @@
  *    lora_act and the packed activation buffer each below 2 GiB, and the
  *    GEMM on packed operands needs the packed activation and packed weight
  *    buffers each below 2 GiB (SVDQ_ERR_UNSUPPORTED otherwise).
- *  - NaN or Inf inputs are not checked; results are then unspecified.
+ *  - NaN or Inf inputs are not checked; results are then unspecified, except where an
+ *    operator below says more.
  */
 #ifndef SVDQ_H
 #define SVDQ_H
@@ -430,7 +431,8 @@ int svdq_linear_mxfp4(const void* x, const void* smooth, const void* w_codes, co
  *   v = x * smooth (fp32, exact; smooth NULL = 1), a[m] = max_k |v|,
  *   codes = rne(v * (127 / a[m])), ascales[m] = a[m] / 127   (fp32 steps; the
  *     quotients correctly rounded; a zero row gives zero codes and scale 0, and a
- *     row whose maximum is so small that 127 / a[m] overflows is taken as zero)
+ *     row whose maximum is so small that 127 / a[m] overflows is taken as zero; a row
+ *     with an infinity or NaN has it as its scale and so NaN in all of its y)
  *   y = bf16( (sum_k codes[m, k] * weight[n, k]) * ascales[m] * wscales[n] + bias[n] )
  *
  *   x [M, K] bf16, smooth [K] bf16 or NULL, codes [M, K] int8, ascales [M] fp32,

@@ -65,6 +65,26 @@ def test_quantize_zero_tiny_and_tie_rows(gpu_lib):
     assert codes[4, 1] == 0 and codes[4, 2] == 2 and codes[4, 3] == 2   # to even
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("M,K", [(5, 48), (5, 2064), (6, 3840), (9, 10240), (40, 512), (5, 20000)])
+def test_non_finite_rows_stay_visible(gpu_lib, M, K, bad):
+    """A row that holds an infinity or NaN has it as its scale and NaN as its y; the other rows do not change."""
+    print(f"[int8] non-finite {M} {K} {bad}", flush=True)
+    w, ws, bias = weights(24, K, 5)
+    x = activations(M, K, 6)
+    clean_codes, clean_scales = gpu_lib.quantize_int8(x)
+    clean = gpu_lib.linear_int8(x, w, ws, bias)
+    rows = [1, 3, 4]
+    for r, k in zip(rows, (0, K - 1, K // 2)):
+        x[r, k] = bad
+    others = [m for m in range(M) if m not in rows]
+    codes, scales = gpu_lib.quantize_int8(x)
+    assert torch.equal(codes[others], clean_codes[others]) and torch.equal(scales[others], clean_scales[others])
+    assert bool((torch.isnan(scales) if bad != bad else torch.isinf(scales))[rows].all())
+    for y in (gpu_lib.linear_int8(x, w, ws, bias), gpu_lib.gemm_int8(codes, scales, w, ws, bias)):
+        assert torch.equal(y[others], clean[others]) and bool(torch.isnan(y[rows]).all())
+
+
 SHAPES = [(31, 1312, 70), (29, 1408, 33), (8, 5120, 48), (4, 10240, 40), (32, 1280, 50), (1, 16, 1), (1, 3840, 3840), (2, 272, 107), (5, 48, 33), (7, 10240, 65), (16, 3840, 257), (17, 64, 40),
           (31, 1040, 130), (33, 96, 64), (48, 3840, 1000), (64, 256, 512), (65, 528, 129), (100, 10240, 300),
           (129, 400, 257), (200, 3840, 1283), (333, 1024, 640), (513, 784, 769), (1000, 272, 96), (1030, 2064, 520),

@@ -112,6 +112,21 @@ def test_zero_and_huge_rows(gpu_lib):
     assert not codes[0].any() and scales[0] == 0
 
 
+@pytest.mark.parametrize("K", [256, 1008, 3840, 10240])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_non_finite_rows_stay_visible(gpu_lib, K, bad):
+    """A NaN or infinity in a row leaves NaN or infinity in it, in the codes' scale too; other rows do not change."""
+    d = make(5, K, 1, 6)
+    want, want8 = gpu_lib.norm_gated(**d), gpu_lib.norm_gated_int8(**d)
+    d["h"][1, K - 1] = bad
+    d["block"][3, 0] = bad
+    got, got8 = gpu_lib.norm_gated(**d), gpu_lib.norm_gated_int8(**d)
+    for w, g in zip(want + want8, got + got8):
+        assert torch.equal(w[[0, 2, 4]], g[[0, 2, 4]])
+    assert not bool(torch.isfinite(got[1].float()).all(1)[[1, 3]].any())
+    assert not bool(torch.isfinite(got8[2])[[1, 3]].any())
+
+
 @pytest.mark.parametrize("cu", [[3, 3, 10, 40], [0, 0, 0, 0], [50, 50, 50, 50], [0, 64, 64, 64], [7, 20, 20, 64]])
 def test_rows_outside_the_groups_are_left(gpu_lib, cu):
     M, K = 64, 528
