@@ -156,7 +156,7 @@ struct I8Split {
 template <int WM, int WN, int TM, int TN, int S, bool PIPE>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_int8_kernel(Int8GemmArgs a, I8Split sp) {
   using C = I8Cfg<WM, WN, TM, TN, S>;
-  static_assert(PIPE || S == 2, "the plain loop has two stages");
+  static_assert(S == 2 || (PIPE && S == 3), "two or three stages, the plain loop two");
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -258,8 +258,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_int8_kernel(Int8GemmArgs a,
     };
     // until the copies of a panel have landed: those of `later` panels may be in flight
     auto wait_panel = [&](int later) {
-      if (S >= 4 && later >= 2) wait_copies<(S >= 4 ? 2 : 0) * C::kPerWave>();
-      else if (S >= 3 && later >= 1) wait_copies<(S >= 3 ? 1 : 0) * C::kPerWave>();
+      if (S >= 3 && later >= 1) wait_copies<(S >= 3 ? 1 : 0) * C::kPerWave>();
       else wait_copies<0>();
     };
     if (p0 < p1) {
@@ -525,14 +524,18 @@ hipError_t launch_few(const Int8GemmArgs& a, const uint16_t* x, const uint16_t* 
   return hipGetLastError();
 }
 
-// Tile shape and split of k by an estimate in microseconds, from measured times (M, N, K from
-// 40 to 4096, 500 to 11520, 1040 to 10240): a workgroup's panel takes `share` of its CU's time, at
-// least `least` when it has the CU to itself (the panel's loads are then the limit), and a CU
-// works through ceil(workgroups / 256) of them; 5 us start and end a product. A split adds a
-// launch (2.5 us on the device, 3 of the caller) and the partial sums' traffic. Measured at 4096 x 10240, K = 3840: 148 us in
-// 256 x 320 tiles, 171 in 256 x 256, 185 in 128 x 128; at 333 x 3840, K = 10240: 36 us in
-// 128 x 64 tiles, 129 in 256 x 320; at 40 x 3840, K = 3840: 9.8 us in 64 x 64 tiles with k
-// split four ways, 12.6 unsplit.
+// Tile shape, stages and split of k by an estimate in microseconds, fitted to times with weights
+// from memory (M from 48 to 6000; ten weights from 1300 x 2064 to 11520 x 3840 and 3840 x 10240; every
+// shape with k split 1 to 8 ways; the choice is within 1% of the best time on average, 11% at
+// worst). A panel takes `share` of its CU's time per workgroup, at least `least` where a CU has
+// too few of them; a CU works through ceil(workgroups / 256) of them; 5.2 us start and end a
+// product. A split adds a launch (2 us on the device) and the partial sums' traffic (1.8 us per
+// way at 333 x 3840). Three stages, where they leave a CU one workgroup, pay while the tiles are
+// few: at 1024 x 3840, K = 3840, 128 x 128 tiles take 24 us with three and 31 with two; at
+// 333 x 3840, K = 10240, 192 x 128 tiles and k split four ways 30 and 33; at 1024 x 10240, K = 3840,
+// 192 x 128 tiles 61 and 47. 4096 x 3840, K = 10240: 148 us in 256 x 256 tiles (240 of them), 165 in
+// 256 x 320; 4096 x 10240, K = 3840: 171 and 158. 48 x 3840, K = 10240: 16 us in 64 x 64 tiles with k
+// split four ways, 33 unsplit.
 struct I8Plan {
   int shape;     // index into the table
   int splits, panels;
@@ -540,18 +543,19 @@ struct I8Plan {
 
 I8Plan plan_int8(int64_t M, int64_t N, int64_t K) {
   static const struct { int bm, bn; double share, least; } shapes[] = {
-      {256, 320, 2.2, 2.2}, {256, 256, 1.85, 1.85}, {128, 128, 0.5, 0.72}, {128, 64, 0.33, 0.39}, {64, 64, 0.23, 0.29}};
+      {256, 320, 1.99, 1.99}, {256, 256, 1.54, 1.67}, {256, 128, 0.92, 1.00}, {192, 128, 0.86, 0.86},
+      {192, 128, 0.67, 0.98}, {128, 128, 0.64, 0.64}, {128, 64, 0.36, 0.42},  {64, 64, 0.22, 0.28}};
   const int64_t panels = (K + 127) / 128;
   I8Plan best{0, 1, (int)panels};
   double best_t = 1e300;
-  for (int s = 0; s < 5; ++s) {
+  for (int s = 0; s < 8; ++s) {
     const int64_t tiles = ((M + shapes[s].bm - 1) / shapes[s].bm) * ((N + shapes[s].bn - 1) / shapes[s].bn);
-    for (int sp = 1; sp <= 8; sp *= 2) {
-      if (sp > 1 && (panels < 3 * sp || tiles * sp > 1024)) break;
+    for (int sp = 1; sp <= 8; ++sp) {
+      if (sp > 1 && (panels < 2 * sp || tiles * sp > 1024)) break;
       const int64_t per = (panels + sp - 1) / sp;
       const double rounds = (double)((tiles * sp + 255) / 256);
-      const double t = 5.0 + (double)per * fmax(shapes[s].least, rounds * shapes[s].share) +
-                       (sp > 1 ? 4.0 + 1e-6 * (double)(M * N) * sp : 0.0);
+      const double t = 5.2 + (double)per * fmax(shapes[s].least, rounds * shapes[s].share) +
+                       (sp > 1 ? 2.0 + 1.4e-6 * (double)(M * N) * sp : 0.0);
       if (t < best_t) {
         best_t = t;
         best = I8Plan{s, (int)((panels + per - 1) / per), (int)per};
@@ -610,8 +614,11 @@ hipError_t launch_gemm_int8(const Int8GemmArgs& a, void* workspace, hipStream_t 
   const I8Split sp{p.panels, p.splits, static_cast<int32_t*>(workspace)};
   hipError_t e = p.shape == 0   ? launch_int8_cfg<4, 2, 2, 5, 2, false>(a, sp, stream)
                  : p.shape == 1 ? launch_int8_cfg<4, 2, 2, 4, 2, true>(a, sp, stream)
-                 : p.shape == 2 ? launch_int8_cfg<2, 2, 2, 2, 2, true>(a, sp, stream)
-                 : p.shape == 3 ? launch_int8_cfg<2, 2, 2, 1, 3, true>(a, sp, stream)
+                 : p.shape == 2 ? launch_int8_cfg<4, 2, 2, 2, 3, true>(a, sp, stream)
+                 : p.shape == 3 ? launch_int8_cfg<2, 2, 3, 2, 3, true>(a, sp, stream)
+                 : p.shape == 4 ? launch_int8_cfg<2, 2, 3, 2, 2, true>(a, sp, stream)
+                 : p.shape == 5 ? launch_int8_cfg<2, 2, 2, 2, 3, true>(a, sp, stream)
+                 : p.shape == 6 ? launch_int8_cfg<2, 2, 2, 1, 3, true>(a, sp, stream)
                                 : launch_int8_cfg<2, 2, 1, 1, 3, true>(a, sp, stream);
   if (e != hipSuccess || p.splits == 1) return e;
   const dim3 grid((unsigned)((a.M * ((a.N + 3) / 4) + 255) / 256));

@@ -119,6 +119,29 @@ def test_large_sampled_rows(gpu_lib, M, N, rows):
     check_y(y[torch.from_numpy(pick).cuda()], codes, scales, w, ws, b)
 
 
+# sizes that take each tile shape, with all of k (3 and 9 panels) and with k split; ragged rows and channels
+TILES = [(1282, 11167, 272), (1547, 9399, 1040), (397, 8596, 9680), (423, 8360, 10096),
+         (964, 10946, 272), (971, 10921, 1040), (197, 11199, 7440), (215, 10896, 8144),
+         (388, 11118, 272), (401, 11050, 1040), (4421, 129, 7712), (4369, 136, 10976),
+         (263, 10966, 272), (258, 11326, 1040), (5733, 66, 7056), (131, 5984, 4048),
+         (646, 10933, 272), (642, 11105, 1040), (129, 11209, 4416), (130, 10960, 5344),
+         (131, 10915, 272), (130, 11038, 1040), (67, 4257, 3568), (67, 3400, 6208),
+         (65, 8285, 272), (65, 8213, 1040), (2755, 66, 2192), (65, 3056, 2720),
+         (33, 60, 1040), (157, 273, 1296), (33, 61, 1200), (36, 72, 1168)]
+
+
+@pytest.mark.parametrize("M,N,K", TILES)
+def test_every_tile_shape(gpu_lib, M, N, K):
+    print(f"[int8] tiles {M} {N} {K}", flush=True)
+    x = activations(M, K, 7)
+    w, ws, b = weights(N, K, 8)
+    y = gpu_lib.linear_int8(x, w, ws, bias=b)
+    pick = np.unique(np.concatenate([[0, 1, M - 2, M - 1], np.random.default_rng(1).integers(0, M, 20)]))
+    at = torch.from_numpy(pick).cuda()
+    codes, scales = B.quantize_int8(f64(x[at]))
+    check_y(y[at], codes, scales, w, ws, b)
+
+
 def test_most_rows(gpu_lib):
     """2^24 rows: quantiser and product, sampled."""
     M, K, N = 1 << 24, 16, 8
