@@ -1302,7 +1302,7 @@ struct Int8Ws {
 };
 static Int8Ws int8_ws(int64_t M, int64_t N, int64_t K) {
   Int8Ws w;
-  w.scales = align256(svdq::linear_int8_codes_bytes(M, K));
+  w.scales = align256(svdq::linear_int8_codes_bytes(M, N, K));
   w.gemm = w.scales > 0 ? align256(w.scales + (size_t)M * 4) : 0;
   w.total = w.gemm + svdq::gemm_int8_workspace_bytes(M, N, K);
   return w;

@@ -395,18 +395,17 @@ __global__ __launch_bounds__(256) void int8_reduce_kernel(Int8GemmArgs a, const 
   }
 }
 
-// Few tokens (M <= 16 MT): the weight streams past the tokens once, straight from memory. A
-// workgroup takes 16 output channels, its eight waves share k in 64-code steps;
-// v_mfma_i32_16x16x64_i8 with the weight rows as A and the tokens as B, and the waves'
-// sums meet in LDS. QUANT: the activations come as x, and each workgroup first makes all
-// the tokens' codes for itself in LDS (small M * K: cheaper than a launch of its own), with
-// the first weight steps already on their way.
+// Few tokens (M <= 16 MT): bound by the weight's bytes, which stream past the tokens once,
+// straight from memory. A workgroup takes 16 output channels, its eight waves share k in
+// 64-code steps; v_mfma_i32_16x16x64_i8 with the weight rows as A and the tokens as B, and the
+// waves' sums meet in LDS. QUANT: the activations come as x, and each workgroup first makes
+// all the tokens' codes for itself in LDS (small M * K: cheaper than a launch of its own), with
+// the first weight steps already on their way. LEAD: weight steps in flight per wave.
 constexpr int kFewWaves = 8;
-constexpr int kFewLead = 4;    // weight steps in flight per wave
 
 __host__ __device__ constexpr int few_pitch(int K) { return (K + 255) / 256 * 256 + 16; }   // LDS bytes of a token
 
-template <int MT, bool QUANT, bool SMOOTH>
+template <int MT, int LEAD, bool QUANT, bool SMOOTH>
 __global__ __launch_bounds__(64 * kFewWaves) void gemm_int8_few_kernel(Int8GemmArgs a, const uint16_t* __restrict__ x,
                                                                       const uint16_t* __restrict__ smooth) {
   __shared__ i32x4 part[kFewWaves][MT][64];
@@ -429,9 +428,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void gemm_int8_few_kernel(Int8GemmA
   constexpr int kLine = 128 * kFewWaves;
   constexpr auto lead = [](int u) { return 64 * (u & 1) + kLine * (u >> 1); };
   const int k_first = 128 * wave;
-  i32x4 fw[kFewLead];
+  i32x4 fw[LEAD];
 #pragma unroll
-  for (int u = 0; u < kFewLead; ++u) fw[u] = weight_at(k_first + lead(u));
+  for (int u = 0; u < LEAD; ++u) fw[u] = weight_at(k_first + lead(u));
 
   const int8_t* pt[MT];
   if constexpr (QUANT) {
@@ -474,10 +473,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void gemm_int8_few_kernel(Int8GemmA
     if (tid < 16 * MT) scales[tid] = tid < M ? a.ascales[tid] : 0.0f;
   }
   i32x4 acc[MT] = {};
-  for (int k = k_first; k < K; k += lead(kFewLead)) {
-    i32x4 ft[kFewLead][MT];
+  for (int k = k_first; k < K; k += lead(LEAD)) {
+    i32x4 ft[LEAD][MT];
 #pragma unroll
-    for (int u = 0; u < kFewLead; ++u)
+    for (int u = 0; u < LEAD; ++u)
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         const i32x4 zero = {};
@@ -485,10 +484,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void gemm_int8_few_kernel(Int8GemmA
         ft[u][t] = at + 16 * q < K ? *reinterpret_cast<const i32x4*>(pt[t] + at) : zero;
       }
 #pragma unroll
-    for (int u = 0; u < kFewLead; ++u) {
+    for (int u = 0; u < LEAD; ++u) {
 #pragma unroll
       for (int t = 0; t < MT; ++t) acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u], ft[u][t], acc[t], 0, 0, 0);
-      fw[u] = weight_at(k + lead(kFewLead + u));
+      fw[u] = weight_at(k + lead(LEAD + u));
     }
   }
 #pragma unroll
@@ -514,14 +513,26 @@ __global__ __launch_bounds__(64 * kFewWaves) void gemm_int8_few_kernel(Int8GemmA
   }
 }
 
-template <int MT>
-hipError_t launch_few(const Int8GemmArgs& a, const uint16_t* x, const uint16_t* smooth, hipStream_t stream) {
+template <int MT, int LEAD>
+hipError_t launch_few_cfg(const Int8GemmArgs& a, const uint16_t* x, const uint16_t* smooth, hipStream_t stream) {
   const dim3 grid((unsigned)((a.N + 15) / 16)), block(64 * kFewWaves);
   const unsigned lds = x != nullptr ? (unsigned)a.M * few_pitch((int)a.K) : 0;
-  if (x == nullptr) hipLaunchKernelGGL((gemm_int8_few_kernel<MT, false, false>), grid, block, 0, stream, a, x, smooth);
-  else if (smooth == nullptr) hipLaunchKernelGGL((gemm_int8_few_kernel<MT, true, false>), grid, block, lds, stream, a, x, smooth);
-  else hipLaunchKernelGGL((gemm_int8_few_kernel<MT, true, true>), grid, block, lds, stream, a, x, smooth);
+  if (x == nullptr)
+    hipLaunchKernelGGL((gemm_int8_few_kernel<MT, LEAD, false, false>), grid, block, 0, stream, a, x, smooth);
+  else if (smooth == nullptr)
+    hipLaunchKernelGGL((gemm_int8_few_kernel<MT, LEAD, true, false>), grid, block, lds, stream, a, x, smooth);
+  else
+    hipLaunchKernelGGL((gemm_int8_few_kernel<MT, LEAD, true, true>), grid, block, lds, stream, a, x, smooth);
   return hipGetLastError();
+}
+
+// Eight steps in flight while a workgroup has its CU to itself, four where more of them fit with
+// fewer registers. Weights from memory, one token, four and eight: 3840 x 3840 6.8 and 5.9 us,
+// 3840 x 10240 14.7 and 13.9, 10240 x 3840 12.7 and 14.1 (3.1 TB/s of 39 MB, 2.5 us of them a launch).
+hipError_t launch_few(const Int8GemmArgs& a, const uint16_t* x, const uint16_t* smooth, hipStream_t stream) {
+  const bool alone = a.N <= 256 * 16;
+  if (a.M <= 16) return alone ? launch_few_cfg<1, 8>(a, x, smooth, stream) : launch_few_cfg<1, 4>(a, x, smooth, stream);
+  return alone ? launch_few_cfg<2, 8>(a, x, smooth, stream) : launch_few_cfg<2, 4>(a, x, smooth, stream);
 }
 
 // Tile shape, stages and split of k by an estimate in microseconds, fitted to times with weights
@@ -578,14 +589,18 @@ hipError_t launch_int8_cfg(const Int8GemmArgs& a, const I8Split& sp, hipStream_t
   return hipGetLastError();
 }
 
-constexpr int kFewTokens = 32;
+// Every workgroup reads all the tokens' codes, so above 8 tokens and 2^24 weights the tiles win (16
+// tokens, weights from memory: 3840 x 3840 7.3 us and 10.3 in tiles, 10240 x 3840 16.1 and 13.4; 8 tokens:
+// 13.9 and 13.4, but one launch instead of two for 3840 x 10240).
+bool few_tokens(int64_t M, int64_t N, int64_t K) { return M <= 8 || (M <= 32 && N * K <= (int64_t(1) << 24)); }
+
 // The layer from x in one launch: every workgroup makes the tokens' codes again, so only while they
-// are few. Against two launches (N = 3840): 7.0 and 8.5 us for 1 x 3840, 9.3 and 9.1 us for
-// 8 x 3840, 12.3 and 9.5 us for 12 x 3840 on the device alone; one launch saves another 3 us
+// are few. Against two launches (N = 3840, on the device): 6.9 and 8.2 us for 1 x 3840, 7.7 and 8.5
+// for 4 x 3840, 9.3 and 8.9 for 8 x 3840, 17.5 and 15.9 for 4 x 10240; one launch saves another 3 us
 // of the caller's time where the calls are not in a graph.
-bool few_from_x(int64_t M, int64_t K) {
+bool few_from_x(int64_t M, int64_t N, int64_t K) {
   // codes and sums together stay inside 64 KB of LDS
-  return M <= kFewTokens && M * K <= 40960 && M * few_pitch((int)K) <= 46 * 1024;
+  return few_tokens(M, N, K) && M * K <= 32768 && M * few_pitch((int)K) <= 46 * 1024;
 }
 
 }  // namespace
@@ -602,14 +617,13 @@ hipError_t launch_quant_int8(const uint16_t* x, const uint16_t* smooth, int64_t 
 }
 
 size_t gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (M <= kFewTokens) return 0;
+  if (few_tokens(M, N, K)) return 0;
   const I8Plan p = plan_int8(M, N, K);
   return p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)N * 4 : 0;
 }
 
 hipError_t launch_gemm_int8(const Int8GemmArgs& a, void* workspace, hipStream_t stream) {
-  if (a.M <= kFewTokens)
-    return a.M <= 16 ? launch_few<1>(a, nullptr, nullptr, stream) : launch_few<2>(a, nullptr, nullptr, stream);
+  if (few_tokens(a.M, a.N, a.K)) return launch_few(a, nullptr, nullptr, stream);
   const I8Plan p = plan_int8(a.M, a.N, a.K);
   const I8Split sp{p.panels, p.splits, static_cast<int32_t*>(workspace)};
   hipError_t e = p.shape == 0   ? launch_int8_cfg<4, 2, 2, 5, 2, false>(a, sp, stream)
@@ -626,11 +640,13 @@ hipError_t launch_gemm_int8(const Int8GemmArgs& a, void* workspace, hipStream_t 
   return hipGetLastError();
 }
 
-size_t linear_int8_codes_bytes(int64_t M, int64_t K) { return few_from_x(M, K) ? 0 : (size_t)M * (size_t)K; }
+size_t linear_int8_codes_bytes(int64_t M, int64_t N, int64_t K) {
+  return few_from_x(M, N, K) ? 0 : (size_t)M * (size_t)K;
+}
 
 hipError_t launch_linear_int8(const Int8GemmArgs& a, const uint16_t* x, const uint16_t* smooth, int8_t* codes,
                               float* ascales, void* workspace, hipStream_t stream) {
-  if (few_from_x(a.M, a.K)) return a.M <= 16 ? launch_few<1>(a, x, smooth, stream) : launch_few<2>(a, x, smooth, stream);
+  if (few_from_x(a.M, a.N, a.K)) return launch_few(a, x, smooth, stream);
   hipError_t e = launch_quant_int8(x, smooth, a.M, a.K, codes, ascales, stream);
   if (e != hipSuccess) return e;
   Int8GemmArgs g = a;

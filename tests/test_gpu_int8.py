@@ -130,6 +130,21 @@ TILES = [(1282, 11167, 272), (1547, 9399, 1040), (397, 8596, 9680), (423, 8360, 
          (33, 60, 1040), (157, 273, 1296), (33, 61, 1200), (36, 72, 1168)]
 
 
+@pytest.mark.parametrize("M,K,N", [(1, 3840, 5003), (3, 10240, 4500), (7, 1040, 4999), (16, 10240, 4100), (17, 1296, 6001),
+                                   (32, 2048, 8190), (24, 10240, 3840), (17, 4112, 4200), (20, 4096, 4096), (16, 48, 20000)])
+@pytest.mark.parametrize("smooth", [False, True])
+def test_few_tokens_many_channels(gpu_lib, M, K, N, smooth):
+    """More channels than 16 for each CU take another kernel; 17 to 32 tokens take tiles above 2^24 weights."""
+    print(f"[int8] few {M} {K} {N} smooth={smooth}", flush=True)
+    x = activations(M, K, 9)
+    w, ws, b = weights(N, K, 10)
+    sm = (torch.rand(K) + 0.5).bfloat16().cuda() if smooth else None
+    y = gpu_lib.linear_int8(x, w, ws, bias=b, smooth=sm)
+    codes, scales = gpu_lib.quantize_int8(x, sm)
+    assert torch.equal(gpu_lib.gemm_int8(codes, scales, w, ws, bias=b), y)
+    check_y(y, *B.quantize_int8(f64(x), None if sm is None else f64(sm)), w, ws, b)
+
+
 @pytest.mark.parametrize("M,N,K", TILES)
 def test_every_tile_shape(gpu_lib, M, N, K):
     print(f"[int8] tiles {M} {N} {K}", flush=True)
