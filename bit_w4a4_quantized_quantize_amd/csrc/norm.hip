@@ -6,8 +6,11 @@
 //
 // One workgroup per row; the row stays in registers between the two sums, so h
 // and block are read once and h_out and x_out (or x's int8 codes) written once:
-// 16896 x 3840 moves 519 MB in 100 us (5.2 TB/s; 103 us without streaming stores).
-// Sums in fp32; x_out comes from h_out before its rounding to bf16.
+// 16896 x 3840 moves 519 MB in 93 us (5.6 TB/s); to codes, with a block 84 us (5.4), without one
+// 42 (4.7): there the vector instructions, about 13 an element, and the two reductions show, so
+// the cases with both weights are code of their own (46 -> 42, 96 -> 93 us). Streaming stores are
+// worth 3 us, weights requested before each sum 4. Long rows take eight waves: 4096 x 10240 to
+// codes 29 us, with sixteen 63. Sums in fp32; x_out comes from h_out before its rounding to bf16.
 #include "common.h"
 #include "kernels.h"
 
@@ -105,12 +108,13 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_gated_kernel(Nor
         float w[8], gt[8];
         if (a.post != nullptr) unpack8(w1[u], w);
         if (a.gate != nullptr) unpack8(w2[u], gt);
+        if (a.post != nullptr && a.gate != nullptr) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float f = r;
-          if (a.post != nullptr) f *= w[e];
-          if (a.gate != nullptr) f *= gt[e];
-          h[u][e] = __builtin_fmaf(b[u][e], f, h[u][e]);
+          for (int e = 0; e < 8; ++e) h[u][e] = __builtin_fmaf(b[u][e], r * w[e] * gt[e], h[u][e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            h[u][e] = __builtin_fmaf(b[u][e], a.post != nullptr ? r * w[e] : a.gate != nullptr ? r * gt[e] : r, h[u][e]);
         }
         __builtin_nontemporal_store(pack8(h[u]), reinterpret_cast<u32x4*>(a.h_out + base + 8 * (size_t)i));
       }
@@ -140,12 +144,12 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_gated_kernel(Nor
       float w[8], sc[8];
       if (a.pre != nullptr) unpack8(w1[u], w);
       if (a.scale != nullptr) unpack8(w2[u], sc);
+      if (a.pre != nullptr && a.scale != nullptr) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float f = r;
-        if (a.pre != nullptr) f *= w[e];
-        if (a.scale != nullptr) f *= 1.0f + sc[e];
-        h[u][e] *= f;
+        for (int e = 0; e < 8; ++e) h[u][e] *= r * __builtin_fmaf(w[e], sc[e], w[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[u][e] *= a.pre != nullptr ? r * w[e] : a.scale != nullptr ? r * (1.0f + sc[e]) : r;
       }
       const u32x4 x = pack8(h[u]);
       if (a.codes == nullptr) {
