@@ -12,6 +12,12 @@
 // step are taken in the order 4 h + {0..3}, 8 + 4 h + {0..3} for half h, so P goes from one
 // product to the next without leaving its lane; V is read in the same order by
 // the transposing LDS read (four keys of one column per lane).
+//
+// Bound: the matrix units' power. 30 heads of 128: 16896 tokens 3600-3800 us (1.15-1.22 PFLOP/s at
+// 1.74 GHz; a large library bf16 product reaches 1.33), 4096 tokens 235-260 us (1.0-1.1, 1.9 rounds
+// of workgroups); 13 causal prompts of 315 tokens on average, 32 heads on 8, 31-35 us (their starts
+// and ends). K and V tiles of 64 keys, double buffered by direct copies to LDS: tiles through
+// registers measured equal or 8% slower, 32 keys 18% slower at 4096 tokens.
 #include "common.h"
 #include "kernels.h"
 

@@ -5,6 +5,11 @@
 //
 // on v_mfma_i32_32x32x32_i8: the sum over k is exact in int32 (127 * 128 * K
 // stays below 2^31 up to K = 131072), so its order is free.
+//
+// Bound by the matrix units' power for many tokens (4096 x 10240, K = 3840: 148-158 us, 2.0-2.2
+// POP/s; a large library int8 product reaches 2.24), by the tiles' way from L2 through LDS for
+// hundreds (333 x 3840, K = 10240: 30 us), by the weight's bytes for few (one token, 39 MB of weight
+// from memory: 12.7 us). The quantiser moves 4096 x 3840 in 8.8 us (5.4 TB/s).
 #include "common.h"
 #include "kernels.h"
 #include <math.h>
@@ -36,8 +41,7 @@ __device__ __forceinline__ void scaled8(const u32x4 x, const u32x4 s, float (&v)
 
 // The row's maximum, then its codes. A row is held in registers by NW waves of NV 8-element
 // pieces per lane (K <= NW * 64 * NV * 8), with NW = 1 a workgroup's four waves take a row each;
-// NV = 0: rows of any length, read twice (the second time from the caches). Memory bound:
-// 4096 x 3840 moves 47 MB.
+// NV = 0: rows of any length, read twice (the second time from the caches). Memory bound.
 template <int NW, int NV, bool SMOOTH>
 __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void quant_int8_kernel(const uint16_t* __restrict__ x,
                                                                              const uint16_t* __restrict__ smooth,
@@ -272,7 +276,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_int8_kernel(Int8GemmArgs a,
       for (int kp = p0; kp < p1; ++kp) {
         const uint8_t* cur = smem + ((kp - p0) % S) * C::kStageBytes;
         const uint8_t* nxt = smem + ((kp + 1 - p0) % S) * C::kStageBytes;
-        // a SIMD's waves run out of step by priority (128 x 128 tiles at 2048 x 3840: 39 -> 35 us)
+        // the waves of two workgroups on a SIMD run out of step by priority (192 x 128 tiles of two
+        // stages: 1024 x 10240 59 -> 52 us, 2048 x 11520 112 -> 104; alone on a CU: equal)
         __builtin_amdgcn_s_setprio(1);
         step(fr[0], fr[1], cur, 1, true);
         step(fr[1], fr[0], cur, 2, true);
