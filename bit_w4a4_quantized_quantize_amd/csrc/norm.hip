@@ -51,6 +51,7 @@ template <int NW, int NV, bool BLOCK>
 __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_gated_kernel(NormArgs a) {
   constexpr int kThreads = 64 * NW;
   constexpr int kRows = NW == 1 ? 4 : 1;
+  constexpr bool kBoth = NW < 16;   // sixteen waves have no registers for the extra code
   __shared__ float part[3][NW];
   const int tid = NW == 1 ? threadIdx.x & 63 : threadIdx.x;
   const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kRows +
@@ -108,13 +109,17 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_gated_kernel(Nor
         float w[8], gt[8];
         if (a.post != nullptr) unpack8(w1[u], w);
         if (a.gate != nullptr) unpack8(w2[u], gt);
-        if (a.post != nullptr && a.gate != nullptr) {
+        if (kBoth && a.post != nullptr && a.gate != nullptr) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) h[u][e] = __builtin_fmaf(b[u][e], r * w[e] * gt[e], h[u][e]);
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            h[u][e] = __builtin_fmaf(b[u][e], a.post != nullptr ? r * w[e] : a.gate != nullptr ? r * gt[e] : r, h[u][e]);
+          for (int e = 0; e < 8; ++e) {
+            float f = r;
+            if (a.post != nullptr) f *= w[e];
+            if (a.gate != nullptr) f *= gt[e];
+            h[u][e] = __builtin_fmaf(b[u][e], f, h[u][e]);
+          }
         }
         __builtin_nontemporal_store(pack8(h[u]), reinterpret_cast<u32x4*>(a.h_out + base + 8 * (size_t)i));
       }
@@ -144,12 +149,17 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_gated_kernel(Nor
       float w[8], sc[8];
       if (a.pre != nullptr) unpack8(w1[u], w);
       if (a.scale != nullptr) unpack8(w2[u], sc);
-      if (a.pre != nullptr && a.scale != nullptr) {
+      if (kBoth && a.pre != nullptr && a.scale != nullptr) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[u][e] *= r * __builtin_fmaf(w[e], sc[e], w[e]);
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[u][e] *= a.pre != nullptr ? r * w[e] : a.scale != nullptr ? r * (1.0f + sc[e]) : r;
+        for (int e = 0; e < 8; ++e) {
+          float f = r;
+          if (a.pre != nullptr) f *= w[e];
+          if (a.scale != nullptr) f *= 1.0f + sc[e];
+          h[u][e] *= f;
+        }
       }
       const u32x4 x = pack8(h[u]);
       if (a.codes == nullptr) {
