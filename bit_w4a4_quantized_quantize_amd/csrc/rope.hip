@@ -37,13 +37,19 @@ constexpr int kMaxTokens = 16;   // tokens of a workgroup
 
 // A workgroup takes `per` whole tokens, as many as fill its 512 pieces of 8 elements (one token,
 // in several passes, where that has more): its loads go out first, then per * D / 2 angles are
-// made in LDS, once for all heads, while they travel. Memory bound: 16896 tokens of 30 + 30
-// heads of 128 move 519 MB in 105 us (4.9 TB/s); 110 us without the streaming stores, 114 with
-// four pieces per thread in flight and no streaming stores.
+// made in LDS, once for all heads, while they travel. Memory bound, close enough that vector
+// instructions show: 16896 tokens of 30 + 30 heads of 128 out of a fused buffer move 519 MB in
+// 93 us with the norm (5.6 TB/s) and 90 without; 113 us with the weights applied to the elements
+// instead of the angles, an exact square root and quotient, and addresses made per lane. Streaming
+// stores are worth 5 us; four pieces per thread 102 us, one 98, 128 threads 97.
 template <int D, bool INTER, bool NORM>
-__global__ __launch_bounds__(kThreadsR) void rope_kernel(RopeArgs a, int per) {
+__global__ __launch_bounds__(kThreadsR) void rope_kernel(RopeArgs a, int per, int by_heads) {
   constexpr int kLanes = D / 8;            // lanes per head, 8 elements each
-  __shared__ float2 turn[kMaxTokens][D / 2];
+  // Per token and pair (u, w), pair 4 l + i of lane l at i * kLanes + l (whole rows of banks per
+  // read): cos and sin; with the norm, for q and for k, the factors of u and w in u' and w' with
+  // the weights in them: weight_u cos, weight_w sin, weight_w cos, weight_u sin
+  extern __shared__ __attribute__((aligned(16))) float turn[];
+  constexpr int kTable = NORM ? 8 * (D / 2) : 2 * (D / 2);   // floats of a token
   const int tid = threadIdx.x;
   const int64_t t0 = (int64_t)blockIdx.x * per;
   const int here = (int)min((int64_t)per, a.T - t0);
@@ -63,15 +69,16 @@ __global__ __launch_bounds__(kThreadsR) void rope_kernel(RopeArgs a, int per) {
 #pragma unroll
     for (int u = 0; u < kItems; ++u) {
       const int it = min(first + (u * kThreadsR + tid) / kLanes, items - 1);   // clamped: read, not stored
-      tok[u] = it / heads;
+      tok[u] = (it * by_heads) >> 16;   // it / heads
       const int n = it - tok[u] * heads;
       is_k[u] = n >= a.H[0];
       const int head = is_k[u] ? n - a.H[0] : n;
-      const int64_t t = t0 + tok[u];
-      const HeadView in = is_k[u] ? a.in[1] : a.in[0];
-      const uint16_t* src = in.p + t * in.st + head * in.sh;
-      dst[u] = (is_k[u] ? a.out[1] : a.out[0]) + t * (is_k[u] ? a.out_st[1] : a.out_st[0]) +
-               head * (is_k[u] ? a.out_sh[1] : a.out_sh[0]);
+      // token bases of the workgroup (scalar), then this lane's token, fewer than 16 strides below
+      // 2^24, and head
+      const uint16_t* src = (is_k[u] ? a.in[1].p + t0 * a.in[1].st : a.in[0].p + t0 * a.in[0].st) +
+                            (tok[u] * (int)(is_k[u] ? a.in[1].st : a.in[0].st) + head * (is_k[u] ? a.in[1].sh : a.in[0].sh));
+      dst[u] = (is_k[u] ? a.out[1] + t0 * a.out_st[1] : a.out[0] + t0 * a.out_st[0]) +
+               (tok[u] * (int)(is_k[u] ? a.out_st[1] : a.out_st[0]) + head * (is_k[u] ? a.out_sh[1] : a.out_sh[0]));
       if (INTER) {
         const u32x4 w = *reinterpret_cast<const u32x4*>(src + e0);
         lo[u] = u32x2{w[0], w[1]};
@@ -87,29 +94,21 @@ __global__ __launch_bounds__(kThreadsR) void rope_kernel(RopeArgs a, int per) {
         const double x = (double)a.positions[(t0 + k) * a.axes + a.axis[p]] * a.turns[p];
         float s, c;
         sincospif(2.0f * (float)(x - __builtin_rint(x)), &s, &c);
-        turn[k][p] = make_float2(c, s);
+        float* at = turn + k * kTable;
+        const int slot = (p & 3) * kLanes + (p >> 2);
+        if constexpr (NORM) {
+#pragma unroll
+          for (int side = 0; side < 2; ++side) {
+            const uint16_t* w = side ? a.weight[1] : a.weight[0];
+            const float wu = w != nullptr ? bf16lo_to_f32(w[INTER ? 2 * p : p]) : 1.0f;
+            const float ww = w != nullptr ? bf16lo_to_f32(w[INTER ? 2 * p + 1 : p + D / 2]) : 1.0f;
+            reinterpret_cast<f32x4*>(at)[side * (D / 2) + slot] = f32x4{wu * c, ww * s, ww * c, wu * s};
+          }
+        } else {
+          reinterpret_cast<float2*>(at)[slot] = make_float2(c, s);
+        }
       }
       __syncthreads();
-    }
-    float wq[8], wk[8];
-    if (NORM) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float* w = i ? wk : wq;
-        const uint16_t* p = i ? a.weight[1] : a.weight[0];
-        u32x2 x0 = {0x3F803F80u, 0x3F803F80u}, x1 = x0;   // ones
-        if (p != nullptr) {
-          x0 = *reinterpret_cast<const u32x2*>(p + e0);
-          x1 = *reinterpret_cast<const u32x2*>(p + e1);
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          w[2 * e] = bf16lo_to_f32(x0[e]);
-          w[2 * e + 1] = bf16hi_to_f32(x0[e]);
-          w[4 + 2 * e] = bf16lo_to_f32(x1[e]);
-          w[5 + 2 * e] = bf16hi_to_f32(x1[e]);
-        }
-      }
     }
 #pragma unroll
     for (int u = 0; u < kItems; ++u) {
@@ -121,23 +120,34 @@ __global__ __launch_bounds__(kThreadsR) void rope_kernel(RopeArgs a, int per) {
         v[4 + 2 * i] = bf16lo_to_f32(hi[u][i]);
         v[5 + 2 * i] = bf16hi_to_f32(hi[u][i]);
       }
-      if (NORM) {
+      float o[8];
+      const float* at = turn + tok[u] * kTable;
+      if constexpr (NORM) {
         float ss = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[e], v[e], ss);
-        ss = sum_lanes<kLanes>(ss);
-        const bool on = (is_k[u] ? a.weight[1] : a.weight[0]) != nullptr;
-        const float r = on ? 1.0f / __builtin_sqrtf(ss * (1.0f / D) + a.eps) : 1.0f;
+        ss = sum_lanes<kLanes>(ss) * (1.0f / D) + a.eps;
+        // v_rsq_f32 (within one unit of the last place) takes no denormals
+        float r = __builtin_amdgcn_rsqf(ss);
+        if (__builtin_expect(__ballot(ss < 1e-30f) != 0, 0) && ss < 1e-30f) r = 1.0f / __builtin_sqrtf(ss);
+        if ((is_k[u] ? a.weight[1] : a.weight[0]) == nullptr) r = 1.0f;
+        const f32x4* f = reinterpret_cast<const f32x4*>(at) + (is_k[u] ? D / 2 : 0) + sub;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= r * (is_k[u] ? wk[e] : wq[e]);
-      }
-      float o[8];
+        for (int i = 0; i < 4; ++i) {
+          const int x = INTER ? 2 * i : i, y = INTER ? 2 * i + 1 : 4 + i;
+          const f32x4 w = f[i * kLanes];
+          o[x] = (v[x] * w[0] - v[y] * w[1]) * r;
+          o[y] = (v[y] * w[2] + v[x] * w[3]) * r;
+        }
+      } else {
+        const float2* f = reinterpret_cast<const float2*>(at) + sub;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int x = INTER ? 2 * i : i, y = INTER ? 2 * i + 1 : 4 + i;
-        const float2 cs = turn[tok[u]][4 * sub + i];
-        o[x] = v[x] * cs.x - v[y] * cs.y;
-        o[y] = v[y] * cs.x + v[x] * cs.y;
+        for (int i = 0; i < 4; ++i) {
+          const int x = INTER ? 2 * i : i, y = INTER ? 2 * i + 1 : 4 + i;
+          const float2 cs = f[i * kLanes];
+          o[x] = v[x] * cs.x - v[y] * cs.y;
+          o[y] = v[y] * cs.x + v[x] * cs.y;
+        }
       }
       if (first + (u * kThreadsR + tid) / kLanes < items) {
         const u32x2 w0 = {pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
@@ -161,10 +171,14 @@ void launch_rope_cfg(const RopeArgs& a, hipStream_t s) {
   int64_t per = full < 1 ? 1 : full > kMaxTokens ? kMaxTokens : full;
   while (per > 1 && (a.T + per - 1) / per < 1024) per /= 2;
   const dim3 grid((unsigned)((a.T + per - 1) / per)), block(kThreadsR);
-  if (a.weight[0] != nullptr || a.weight[1] != nullptr)
-    hipLaunchKernelGGL((rope_kernel<D, INTER, true>), grid, block, 0, s, a, (int)per);
+  const bool norm = a.weight[0] != nullptr || a.weight[1] != nullptr;
+  // 1 / heads in units of 2^-16, rounded up: exact for the heads of several tokens (at most 64 in all)
+  const int by_heads = per == 1 ? 0 : (65536 + a.H[0] + a.H[1] - 1) / (a.H[0] + a.H[1]);
+  const unsigned lds = (unsigned)(per * (D / 2) * (norm ? 32 : 8));   // at most 32 KB
+  if (norm)
+    hipLaunchKernelGGL((rope_kernel<D, INTER, true>), grid, block, lds, s, a, (int)per, by_heads);
   else
-    hipLaunchKernelGGL((rope_kernel<D, INTER, false>), grid, block, 0, s, a, (int)per);
+    hipLaunchKernelGGL((rope_kernel<D, INTER, false>), grid, block, lds, s, a, (int)per, by_heads);
 }
 
 }  // namespace

@@ -113,6 +113,40 @@ def test_zero_heads_rows_and_eps(gpu_lib):
     assert not qo.any()
 
 
+@pytest.mark.parametrize("D,axes", [(64, (16, 24, 24)), (128, (32, 48, 48))])
+@pytest.mark.parametrize("inter", [True, False])
+def test_tiny_and_huge_heads(gpu_lib, D, axes, inter):
+    """Mean squares among fp32's denormals (eps 0; 2^-64 squared is 2^-128), at the border of the fast square
+    root, and up to 1e34: the norm's bound holds relative to the result for all of them. A sum of D denormal
+    squares rounds to multiples of 2^-149, D 2^-150 of 2^-128 D here: 2^-22 of it."""
+    T, H = 12, 5
+    z = torch.randn(T, H, D, generator=torch.Generator().manual_seed(3))
+    for h, size in enumerate((2.0 ** -64, 1e-15, 1.0, 1e8, 1e17)):
+        z[:, h] *= size
+    z = z.bfloat16().cuda()
+    w = (1 + 0.1 * torch.randn(D, generator=torch.Generator().manual_seed(4))).bfloat16().cuda()
+    pos = positions(T, 3, 300, 5)
+    zo, _ = gpu_lib.rope_axes(z, None, pos, axes, interleaved=inter, q_weight=w, eps=0.0)
+    ref, mag = B.rope_axes(f64(z), pos.cpu().numpy(), axes, 10000.0, inter, f64(w), 0.0)
+    tol = 2.0 ** -8 * np.abs(ref) + (6e-7 + (D / 2 + 10) * 2.0 ** -24 + 2.0 ** -22) * 1.01 * mag
+    assert (np.abs(f64(zo) - ref) <= tol).all()
+
+
+def test_non_finite_heads(gpu_lib):
+    """A NaN makes its own head NaN under the norm and reaches no other head or token."""
+    T, H, D, axes = 6, 4, 128, (64, 64)
+    z = torch.randn(T, H, D, generator=torch.Generator().manual_seed(6)).bfloat16().cuda()
+    w = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    pos = positions(T, 2, 50, 7)
+    want, _ = gpu_lib.rope_axes(z, None, pos, axes, q_weight=w)
+    z[2, 1, 77] = float("nan")
+    got, _ = gpu_lib.rope_axes(z, None, pos, axes, q_weight=w)
+    assert bool(torch.isnan(got[2, 1]).all())
+    rest = torch.ones(T, H, dtype=torch.bool, device="cuda")
+    rest[2, 1] = False
+    assert torch.equal(got[rest], want[rest])
+
+
 def test_most_tokens(gpu_lib):
     T = (1 << 24) - 1
     q = torch.randn(T, 1, 64, generator=torch.Generator(device="cuda").manual_seed(12), device="cuda", dtype=torch.bfloat16)
