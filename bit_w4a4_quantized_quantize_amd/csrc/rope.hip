@@ -39,10 +39,12 @@ constexpr int kMaxTokens = 16;   // tokens of a workgroup
 // in several passes, where that has more): its loads go out first, then per * D / 2 angles are
 // made in LDS, once for all heads, while they travel. Memory bound, close enough that vector
 // instructions show: 16896 tokens of 30 + 30 heads of 128 out of a fused buffer move 519 MB in
-// 93 us with the norm (5.6 TB/s) and 90 without; 113 us with the weights applied to the elements
-// instead of the angles, an exact square root and quotient, and addresses made per lane. Streaming
-// stores are worth 5 us; four pieces per thread 102 us, one 98, 128 threads 97.
-template <int D, bool INTER, bool NORM>
+// 87 us with the norm (6.0 TB/s); 103 us with the weights applied to the elements instead of the
+// angles, an exact square root and quotient, and addresses made per lane. Scalar bases pay for
+// one token per workgroup (ONE: 89 -> 87) and cost for several (8190 tokens of 24 + 8 heads of
+// 64: 11.0 -> 11.6). Streaming stores are worth 5 us, against four pieces per thread 8, against
+// one 2.
+template <int D, bool INTER, bool NORM, bool ONE>
 __global__ __launch_bounds__(kThreadsR) void rope_kernel(RopeArgs a, int per, int by_heads) {
   constexpr int kLanes = D / 8;            // lanes per head, 8 elements each
   // Per token and pair (u, w), pair 4 l + i of lane l at i * kLanes + l (whole rows of banks per
@@ -69,16 +71,23 @@ __global__ __launch_bounds__(kThreadsR) void rope_kernel(RopeArgs a, int per, in
 #pragma unroll
     for (int u = 0; u < kItems; ++u) {
       const int it = min(first + (u * kThreadsR + tid) / kLanes, items - 1);   // clamped: read, not stored
-      tok[u] = (it * by_heads) >> 16;   // it / heads
+      tok[u] = ONE ? 0 : (it * by_heads) >> 16;   // it / heads
       const int n = it - tok[u] * heads;
       is_k[u] = n >= a.H[0];
       const int head = is_k[u] ? n - a.H[0] : n;
-      // token bases of the workgroup (scalar), then this lane's token, fewer than 16 strides below
-      // 2^24, and head
-      const uint16_t* src = (is_k[u] ? a.in[1].p + t0 * a.in[1].st : a.in[0].p + t0 * a.in[0].st) +
-                            (tok[u] * (int)(is_k[u] ? a.in[1].st : a.in[0].st) + head * (is_k[u] ? a.in[1].sh : a.in[0].sh));
-      dst[u] = (is_k[u] ? a.out[1] + t0 * a.out_st[1] : a.out[0] + t0 * a.out_st[0]) +
-               (tok[u] * (int)(is_k[u] ? a.out_st[1] : a.out_st[0]) + head * (is_k[u] ? a.out_sh[1] : a.out_sh[0]));
+      const uint16_t* src;
+      if constexpr (ONE) {   // the token's bases are scalar
+        src = (is_k[u] ? a.in[1].p + t0 * a.in[1].st : a.in[0].p + t0 * a.in[0].st) +
+              head * (is_k[u] ? a.in[1].sh : a.in[0].sh);
+        dst[u] = (is_k[u] ? a.out[1] + t0 * a.out_st[1] : a.out[0] + t0 * a.out_st[0]) +
+                 head * (is_k[u] ? a.out_sh[1] : a.out_sh[0]);
+      } else {
+        const int64_t t = t0 + tok[u];
+        const HeadView in = is_k[u] ? a.in[1] : a.in[0];
+        src = in.p + t * in.st + head * in.sh;
+        dst[u] = (is_k[u] ? a.out[1] : a.out[0]) + t * (is_k[u] ? a.out_st[1] : a.out_st[0]) +
+                 head * (is_k[u] ? a.out_sh[1] : a.out_sh[0]);
+      }
       if (INTER) {
         const u32x4 w = *reinterpret_cast<const u32x4*>(src + e0);
         lo[u] = u32x2{w[0], w[1]};
@@ -173,12 +182,12 @@ void launch_rope_cfg(const RopeArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)((a.T + per - 1) / per)), block(kThreadsR);
   const bool norm = a.weight[0] != nullptr || a.weight[1] != nullptr;
   // 1 / heads in units of 2^-16, rounded up: exact for the heads of several tokens (at most 64 in all)
-  const int by_heads = per == 1 ? 0 : (65536 + a.H[0] + a.H[1] - 1) / (a.H[0] + a.H[1]);
+  const int by_heads = (65536 + a.H[0] + a.H[1] - 1) / (a.H[0] + a.H[1]);
   const unsigned lds = (unsigned)(per * (D / 2) * (norm ? 32 : 8));   // at most 32 KB
-  if (norm)
-    hipLaunchKernelGGL((rope_kernel<D, INTER, true>), grid, block, lds, s, a, (int)per, by_heads);
-  else
-    hipLaunchKernelGGL((rope_kernel<D, INTER, false>), grid, block, lds, s, a, (int)per, by_heads);
+  if (norm && per == 1) hipLaunchKernelGGL((rope_kernel<D, INTER, true, true>), grid, block, lds, s, a, 1, 0);
+  else if (norm) hipLaunchKernelGGL((rope_kernel<D, INTER, true, false>), grid, block, lds, s, a, (int)per, by_heads);
+  else if (per == 1) hipLaunchKernelGGL((rope_kernel<D, INTER, false, true>), grid, block, lds, s, a, 1, 0);
+  else hipLaunchKernelGGL((rope_kernel<D, INTER, false, false>), grid, block, lds, s, a, (int)per, by_heads);
 }
 
 }  // namespace
