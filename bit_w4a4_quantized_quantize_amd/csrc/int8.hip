@@ -521,23 +521,31 @@ __global__ __launch_bounds__(64 * kFewWaves) void gemm_int8_few_kernel(Int8GemmA
 template <int MT, int LEAD>
 hipError_t launch_few_cfg(const Int8GemmArgs& a, const uint16_t* x, const uint16_t* smooth, hipStream_t stream) {
   const dim3 grid((unsigned)((a.N + 15) / 16)), block(64 * kFewWaves);
-  const unsigned lds = x != nullptr ? (unsigned)a.M * few_pitch((int)a.K) : 0;
   if (x == nullptr)
     hipLaunchKernelGGL((gemm_int8_few_kernel<MT, LEAD, false, false>), grid, block, 0, stream, a, x, smooth);
-  else if (smooth == nullptr)
-    hipLaunchKernelGGL((gemm_int8_few_kernel<MT, LEAD, true, false>), grid, block, lds, stream, a, x, smooth);
-  else
-    hipLaunchKernelGGL((gemm_int8_few_kernel<MT, LEAD, true, true>), grid, block, lds, stream, a, x, smooth);
+  if constexpr (MT <= 2) {   // few_from_x: at most 32 tokens
+    const unsigned lds = (unsigned)a.M * few_pitch((int)a.K);
+    if (x != nullptr && smooth == nullptr)
+      hipLaunchKernelGGL((gemm_int8_few_kernel<MT, LEAD, true, false>), grid, block, lds, stream, a, x, smooth);
+    else if (x != nullptr)
+      hipLaunchKernelGGL((gemm_int8_few_kernel<MT, LEAD, true, true>), grid, block, lds, stream, a, x, smooth);
+  }
   return hipGetLastError();
 }
 
 // Eight steps in flight while a workgroup has its CU to itself, four where more of them fit with
 // fewer registers. Weights from memory, one token, four and eight: 3840 x 3840 6.8 and 5.9 us,
 // 3840 x 10240 14.7 and 13.9, 10240 x 3840 12.7 and 14.1 (3.1 TB/s of 39 MB, 2.5 us of them a launch).
+template <int MT>
+hipError_t launch_few_mt(const Int8GemmArgs& a, const uint16_t* x, const uint16_t* smooth, hipStream_t stream) {
+  return a.N <= 256 * 16 ? launch_few_cfg<MT, 8>(a, x, smooth, stream) : launch_few_cfg<MT, 4>(a, x, smooth, stream);
+}
+
 hipError_t launch_few(const Int8GemmArgs& a, const uint16_t* x, const uint16_t* smooth, hipStream_t stream) {
-  const bool alone = a.N <= 256 * 16;
-  if (a.M <= 16) return alone ? launch_few_cfg<1, 8>(a, x, smooth, stream) : launch_few_cfg<1, 4>(a, x, smooth, stream);
-  return alone ? launch_few_cfg<2, 8>(a, x, smooth, stream) : launch_few_cfg<2, 4>(a, x, smooth, stream);
+  return a.M <= 16   ? launch_few_mt<1>(a, x, smooth, stream)
+         : a.M <= 32 ? launch_few_mt<2>(a, x, smooth, stream)
+         : a.M <= 48 ? launch_few_mt<3>(a, x, smooth, stream)
+                     : launch_few_mt<4>(a, x, smooth, stream);
 }
 
 // Tile shape, stages and split of k by an estimate in microseconds, fitted to times with weights
@@ -594,18 +602,23 @@ hipError_t launch_int8_cfg(const Int8GemmArgs& a, const I8Split& sp, hipStream_t
   return hipGetLastError();
 }
 
-// Every workgroup reads all the tokens' codes, so above 8 tokens and 2^24 weights the tiles win (16
-// tokens, weights from memory: 3840 x 3840 7.3 us and 10.3 in tiles, 10240 x 3840 16.1 and 13.4; 8 tokens:
-// 13.9 and 13.4, but one launch instead of two for 3840 x 10240).
-bool few_tokens(int64_t M, int64_t N, int64_t K) { return M <= 8 || (M <= 32 && N * K <= (int64_t(1) << 24)); }
+// Every workgroup reads all the tokens' codes, and one of 16 channels works through all of k: above 8
+// tokens only up to 2^17 codes and 2^24 weights (from memory, here and in tiles: 33 x 2064 for 1300
+// channels 4.9 and 7.9 us, 48 x 2560 for 3840 8.5 and 9.4, 32 x 3840 for 3840 9.3 and 10.4, 48 x 3840
+// 11.1 and 10.6, 16 x 3840 for 10240 16.1 and 13.4, 33 x 8192 for 1024 15.2 and 10.1). With up to 8 the
+// tiles gain nothing (8 x 3840 for 10240: 13.9 and 13.4).
+bool few_tokens(int64_t M, int64_t N, int64_t K) {
+  return M <= 8 || (M <= 64 && M * K <= (int64_t(1) << 17) && N * K <= (int64_t(1) << 24));
+}
 
 // The layer from x in one launch: every workgroup makes the tokens' codes again, so only while they
 // are few. Against two launches (N = 3840, on the device): 6.9 and 8.2 us for 1 x 3840, 7.7 and 8.5
-// for 4 x 3840, 9.3 and 8.9 for 8 x 3840, 17.5 and 15.9 for 4 x 10240; one launch saves another 3 us
-// of the caller's time where the calls are not in a graph.
+// for 4 x 3840, 9.3 and 8.9 for 8 x 3840, 17.5 and 15.9 for 4 x 10240 (N = 1300: 7.4 and 6.2 for
+// 9 x 2064); one launch saves another 3 us of the caller's time where the calls are not in a graph.
 bool few_from_x(int64_t M, int64_t N, int64_t K) {
   // codes and sums together stay inside 64 KB of LDS
-  return few_tokens(M, N, K) && M * K <= 32768 && M * few_pitch((int)K) <= 46 * 1024;
+  const int64_t rows = M <= 8 ? M : (M + 7) / 8 * 8;   // above 8 a wave makes several rows
+  return M <= 32 && few_tokens(M, N, K) && rows * K <= 32768 && M * few_pitch((int)K) <= 46 * 1024;
 }
 
 }  // namespace

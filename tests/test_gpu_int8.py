@@ -131,10 +131,12 @@ TILES = [(1282, 11167, 272), (1547, 9399, 1040), (397, 8596, 9680), (423, 8360, 
 
 
 @pytest.mark.parametrize("M,K,N", [(1, 3840, 5003), (3, 10240, 4500), (7, 1040, 4999), (16, 10240, 4100), (17, 1296, 6001),
-                                   (32, 2048, 8190), (24, 10240, 3840), (17, 4112, 4200), (20, 4096, 4096), (16, 48, 20000)])
+                                   (32, 2048, 8190), (33, 2064, 1300), (48, 1040, 5003), (49, 400, 4097), (64, 2048, 333),
+                                   (64, 1024, 9001), (63, 2064, 77), (9, 10240, 640), (24, 10240, 3840), (17, 4112, 4200), (20, 4096, 4096), (16, 48, 20000)])
 @pytest.mark.parametrize("smooth", [False, True])
 def test_few_tokens_many_channels(gpu_lib, M, K, N, smooth):
-    """More channels than 16 for each CU take another kernel; 17 to 32 tokens take tiles above 2^24 weights."""
+    """More channels than 16 for each CU take another kernel; 9 to 64 tokens take tiles above 2^17 codes or 2^24
+    weights."""
     print(f"[int8] few {M} {K} {N} smooth={smooth}", flush=True)
     x = activations(M, K, 9)
     w, ws, b = weights(N, K, 10)
