@@ -146,7 +146,7 @@ struct I8Cfg {
   static constexpr int kStageBytes = kChunks * kChunkBytes;
   static constexpr int kCopies = kChunks * 4;                    // 1 KB copies of a panel
   static constexpr int kPerWave = kCopies / kWaves;
-  static constexpr int kOutBytes = kWaves * 32 * (32 * TN) * 2 + BM * 4;   // output staging and row scales
+  static constexpr int kOutBytes = kWaves * 32 * (32 * TN + 8) * 2 + BM * 4;   // output staging and row scales
   static constexpr int kLdsBytes = S * kStageBytes > kOutBytes ? S * kStageBytes : kOutBytes;
   static_assert(kCopies % kWaves == 0, "copies per wave");
 };
@@ -329,8 +329,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_int8_kernel(Int8GemmArgs a,
 
   // the rows' scales in LDS, then bf16 output through LDS: each wave stages 32-row slices
   // row-major and stores whole 16-byte row pieces
-  constexpr int kCols = 32 * TN, kPieces = kCols / 8;
-  float* row_scale = reinterpret_cast<float*>(smem + C::kWaves * 32 * kCols * 2);
+  constexpr int kCols = 32 * TN, kPieces = kCols / 8, kPitch = kCols + 8;
+  float* row_scale = reinterpret_cast<float*>(smem + C::kWaves * 32 * kPitch * 2);
   for (int i = tid; i < C::BM; i += 64 * C::kWaves) row_scale[i] = m0 + i < M ? a.ascales[m0 + i] : 0.0f;
   float ws[TN], bias[TN];
 #pragma unroll
@@ -340,8 +340,13 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_int8_kernel(Int8GemmArgs a,
     bias[j] = a.bias != nullptr && n < N ? bf16lo_to_f32(a.bias[n]) : 0.0f;
   }
   __syncthreads();
-  uint16_t* stage = reinterpret_cast<uint16_t*>(smem + wave * (32 * kCols * 2));
-  const bool vec_ok = N % 8 == 0;
+  uint16_t* stage = reinterpret_cast<uint16_t*>(smem + wave * (32 * kPitch * 2));
+  // A row of y starts (m N) mod 8 elements past a 16-byte address; it is staged with that shift, so
+  // that whole pieces stay aligned on both sides (7345 x 11459, K = 528: 136 us, 204 by elements, 98
+  // where 8 divides N)
+  int shift[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) shift[r] = ((4 * h + r) * N) & 7;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
 #pragma unroll
@@ -350,21 +355,33 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_int8_kernel(Int8GemmArgs a,
       const float as = row_scale[wave_m * TM * 32 + 32 * i + row];
 #pragma unroll
       for (int j = 0; j < TN; ++j)
-        stage[row * kCols + 32 * j + l32] = (uint16_t)f32_to_bf16_rne((float)acc[i][j][r] * as * ws[j] + bias[j]);
+        stage[row * kPitch + shift[r & 3] + 32 * j + l32] = (uint16_t)f32_to_bf16_rne((float)acc[i][j][r] * as * ws[j] + bias[j]);
     }
     __syncthreads();
+    const int cols = min(kCols, N - n_w);
+    if (N % 8 == 0) {
 #pragma unroll
-    for (int u = 0; u < 32 * kPieces / 64; ++u) {
-      const int idx = lane + 64 * u;
-      const int row = idx / kPieces, piece = idx % kPieces;
-      const int m = m_w + 32 * i + row, n = n_w + 8 * piece;
-      if (m < M && n < N) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(stage + row * kCols + 8 * piece);
-        uint16_t* dst = a.y + (size_t)m * (size_t)N + n;
-        if (vec_ok) {
-          *reinterpret_cast<u32x4*>(dst) = v;
+      for (int u = 0; u < 32 * kPieces / 64; ++u) {
+        const int idx = lane + 64 * u;
+        const int row = idx / kPieces, c = 8 * (idx % kPieces);
+        const int m = m_w + 32 * i + row;
+        if (m < M && c < cols)
+          *reinterpret_cast<u32x4*>(a.y + (size_t)m * (size_t)N + n_w + c) =
+              *reinterpret_cast<const u32x4*>(stage + row * kPitch + c);
+      }
+    } else {   // a piece more per row, the first and the last one by elements
+      for (int idx = lane; idx < 32 * (kPieces + 1); idx += 64) {
+        const int row = idx / (kPieces + 1), m = m_w + 32 * i + row;
+        const int sh = ((row & 7) * N) & 7, c = 8 * (idx % (kPieces + 1)) - sh;
+        if (m >= M || c >= cols) continue;
+        uint16_t* dst = a.y + (size_t)m * (size_t)N + n_w;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(stage + row * kPitch + sh + c);
+        if (c >= 0 && c + 8 <= cols) {
+          *reinterpret_cast<u32x4*>(dst + c) = v;
         } else {
-          for (int e = 0; e < 8 && n + e < N; ++e) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (c + e >= 0 && c + e < cols) dst[c + e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
         }
       }
     }
@@ -372,16 +389,18 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_int8_kernel(Int8GemmArgs a,
   }
 }
 
-// Ends a split product: sum of the partial sums, scales, bias, bf16; four channels per thread.
+// Ends a split product: sum of the partial sums, scales, bias, bf16; W channels per thread, 4 where
+// that divides N, else 1 (M * N stays below 2^31: a split has at most 1024 workgroups).
+template <int W>
 __global__ __launch_bounds__(256) void int8_reduce_kernel(Int8GemmArgs a, const int32_t* __restrict__ partial,
                                                           int splits) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t quads = (a.N + 3) / 4;
-  const int64_t m = id / quads, n = 4 * (id % quads);
-  if (m >= a.M) return;
-  const size_t mn = (size_t)a.M * (size_t)a.N, at = (size_t)m * (size_t)a.N + (size_t)n;
+  const uint32_t per_row = (uint32_t)a.N / W;
+  const uint32_t id = blockIdx.x * 256u + threadIdx.x;
+  const uint32_t m = id / per_row, n = W * (id % per_row);
+  if (m >= (uint32_t)a.M) return;
+  const size_t mn = (size_t)a.M * (size_t)a.N, at = (size_t)m * (size_t)a.N + n;
   const float as = a.ascales[m];
-  if (a.N % 4 == 0) {
+  if constexpr (W == 4) {
     i32x4 s = *reinterpret_cast<const i32x4*>(partial + at);
     for (int i = 1; i < splits; ++i) s += *reinterpret_cast<const i32x4*>(partial + (size_t)i * mn + at);
     const f32x4 ws = *reinterpret_cast<const f32x4*>(a.wscales + n);
@@ -391,12 +410,10 @@ __global__ __launch_bounds__(256) void int8_reduce_kernel(Int8GemmArgs a, const 
     const float y2 = (float)s[2] * as * ws[2] + bf16lo_to_f32(b[1]), y3 = (float)s[3] * as * ws[3] + bf16hi_to_f32(b[1]);
     *reinterpret_cast<u32x2*>(a.y + at) = u32x2{pack_bf16x2(y0, y1), pack_bf16x2(y2, y3)};
   } else {
-    for (int e = 0; e < 4 && n + e < a.N; ++e) {
-      int32_t s = 0;
-      for (int i = 0; i < splits; ++i) s += partial[(size_t)i * mn + at + e];
-      const float b = a.bias != nullptr ? bf16lo_to_f32(a.bias[n + e]) : 0.0f;
-      a.y[at + e] = (uint16_t)f32_to_bf16_rne((float)s * as * a.wscales[n + e] + b);
-    }
+    int32_t s = partial[at];
+    for (int i = 1; i < splits; ++i) s += partial[(size_t)i * mn + at];
+    const float b = a.bias != nullptr ? bf16lo_to_f32(a.bias[n]) : 0.0f;
+    a.y[at] = (uint16_t)f32_to_bf16_rne((float)s * as * a.wscales[n] + b);
   }
 }
 
@@ -653,8 +670,10 @@ hipError_t launch_gemm_int8(const Int8GemmArgs& a, void* workspace, hipStream_t 
                  : p.shape == 6 ? launch_int8_cfg<2, 2, 2, 1, 3, true>(a, sp, stream)
                                 : launch_int8_cfg<2, 2, 1, 1, 3, true>(a, sp, stream);
   if (e != hipSuccess || p.splits == 1) return e;
-  const dim3 grid((unsigned)((a.M * ((a.N + 3) / 4) + 255) / 256));
-  hipLaunchKernelGGL(int8_reduce_kernel, grid, dim3(256), 0, stream, a, sp.partial, p.splits);
+  const int w = a.N % 4 == 0 ? 4 : 1;
+  const dim3 grid((unsigned)((a.M * (a.N / w) + 255) / 256));
+  if (w == 4) hipLaunchKernelGGL(int8_reduce_kernel<4>, grid, dim3(256), 0, stream, a, sp.partial, p.splits);
+  else hipLaunchKernelGGL(int8_reduce_kernel<1>, grid, dim3(256), 0, stream, a, sp.partial, p.splits);
   return hipGetLastError();
 }
 
