@@ -128,9 +128,9 @@ TILES = [(1282, 11167, 272), (1547, 9399, 1040), (397, 8596, 9680), (423, 8360, 
          (131, 10915, 272), (130, 11038, 1040), (67, 4257, 3568), (67, 3400, 6208),
          (65, 8285, 272), (65, 8213, 1040), (2755, 66, 2192), (65, 3056, 2720),
          (33, 60, 1040), (157, 273, 1296), (33, 61, 1200), (36, 72, 1168),
-         (389, 5520, 8208), (404, 5385, 8048), (5479, 132, 6960), (5519, 130, 6176), (6699, 72, 6864), (6779,
-         69, 6160), (4171, 72, 4384), (4157, 66, 4544), (66, 2140, 3136), (69, 2054, 3120), (81, 60, 1696),
-         (68, 61, 1952)]
+         (389, 5520, 8208), (404, 5385, 8048), (5479, 132, 6960), (5519, 130, 6176), (6699, 72, 6864),
+         (6779, 69, 6160), (4171, 72, 4384), (4157, 66, 4544), (66, 2140, 3136), (69, 2054, 3120),
+         (81, 60, 1696), (68, 61, 1952)]
 
 
 @pytest.mark.parametrize("M,K,N", [(1, 3840, 5003), (3, 10240, 4500), (7, 1040, 4999), (16, 10240, 4100), (17, 1296, 6001),
