@@ -186,10 +186,10 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a, int l
   for (int j = 0; j < JD; ++j) acc[j] = f32x16{};
   const float c = a.scale * 1.4426950408889634f;   // exponents in base 2
   // The maximum starts below every finite score whose exponent is finite. Exponents are x c - mc,
-  // mc = m c: its rounding is a factor common to the row, unless it is so large (`far`) that the
-  // factor leaves fp32: then m is taken off the scores first and mc is 0.
+  // mc = m c: its rounding is a factor common to the row (raise() carries it over), unless it is so
+  // large (`far`) that the factor leaves fp32: then m is taken off the scores first and mc is 0.
   float m = -3.4028234663852886e38f / fmaxf(c, 1.0f), l = 0.0f, mc = 0.0f;
-  bool far = false;   // the same in every lane
+  bool far = true;   // the same in every lane
   const float slack = kSlack / c;
 
   // probabilities of score pair r (0..15) of a tile; their sum is taken before they are
@@ -217,15 +217,19 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a, int l
   };
   // The running maximum moves only when a score passes it by more than kSlack powers of
   // two: until then the probabilities are at most 2^kSlack, with the same relative rounding.
-  // Returns the factor for what was accumulated so far (l has it already).
+  // Returns the factor for what was accumulated so far (l has it already): the difference of what is
+  // really taken off the exponents, rounded products included. (m - mn) c in its place would weigh
+  // the keys before against those after by up to 2^(1/16), at products of 2^20.
   auto raise = [&](float mx) {
     mx = fmaxf(mx, __shfl_xor(mx, 32));
     const float mn = fmaxf(m, mx);
-    const float alpha = __builtin_amdgcn_exp2f((m - mn) * c);
+    float mcn = mn * c;
+    const bool far_n = __ballot(fabsf(mcn) > 1048576.0f) != 0;
+    if (far_n) mcn = 0.0f;
+    const float alpha = __builtin_amdgcn_exp2f(__builtin_fmaf((far ? m : 0.0f) - (far_n ? mn : 0.0f), c, mc - mcn));
     m = mn;
-    mc = mn * c;
-    far = __ballot(fabsf(mc) > 1048576.0f) != 0;
-    if (far) mc = 0.0f;
+    mc = mcn;
+    far = far_n;
     l *= alpha;
     return alpha;
   };
