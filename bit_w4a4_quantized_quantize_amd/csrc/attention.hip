@@ -188,18 +188,28 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a, int l
   // The maximum starts below every finite score whose exponent is finite. Exponents are x c - mc,
   // mc = m c: its rounding is a factor common to the row (raise() carries it over), unless it is so
   // large (`far`) that the factor leaves fp32: then m is taken off the scores first and mc is 0.
-  float m = -3.4028234663852886e38f / fmaxf(c, 1.0f), l = 0.0f, mc = 0.0f;
+  float m = -3.4028234663852886e38f / fmaxf(c, 1.0f), mc = 0.0f;
   bool far = true;   // the same in every lane
   const float slack = kSlack / c;
 
+  // Sum of the probabilities: a tile's own (at most 32 a lane), then l with what its last addition
+  // lost, so that the error does not grow with the sequence (one running sum of 2^18 equal ones
+  // drifts by up to 1e-3, of 2^24 by 1e-2).
+  float l = 0.0f, lost = 0.0f, tile_sum = 0.0f;
+  auto add_tile = [&] {
+    const float y = tile_sum - lost, t = l + y;
+    lost = (t - l) - y;
+    l = t;
+    tile_sum = 0.0f;
+  };
   // probabilities of score pair r (0..15) of a tile; their sum is taken before they are
   // rounded to bf16 (v_dot2 on the rounded pairs holds up the matrix unit)
   auto pair = [&](const f32x16 (&x)[2], uint32_t (&p)[16], int r) {
     const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r >> 3][2 * (r & 7)], c, -mc));
     const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r >> 3][2 * (r & 7) + 1], c, -mc));
     p[r] = pack_bf16x2(p0, p1);
-    l += p0 + p1;
-    asm volatile("" : "+v"(p[r]), "+v"(l));   // made here: not moved to their use
+    tile_sum += p0 + p1;
+    asm volatile("" : "+v"(p[r]), "+v"(tile_sum));   // made here: not moved to their use
   };
   auto prob_operand = [&](const uint32_t (&p)[16], int t) {
     return __builtin_bit_cast(bf16x8, u32x4{p[4 * t], p[4 * t + 1], p[4 * t + 2], p[4 * t + 3]});
@@ -231,6 +241,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a, int l
     mc = mcn;
     far = far_n;
     l *= alpha;
+    lost *= alpha;
     return alpha;
   };
 
@@ -271,6 +282,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a, int l
       __builtin_amdgcn_sched_barrier(0);
     }
     __builtin_amdgcn_s_setprio(0);
+    add_tile();
     mask(nxt, kt + 1);
     constexpr int kMax = NV / 4;   // products that cover the maximum
     auto value = [&](int u) {
@@ -345,6 +357,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a, int l
     ++kt;
 #pragma unroll
     for (int r = 8; r < 16; ++r) pair(s0, p0, r);
+    add_tile();
 #pragma unroll
     for (int u = 0; u < NV; ++u)
       acc[u % JD] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_v(sv, u), prob_operand(p0, u / JD), acc[u % JD], 0, 0, 0);

@@ -540,7 +540,10 @@ int svdq_rope_axes(const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_
  *   scale in (0, 2^20]. o must not overlap q, k or v.
  * Scores and softmax statistics are fp32; the probabilities are rounded to bf16
  * for the second product (relative to a running maximum), their sum is taken
- * before that, and o is rounded once to bf16. A non-finite value reaches no
+ * before that, with what its additions lose carried along, and o is rounded once to bf16. The
+ * second product adds 16 keys at a time in fp32: for a sequence of L tokens its sums are off by up to
+ * about L 2^-28 of sum p |v| (2^-8, o's own rounding, at 2^20 tokens; values of one sign there measured
+ * 1.6e-3). A non-finite value reaches no
  * other sequence's rows; within a causal sequence a non-finite v may reach rows
  * before it (they multiply it by zero), a non-finite k does not.
  * D: 64 or 128; H a multiple of Hk; T below 2^24; H, B at most 65535; 2 T H + 512 B H
