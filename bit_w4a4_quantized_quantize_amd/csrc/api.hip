@@ -1461,16 +1461,33 @@ static bool heads_distinct(const Heads& a) {
   return token_major || head_major;
 }
 
-// No element in common: disjoint ranges, or (views of one fused buffer) the same
-// token stride with the heads of a token in disjoint spans of it.
+// No element in common: disjoint ranges; the same token stride with the heads of a token in
+// disjoint spans of it (q and k of [T, H + 2 Hk, D]); or the same strides, interleaved in any way
+// (of [T, H, 3, D], [H, T, 3, D], [H, 3, T, D]), compared head distance by head distance. Views of
+// different strides that interleave count as overlapping.
 static bool heads_disjoint(const Heads& a, const Heads& b) {
   if (!overlaps(range("", a.p, (size_t)a.span * 2), range("", b.p, (size_t)b.span * 2))) return true;
+  const int64_t st = a.st;
+  if (a.T > 1 && b.st != st) return false;
   const int64_t sa = (a.heads - 1) * a.sh + a.D, sb = (b.heads - 1) * b.sh + b.D;
-  if (a.T == 1 || a.st != b.st || sa > a.st || sb > b.st) return false;
-  const int64_t bytes = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
-  int64_t off = bytes % (2 * a.st);
-  if (off < 0) off += 2 * a.st;
-  return off >= 2 * sa && off + 2 * sb <= 2 * a.st;
+  const int64_t off =
+      ((int64_t)reinterpret_cast<uintptr_t>(b.p) - (int64_t)reinterpret_cast<uintptr_t>(a.p)) / 2;   // both 16-byte aligned
+  auto mod = [](int64_t x, int64_t m) { return (x % m + m) % m; };
+  if (a.T > 1 && sa <= st && sb <= st && mod(off, st) >= sa && mod(off, st) + sb <= st) return true;
+  if (a.heads > 1 && b.heads > 1 && a.sh != b.sh) return false;
+  const int64_t sh = a.heads > 1 ? a.sh : b.sh;
+  for (int64_t dh = 1 - a.heads; dh < b.heads; ++dh) {
+    // b's elements are d + (a multiple of st) after a's: the multiples that bring them closest to 0
+    const int64_t d = off + dh * sh;
+    if (a.T == 1) {
+      if (d > -a.D && d < a.D) return false;
+      continue;
+    }
+    const int64_t r = mod(d, st), n = (r - d) / st;   // d + n st = r, d + (n - 1) st = r - st
+    if (r < a.D && n > -a.T && n < a.T) return false;
+    if (st - r < a.D && n - 1 > -a.T && n - 1 < a.T) return false;
+  }
+  return true;
 }
 
 static Range heads_range(const Heads& h) { return range(h.name, h.p, (size_t)h.span * 2); }

@@ -513,7 +513,9 @@ int svdq_norm_gated_int8(const void* h, const void* block, const void* post_weig
  *   axis_dims: a HOST array of `axes` (1..4) positive even numbers of sum D.
  *   q_out, k_out: same shapes with their own strides; either may be exactly its
  *     input (same pointer and strides: in place). Any other overlap with an input or
- *     the other output is SVDQ_ERR_ALIAS.
+ *     the other output is SVDQ_ERR_ALIAS. Views that interleave in one buffer, as in
+ *     [T, H + 2 Hk, D] or [T, H, 3, D], do not overlap; to be told apart they need the same
+ *     token stride, and where their heads interleave the same head stride.
  * Angles are reduced in fp64; norm and rotation run in fp32 with one rounding to
  * bf16. D: 64 or 128 (SVDQ_ERR_UNSUPPORTED); theta in [1, 1e9]; T below 2^24; H, Hk at
  * most 65535; T * (H + Hk) < 2^31.
@@ -537,7 +539,8 @@ int svdq_rope_axes(const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_
  *     allowed), or NULL: one sequence of T tokens and B must be 1. Rows of o
  *     outside [cu_seqlens[0], cu_seqlens[B]) are left as they were. Offsets outside
  *     0..T, or decreasing ones, cause no access outside the tensors.
- *   scale in (0, 2^20]. o must not overlap q, k or v.
+ *   scale in (0, 2^20]. o must not overlap q, k or v (views that interleave as in
+ *     svdq_rope_axes do not).
  * Scores and softmax statistics are fp32; the probabilities are rounded to bf16
  * for the second product (relative to a running maximum), their sum is taken
  * before that, with what its additions lose carried along, and o is rounded once to bf16. The
