@@ -80,6 +80,7 @@ SIGNATURES = {
     "svdq_gemm_int8_workspace_bytes": (_size, [_i64, _i64, _i64]),
     "svdq_gemm_int8": (_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p,
                               _c_void_p, _size, _c_void_p]),
+    "svdq_gemm_int8_plan": (_int, [_i64, _i64, _i64, ctypes.POINTER(_int), ctypes.POINTER(_int)]),
     "svdq_linear_int8_workspace_bytes": (_size, [_i64, _i64, _i64]),
     "svdq_linear_int8": (_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p,
                                 _c_void_p, _size, _c_void_p]),

@@ -1238,6 +1238,15 @@ size_t svdq_gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   return svdq::gemm_int8_workspace_bytes(M, N, K);
 }
 
+int svdq_gemm_int8_plan(int64_t M, int64_t N, int64_t K, int* tile, int* splits) {
+  int st = check_int8_mnk(M, N, K);
+  if (st) return st;
+  if (M == 0 || N == 0) return fail(SVDQ_ERR_SHAPE, "M = %lld and N = %lld must be positive", (long long)M, (long long)N);
+  if (tile == nullptr || splits == nullptr) return fail(SVDQ_ERR_NULL, "%s is NULL", tile == nullptr ? "tile" : "splits");
+  svdq::gemm_int8_plan(M, N, K, tile, splits);
+  return ok();
+}
+
 // what the two products share: pointers, workspace, overlaps (the outputs and the
 // inputs besides the activations), with the activations' own ranges from the caller
 static int check_int8_gemm(const Range* act, int n_act, const void* weight, const void* wscales, const void* bias,

@@ -657,6 +657,13 @@ size_t gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   return p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)N * 4 : 0;
 }
 
+void gemm_int8_plan(int64_t M, int64_t N, int64_t K, int* tile, int* splits) {
+  const bool few = few_tokens(M, N, K);
+  const I8Plan p = few ? I8Plan{-1, 1, 0} : plan_int8(M, N, K);
+  *tile = p.shape;
+  *splits = p.splits;
+}
+
 hipError_t launch_gemm_int8(const Int8GemmArgs& a, void* workspace, hipStream_t stream) {
   if (few_tokens(a.M, a.N, a.K)) return launch_few(a, nullptr, nullptr, stream);
   const I8Plan p = plan_int8(a.M, a.N, a.K);

@@ -171,6 +171,7 @@ struct Int8GemmArgs {
 };
 hipError_t launch_gemm_int8(const Int8GemmArgs& a, void* workspace, hipStream_t stream);
 size_t gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+void gemm_int8_plan(int64_t M, int64_t N, int64_t K, int* tile, int* splits);   // tile -1: few tokens
 // The layer from x (a.codes and a.ascales unset): the quantisation into codes and ascales, then
 // the product; or, where linear_int8_codes_bytes(M, N, K) is 0, one launch without them.
 size_t linear_int8_codes_bytes(int64_t M, int64_t N, int64_t K);

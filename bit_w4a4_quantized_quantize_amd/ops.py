@@ -755,6 +755,14 @@ def gemm_int8_workspace_bytes(M, N, K):
     return _lib.lib().svdq_gemm_int8_workspace_bytes(M, N, K)
 
 
+def gemm_int8_plan(M, N, K):
+    """How gemm_int8 runs a size (tests and tuning): (tile, ways k is split), tile 0..7 as in svdq.h or -1 for
+    the kernel for few tokens."""
+    tile, splits = ctypes.c_int(0), ctypes.c_int(0)
+    _lib.check("svdq_gemm_int8_plan", _lib.lib().svdq_gemm_int8_plan(M, N, K, ctypes.byref(tile), ctypes.byref(splits)))
+    return tile.value, splits.value
+
+
 def linear_int8_workspace_bytes(M, N, K):
     """Scratch bytes linear_int8 needs."""
     return _lib.lib().svdq_linear_int8_workspace_bytes(M, N, K)

@@ -1,0 +1,52 @@
+"""The 8-bit product's choice of tile shape and split: each is reached, whole and split, by named sizes (CPU), and is
+right there (GPU). A refit of the choice that leaves a kernel without a size fails here."""
+
+import numpy as np
+import pytest
+import torch
+
+from bit_w4a4_quantized_quantize_amd import _lib, ops
+from oracle import block as B
+from tests.test_gpu_int8 import activations, check_y, f64, weights
+
+# tile, ways of k, M, N, K: for each tile a split with rows of y that leave four at a time (4 divides N) and one at a
+# time, all of k with N odd (K of 9 panels, the last one short) and a multiple of 8 (3 panels)
+SIZES = [
+    (-1, 1, 9, 60, 1040), (-1, 1, 17, 72, 272), (-1, 1, 33, 4200, 1040), (-1, 1, 64, 333, 2048),
+    (0, 3, 389, 11005, 10416), (0, 3, 405, 11120, 10944), (0, 1, 1321, 11014, 1040), (0, 1, 1286, 11448, 272),
+    (1, 5, 391, 5462, 8256), (1, 5, 430, 5400, 8944), (1, 1, 986, 11055, 1040), (1, 1, 1745, 6552, 272),
+    (2, 7, 4490, 143, 10720), (2, 7, 4593, 144, 8928), (2, 1, 386, 10932, 1040), (2, 1, 388, 11344, 272),
+    (3, 5, 137, 5707, 4752), (3, 8, 5430, 72, 9120), (3, 1, 257, 10910, 1040), (3, 1, 258, 11416, 272),
+    (4, 5, 129, 10998, 5776), (4, 7, 134, 8788, 9280), (4, 1, 657, 10946, 1040), (4, 1, 1046, 7208, 272),
+    (5, 7, 4114, 69, 5472), (5, 7, 68, 4568, 4304), (5, 1, 129, 10930, 1040), (5, 1, 141, 10920, 272),
+    (6, 7, 2059, 65, 3472), (6, 6, 68, 2116, 3616), (6, 1, 65, 8276, 1040), (6, 1, 65, 9272, 272),
+    (7, 8, 35, 61, 3872), (7, 8, 16, 60, 8288), (7, 1, 65, 60, 1040), (7, 1, 66, 72, 272)]
+
+
+def test_every_tile_has_its_sizes():
+    kinds = set()
+    for tile, splits, M, N, K in SIZES:
+        assert ops.gemm_int8_plan(M, N, K) == (tile, splits), (M, N, K)
+        kinds.add((tile, splits > 1, N % 4 == 0 if splits > 1 else N % 8 == 0))
+    assert kinds >= {(t, s, a) for t in range(8) for s in (False, True) for a in (False, True)}
+
+
+def test_plan_refusals():
+    L = _lib.lib()
+    for M, N, K in ((0, 8, 16), (8, 0, 16), (-1, 8, 16), (8, 8, 24), (8, 8, 131072 + 16)):
+        with pytest.raises(_lib.SvdqError):
+            ops.gemm_int8_plan(M, N, K)
+    assert L.svdq_gemm_int8_plan(8, 8, 16, None, None) == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tile,splits,M,N,K", SIZES)
+def test_tile(gpu_lib, tile, splits, M, N, K):
+    print(f"[int8] tile {tile} / {splits}: {M} {N} {K}", flush=True)
+    x = activations(M, K, 7)
+    w, ws, b = weights(N, K, 8)
+    codes, scales = gpu_lib.quantize_int8(x)
+    y = gpu_lib.gemm_int8(codes, scales, w, ws, bias=b)
+    pick = np.unique(np.concatenate([[0, 1, M - 2, M - 1], np.random.default_rng(1).integers(0, M, 20)]))
+    at = torch.from_numpy(pick).cuda()
+    check_y(y[at], codes[at].cpu().numpy(), f64(scales[at]), w, ws, b)
