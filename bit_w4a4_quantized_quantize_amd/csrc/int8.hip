@@ -567,15 +567,20 @@ hipError_t launch_few(const Int8GemmArgs& a, const uint16_t* x, const uint16_t* 
 
 // Tile shape, stages and split of k by an estimate in microseconds, fitted to times with weights
 // from memory (M from 48 to 6000; ten weights from 1300 x 2064 to 11520 x 3840 and 3840 x 10240; every
-// shape with k split 1 to 8 ways; the choice is within 1% of the best time on average, 11% at
-// worst). A panel takes `share` of its CU's time per workgroup, at least `least` where a CU has
-// too few of them; a CU works through ceil(workgroups / 256) of them; 5.2 us start and end a
-// product. A split adds a launch (2 us on the device, 3 of the caller) and the partial sums'
-// traffic (1.8 us per way at 333 x 3840). Three stages, where they leave a CU one workgroup, pay
-// while the tiles are few: at 1024 x 3840, K = 3840, 128 x 128 tiles take 24 us with three and 31 with
-// two; at 333 x 3840, K = 10240, 192 x 128 tiles and k split four ways 30 and 33; at 1024 x 10240,
-// K = 3840, 192 x 128 tiles 61 and 47. 4096 x 3840, K = 10240: 148 us in 256 x 256 tiles (240 of
-// them), 165 in 256 x 320; 4096 x 10240, K = 3840: 171 and 158. 48 x 3840, K = 10240: 16 us in
+// shape with k split 1 to 8 ways: profiles/gemm_int8_tile_grid.txt). A panel takes `share` of its
+// CU's time per workgroup, at least `least` where a CU has too few of them; a CU works through
+// ceil(workgroups / 256) of them; 5.2 us start and end a product. A split adds a launch (2 us on the
+// device) and the partial sums' traffic (1.8 us per way at 333 x 3840). A call that is not in a graph
+// takes no less than its caller, about 10 us and 3 more for a split's launch, so a split pays only
+// where the device takes longer than that; among those that take the caller's time the shortest on
+// the device. The choice is within 1% of the best device time on average and 8% at worst, but for 100
+// to 200 tokens of 1300 x 2064 (18% to 9%: 9.8 us unsplit, 8.4 split three ways, where calls in a
+// loop take 13). The 3 us added to a split's time instead cost 512 x 3840,
+// K = 10240, 17% (41.6 us unsplit, 35.5 split four ways). Three stages, where they leave a CU one
+// workgroup, pay while the tiles are few: at 1024 x 3840, K = 3840, 128 x 128 tiles take 24 us with
+// three and 31 with two; at 333 x 3840, K = 10240, 192 x 128 tiles and k split four ways 30 and 33; at
+// 1024 x 10240, K = 3840, 192 x 128 tiles 61 and 47. 4096 x 3840, K = 10240: 148 us in 256 x 256 tiles
+// (240 of them), 165 in 256 x 320; 4096 x 10240, K = 3840: 171 and 158. 48 x 3840, K = 10240: 16 us in
 // 64 x 64 tiles with k split four ways, 33 unsplit.
 struct I8Plan {
   int shape;     // index into the table
@@ -595,8 +600,9 @@ I8Plan plan_int8(int64_t M, int64_t N, int64_t K) {
       if (sp > 1 && (panels < 2 * sp || tiles * sp > 1024)) break;
       const int64_t per = (panels + sp - 1) / sp;
       const double rounds = (double)((tiles * sp + 255) / 256);
-      const double t = 5.2 + (double)per * fmax(shapes[s].least, rounds * shapes[s].share) +
-                       (sp > 1 ? 3.0 + 1.4e-6 * (double)(M * N) * sp : 0.0);
+      const double device = 5.2 + (double)per * fmax(shapes[s].least, rounds * shapes[s].share) +
+                            (sp > 1 ? 2.0 + 1.4e-6 * (double)(M * N) * sp : 0.0);
+      const double t = fmax(device, sp > 1 ? 13.0 : 10.0) + 0.01 * device;
       if (t < best_t) {
         best_t = t;
         best = I8Plan{s, (int)((panels + per - 1) / per), (int)per};

@@ -1,6 +1,8 @@
 """The 8-bit product's choice of tile shape and split: each is reached, whole and split, by named sizes (CPU), and is
 right there (GPU). A refit of the choice that leaves a kernel without a size fails here."""
 
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -29,6 +31,30 @@ def test_every_tile_has_its_sizes():
         assert ops.gemm_int8_plan(M, N, K) == (tile, splits), (M, N, K)
         kinds.add((tile, splits > 1, N % 4 == 0 if splits > 1 else N % 8 == 0))
     assert kinds >= {(t, s, a) for t in range(8) for s in (False, True) for a in (False, True)}
+
+
+def measured_grid():
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "profiles", "gemm_int8_tile_grid.txt")
+    for line in open(path):
+        if not line.startswith("#"):
+            M, N, K, _, *times = line.split()
+            yield int(M), int(N), int(K), {tuple(map(int, t.split(":")[0].split("/"))): float(t.split(":")[1]) for t in times}
+
+
+def test_choice_against_the_measured_grid():
+    """The chosen shape and split, by the times measured for all of them: what a refit may lose."""
+    loss = {}
+    for M, N, K, times in measured_grid():
+        best, got = min(times.values()), ops.gemm_int8_plan(M, N, K)
+        if got[1] == 7:
+            continue                                 # not measured
+        assert got in times, (M, N, K, got)          # within 1.5 times the best
+        loss[M, N, K] = (times[got] / best, best)
+    assert len(loss) > 100
+    assert np.mean([x for x, _ in loss.values()]) <= 1.01
+    worst = {k: x for k, (x, best) in loss.items() if x > (1.05 if best > 15 else 1.08)}
+    # bound by the caller: a split would cost its launch
+    assert sorted(worst) == [(100, 1300, 2064), (160, 1300, 2064), (200, 1300, 2064)], worst
 
 
 def test_plan_refusals():
