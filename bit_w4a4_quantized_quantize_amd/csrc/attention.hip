@@ -13,10 +13,12 @@
 // product to the next without leaving its lane; V is read in the same order by
 // the transposing LDS read (four keys of one column per lane).
 //
-// Bound: the matrix units' power. 30 heads of 128: 16896 tokens 3600-3800 us (1.15-1.22 PFLOP/s at
-// 1.74 GHz; a large library bf16 product reaches 1.33), 4096 tokens 235-260 us (1.0-1.1, 1.9 rounds
-// of workgroups); 13 causal prompts of 315 tokens on average, 32 heads on 8, 31-35 us (their starts
-// and ends). K and V tiles of 64 keys, double buffered by direct copies to LDS: tiles through
+// Bound: the matrix units' power. 30 heads of 128: 16896 tokens 3600-3950 us (1.11-1.22 PFLOP/s at
+// 1.65-1.74 GHz; a large library bf16 product reaches 1.33), 4096 tokens 230-255 us (1.0-1.1, 1.9
+// rounds of workgroups); 13 causal prompts of 315 tokens on average, 32 heads on 8, 31-37 us (their
+// starts and ends); 1024 tokens, 29-30 us (240 workgroups, a wave a SIMD, 16 tiles each one after the
+// other). 30 heads of 64, 16896 tokens: 2240 us (0.98: as many exponentials for half the products).
+// K and V tiles of 64 keys, double buffered by direct copies to LDS: tiles through
 // registers measured equal or 8% slower, 32 keys 18% slower at 4096 tokens.
 #include "common.h"
 #include "kernels.h"
@@ -202,8 +204,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a, int l
     l = t;
     tile_sum = 0.0f;
   };
-  // probabilities of score pair r (0..15) of a tile; their sum is taken before they are
-  // rounded to bf16 (v_dot2 on the rounded pairs holds up the matrix unit)
+  // Probabilities of score pair r (0..15) of a tile, rounded to bf16 for the product with V, whose
+  // matrix instruction takes both operands in one type: o is off from float64 by 0.0024 of its norm,
+  // 0.0017 with fp32 probabilities (both with o's own rounding; their rest as a second bf16 operand
+  // would double that product). Their sum is taken before (v_dot2 on the rounded pairs holds up the
+  // matrix unit).
   auto pair = [&](const f32x16 (&x)[2], uint32_t (&p)[16], int r) {
     const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r >> 3][2 * (r & 7)], c, -mc));
     const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r >> 3][2 * (r & 7) + 1], c, -mc));
@@ -399,14 +404,21 @@ void launch_attention_cfg(const AttnArgs& a, hipStream_t s) {
   else hipLaunchKernelGGL((attention_kernel<D, false, NW>), grid, block, 0, s, a, lg_heads);
 }
 
-// Four waves or eight: eight load each tile half as often, four leave two workgroups on a CU,
-// whose starts and ends overlap, and waste less at the ends of short sequences. Measured, 4
-// and 8 waves: 30 heads of 128, one sequence of 16896: 3900 and 3710 us; of 4096: 267 and
-// 270 us; 13 causal prompts of 315 on average, 32 heads on 8: 34.5 and 39.0 us.
+// Four waves or eight: eight load each tile half as often, four leave two workgroups on a CU (three
+// of heads of 64), whose starts and ends overlap, and waste less at the ends of short sequences.
+// Measured, 4 and 8 waves, one sequence, 30 heads of 128: 16896 tokens 3920 and 3700 us (causal 2195
+// and 2140), 8192 909 and 882 (562 and 585), 4096 235 and 230 (162 and 164), 2048 75 and 106; 13 causal
+// prompts of 315 on average, 32 heads on 8: 36.5 and 40.2; 20 sequences of 400, 30 heads on 15: 85 and
+// 91. Heads of 64, 30 of them: 16896 2240 and 2335 (1230 and 1320), 8192 553 and 570 (325 and 384), 4096 153
+// and 150 (99 and 112); 16 of them, 12000 611 and 619 (318 and 338), 8192 295 and 288 (179 and 158: 3.5 and 4
+// rounds of workgroups). So eight from a mean length of 8192 on, for heads of 128 alone: two waves a
+// SIMD are all that their registers leave either way, where four-wave workgroups of 64 make three.
 template <int D>
 void launch_attention_d(const AttnArgs& a, hipStream_t s) {
-  if (a.T >= 8192 * (int64_t)a.B) launch_attention_cfg<D, 8>(a, s);
-  else launch_attention_cfg<D, 4>(a, s);
+  if constexpr (D == 128) {
+    if (a.T >= 8192 * (int64_t)a.B) return launch_attention_cfg<D, 8>(a, s);
+  }
+  launch_attention_cfg<D, 4>(a, s);
 }
 
 }  // namespace

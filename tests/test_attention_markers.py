@@ -13,13 +13,14 @@ def offsets(lens, start=0):
     return [int(c) for c in np.cumsum([start] + list(lens))]
 
 
-def marked(T, H, D, cu, causal, seed, rows=160):
-    """q, k, v [T, H, D] (bf16 values) and the marked queries. Keys are normal; a marked query is 3 times one key:
+def marked(T, H, D, cu, causal, seed, rows=160, Hk=None):
+    """q [T, H, D], k, v [T, Hk, D] (bf16 values) and the marked queries. Keys are normal; a marked query is 3 times one key:
     its score is 3 sqrt(D) (24 and 34) against normal ones of deviation 3. Its key is one that it may see (first, last,
     tile borders, its own) or, for a third of the rows, one just outside: behind the query where causal, else in the
     neighbouring sequence or behind the last."""
     rng = np.random.default_rng(seed)
-    q, k, v = (torch.from_numpy(rng.standard_normal((T, H, D))).bfloat16() for _ in range(3))
+    Hk = Hk or H
+    q, k, v = (torch.from_numpy(rng.standard_normal((T, n, D))).bfloat16() for n in (H, Hk, Hk))
     picks = []
     for a, b in zip(cu[:-1], cu[1:]):
         L = b - a
@@ -38,7 +39,7 @@ def marked(T, H, D, cu, causal, seed, rows=160):
                 may = [e for e in edges if not causal or e <= i] + ([i] if causal else [])
                 j = a + may[rng.integers(len(may))]
             picks.append(a + i)
-            q[a + i] = (3.0 * k[j].float()).bfloat16()
+            q[a + i] = (3.0 * k[j].float()).bfloat16().repeat_interleave(H // Hk, 0)
     return q, k, v, np.array(sorted(picks))
 
 
@@ -61,6 +62,20 @@ def test_marked_keys(gpu_lib, lens, start, behind, D, causal):
     q, k, v, at = marked(T, 1, D, cu, causal, T)
     o = gpu_lib.attention_packed(q.cuda(), k.cuda(), v.cuda(), torch.tensor(cu, dtype=torch.int32).cuda(), causal=causal)
     ref, tol = reference(q, k, v, cu, causal, at)
+    err = np.abs(o.double().cpu().numpy() - ref)[at]
+    assert (err <= tol[at]).all(), float((err / tol[at]).max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,Hk", [(8, 1), (12, 2), (6, 2), (16, 1)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_marked_keys_of_head_groups(gpu_lib, H, Hk, causal):
+    """Eight waves dealt to 8, 2, 1 and 8 heads of a group: rows of 32, 128, 256 and 32 queries."""
+    print(f"[attention] marked groups {H} {Hk} causal={causal}", flush=True)
+    T, D = 8200, 128
+    q, k, v, at = marked(T, H, D, [0, T], causal, H, 12, Hk)
+    o = gpu_lib.attention_packed(q.cuda(), k.cuda(), v.cuda(), causal=causal)
+    ref, tol = reference(q, k, v, None, causal, at)
     err = np.abs(o.double().cpu().numpy() - ref)[at]
     assert (err <= tol[at]).all(), float((err / tol[at]).max())
 
