@@ -1623,8 +1623,9 @@ int svdq_attention_packed(const void* q, int64_t q_stride_t, int64_t q_stride_h,
   if (cu_seqlens == nullptr && B != 1)
     return fail(SVDQ_ERR_INVALID, "B = %lld sequences need cu_seqlens", (long long)B);
   if (!(scale > 0.0f && scale <= 1048576.0f)) return fail(SVDQ_ERR_INVALID, "scale = %g is not in (0, 2^20]", scale);
-  if (2 * T * H + 512 * B * H >= (int64_t(1) << 32))   // work items of the grid
-    return fail(SVDQ_ERR_UNSUPPORTED, "2 T H + 512 B H must be below 2^32 (T=%lld B=%lld H=%lld)", (long long)T,
+  // work items of the grid, whose workgroups (of up to 512) come in eights
+  if (2 * T * H + 512 * B * H >= (int64_t(1) << 32) - 4096)
+    return fail(SVDQ_ERR_UNSUPPORTED, "2 T H + 512 B H must be below 2^32 - 4096 (T=%lld B=%lld H=%lld)", (long long)T,
                 (long long)B, (long long)H);
   if (T == 0 || B == 0) return ok();
   Heads hq, hk, hv, ho;

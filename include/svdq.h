@@ -554,7 +554,7 @@ int svdq_rope_axes(const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_
  * other sequence's rows; within a causal sequence a non-finite v may reach rows
  * before it (they multiply it by zero), a non-finite k does not.
  * D: 64 or 128; H a multiple of Hk; T below 2^24; H, B at most 65535; 2 T H + 512 B H
- * below 2^32; token strides below 2^24 elements. No workspace.
+ * below 2^32 - 4096; token strides below 2^24 elements. No workspace.
  */
 int svdq_attention_packed(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
                           int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
