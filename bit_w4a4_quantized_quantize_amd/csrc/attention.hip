@@ -19,7 +19,9 @@
 // starts and ends); 1024 tokens, 29-30 us (240 workgroups, a wave a SIMD, 16 tiles each one after the
 // other). 30 heads of 64, 16896 tokens: 2240 us (0.98: as many exponentials for half the products).
 // K and V tiles of 64 keys, double buffered by direct copies to LDS: tiles through
-// registers measured equal or 8% slower, 32 keys 18% slower at 4096 tokens.
+// registers measured equal or 8% slower, 32 keys 18% slower at 4096 tokens. Up to 39 scalars (constants
+// of the loop) are spilled into lanes of a vector register; 4 to 13 are read back per two tiles, of about
+// 1000 instructions, while the next tiles are requested. No vector register spills.
 #include "common.h"
 #include "kernels.h"
 
