@@ -39,7 +39,8 @@ constexpr int kMaxTokens = 16;   // tokens of a workgroup
 // in several passes, where that has more): its loads go out first, then per * D / 2 angles are
 // made in LDS, once for all heads, while they travel. Memory bound, close enough that vector
 // instructions show: 16896 tokens of 30 + 30 heads of 128 out of a fused buffer move 519 MB in
-// 87 us with the norm (6.0 TB/s); 103 us with the weights applied to the elements instead of the
+// 87-91 us with the norm (5.7-6.0 TB/s, also over four sets of buffers in turn; in place inside the
+// fused buffer 100-103); 103 us with the weights applied to the elements instead of the
 // angles, an exact square root and quotient, and addresses made per lane. Scalar bases pay for
 // one token per workgroup (ONE: 89 -> 87) and cost for several (8190 tokens of 24 + 8 heads of
 // 64: 11.0 -> 11.6). Streaming stores are worth 5 us, against four pieces per thread 8, against
