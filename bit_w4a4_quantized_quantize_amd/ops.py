@@ -973,5 +973,5 @@ def attention_packed(q, k, v, cu_seqlens=None, causal=False, scale=None, out=Non
     oa = _need_heads(out, "out", q.shape)
     _on_one_device(q.get_device(), q=q, k=k, v=v, cu_seqlens=cu_seqlens, out=out)
     _launch("svdq_attention_packed", q.device, *qa, *ka, *va, _p(cu_seqlens), B, T, H, Hk, D, 1 if causal else 0,
-            D ** -0.5 if scale is None else scale, *oa)
+            scale if scale is not None else D ** -0.5 if D > 0 else 1.0, *oa)   # D = 0 is refused there
     return out

@@ -94,3 +94,12 @@ def test_rotary_and_attention_in_one_buffer(gpu_lib, layout, T, H):
     assert torch.equal(gpu_lib.attention_packed(q, k, v), want)
     gpu_lib.attention_packed(q1, k, v, out=q)
     assert torch.equal(q, want) and torch.equal(k, k1) and torch.equal(v, apart[2])
+
+
+@pytest.mark.gpu
+def test_heads_of_no_elements_are_refused(gpu_lib):
+    z = torch.zeros(4, 2, 0, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(_lib.SvdqError, match="head size"):
+        gpu_lib.attention_packed(z, z, z)
+    with pytest.raises(_lib.SvdqError, match="head size"):
+        gpu_lib.rope_axes(z, None, torch.zeros(4, 1, dtype=torch.int32, device="cuda"), (2,))
