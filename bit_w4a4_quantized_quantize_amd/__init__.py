@@ -4,7 +4,8 @@
         + (x @ proj_down) @ proj_up^T + bias
 
 and the operators between a transformer block's linears: an 8-bit linear, gated norms,
-rotary positions with several axes, packed attention.
+rotary positions with several axes, packed attention; and those of serving in 8-bit floating point: a linear
+with block scales, scaled rotary positions, a paged cache and attention over it.
 
 The compute lives in libsvdq.so (csrc/*.hip, C ABI in include/svdq.h);
 ``ops`` is the PyTorch-facing binding. Importing this package does not load

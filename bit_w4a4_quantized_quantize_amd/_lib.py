@@ -15,6 +15,7 @@ _i64 = ctypes.c_int64
 _size = ctypes.c_size_t
 _int = ctypes.c_int
 _f32 = ctypes.c_float
+_f64 = ctypes.c_double
 
 # name -> (restype, argtypes); mirrors include/svdq.h
 SIGNATURES = {
@@ -93,6 +94,27 @@ SIGNATURES = {
                               _c_void_p, _i64, _i64, _c_void_p, _i64, _i64, _c_void_p]),
     "svdq_attention_packed": (_int, [_c_void_p, _i64, _i64, _c_void_p, _i64, _i64, _c_void_p, _i64, _i64, _c_void_p,
                                      _i64, _i64, _i64, _i64, _i64, _int, _f32, _c_void_p, _i64, _i64, _c_void_p]),
+    "svdq_quantize_fp8": (_int, [_c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p, _c_void_p]),
+    "svdq_quantize_weight_fp8": (_int, [_c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p, _c_void_p]),
+    "svdq_gemm_fp8_workspace_bytes": (_size, [_i64, _i64, _i64]),
+    "svdq_gemm_fp8": (_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p,
+                             _c_void_p, _size, _c_void_p]),
+    "svdq_gemm_fp8_plan": (_int, [_i64, _i64, _i64, ctypes.POINTER(_int), ctypes.POINTER(_int)]),
+    "svdq_linear_fp8_workspace_bytes": (_size, [_i64, _i64, _i64]),
+    "svdq_linear_fp8": (_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p,
+                               _c_void_p, _size, _c_void_p]),
+    "svdq_rope_scaled": (_int, [_c_void_p, _i64, _i64, _i64, _c_void_p, _i64, _i64, _i64, _c_void_p, _i64, _f64, _f64,
+                                _f64, _f64, _f64, _f32, _int, _i64, _i64, _c_void_p, _i64, _i64, _c_void_p, _i64, _i64,
+                                _c_void_p]),
+    "svdq_cache_append_fp8": (_int, [_c_void_p, _i64, _i64, _c_void_p, _i64, _i64, _c_void_p, _c_void_p, _c_void_p,
+                                     _c_void_p, _i64, _i64, _i64, _i64, _c_void_p, _i64, _c_void_p, _c_void_p, _i64,
+                                     _i64, _c_void_p]),
+    "svdq_cache_read_fp8": (_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, _i64, _c_void_p, _i64,
+                                   _c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p, _c_void_p]),
+    "svdq_attention_cache_fp8_workspace_bytes": (_size, [_i64, _i64, _i64, _i64, _i64, _i64, _int]),
+    "svdq_attention_cache_fp8": (_int, [_c_void_p, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i64,
+                                        _i64, _i64, _c_void_p, _i64, _c_void_p, _c_void_p, _i64, _i64, _i64, _i64, _int,
+                                        _f32, _c_void_p, _i64, _i64, _c_void_p, _size, _c_void_p]),
     "svdq_calib_table_bytes": (_size, []),
     "svdq_calib_flop_per_iteration": (_i64, [_i64]),
     "svdq_calib_mfma": (_int, [_c_void_p, _size, _i64, _i64, _c_void_p, _size, _c_void_p, _size, _c_void_p]),

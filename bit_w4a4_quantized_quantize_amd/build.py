@@ -19,8 +19,8 @@ LIB_PATH = os.path.join(HERE, "libsvdq.so")
 
 SOURCES = ["api.hip", "quant_act.hip", "quant_lora.hip", "gemm_w4a4.hip", "gemm_lds.hip", "gemm_bf16.hip",
            "repack.hip", "prep.hip", "gemm_mx.hip", "calib.hip", "gemm_bf16_blaslt.hip", "int8.hip", "norm.hip",
-           "rope.hip", "attention.hip"]
-HEADERS = ["common.h", "kernels.h"]
+           "rope.hip", "attention.hip", "fp8.hip", "cache.hip", "attention_cache.hip"]
+HEADERS = ["common.h", "kernels.h", "cache.h"]
 
 
 def hipcc():

@@ -1659,6 +1659,445 @@ int svdq_attention_packed(const void* q, int64_t q_stride_t, int64_t q_stride_h,
   return ok();
 }
 
+// ---- serving in 8-bit floating point ----
+
+static int check_fp8_mnk(int64_t M, int64_t N, int64_t K) {
+  int st = check_mk(M, K, 0);
+  if (st) return st;
+  if (N < 0) return fail(SVDQ_ERR_SHAPE, "N = %lld is negative", (long long)N);
+  if (N > kMaxDim) return fail(SVDQ_ERR_UNSUPPORTED, "dimension above 2^24 (N=%lld)", (long long)N);
+  if (M * N > (int64_t(1) << 38))
+    return fail(SVDQ_ERR_UNSUPPORTED, "more than 2^38 outputs (M=%lld N=%lld)", (long long)M, (long long)N);
+  if (K > svdq::kFp8MaxK)
+    return fail(SVDQ_ERR_UNSUPPORTED, "K = %lld is above %lld", (long long)K, (long long)svdq::kFp8MaxK);
+  return SVDQ_OK;
+}
+
+static int64_t blocks128(int64_t n) { return (n + 127) / 128; }
+
+static int quantize_fp8_impl(const void* x, const void* smooth, int64_t M, int64_t K, void* codes, void* scales,
+                             bool weight, void* stream) {
+  int st = check_fp8_mnk(M, 0, K);
+  if (st) return st;
+  if (M * blocks128(K) >= (int64_t(1) << 31))
+    return fail(SVDQ_ERR_UNSUPPORTED, "2^31 blocks of 128 or more (rows=%lld K=%lld)", (long long)M, (long long)K);
+  if (weight && blocks128(M) > 65535)
+    return fail(SVDQ_ERR_UNSUPPORTED, "N = %lld is above %d", (long long)M, 65535 * 128);
+  if (M == 0) return ok();
+  const char* names[] = {weight ? "w" : "x", "codes", "scales"};
+  const void* ptrs[] = {x, codes, scales};
+  if ((st = check_ptrs(names, ptrs, 3))) return st;
+  if (smooth != nullptr && !aligned16(smooth)) return fail(SVDQ_ERR_ALIGN, "smooth is not 16-byte aligned");
+  const size_t n_scales = (size_t)(weight ? blocks128(M) : M) * (size_t)blocks128(K);
+  const Range in[] = {range(names[0], x, (size_t)M * K * 2), range("smooth", smooth, (size_t)K * 2)};
+  const Range out[] = {range("codes", codes, (size_t)M * K), range("scales", scales, n_scales * 4)};
+  if ((st = check_alias(in, 2, out, 2))) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const auto launch = weight ? svdq::launch_quant_weight_fp8 : svdq::launch_quant_fp8;
+  hipError_t e = launch(static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(smooth), M, K,
+                        static_cast<uint8_t*>(codes), static_cast<float*>(scales), s);
+  if (int st_ = launched(e, "fp8 quantisation", s)) return st_;
+  return ok();
+}
+
+int svdq_quantize_fp8(const void* x, const void* smooth, int64_t M, int64_t K, void* codes, void* ascales,
+                      void* stream) {
+  return quantize_fp8_impl(x, smooth, M, K, codes, ascales, false, stream);
+}
+
+int svdq_quantize_weight_fp8(const void* w, const void* smooth, int64_t N, int64_t K, void* codes, void* wscales,
+                             void* stream) {
+  return quantize_fp8_impl(w, smooth, N, K, codes, wscales, true, stream);
+}
+
+size_t svdq_gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  return svdq::gemm_fp8_workspace_bytes(M, N, K);
+}
+
+int svdq_gemm_fp8_plan(int64_t M, int64_t N, int64_t K, int* tile, int* splits) {
+  int st = check_fp8_mnk(M, N, K);
+  if (st) return st;
+  if (M == 0 || N == 0) return fail(SVDQ_ERR_SHAPE, "M = %lld and N = %lld must be positive", (long long)M, (long long)N);
+  if (tile == nullptr || splits == nullptr) return fail(SVDQ_ERR_NULL, "%s is NULL", tile == nullptr ? "tile" : "splits");
+  svdq::gemm_fp8_plan(M, N, K, tile, splits);
+  return ok();
+}
+
+// what the two products share, as in check_int8_gemm
+static int check_fp8_gemm(const Range* act, int n_act, const void* weight, const void* wscales, const void* bias,
+                          int64_t M, int64_t N, int64_t K, const void* y, const void* workspace,
+                          size_t workspace_bytes, size_t need) {
+  int st;
+  const char* names[] = {"weight", "wscales", "y"};
+  const void* ptrs[] = {weight, wscales, y};
+  if ((st = check_ptrs(names, ptrs, 3))) return st;
+  if (bias != nullptr && !aligned16(bias)) return fail(SVDQ_ERR_ALIGN, "bias is not 16-byte aligned");
+  if (need > 0) {
+    if (workspace_bytes < need)
+      return fail(SVDQ_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+    const char* wn[] = {"workspace"};
+    const void* wp[] = {workspace};
+    if ((st = check_ptrs(wn, wp, 1))) return st;
+  }
+  Range in[5];
+  for (int i = 0; i < n_act; ++i) in[i] = act[i];
+  in[n_act] = range("weight", weight, (size_t)N * K);
+  in[n_act + 1] = range("wscales", wscales, (size_t)(blocks128(N) * blocks128(K)) * 4);
+  in[n_act + 2] = range("bias", bias, (size_t)N * 2);
+  const Range out[] = {range("y", y, (size_t)M * N * 2), range("workspace", need > 0 ? workspace : nullptr, need)};
+  return check_alias(in, n_act + 3, out, 2);
+}
+
+static svdq::Fp8GemmArgs fp8_args(const void* codes, const void* ascales, const void* weight, const void* wscales,
+                                  const void* bias, int64_t M, int64_t N, int64_t K, void* y) {
+  svdq::Fp8GemmArgs a{};
+  a.codes = static_cast<const uint8_t*>(codes);
+  a.ascales = static_cast<const float*>(ascales);
+  a.weight = static_cast<const uint8_t*>(weight);
+  a.wscales = static_cast<const float*>(wscales);
+  a.bias = static_cast<const uint16_t*>(bias);
+  a.y = static_cast<uint16_t*>(y);
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  return a;
+}
+
+int svdq_gemm_fp8(const void* codes, const void* ascales, const void* weight, const void* wscales, const void* bias,
+                  int64_t M, int64_t N, int64_t K, void* y, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_fp8_mnk(M, N, K);
+  if (st) return st;
+  if (M == 0 || N == 0) return ok();
+  const char* names[] = {"codes", "ascales"};
+  const void* ptrs[] = {codes, ascales};
+  if ((st = check_ptrs(names, ptrs, 2))) return st;
+  const Range act[] = {range("codes", codes, (size_t)M * K), range("ascales", ascales, (size_t)(M * blocks128(K)) * 4)};
+  const size_t need = svdq::gemm_fp8_workspace_bytes(M, N, K);
+  if ((st = check_fp8_gemm(act, 2, weight, wscales, bias, M, N, K, y, workspace, workspace_bytes, need))) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = svdq::launch_gemm_fp8(fp8_args(codes, ascales, weight, wscales, bias, M, N, K, y), workspace, s);
+  if (int st_ = launched(e, "fp8 gemm", s)) return st_;
+  return ok();
+}
+
+// workspace of the whole layer: codes, scales, then the product's own scratch
+struct Fp8Ws {
+  size_t scales, gemm, total;
+};
+static Fp8Ws fp8_ws(int64_t M, int64_t N, int64_t K) {
+  Fp8Ws w;
+  w.scales = align256(svdq::linear_fp8_codes_bytes(M, N, K));
+  w.gemm = w.scales > 0 ? align256(w.scales + (size_t)(M * blocks128(K)) * 4) : 0;
+  w.total = w.gemm + svdq::gemm_fp8_workspace_bytes(M, N, K);
+  return w;
+}
+
+size_t svdq_linear_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  return fp8_ws(M, N, K).total;
+}
+
+int svdq_linear_fp8(const void* x, const void* smooth, const void* weight, const void* wscales, const void* bias,
+                    int64_t M, int64_t N, int64_t K, void* y, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_fp8_mnk(M, N, K);
+  if (st) return st;
+  if (M * blocks128(K) >= (int64_t(1) << 31))
+    return fail(SVDQ_ERR_UNSUPPORTED, "2^31 blocks of 128 or more (M=%lld K=%lld)", (long long)M, (long long)K);
+  if (M == 0 || N == 0) return ok();
+  const char* names[] = {"x"};
+  const void* ptrs[] = {x};
+  if ((st = check_ptrs(names, ptrs, 1))) return st;
+  if (smooth != nullptr && !aligned16(smooth)) return fail(SVDQ_ERR_ALIGN, "smooth is not 16-byte aligned");
+  const Fp8Ws ws = fp8_ws(M, N, K);
+  const Range act[] = {range("x", x, (size_t)M * K * 2), range("smooth", smooth, (size_t)K * 2)};
+  if ((st = check_fp8_gemm(act, 2, weight, wscales, bias, M, N, K, y, workspace, workspace_bytes, ws.total))) return st;
+  uint8_t* w = static_cast<uint8_t*>(ws.total > 0 ? workspace : nullptr);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = svdq::launch_linear_fp8(fp8_args(nullptr, nullptr, weight, wscales, bias, M, N, K, y),
+                                         static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(smooth), w,
+                                         reinterpret_cast<float*>(w + ws.scales), w + ws.gemm, s);
+  if (int st_ = launched(e, "fp8 linear", s)) return st_;
+  return ok();
+}
+
+int svdq_rope_scaled(const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t H, const void* k,
+                     int64_t k_stride_t, int64_t k_stride_h, int64_t Hk, const void* positions, int64_t R, double theta,
+                     double factor, double original_length, double low_rotations, double high_rotations,
+                     float amplitude, int interleaved, int64_t T, int64_t D, void* q_out, int64_t qo_stride_t,
+                     int64_t qo_stride_h, void* k_out, int64_t ko_stride_t, int64_t ko_stride_h, void* stream) {
+  int st;
+  if (T < 0) return fail(SVDQ_ERR_SHAPE, "T = %lld is negative", (long long)T);
+  if (T >= kMaxDim) return fail(SVDQ_ERR_UNSUPPORTED, "T = %lld must be below 2^24", (long long)T);
+  if (D < 8 || D > 256 || D % 8 != 0)
+    return fail(SVDQ_ERR_UNSUPPORTED, "head size D = %lld is not a multiple of 8 in 8..256", (long long)D);
+  if (R < 8 || R > D || R % 8 != 0)
+    return fail(SVDQ_ERR_SHAPE, "R = %lld is not a multiple of 8 in 8..D = %lld", (long long)R, (long long)D);
+  if (H < 0 || Hk < 0 || H + Hk == 0)
+    return fail(SVDQ_ERR_SHAPE, "H = %lld and Hk = %lld: at least one head, none negative", (long long)H, (long long)Hk);
+  // a token's pieces of 8 elements are counted in 16 bits
+  if ((H + Hk) * (D / 8) > 65535)
+    return fail(SVDQ_ERR_UNSUPPORTED, "(H + Hk) * D = %lld is above %d", (long long)((H + Hk) * D), 65535 * 8);
+  if (!(theta >= 1.0 && theta <= 1e9)) return fail(SVDQ_ERR_INVALID, "theta = %g is not in [1, 1e9]", theta);
+  if (!(factor >= 1.0 && factor <= 1e6)) return fail(SVDQ_ERR_INVALID, "factor = %g is not in [1, 1e6]", factor);
+  if (!(original_length >= 0.0 && original_length <= 1e9))
+    return fail(SVDQ_ERR_INVALID, "original_length = %g is not in [0, 1e9]", original_length);
+  if (original_length > 0.0 && !(low_rotations >= 0.0 && high_rotations > low_rotations && high_rotations <= 1e9))
+    return fail(SVDQ_ERR_INVALID, "rotations from %g to %g: 0 <= low < high <= 1e9", low_rotations, high_rotations);
+  if (!(amplitude > 0.0f && amplitude <= 1e6f))
+    return fail(SVDQ_ERR_INVALID, "amplitude = %g is not in (0, 1e6]", amplitude);
+  if (T == 0) return ok();
+  {
+    const char* names[] = {"positions"};
+    const void* ptrs[] = {positions};
+    if ((st = check_ptrs(names, ptrs, 1))) return st;
+  }
+  Heads in[2], out[2];
+  const int64_t n[2] = {H, Hk};
+  const void* ip[2] = {q, k};
+  void* op[2] = {q_out, k_out};
+  const int64_t is[2][2] = {{q_stride_t, q_stride_h}, {k_stride_t, k_stride_h}};
+  const int64_t os[2][2] = {{qo_stride_t, qo_stride_h}, {ko_stride_t, ko_stride_h}};
+  static const char* const in_name[2] = {"q", "k"};
+  static const char* const out_name[2] = {"q_out", "k_out"};
+  for (int i = 0; i < 2; ++i) {
+    if (n[i] == 0) {
+      if (ip[i] != nullptr || op[i] != nullptr)
+        return fail(SVDQ_ERR_INVALID, "%s has no heads, so its tensors must be NULL", in_name[i]);
+      continue;
+    }
+    if ((st = make_heads(&in[i], in_name[i], ip[i], is[i][0], is[i][1], T, n[i], D))) return st;
+    if ((st = make_heads(&out[i], out_name[i], op[i], os[i][0], os[i][1], T, n[i], D))) return st;
+    if (!heads_distinct(out[i])) return fail(SVDQ_ERR_SHAPE, "%s: heads overlap under its strides", out_name[i]);
+  }
+  bool all_in_place = true;
+  for (int o = 0; o < 2; ++o) {
+    if (n[o] == 0) continue;
+    for (int i = 0; i < 2; ++i) {
+      if (n[i] == 0) continue;
+      const bool in_place = i == o && in[i].p == out[o].p && in[i].st == out[o].st && in[i].sh == out[o].sh;
+      if (i == o && !in_place) all_in_place = false;
+      if (!in_place && !heads_disjoint(in[i], out[o]))
+        return fail(SVDQ_ERR_ALIAS, "output %s overlaps input %s", out[o].name, in[i].name);
+    }
+    if (overlaps(heads_range(out[o]), range("positions", positions, (size_t)T * 4)))
+      return fail(SVDQ_ERR_ALIAS, "output %s overlaps input positions", out[o].name);
+  }
+  if (H > 0 && Hk > 0 && !heads_disjoint(out[0], out[1]))
+    return fail(SVDQ_ERR_ALIAS, "output q_out overlaps output k_out");
+  svdq::RopeScaledArgs a{};
+  for (int i = 0; i < 2; ++i) {
+    a.H[i] = (int)n[i];
+    if (n[i] == 0) continue;
+    a.in[i] = view_of(in[i]);
+    a.out[i] = static_cast<uint16_t*>(op[i]);
+    a.out_st[i] = out[i].st;
+    a.out_sh[i] = out[i].sh;
+  }
+  a.positions = static_cast<const int32_t*>(positions);
+  a.T = T;
+  a.D = (int)D;
+  a.R = (int)R;
+  a.copy = !all_in_place;
+  a.amplitude = amplitude;
+  // theta^(-2 i / R) / 2 pi by products of the ratio: the long double's 64 bits leave 127 of them at
+  // half a unit of a double or below
+  const long double ratio = powl((long double)theta, -2.0L / (long double)R);
+  long double f = 0.159154943091895335768883763372514362L;
+  for (int i = 0; i < (int)R / 2; ++i, f *= ratio) {
+    long double kept = 0.0L;
+    if (original_length > 0.0) {
+      kept = ((long double)original_length * f - low_rotations) / ((long double)high_rotations - low_rotations);
+      kept = kept < 0.0L ? 0.0L : kept > 1.0L ? 1.0L : kept;
+    }
+    a.turns[i] = (double)(f * (kept + (1.0L - kept) / (long double)factor));
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = svdq::launch_rope_scaled(a, interleaved != 0, s);
+  if (int st_ = launched(e, "rotary positions", s)) return st_;
+  return ok();
+}
+
+// ---- the e4m3 cache ----
+
+// codes, scales and sizes of a cache, the sequences' tables; fills the launchers' views
+static int check_cache(const void* k_codes, const void* v_codes, const void* k_scales, const void* v_scales,
+                       int64_t pages, int64_t Hk, int64_t page, int64_t D, const void* table, int64_t width,
+                       const void* lengths, const char* lengths_name, const void* cu_seqlens, int64_t B, int64_t T,
+                       svdq::CacheShape* c, Range* caches, Range* lists) {
+  int st = check_heads_shape(T, D);
+  if (st) return st;
+  if (page != 16 && page != 32 && page != 64 && page != 128)
+    return fail(SVDQ_ERR_UNSUPPORTED, "pages of %lld tokens: 16, 32, 64 and 128 are supported", (long long)page);
+  if (pages < 1 || pages >= (int64_t(1) << 31))
+    return fail(SVDQ_ERR_SHAPE, "pages = %lld is not in 1..2^31 - 1", (long long)pages);
+  if (Hk < 1) return fail(SVDQ_ERR_SHAPE, "Hk = %lld must be positive", (long long)Hk);
+  if (B < 0) return fail(SVDQ_ERR_SHAPE, "B = %lld is negative", (long long)B);
+  if (Hk > 65535 || B > 65535)
+    return fail(SVDQ_ERR_UNSUPPORTED, "Hk = %lld and B = %lld may be at most 65535", (long long)Hk, (long long)B);
+  if (cu_seqlens == nullptr && T != B)
+    return fail(SVDQ_ERR_INVALID, "without cu_seqlens each of the B = %lld sequences has one token, but T = %lld",
+                (long long)B, (long long)T);
+  if (width < 1 || width > kMaxDim) return fail(SVDQ_ERR_SHAPE, "table width %lld is not in 1..2^24", (long long)width);
+  const char* names[] = {"k_codes", "v_codes"};
+  const void* ptrs[] = {k_codes, v_codes};
+  if ((st = check_ptrs(names, ptrs, 2))) return st;
+  if (k_scales == nullptr || v_scales == nullptr)
+    return fail(SVDQ_ERR_NULL, "%s is NULL", k_scales == nullptr ? "k_scales" : "v_scales");
+  if (B > 0) {
+    const char* ln[] = {"block_table", lengths_name, "cu_seqlens"};
+    const void* lp[] = {table, lengths, cu_seqlens};
+    for (int i = 0; i < 3; ++i) {
+      if (lp[i] == nullptr && i < 2) return fail(SVDQ_ERR_NULL, "%s is NULL", ln[i]);
+      if (reinterpret_cast<uintptr_t>(lp[i]) & 3u) return fail(SVDQ_ERR_ALIGN, "%s is not 4-byte aligned", ln[i]);
+    }
+  }
+  const size_t codes = (size_t)pages * (size_t)(Hk * page * D), scales = (size_t)pages * (size_t)Hk;
+  caches[0] = range("k_codes", k_codes, codes);
+  caches[1] = range("v_codes", v_codes, codes);
+  caches[2] = range("k_scales", k_scales, scales);
+  caches[3] = range("v_scales", v_scales, scales);
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlaps(caches[i], caches[j])) return fail(SVDQ_ERR_ALIAS, "%s overlaps %s", caches[j].name, caches[i].name);
+  lists[0] = range("block_table", table, (size_t)B * (size_t)width * 4);
+  lists[1] = range(lengths_name, lengths, (size_t)B * 4);
+  lists[2] = range("cu_seqlens", cu_seqlens, cu_seqlens != nullptr ? (size_t)(B + 1) * 4 : 0);
+  c->k = static_cast<uint8_t*>(const_cast<void*>(k_codes));
+  c->v = static_cast<uint8_t*>(const_cast<void*>(v_codes));
+  c->ks = static_cast<uint8_t*>(const_cast<void*>(k_scales));
+  c->vs = static_cast<uint8_t*>(const_cast<void*>(v_scales));
+  c->pages = pages;
+  c->Hk = (int)Hk;
+  c->lg_page = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
+  c->D = (int)D;
+  return SVDQ_OK;
+}
+
+static svdq::CacheTokens cache_tokens(const void* table, int64_t width, const void* starts, const void* cu_seqlens,
+                                      int64_t B, int64_t T) {
+  svdq::CacheTokens a{};
+  a.table = static_cast<const int32_t*>(table);
+  a.starts = static_cast<const int32_t*>(starts);
+  a.cu = static_cast<const int32_t*>(cu_seqlens);
+  a.T = T;
+  a.width = width;
+  a.B = (int)B;
+  return a;
+}
+
+int svdq_cache_append_fp8(const void* k, int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                          int64_t v_stride_h, void* k_codes, void* v_codes, void* k_scales, void* v_scales,
+                          int64_t pages, int64_t Hk, int64_t page, int64_t D, const void* block_table, int64_t width,
+                          const void* lengths, const void* cu_seqlens, int64_t B, int64_t T, void* stream) {
+  svdq::CacheShape c{};
+  Range caches[4], in[5];
+  int st = check_cache(k_codes, v_codes, k_scales, v_scales, pages, Hk, page, D, block_table, width, lengths, "lengths",
+                       cu_seqlens, B, T, &c, caches, in);
+  if (st) return st;
+  if (T == 0 || B == 0) return ok();
+  Heads hk, hv;
+  if ((st = make_heads(&hk, "k", k, k_stride_t, k_stride_h, T, Hk, D))) return st;
+  if ((st = make_heads(&hv, "v", v, v_stride_t, v_stride_h, T, Hk, D))) return st;
+  in[3] = heads_range(hk);
+  in[4] = heads_range(hv);
+  if ((st = check_alias(in, 5, caches, 4))) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = svdq::launch_cache_append(cache_tokens(block_table, width, lengths, cu_seqlens, B, T), c, view_of(hk),
+                                           view_of(hv), s);
+  if (int st_ = launched(e, "cache append", s)) return st_;
+  return ok();
+}
+
+int svdq_cache_read_fp8(const void* k_codes, const void* v_codes, const void* k_scales, const void* v_scales,
+                        int64_t pages, int64_t Hk, int64_t page, int64_t D, const void* block_table, int64_t width,
+                        const void* starts, const void* cu_seqlens, int64_t B, int64_t T, void* k_out, void* v_out,
+                        void* stream) {
+  svdq::CacheShape c{};
+  Range in[7];
+  int st = check_cache(k_codes, v_codes, k_scales, v_scales, pages, Hk, page, D, block_table, width, starts, "starts",
+                       cu_seqlens, B, T, &c, in, in + 4);
+  if (st) return st;
+  if (T == 0 || B == 0) return ok();
+  const char* names[] = {"k_out", "v_out"};
+  const void* ptrs[] = {k_out, v_out};
+  if ((st = check_ptrs(names, ptrs, 2))) return st;
+  const size_t bytes = (size_t)T * (size_t)(Hk * D) * 2;
+  const Range out[] = {range("k_out", k_out, bytes), range("v_out", v_out, bytes)};
+  if ((st = check_alias(in, 7, out, 2))) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = svdq::launch_cache_read(cache_tokens(block_table, width, starts, cu_seqlens, B, T), c,
+                                         static_cast<uint16_t*>(k_out), static_cast<uint16_t*>(v_out), s);
+  if (int st_ = launched(e, "cache read", s)) return st_;
+  return ok();
+}
+
+size_t svdq_attention_cache_fp8_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D,
+                                                int64_t max_length, int packed) {
+  if (T <= 0 || B <= 0 || Hk <= 0 || H < Hk || H % Hk != 0 || max_length <= 0) return 0;
+  return svdq::attention_cache_workspace_bytes(T, B, H, Hk, D, max_length, packed != 0);
+}
+
+int svdq_attention_cache_fp8(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_codes,
+                             const void* v_codes, const void* k_scales, const void* v_scales, int64_t pages,
+                             int64_t Hk, int64_t page, int64_t D, const void* block_table, int64_t width,
+                             const void* lengths, const void* cu_seqlens, int64_t B, int64_t T, int64_t H,
+                             int64_t max_length, int causal, float scale, void* o, int64_t o_stride_t,
+                             int64_t o_stride_h, void* workspace, size_t workspace_bytes, void* stream) {
+  svdq::CacheShape c{};
+  Range in[7];
+  int st = check_cache(k_codes, v_codes, k_scales, v_scales, pages, Hk, page, D, block_table, width, lengths, "lengths",
+                       cu_seqlens, B, T, &c, in, in + 4);
+  if (st) return st;
+  if (H < 1 || H % Hk != 0)
+    return fail(SVDQ_ERR_SHAPE, "H = %lld is not a positive multiple of Hk = %lld", (long long)H, (long long)Hk);
+  if (H > 65535) return fail(SVDQ_ERR_UNSUPPORTED, "H = %lld may be at most 65535", (long long)H);
+  if (!(scale > 0.0f && scale <= 1048576.0f)) return fail(SVDQ_ERR_INVALID, "scale = %g is not in (0, 2^20]", scale);
+  if (max_length < 1) return fail(SVDQ_ERR_SHAPE, "max_length = %lld must be positive", (long long)max_length);
+  // work items of the grid, 256 for 16 rows
+  if (16 * T * (H / Hk) + 512 * B >= (int64_t(1) << 32) - 65536)
+    return fail(SVDQ_ERR_UNSUPPORTED, "16 T H / Hk + 512 B must be below 2^32 - 65536 (T=%lld B=%lld H=%lld Hk=%lld)",
+                (long long)T, (long long)B, (long long)H, (long long)Hk);
+  if (T == 0 || B == 0) return ok();
+  Heads hq, ho;
+  if ((st = make_heads(&hq, "q", q, q_stride_t, q_stride_h, T, H, D))) return st;
+  if ((st = make_heads(&ho, "o", o, o_stride_t, o_stride_h, T, H, D))) return st;
+  if (!heads_distinct(ho)) return fail(SVDQ_ERR_SHAPE, "o: heads overlap under its strides");
+  if (!heads_disjoint(hq, ho)) return fail(SVDQ_ERR_ALIAS, "output o overlaps input q");
+  max_length = max_length < width * page ? max_length : width * page;
+  const size_t need = svdq::attention_cache_workspace_bytes(T, B, H, Hk, D, max_length, cu_seqlens != nullptr);
+  if (need > 0) {
+    if (workspace_bytes < need)
+      return fail(SVDQ_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+    const char* wn[] = {"workspace"};
+    const void* wp[] = {workspace};
+    if ((st = check_ptrs(wn, wp, 1))) return st;
+  }
+  const Range out[] = {heads_range(ho), range("workspace", need > 0 ? workspace : nullptr, need)};
+  if ((st = check_alias(in, 7, out, 2))) return st;
+  if (need > 0 && overlaps(out[1], heads_range(hq))) return fail(SVDQ_ERR_ALIAS, "output workspace overlaps input q");
+  svdq::AttnCacheArgs a{};
+  a.q = view_of(hq);
+  a.o = static_cast<uint16_t*>(o);
+  a.o_st = ho.st;
+  a.o_sh = ho.sh;
+  a.c = c;
+  a.table = static_cast<const int32_t*>(block_table);
+  a.lengths = static_cast<const int32_t*>(lengths);
+  a.cu = static_cast<const int32_t*>(cu_seqlens);
+  a.T = T;
+  a.width = width;
+  a.B = (int)B;
+  a.H = (int)H;
+  a.causal = causal != 0;
+  a.scale = scale;
+  a.partial = static_cast<float*>(need > 0 ? workspace : nullptr);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = svdq::launch_attention_cache(a, max_length, s);
+  if (int st_ = launched(e, "attention over a cache", s)) return st_;
+  return ok();
+}
+
 // ---- measurement helpers (not part of the layer) ----
 
 size_t svdq_calib_table_bytes(void) { return svdq::calib_table_bytes(); }

@@ -1,0 +1,269 @@
+// A cache of keys and values in pages, held in e4m3 with a power-of-two scale per page and head:
+//
+//   keys   [pages, Hk, P, D]: token-major within a page        value = code * 2^(scale - 127)
+//   values [pages, Hk, D, P]: element-major, so that the tokens a product with the probabilities sums over
+//                             are contiguous                   scales [pages, Hk], bytes (E8M0, 255 = NaN)
+//
+// Appending: a page's scale is the least power of two (from 2^-100) that holds its tokens' maximum within 448 when
+// its first token is written, and grows when a later one needs more; what was there is rescaled, which is exact but
+// for codes that become subnormal. One workgroup per page touched, head and tensor.
+#include "cache.h"
+
+namespace svdq {
+
+namespace {
+
+constexpr int kThreadsC = 256;
+
+// The pages that a sequence of n tokens touches from any start are at most floor((n - 2) / P) + 2, so blocks
+// of P packed tokens are numbered with two more per sequence: sequence b starts at floor(cu[b] / P) + 2 b.
+// Finds the sequence of block t and its local number; false where there is none.
+struct Touched {
+  int b, first, count;   // sequence, its first packed token and its tokens
+  int64_t local;
+};
+__device__ __forceinline__ bool touched_block(const CacheTokens& a, int lg, int64_t t, Touched& o) {
+  if (a.cu == nullptr) {   // a token per sequence
+    o = Touched{(int)t, (int)t, 1, 0};
+    return t < a.B;
+  }
+  // last sequence whose first block is at most t
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = a.B;
+  while (true) {
+    const int step = (hi - lo + 63) / 64;
+    const int idx = lo + lane * step;
+    const int c0 = min(max(a.cu[min(idx, a.B)], 0), (int)a.T);
+    const int n = __popcll(__ballot(idx < hi && (int64_t)(c0 >> lg) + 2 * (int64_t)idx <= t));
+    if (n == 0) return false;
+    lo += (n - 1) * step;
+    if (step == 1) break;
+    hi = min(hi, lo + step);
+  }
+  const int c0 = min(max(a.cu[lo], 0), (int)a.T), c1 = min(max(a.cu[lo + 1], 0), (int)a.T);
+  o = Touched{lo, c0, c1 - c0, t - (c0 >> lg) - 2 * (int64_t)lo};
+  return o.local >= 0;
+}
+
+// The page of a block and the tokens in it: packed tokens tok0 .. tok0 + (s1 - s0) - 1 go to slots s0 .. s1 - 1.
+// page is -1 where the table has none.
+struct Block {
+  int64_t page;
+  int tok0, s0, s1;
+};
+__device__ __forceinline__ bool find_block(const CacheTokens& a, const CacheShape& c, Block& o) {
+  Touched t;
+  if (!touched_block(a, c.lg_page, (int64_t)blockIdx.x, t) || t.count <= 0) return false;
+  const int64_t start = max(a.starts[t.b], 0), end = start + t.count;
+  const int64_t block = (start >> c.lg_page) + t.local;
+  const int64_t p0 = block << c.lg_page;
+  if (p0 >= end) return false;
+  const int64_t from = max(start, p0), to = min(end, p0 + (1 << c.lg_page));
+  const int page = block < a.width ? a.table[(int64_t)t.b * a.width + block] : -1;
+  o = Block{(uint32_t)page < (uint32_t)c.pages ? page : -1, t.first + (int)(from - start), (int)(from - p0), (int)(to - p0)};
+  return true;
+}
+
+// 16 codes times 2^(from - to), nearest even
+__device__ __forceinline__ u32x4 rescale16(u32x4 w, float by) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float v0 = __builtin_amdgcn_cvt_f32_fp8((int)w[i], 0) * by, v1 = __builtin_amdgcn_cvt_f32_fp8((int)w[i], 1) * by;
+    const float v2 = __builtin_amdgcn_cvt_f32_fp8((int)w[i], 2) * by, v3 = __builtin_amdgcn_cvt_f32_fp8((int)w[i], 3) * by;
+    w[i] = fp8_codes4(v0, v1, v2, v3);
+  }
+  return w;
+}
+
+// bytes lo .. hi - 1 of a 16-byte piece (whole if 0, 16)
+__device__ __forceinline__ void store_bytes(uint8_t* dst, u32x4 w, int lo, int hi) {
+  if (lo <= 0 && hi >= 16) {
+    *reinterpret_cast<u32x4*>(dst) = w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (e >= lo && e < hi) dst[e] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
+  }
+}
+
+template <int D>
+__global__ __launch_bounds__(kThreadsC) void append_kernel(CacheTokens a, CacheShape c, HeadView k, HeadView v) {
+  constexpr int kLanes = D / 8;                       // lanes of a token, 8 elements each
+  constexpr int kRows = kThreadsC / kLanes;           // tokens of a pass
+  constexpr int kPasses = kMaxPage / kRows;
+  __shared__ __attribute__((aligned(16))) uint8_t image[D * (kMaxPage + 16)];
+  __shared__ float part[kThreadsC / 64];
+  Block blk;
+  if (!find_block(a, c, blk) || blk.page < 0) return;
+  const int tid = threadIdx.x, P = 1 << c.lg_page;
+  const int head = (int)blockIdx.y;
+  const bool is_v = blockIdx.z != 0;
+  const HeadView in = is_v ? v : k;
+  const int row = tid / kLanes, e0 = 8 * (tid % kLanes);
+  const int n = blk.s1 - blk.s0;
+
+  u32x4 w[kPasses];
+  float amax = 0.0f;
+#pragma unroll
+  for (int u = 0; u < kPasses; ++u) {
+    const int r = row + kRows * u;
+    w[u] = r < n ? *reinterpret_cast<const u32x4*>(in.p + (int64_t)(blk.tok0 + r) * in.st + head * in.sh + e0) : zero4();
+  }
+  uint8_t* scale_at = (is_v ? c.vs : c.ks) + blk.page * c.Hk + head;
+  const int old = blk.s0 > 0 ? *scale_at : 0;         // below every scale that is written
+#pragma unroll
+  for (int u = 0; u < kPasses; ++u)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      amax = max_or_nan(amax, max_or_nan(fabsf(bf16lo_to_f32(w[u][i])), fabsf(bf16hi_to_f32(w[u][i]))));
+  amax = wave_reduce<true>(amax);
+  if ((tid & 63) == 0) part[tid >> 6] = amax;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kThreadsC / 64; ++i) amax = max_or_nan(amax, part[i]);
+  const bool fine = amax <= 3.4028234663852886e38f;
+  const int now = fine ? max(fp8_exponent(amax) + 127, old) : 255;
+  if (tid == 0 && now != old) *scale_at = (uint8_t)now;
+  // a NaN scale says it all: codes are left as they are, new ones are zero
+  const float inv = now < 255 ? __uint_as_float((uint32_t)(254 - now) << 23) : 0.0f;
+  const bool grown = blk.s0 > 0 && now > old && now < 255;
+  // 2^(old - now); below 2^-126 every code becomes zero
+  const float by = now - old < 127 ? __uint_as_float((uint32_t)(127 + old - now) << 23) : 0.0f;
+
+  uint8_t* page = (is_v ? c.v : c.k) + (blk.page * c.Hk + head) * ((int64_t)P * D);
+  if (!is_v) {
+    if (grown) {
+      for (int i = tid; i < blk.s0 * (D / 16); i += kThreadsC) {
+        u32x4* at = reinterpret_cast<u32x4*>(page) + i;
+        *at = rescale16(*at, by);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kPasses; ++u) {
+      const int r = row + kRows * u;
+      if (r < n) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[2 * i] = bf16lo_to_f32(w[u][i]);
+          x[2 * i + 1] = bf16hi_to_f32(w[u][i]);
+        }
+        *reinterpret_cast<u32x2*>(page + (blk.s0 + r) * D + e0) = fp8_codes8(x, inv);
+      }
+    }
+    return;
+  }
+  // values: the page's image [D][P] is put together in LDS and leaves by rows
+  const int pitch = P + 16;
+  if (grown) {
+    for (int i = tid; i < D * (P / 16); i += kThreadsC) {
+      const int d = i >> (c.lg_page - 4), s = 16 * (i & (P / 16 - 1));
+      if (s < blk.s0)
+        *reinterpret_cast<u32x4*>(image + d * pitch + s) = rescale16(*reinterpret_cast<const u32x4*>(page + d * P + s), by);
+    }
+    __syncthreads();   // the last piece may hold new tokens' slots too
+  }
+#pragma unroll
+  for (int u = 0; u < kPasses; ++u) {
+    const int r = row + kRows * u;
+    if (r < n) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16lo_to_f32(w[u][i]);
+        x[2 * i + 1] = bf16hi_to_f32(w[u][i]);
+      }
+      const u32x2 q = fp8_codes8(x, inv);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) image[(e0 + e) * pitch + blk.s0 + r] = (uint8_t)(q[e >> 2] >> (8 * (e & 3)));
+    }
+  }
+  __syncthreads();
+  const int from = grown ? 0 : blk.s0;
+  for (int i = tid; i < D * (P / 16); i += kThreadsC) {
+    const int d = i >> (c.lg_page - 4), s = 16 * (i & (P / 16 - 1));
+    if (s + 16 > from && s < blk.s1)
+      store_bytes(page + d * P + s, *reinterpret_cast<const u32x4*>(image + d * pitch + s), from - s, blk.s1 - s);
+  }
+}
+
+// 16 codes -> 16 bf16, exact
+__device__ __forceinline__ void widen16(u32x4 w, float scale, u32x4 (&o)[2]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[i >> 1][2 * (i & 1)] = fp8_pair_to_bf16<0>(w[i], scale);
+    o[i >> 1][2 * (i & 1) + 1] = fp8_pair_to_bf16<1>(w[i], scale);
+  }
+}
+
+// Packed tokens' keys and values back in bf16; zeros where the table has no page.
+template <int D>
+__global__ __launch_bounds__(kThreadsC) void read_kernel(CacheTokens a, CacheShape c, uint16_t* k_out, uint16_t* v_out) {
+  __shared__ __attribute__((aligned(16))) uint8_t image[D * (kMaxPage + 16)];
+  Block blk;
+  if (!find_block(a, c, blk)) return;
+  const int tid = threadIdx.x, P = 1 << c.lg_page;
+  const int head = (int)blockIdx.y;
+  const bool is_v = blockIdx.z != 0;
+  const int n = blk.s1 - blk.s0;
+  const int64_t page_at = max(blk.page, (int64_t)0);
+  const uint8_t* page = (is_v ? c.v : c.k) + (page_at * c.Hk + head) * ((int64_t)P * D);
+  const float scale = cache_scale((is_v ? c.vs : c.ks)[page_at * c.Hk + head]);
+  const bool none = blk.page < 0;
+  uint16_t* out = (is_v ? v_out : k_out) + ((int64_t)blk.tok0 * c.Hk + head) * D;
+  if (is_v) {
+    const int pitch = P + 16;
+    for (int i = tid; i < D * (P / 16); i += kThreadsC) {
+      const int d = i >> (c.lg_page - 4), s = 16 * (i & (P / 16 - 1));
+      *reinterpret_cast<u32x4*>(image + d * pitch + s) = *reinterpret_cast<const u32x4*>(page + d * P + s);
+    }
+    __syncthreads();
+    for (int i = tid; i < n * (D / 16); i += kThreadsC) {
+      const int r = i / (D / 16), e = 16 * (i % (D / 16));
+      u32x4 w;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint8_t* at = image + (e + 4 * j) * pitch + blk.s0 + r;
+        w[j] = (uint32_t)at[0] | (uint32_t)at[pitch] << 8 | (uint32_t)at[2 * pitch] << 16 | (uint32_t)at[3 * pitch] << 24;
+      }
+      u32x4 o[2];
+      widen16(w, scale, o);
+      u32x4* dst = reinterpret_cast<u32x4*>(out + (int64_t)r * c.Hk * D + e);
+      dst[0] = none ? zero4() : o[0];
+      dst[1] = none ? zero4() : o[1];
+    }
+  } else {
+    for (int i = tid; i < n * (D / 16); i += kThreadsC) {
+      const int r = i / (D / 16), e = 16 * (i % (D / 16));
+      u32x4 o[2];
+      widen16(*reinterpret_cast<const u32x4*>(page + (blk.s0 + r) * D + e), scale, o);
+      u32x4* dst = reinterpret_cast<u32x4*>(out + (int64_t)r * c.Hk * D + e);
+      dst[0] = none ? zero4() : o[0];
+      dst[1] = none ? zero4() : o[1];
+    }
+  }
+}
+
+unsigned touched_blocks(const CacheTokens& a, int lg) {
+  return (unsigned)(a.cu == nullptr ? a.B : (a.T >> lg) + 2 * (int64_t)a.B);
+}
+
+}  // namespace
+
+hipError_t launch_cache_append(const CacheTokens& a, const CacheShape& c, const HeadView& k, const HeadView& v,
+                               hipStream_t stream) {
+  const dim3 grid(touched_blocks(a, c.lg_page), (unsigned)c.Hk, 2), block(kThreadsC);
+  if (c.D == 64) hipLaunchKernelGGL(append_kernel<64>, grid, block, 0, stream, a, c, k, v);
+  else hipLaunchKernelGGL(append_kernel<128>, grid, block, 0, stream, a, c, k, v);
+  return hipGetLastError();
+}
+
+hipError_t launch_cache_read(const CacheTokens& a, const CacheShape& c, uint16_t* k_out, uint16_t* v_out,
+                             hipStream_t stream) {
+  const dim3 grid(touched_blocks(a, c.lg_page), (unsigned)c.Hk, 2), block(kThreadsC);
+  if (c.D == 64) hipLaunchKernelGGL(read_kernel<64>, grid, block, 0, stream, a, c, k_out, v_out);
+  else hipLaunchKernelGGL(read_kernel<128>, grid, block, 0, stream, a, c, k_out, v_out);
+  return hipGetLastError();
+}
+
+}  // namespace svdq

@@ -160,6 +160,36 @@ __device__ __forceinline__ u32x2 int8_codes8(const float (&v)[8], float inv) {
   return r;
 }
 
+// Scale of a block of e4m3 codes with maximum magnitude amax: the least power of two 2^e, e >= -100, with
+// amax <= 448 * 2^e; inv = 2^-e. A block with an infinity or NaN has scale NaN and zero codes.
+struct Fp8Scale {
+  float inv, scale;
+};
+__device__ __forceinline__ int fp8_exponent(float amax) {   // finite amax >= 0
+  const uint32_t u = __float_as_uint(amax);
+  const int e = (int)(u >> 23) - 135 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);   // 448 = 1.75 * 2^8
+  return e < -100 ? -100 : e;
+}
+__device__ __forceinline__ Fp8Scale fp8_scale(float amax) {
+  const bool fine = amax <= 3.4028234663852886e38f;
+  const int e = fp8_exponent(fine ? amax : 0.0f);
+  Fp8Scale q;
+  q.inv = fine ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.0f;
+  q.scale = fine ? __uint_as_float((uint32_t)(127 + e) << 23) : __builtin_nanf("");
+  return q;
+}
+// 4 and 8 codes of v * inv (finite, at most 448 in magnitude), nearest even, packed in order; where inv is 0 the codes are
+// zero whatever v is.
+__device__ __forceinline__ uint32_t fp8_codes4(float a, float b, float c, float d) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+}
+__device__ __forceinline__ u32x2 fp8_codes8(const float (&v)[8], float inv) {
+  const u32x2 r = {fp8_codes4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                   fp8_codes4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv)};
+  return inv != 0.0f ? r : u32x2{0u, 0u};
+}
+
 __device__ __forceinline__ u32x4 zero4() { u32x4 z = {0u, 0u, 0u, 0u}; return z; }
 
 // Sum (or maximum) over the wave's 64 lanes, the same value in each: within rows of 16 lanes by

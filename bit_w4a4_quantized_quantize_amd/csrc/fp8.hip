@@ -1,0 +1,611 @@
+// Linear in 8-bit floating point (OCP e4m3) with a scale per block of 128 input channels:
+//
+//   v = x * smooth,  e = the least integer >= -100 with max |v| <= 448 * 2^e over 128 channels of a token,
+//   codes = e4m3(v * 2^-e),  ascales = 2^e     (weights: over 128 x 128, the same rule)
+//   y = bf16( sum_p ascales[p, m] * wscales[n / 128, p] * (sum_{k in p} codes[m, k] * weight[n, k]) + bias[n] )
+//
+// A power of two costs no precision (e4m3 keeps its three fraction bits down to 2^-15 of a block's maximum) and makes
+// v * 2^-e exact, so the codes are bit-exact functions of x. The product takes any fp32 scales.
+//
+// A block of 128 is two v_mfma_f32_32x32x64_f8f6f4, the first from zero; their sum is added to the fp32 result times
+// the block's two scales. The weight is the A operand, so that a lane holds channels of one token and its
+// two scales are one factor per lane.
+#include "common.h"
+#include "kernels.h"
+#include <math.h>
+
+#define F8_LDS_PTR(p) ((__attribute__((address_space(3))) void*)(p))
+
+namespace svdq {
+
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kGroupM = 4;
+
+// 8 bf16 of x times 8 of smooth, in fp32 (exact)
+template <bool SMOOTH>
+__device__ __forceinline__ void f8_scaled8(const u32x4 x, const u32x4 s, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16lo_to_f32(x[i]);
+    v[2 * i + 1] = bf16hi_to_f32(x[i]);
+    if (SMOOTH) {
+      v[2 * i] *= bf16lo_to_f32(s[i]);
+      v[2 * i + 1] *= bf16hi_to_f32(s[i]);
+    }
+  }
+}
+
+// maximum over the 16 lanes of a row of the wave, the same value in each
+__device__ __forceinline__ float max_row16(float v) {
+#define SVDQ_DPP(x, ctrl) \
+  __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), ctrl, 0xF, 0xF, true))
+  v = max_or_nan(v, SVDQ_DPP(v, 0xB1));
+  v = max_or_nan(v, SVDQ_DPP(v, 0x4E));
+  v = max_or_nan(v, SVDQ_DPP(v, 0x141));
+  v = max_or_nan(v, SVDQ_DPP(v, 0x140));
+#undef SVDQ_DPP
+  return v;
+}
+
+// A workgroup's threads are dealt to blocks of 128 channels, 16 lanes of 8 channels each, U blocks a
+// thread with their loads in flight together. Memory bound.
+template <bool SMOOTH, int U>
+__global__ __launch_bounds__(256) void quant_fp8_kernel(const uint16_t* __restrict__ x,
+                                                        const uint16_t* __restrict__ smooth, uint32_t M, uint32_t K,
+                                                        uint8_t* __restrict__ codes, float* __restrict__ ascales) {
+  const uint32_t KB = (K + 127) / 128, blocks = M * KB;
+  const uint32_t sub = threadIdx.x & 15;
+  u32x4 w[U], f[U];
+  uint32_t row[U], blk[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t g = ((uint32_t)blockIdx.x * U + u) * 16 + threadIdx.x / 16;
+    row[u] = g / KB;
+    blk[u] = g - row[u] * KB;
+    const uint32_t k = 128 * blk[u] + 8 * sub;
+    const bool in = g < blocks && k < K;
+    w[u] = in ? *reinterpret_cast<const u32x4*>(x + (size_t)row[u] * K + k) : zero4();
+    f[u] = SMOOTH && in ? *reinterpret_cast<const u32x4*>(smooth + k) : zero4();
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float v[8];
+    f8_scaled8<SMOOTH>(w[u], f[u], v);
+    float amax = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = max_or_nan(amax, fabsf(v[e]));
+    amax = max_row16(amax);
+    const Fp8Scale q = fp8_scale(amax);
+    const uint32_t k = 128 * blk[u] + 8 * sub;
+    if (row[u] < M && k < K) {
+      *reinterpret_cast<u32x2*>(codes + (size_t)row[u] * K + k) = fp8_codes8(v, q.inv);
+      if (sub == 0) ascales[(size_t)blk[u] * M + row[u]] = q.scale;
+    }
+  }
+}
+
+// A weight's block of 128 x 128 per workgroup: two threads a row, 64 channels each. Load time.
+template <bool SMOOTH>
+__global__ __launch_bounds__(256) void quant_weight_fp8_kernel(const uint16_t* __restrict__ w,
+                                                               const uint16_t* __restrict__ smooth, int N, int K,
+                                                               uint8_t* __restrict__ codes,
+                                                               float* __restrict__ wscales) {
+  __shared__ float part[4];
+  const int n = 128 * (int)blockIdx.y + (int)threadIdx.x / 2;
+  const int k0 = 128 * (int)blockIdx.x + 64 * ((int)threadIdx.x & 1);
+  const int KB = (K + 127) / 128;
+  u32x4 held[8];
+  float amax = 0.0f;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const bool in = n < N && k0 + 8 * u < K;
+    held[u] = in ? *reinterpret_cast<const u32x4*>(w + (size_t)n * K + k0 + 8 * u) : zero4();
+    float v[8];
+    f8_scaled8<SMOOTH>(held[u], SMOOTH && in ? *reinterpret_cast<const u32x4*>(smooth + k0 + 8 * u) : zero4(), v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = max_or_nan(amax, fabsf(v[e]));
+  }
+  amax = wave_reduce<true>(amax);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = amax;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) amax = max_or_nan(amax, part[i]);
+  const Fp8Scale q = fp8_scale(amax);
+  if (threadIdx.x == 0) wscales[(size_t)blockIdx.y * KB + blockIdx.x] = q.scale;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    if (n < N && k0 + 8 * u < K) {
+      float v[8];
+      f8_scaled8<SMOOTH>(held[u], SMOOTH ? *reinterpret_cast<const u32x4*>(smooth + k0 + 8 * u) : zero4(), v);
+      *reinterpret_cast<u32x2*>(codes + (size_t)n * K + k0 + 8 * u) = fp8_codes8(v, q.inv);
+    }
+  }
+}
+
+// (copies into LDS stay outside template-dependent code, see gemm_mx.hip)
+__device__ __forceinline__ void f8_to_lds(__amdgpu_buffer_rsrc_t r, void* lds, int voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, F8_LDS_PTR(lds), 16, voff, soff, 0, 0);
+}
+__device__ __forceinline__ f32x16 f8_mfma32(i32x8 a, i32x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);   // e4m3 both, unscaled
+}
+__device__ __forceinline__ f32x4 f8_mfma16(i32x8 a, i32x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ i32x8 join8(i32x4 a, i32x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
+__device__ __forceinline__ void f8_barrier() {   // as in gemm_bf16.hip: the waits are explicit
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Tile of a workgroup: WM x WN waves of TM x TN blocks of 32 tokens x 32 channels. A panel is the 128 codes of a
+// scale block: chunks of 32 rows x 128 bytes, row r at r * 128 with its eight 16-byte pieces
+// permuted by piece ^ swz(r), so that an operand read (32 rows, one piece each) meets every LDS
+// bank evenly and a copy reads whole 128-byte row segments.
+template <int WM, int WN, int TM, int TN, int S>
+struct F8Cfg {
+  static constexpr int kWaves = WM * WN;
+  static constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN;
+  static constexpr int kChunksA = BM / 32, kChunks = (BM + BN) / 32;
+  static constexpr int kChunkBytes = 4096;
+  static constexpr int kStageBytes = kChunks * kChunkBytes;
+  static constexpr int kCopies = kChunks * 4;                    // 1 KB copies of a panel
+  static constexpr int kPerWave = kCopies / kWaves;
+  static constexpr int kOutBytes = kWaves * 32 * (32 * TN + 8) * 2;   // output staging
+  static constexpr int kLdsBytes = S * kStageBytes > kOutBytes ? S * kStageBytes : kOutBytes;
+  static_assert(kCopies % kWaves == 0, "copies per wave");
+};
+
+struct F8Split {
+  int panels;        // panels of k per split
+  int splits;
+  float* partial;    // [splits, M, N] sums when splits > 1
+};
+
+template <int WM, int WN, int TM, int TN, int S>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_kernel(Fp8GemmArgs a, F8Split sp) {
+  using C = F8Cfg<WM, WN, TM, TN, S>;
+  static_assert(S == 2, "two stages");
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = tid & 63;
+  const int h = lane >> 5, l32 = lane & 31;
+  const int wave_m = wave % WM, wave_n = wave / WM;
+  const int M = (int)a.M, N = (int)a.N, K = (int)a.K;
+  const int KB = (K + 127) / 128;
+
+  // XCD-contiguous tile ranges, kGroupM row blocks per column sweep
+  const int NBX = (N + C::BN - 1) / C::BN, NBY = (M + C::BM - 1) / C::BM;
+  const int per_xcd = (int)(gridDim.x / 8);
+  int tile = (int)(blockIdx.x % 8) * per_xcd + (int)(blockIdx.x / 8);
+  if (tile >= NBX * NBY * sp.splits) return;
+  const int split = tile / (NBX * NBY);
+  tile -= split * (NBX * NBY);
+  const int per_group = kGroupM * NBX;
+  const int first_row = (tile / per_group) * kGroupM;
+  const int group_rows = min(NBY - first_row, kGroupM);
+  const int m0 = (first_row + (tile % per_group) % group_rows) * C::BM;
+  const int n0 = ((tile % per_group) / group_rows) * C::BN;
+  const int m_w = m0 + wave_m * TM * 32, n_w = n0 + wave_n * TN * 32;
+
+  const int rows_a = min(C::BM, M - m0), rows_b = min(C::BN, N - n0);
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(a.codes + (size_t)m0 * K, (uint32_t)rows_a * (uint32_t)K);
+  const __amdgpu_buffer_rsrc_t rb = make_rsrc(a.weight + (size_t)n0 * K, (uint32_t)rows_b * (uint32_t)K);
+  const int p0 = split * sp.panels;
+  const int p1 = min(p0 + sp.panels, KB);
+
+  auto swz = [](int r) { return (r ^ (r >> 3)) & 7; };
+  // copy c of a panel: chunk c / 4, rows 8 (c % 4) .. + 7; an offset past the buffer reads
+  // zero (rows past the tensor, and pieces past K in the last panel)
+  constexpr int kPast = 0x7FFFFFF0;
+  int off[C::kPerWave];
+#pragma unroll
+  for (int u = 0; u < C::kPerWave; ++u) {
+    const int c = wave + C::kWaves * u;
+    const int r32 = 8 * (c & 3) + (lane >> 3);
+    const bool is_a = c / 4 < C::kChunksA;
+    const int row = 32 * (is_a ? c / 4 : c / 4 - C::kChunksA) + r32;
+    off[u] = row < (is_a ? rows_a : rows_b) ? row * K + 16 * ((lane & 7) ^ swz(r32)) : kPast;
+  }
+  auto load_panel = [&](int kp) {
+    uint8_t* st = smem + ((kp - p0) % S) * C::kStageBytes;
+    const int k0 = kp * 128;
+    const bool tail = k0 + 128 > K;
+#pragma unroll
+    for (int u = 0; u < C::kPerWave; ++u) {
+      const int c = wave + C::kWaves * u;
+      int v = off[u];
+      if (tail && k0 + 16 * ((lane & 7) ^ swz(8 * (c & 3) + (lane >> 3))) >= K) v = kPast;
+      if (c / 4 < C::kChunksA) f8_to_lds(ra, st + c * 1024, v, k0);
+      else f8_to_lds(rb, st + c * 1024, v, k0);
+    }
+  };
+
+  // a panel's scales: this lane's token of each block of 32, and the wave's channels' (one block of 128
+  // holds whole blocks of 32)
+  const float* as_at[TM];
+  const float* ws_at[TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i) as_at[i] = a.ascales + min(m_w + 32 * i + l32, M - 1);
+#pragma unroll
+  for (int j = 0; j < TN; ++j) ws_at[j] = a.wscales + (size_t)(min(n_w + 32 * j, N - 1) / 128) * KB;
+
+  f32x16 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = f32x16{};
+
+  int frag[4];   // this lane's operand pieces (row l32, piece 2 t + h) within a chunk
+#pragma unroll
+  for (int t = 0; t < 4; ++t) frag[t] = l32 * 128 + (((2 * t + h) ^ swz(l32)) * 16);
+  auto operand = [&](const uint8_t* chunk, int s) {
+    return join8(*reinterpret_cast<const i32x4*>(chunk + frag[2 * s]),
+                 *reinterpret_cast<const i32x4*>(chunk + frag[2 * s + 1]));
+  };
+
+  if (p0 < p1) load_panel(p0);
+  for (int kp = p0; kp < p1; ++kp) {
+    float as[TM], ws[TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) as[i] = as_at[i][(size_t)kp * M];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) ws[j] = ws_at[j][kp];
+    __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0), lgkmcnt(0)
+    f8_barrier();   // panel kp visible to every wave, the other stage is read to its end
+    if (kp + 1 < p1) load_panel(kp + 1);
+    const uint8_t* st = smem + ((kp - p0) & 1) * C::kStageBytes;
+    i32x8 ft[TM][2];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) ft[i][s] = operand(st + (wave_m * TM + i) * C::kChunkBytes, s);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const uint8_t* chunk = st + (C::kChunksA + wave_n * TN + j) * C::kChunkBytes;
+      const i32x8 fw0 = operand(chunk, 0), fw1 = operand(chunk, 1);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const f32x16 sum = f8_mfma32(fw1, ft[i][1], f8_mfma32(fw0, ft[i][0], f32x16{}));
+        const float s = as[i] * ws[j];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_fmaf(sum[r], s, acc[i][j][r]);
+      }
+    }
+  }
+
+  // this lane holds channels n_w + 32 j + 8 (r / 4) + 4 h + r % 4 of token m_w + 32 i + l32
+  if (sp.splits > 1) {   // the partial sums; fp8_reduce_kernel adds them and ends the product
+    float* out = sp.partial + (size_t)split * (size_t)M * (size_t)N;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int m = m_w + 32 * i + l32;
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          const int n = n_w + 32 * j + 2 * r + 4 * h;
+          float* dst = out + (size_t)m * (size_t)N + n;
+          if (m < M && n < N) {
+            if (N % 4 == 0) {
+              *reinterpret_cast<f32x4*>(dst) = f32x4{acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]};
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (n + e < N) dst[e] = acc[i][j][r + e];
+            }
+          }
+        }
+    }
+    return;
+  }
+
+  // bf16 output through LDS: each wave stages 32 tokens row-major and stores whole 16-byte row pieces. A
+  // row of y starts (m N) mod 8 elements past a 16-byte address; it is staged with that shift, so
+  // that whole pieces stay aligned on both sides.
+  __syncthreads();
+  constexpr int kCols = 32 * TN, kPieces = kCols / 8, kPitch = kCols + 8;
+  uint16_t* stage = reinterpret_cast<uint16_t*>(smem + wave * (32 * kPitch * 2));
+  const int shift = (l32 * N) & 7;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; r += 4) {
+        const int c = 32 * j + 2 * r + 4 * h;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = acc[i][j][r + e];
+          if (a.bias != nullptr) v[e] += n_w + c + e < N ? bf16lo_to_f32(a.bias[n_w + c + e]) : 0.0f;
+        }
+        uint16_t* dst = stage + l32 * kPitch + shift + c;
+        const uint32_t w0 = pack_bf16x2(v[0], v[1]), w1 = pack_bf16x2(v[2], v[3]);
+        if (N % 4 == 0) {
+          *reinterpret_cast<u32x2*>(dst) = u32x2{w0, w1};
+        } else {
+          dst[0] = (uint16_t)w0;
+          dst[1] = (uint16_t)(w0 >> 16);
+          dst[2] = (uint16_t)w1;
+          dst[3] = (uint16_t)(w1 >> 16);
+        }
+      }
+    __syncthreads();
+    const int cols = min(kCols, N - n_w);
+    if (N % 8 == 0) {
+#pragma unroll
+      for (int u = 0; u < 32 * kPieces / 64; ++u) {
+        const int idx = lane + 64 * u;
+        const int row = idx / kPieces, c = 8 * (idx % kPieces);
+        const int m = m_w + 32 * i + row;
+        if (m < M && c < cols)
+          *reinterpret_cast<u32x4*>(a.y + (size_t)m * (size_t)N + n_w + c) =
+              *reinterpret_cast<const u32x4*>(stage + row * kPitch + c);
+      }
+    } else {   // a piece more per row, the first and the last one by elements
+      for (int idx = lane; idx < 32 * (kPieces + 1); idx += 64) {
+        const int row = idx / (kPieces + 1), m = m_w + 32 * i + row;
+        const int sh = (row * N) & 7, c = 8 * (idx % (kPieces + 1)) - sh;
+        if (m >= M || c >= cols) continue;
+        uint16_t* dst = a.y + (size_t)m * (size_t)N + n_w;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(stage + row * kPitch + sh + c);
+        if (c >= 0 && c + 8 <= cols) {
+          *reinterpret_cast<u32x4*>(dst + c) = v;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (c + e >= 0 && c + e < cols) dst[c + e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Ends a split product: the partial sums in split order, bias, bf16; W channels per thread, 4 where
+// that divides N, else 1 (M * N stays below 2^31: a split has at most 1024 workgroups).
+template <int W>
+__global__ __launch_bounds__(256) void fp8_reduce_kernel(Fp8GemmArgs a, const float* __restrict__ partial, int splits) {
+  const uint32_t per_row = (uint32_t)a.N / W;
+  const uint32_t id = blockIdx.x * 256u + threadIdx.x;
+  const uint32_t m = id / per_row, n = W * (id % per_row);
+  if (m >= (uint32_t)a.M) return;
+  const size_t mn = (size_t)a.M * (size_t)a.N, at = (size_t)m * (size_t)a.N + n;
+  if constexpr (W == 4) {
+    f32x4 s = *reinterpret_cast<const f32x4*>(partial + at);
+    for (int i = 1; i < splits; ++i) s += *reinterpret_cast<const f32x4*>(partial + (size_t)i * mn + at);
+    u32x2 b = {0u, 0u};
+    if (a.bias != nullptr) b = *reinterpret_cast<const u32x2*>(a.bias + n);
+    *reinterpret_cast<u32x2*>(a.y + at) =
+        u32x2{pack_bf16x2(s[0] + bf16lo_to_f32(b[0]), s[1] + bf16hi_to_f32(b[0])),
+              pack_bf16x2(s[2] + bf16lo_to_f32(b[1]), s[3] + bf16hi_to_f32(b[1]))};
+  } else {
+    float s = partial[at];
+    for (int i = 1; i < splits; ++i) s += partial[(size_t)i * mn + at];
+    a.y[at] = (uint16_t)f32_to_bf16_rne(a.bias != nullptr ? s + bf16lo_to_f32(a.bias[n]) : s);
+  }
+}
+
+// Few tokens (M <= 16 MT): bound by the weight's bytes, which stream past the tokens once, straight
+// from memory. A workgroup takes 16 output channels, its eight waves share k in blocks of 128;
+// v_mfma_f32_16x16x128_f8f6f4 with the weight rows as A and the tokens as B, and the waves' sums
+// meet in LDS. FROM_X: the activations come as x; a block's maximum lies within the 32 channels of
+// four lanes, so every wave makes its own operands in registers.
+constexpr int kFewWaves = 8;
+
+template <int MT, int LEAD, bool FROM_X, bool SMOOTH>
+__global__ __launch_bounds__(64 * kFewWaves) void gemm_fp8_few_kernel(Fp8GemmArgs a, const uint16_t* __restrict__ x,
+                                                                     const uint16_t* __restrict__ smooth) {
+  __shared__ f32x4 part[kFewWaves][MT][64];
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = tid & 63;
+  const int q = lane >> 4, l16 = lane & 15;
+  const int M = (int)a.M, N = (int)a.N, K = (int)a.K;
+  const int KB = (K + 127) / 128;
+  const int n0 = (int)blockIdx.x * 16;
+  // a lane's operand: pieces q and q + 4 of the row's eight 16-byte pieces; K % 16 == 0, so a piece is
+  // entirely before or past K, and zero past it
+  const uint8_t* pw = a.weight + (size_t)min(n0 + l16, N - 1) * K + 16 * q;
+  auto codes_at = [&](const uint8_t* row, int p) {
+    const i32x4 zero = {};
+    const int k = 128 * p + 16 * q;
+    return join8(k < K ? *reinterpret_cast<const i32x4*>(row + 128 * p) : zero,
+                 k + 64 < K ? *reinterpret_cast<const i32x4*>(row + 128 * p + 64) : zero);
+  };
+  const float* ws = a.wscales + (size_t)(n0 / 128) * KB;
+  i32x8 fw[LEAD];
+#pragma unroll
+  for (int u = 0; u < LEAD; ++u) fw[u] = codes_at(pw, wave + kFewWaves * u);
+
+  f32x4 acc[MT] = {};
+  for (int p = wave; p < KB; p += kFewWaves * LEAD) {
+#pragma unroll
+    for (int u = 0; u < LEAD; ++u) {
+      const int pu = p + kFewWaves * u;
+      const float wsu = ws[min(pu, KB - 1)];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const int m = min(16 * t + l16, M - 1);
+        i32x8 ft;
+        float as;
+        if constexpr (FROM_X) {
+          float v[4][8], amax = 0.0f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int k = 128 * pu + 64 * (c >> 1) + 16 * q + 8 * (c & 1);
+            const bool in = k < K;
+            f8_scaled8<SMOOTH>(in ? *reinterpret_cast<const u32x4*>(x + (size_t)m * K + k) : zero4(),
+                               SMOOTH && in ? *reinterpret_cast<const u32x4*>(smooth + k) : zero4(), v[c]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) amax = max_or_nan(amax, fabsf(v[c][e]));
+          }
+          amax = max_or_nan(amax, __shfl_xor(amax, 16));
+          amax = max_or_nan(amax, __shfl_xor(amax, 32));
+          const Fp8Scale s = fp8_scale(amax);
+          as = s.scale;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const u32x2 w = fp8_codes8(v[c], s.inv);
+            ft[2 * c] = (int)w[0];
+            ft[2 * c + 1] = (int)w[1];
+          }
+        } else {
+          ft = codes_at(a.codes + (size_t)m * K + 16 * q, pu);
+          as = a.ascales[(size_t)min(pu, KB - 1) * M + m];
+        }
+        const f32x4 sum = f8_mfma16(fw[u], ft, f32x4{});
+        const float s = pu < KB ? as * wsu : 0.0f;
+        if (pu < KB) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[t][r] = __builtin_fmaf(sum[r], s, acc[t][r]);
+        }
+      }
+      fw[u] = codes_at(pw, pu + kFewWaves * LEAD);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t) part[wave][t][lane] = acc[t];
+  __syncthreads();
+  // wave t ends token group t: lane l holds token l % 16, channels 4 (l / 16) .. + 3
+  if (wave < MT) {
+    f32x4 s = part[0][wave][lane];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) s += part[w][wave][lane];
+    const int m = 16 * wave + l16;
+    if (m < M) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int n = n0 + 4 * q + r;
+        if (n < N) {
+          const float b = a.bias != nullptr ? bf16lo_to_f32(a.bias[n]) : 0.0f;
+          a.y[(size_t)m * (size_t)N + n] = (uint16_t)f32_to_bf16_rne(s[r] + b);
+        }
+      }
+    }
+  }
+}
+
+template <int MT, int LEAD>
+hipError_t launch_few_cfg(const Fp8GemmArgs& a, const uint16_t* x, const uint16_t* smooth, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.N + 15) / 16)), block(64 * kFewWaves);
+  if (x == nullptr)
+    hipLaunchKernelGGL((gemm_fp8_few_kernel<MT, LEAD, false, false>), grid, block, 0, stream, a, x, smooth);
+  else if (smooth == nullptr)
+    hipLaunchKernelGGL((gemm_fp8_few_kernel<MT, LEAD, true, false>), grid, block, 0, stream, a, x, smooth);
+  else
+    hipLaunchKernelGGL((gemm_fp8_few_kernel<MT, LEAD, true, true>), grid, block, 0, stream, a, x, smooth);
+  return hipGetLastError();
+}
+
+hipError_t launch_few(const Fp8GemmArgs& a, const uint16_t* x, const uint16_t* smooth, hipStream_t stream) {
+  return launch_few_cfg<1, 4>(a, x, smooth, stream);
+}
+
+bool few_tokens(int64_t M, int64_t, int64_t) { return M <= 16; }
+bool few_from_x(int64_t M, int64_t N, int64_t K) { return few_tokens(M, N, K); }
+
+struct F8Plan {
+  int shape;     // index into the table
+  int splits, panels;
+};
+
+F8Plan plan_fp8(int64_t M, int64_t N, int64_t K) {
+  const int64_t panels = (K + 127) / 128;
+  const int shape = M > 1024 ? 0 : M > 64 ? 1 : 2;
+  static const int bm[] = {256, 128, 64}, bn[] = {256, 128, 64};
+  const int64_t tiles = ((M + bm[shape] - 1) / bm[shape]) * ((N + bn[shape] - 1) / bn[shape]);
+  int64_t sp = 1;
+  while (sp < 8 && tiles * sp * 2 <= 512 && panels >= 4 * sp) sp *= 2;
+  const int64_t per = (panels + sp - 1) / sp;
+  return F8Plan{shape, (int)((panels + per - 1) / per), (int)per};
+}
+
+template <int WM, int WN, int TM, int TN, int S>
+hipError_t launch_fp8_cfg(const Fp8GemmArgs& a, const F8Split& sp, hipStream_t stream) {
+  using C = F8Cfg<WM, WN, TM, TN, S>;
+  static std::atomic<uint64_t> lds_set{0};
+  const void* fn = reinterpret_cast<const void*>(&gemm_fp8_kernel<WM, WN, TM, TN, S>);
+  hipError_t e = set_lds_limit_once(fn, C::kLdsBytes, lds_set);
+  if (e != hipSuccess) return e;
+  const int64_t tiles = ((a.N + C::BN - 1) / C::BN) * ((a.M + C::BM - 1) / C::BM) * sp.splits;
+  const dim3 grid((unsigned)((tiles + 7) / 8 * 8));
+  hipLaunchKernelGGL((gemm_fp8_kernel<WM, WN, TM, TN, S>), grid, dim3(64 * C::kWaves), C::kLdsBytes, stream, a, sp);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quant_fp8(const uint16_t* x, const uint16_t* smooth, int64_t M, int64_t K, uint8_t* codes,
+                            float* ascales, hipStream_t stream) {
+  const int64_t blocks = M * ((K + 127) / 128);
+  constexpr int U = 4;
+  const dim3 grid((unsigned)((blocks + 16 * U - 1) / (16 * U)));
+  if (smooth != nullptr)
+    hipLaunchKernelGGL((quant_fp8_kernel<true, U>), grid, dim3(256), 0, stream, x, smooth, (uint32_t)M, (uint32_t)K, codes, ascales);
+  else
+    hipLaunchKernelGGL((quant_fp8_kernel<false, U>), grid, dim3(256), 0, stream, x, smooth, (uint32_t)M, (uint32_t)K, codes, ascales);
+  return hipGetLastError();
+}
+
+hipError_t launch_quant_weight_fp8(const uint16_t* w, const uint16_t* smooth, int64_t N, int64_t K, uint8_t* codes,
+                                   float* wscales, hipStream_t stream) {
+  const dim3 grid((unsigned)((K + 127) / 128), (unsigned)((N + 127) / 128));
+  if (smooth != nullptr)
+    hipLaunchKernelGGL(quant_weight_fp8_kernel<true>, grid, dim3(256), 0, stream, w, smooth, (int)N, (int)K, codes, wscales);
+  else
+    hipLaunchKernelGGL(quant_weight_fp8_kernel<false>, grid, dim3(256), 0, stream, w, smooth, (int)N, (int)K, codes, wscales);
+  return hipGetLastError();
+}
+
+size_t gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (few_tokens(M, N, K)) return 0;
+  const F8Plan p = plan_fp8(M, N, K);
+  return p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)N * 4 : 0;
+}
+
+void gemm_fp8_plan(int64_t M, int64_t N, int64_t K, int* tile, int* splits) {
+  const bool few = few_tokens(M, N, K);
+  const F8Plan p = few ? F8Plan{-1, 1, 0} : plan_fp8(M, N, K);
+  *tile = p.shape;
+  *splits = p.splits;
+}
+
+hipError_t launch_gemm_fp8(const Fp8GemmArgs& a, void* workspace, hipStream_t stream) {
+  if (few_tokens(a.M, a.N, a.K)) return launch_few(a, nullptr, nullptr, stream);
+  const F8Plan p = plan_fp8(a.M, a.N, a.K);
+  const F8Split sp{p.panels, p.splits, static_cast<float*>(workspace)};
+  hipError_t e = p.shape == 0   ? launch_fp8_cfg<4, 2, 2, 4, 2>(a, sp, stream)
+                 : p.shape == 1 ? launch_fp8_cfg<2, 2, 2, 2, 2>(a, sp, stream)
+                                : launch_fp8_cfg<2, 2, 1, 1, 2>(a, sp, stream);
+  if (e != hipSuccess || p.splits == 1) return e;
+  const int w = a.N % 4 == 0 ? 4 : 1;
+  const dim3 grid((unsigned)((a.M * (a.N / w) + 255) / 256));
+  if (w == 4) hipLaunchKernelGGL(fp8_reduce_kernel<4>, grid, dim3(256), 0, stream, a, sp.partial, p.splits);
+  else hipLaunchKernelGGL(fp8_reduce_kernel<1>, grid, dim3(256), 0, stream, a, sp.partial, p.splits);
+  return hipGetLastError();
+}
+
+size_t linear_fp8_codes_bytes(int64_t M, int64_t N, int64_t K) {
+  return few_from_x(M, N, K) ? 0 : (size_t)M * (size_t)K;
+}
+
+hipError_t launch_linear_fp8(const Fp8GemmArgs& a, const uint16_t* x, const uint16_t* smooth, uint8_t* codes,
+                             float* ascales, void* workspace, hipStream_t stream) {
+  if (few_from_x(a.M, a.N, a.K)) return launch_few(a, x, smooth, stream);
+  hipError_t e = launch_quant_fp8(x, smooth, a.M, a.K, codes, ascales, stream);
+  if (e != hipSuccess) return e;
+  Fp8GemmArgs g = a;
+  g.codes = codes;
+  g.ascales = ascales;
+  return launch_gemm_fp8(g, workspace, stream);
+}
+
+}  // namespace svdq

@@ -178,6 +178,32 @@ size_t linear_int8_codes_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_linear_int8(const Int8GemmArgs& a, const uint16_t* x, const uint16_t* smooth, int8_t* codes,
                               float* ascales, void* workspace, hipStream_t stream);
 
+// Linear in 8-bit floating point: e4m3 codes and fp32 scales of x * smooth per 128 channels, and
+// y = bf16(sum_p ascales[p, m] * wscales[n / 128, p] * (codes @ weight^T over block p) + bias).
+// K % 16 == 0, K <= kFp8MaxK; M * ceil(K / 128) < 2^31 for the quantisation.
+constexpr int64_t kFp8MaxK = int64_t(1) << 20;
+hipError_t launch_quant_fp8(const uint16_t* x, const uint16_t* smooth, int64_t M, int64_t K, uint8_t* codes,
+                            float* ascales, hipStream_t stream);
+hipError_t launch_quant_weight_fp8(const uint16_t* w, const uint16_t* smooth, int64_t N, int64_t K, uint8_t* codes,
+                                   float* wscales, hipStream_t stream);
+struct Fp8GemmArgs {
+  const uint8_t* codes;    // [M, K]
+  const float* ascales;    // [ceil(K / 128), M]
+  const uint8_t* weight;   // [N, K]
+  const float* wscales;    // [ceil(N / 128), ceil(K / 128)]
+  const uint16_t* bias;    // [N] or NULL
+  uint16_t* y;             // [M, N]
+  int64_t M, N, K;
+};
+hipError_t launch_gemm_fp8(const Fp8GemmArgs& a, void* workspace, hipStream_t stream);
+size_t gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+void gemm_fp8_plan(int64_t M, int64_t N, int64_t K, int* tile, int* splits);   // tile -1: few tokens
+// As for the 8-bit integer layer: codes and scales, then the product; one launch where
+// linear_fp8_codes_bytes(M, N, K) is 0.
+size_t linear_fp8_codes_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_linear_fp8(const Fp8GemmArgs& a, const uint16_t* x, const uint16_t* smooth, uint8_t* codes,
+                             float* ascales, void* workspace, hipStream_t stream);
+
 // Norms around a block: h_out = h + rs * gate[g] * rms(block, post), and
 // x_out = rms(h_out, pre) * (1 + scale[g]) in bf16 or, with codes, in int8 with
 // a scale per row. Optional pointers may be NULL (svdq.h, svdq_norm_gated).
@@ -222,6 +248,21 @@ struct RopeArgs {
 };
 hipError_t launch_rope(const RopeArgs& a, int D, bool interleaved, hipStream_t stream);
 
+// Rotary positions on the first R elements of heads of D (R, D multiples of 8, D <= 256): cos and sin times
+// `amplitude`; the rest is copied (copy) or, in place, left alone.
+struct RopeScaledArgs {
+  HeadView in[2];          // q, k
+  uint16_t* out[2];
+  int64_t out_st[2], out_sh[2];
+  int H[2];
+  const int32_t* positions;  // [T]
+  int64_t T;
+  int D, R, copy;
+  float amplitude;
+  double turns[128];         // per pair: its frequency in turns
+};
+hipError_t launch_rope_scaled(const RopeScaledArgs& a, bool interleaved, hipStream_t stream);
+
 // Attention over packed sequences.
 struct AttnArgs {
   HeadView q, k, v;
@@ -233,6 +274,49 @@ struct AttnArgs {
   float scale;
 };
 hipError_t launch_attention(const AttnArgs& a, int D, hipStream_t stream);
+
+// A cache of keys [pages, Hk, P, D] and values [pages, Hk, D, P] in e4m3 with an exponent byte per page and head
+// (cache.hip), P = 1 << lg_page tokens.
+constexpr int kMaxPage = 128;
+struct CacheShape {
+  uint8_t *k, *v, *ks, *vs;
+  int64_t pages;
+  int Hk, lg_page, D;
+};
+// Packed tokens of B sequences and where they lie in the cache: sequence b's first is token starts[b] of it, in
+// the page table[b, starts[b] / P].
+struct CacheTokens {
+  const int32_t* table;    // [B, width]
+  const int32_t* starts;   // [B]
+  const int32_t* cu;       // [B + 1], or NULL: one token each
+  int64_t T, width;
+  int B;
+};
+hipError_t launch_cache_append(const CacheTokens& a, const CacheShape& c, const HeadView& k, const HeadView& v,
+                               hipStream_t stream);
+hipError_t launch_cache_read(const CacheTokens& a, const CacheShape& c, uint16_t* k_out, uint16_t* v_out,
+                             hipStream_t stream);
+
+// Attention over such a cache: queries packed as in AttnArgs (cu NULL: one each), keys 0 .. lengths[b] - 1 of
+// sequence b; causal: its queries are the last of them. partial: attention_cache_workspace_bytes(...).
+struct AttnCacheArgs {
+  HeadView q;
+  uint16_t* o;
+  int64_t o_st, o_sh;
+  CacheShape c;
+  const int32_t* table;    // [B, width]
+  const int32_t* lengths;  // [B]
+  const int32_t* cu;       // [B + 1] or NULL
+  int64_t T, width;
+  int B, H, causal;
+  float scale;
+  // the keys of a sequence are shared among `splits` workgroups, whole tiles of 64 each, at least `least`
+  int splits, least;
+  float* partial;          // [splits, T * H, D], then [splits, T * H, 2]: maximum and sum
+};
+size_t attention_cache_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_length,
+                                       bool packed);
+hipError_t launch_attention_cache(AttnCacheArgs a, int64_t max_length, hipStream_t stream);
 
 // Measurement helpers (not part of the layer): sustained f16 matrix-instruction
 // rate on a caller-filled operand table of calib_table_bytes() bytes, with the

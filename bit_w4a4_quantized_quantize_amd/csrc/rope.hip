@@ -191,7 +191,113 @@ void launch_rope_cfg(const RopeArgs& a, hipStream_t s) {
   else hipLaunchKernelGGL((rope_kernel<D, INTER, false, false>), grid, block, lds, s, a, (int)per, by_heads);
 }
 
+// Rotary positions on the first R elements of any head size, one position per token. A workgroup takes `per` whole
+// tokens (one token in several passes, where that has more than 512 pieces): loads first, then the tokens' angles
+// in LDS, once for all heads. A piece is 8 elements: of the turned part, 8 consecutive ones
+// (interleaved) or 4 of each half; then, out of place, the rest 8 at a time. Memory bound.
+// by_heads, by_pieces: 2^32 / heads and / pieces of a head, rounded up (exact quotients below 2^16).
+template <bool INTER>
+__global__ __launch_bounds__(kThreadsR) void rope_scaled_kernel(RopeScaledArgs a, int per, uint32_t by_heads,
+                                                                uint32_t by_pieces) {
+  extern __shared__ __attribute__((aligned(16))) float turn[];   // per token and pair: cos and sin
+  const int tid = threadIdx.x;
+  const int64_t t0 = (int64_t)blockIdx.x * per;
+  const int here = (int)min((int64_t)per, a.T - t0);
+  const int heads = a.H[0] + a.H[1], half = a.R / 2;
+  const int turned = a.R / 8, pieces = a.copy ? a.D / 8 : turned;
+  const int token_items = heads * pieces, items = here * token_items;
+
+  for (int first = 0; first < items; first += kItems * kThreadsR) {
+    u32x2 lo[kItems], hi[kItems];
+    int tok[kItems], piece[kItems];
+    uint16_t* dst[kItems];
+#pragma unroll
+    for (int u = 0; u < kItems; ++u) {
+      const int it = min(first + u * kThreadsR + tid, items - 1);   // clamped: read, not stored
+      const int n = pieces == 1 ? it : (int)__umulhi((uint32_t)it, by_pieces);
+      piece[u] = it - n * pieces;
+      tok[u] = heads == 1 ? n : (int)__umulhi((uint32_t)n, by_heads);
+      const int head_all = n - tok[u] * heads;
+      const bool is_k = head_all >= a.H[0];
+      const int head = is_k ? head_all - a.H[0] : head_all;
+      const int64_t t = t0 + tok[u];
+      const HeadView in = is_k ? a.in[1] : a.in[0];
+      const uint16_t* src = in.p + t * in.st + head * in.sh;
+      dst[u] = (is_k ? a.out[1] : a.out[0]) + t * (is_k ? a.out_st[1] : a.out_st[0]) +
+               head * (is_k ? a.out_sh[1] : a.out_sh[0]);
+      if (INTER || piece[u] >= turned) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(src + 8 * piece[u]);
+        lo[u] = u32x2{w[0], w[1]};
+        hi[u] = u32x2{w[2], w[3]};
+      } else {
+        lo[u] = *reinterpret_cast<const u32x2*>(src + 4 * piece[u]);
+        hi[u] = *reinterpret_cast<const u32x2*>(src + half + 4 * piece[u]);
+      }
+    }
+    if (first == 0) {
+      for (int i = tid; i < here * half; i += kThreadsR) {
+        const int k = i / half, p = i - k * half;
+        const double x = (double)a.positions[t0 + k] * a.turns[p];
+        float s, c;
+        sincospif(2.0f * (float)(x - __builtin_rint(x)), &s, &c);
+        reinterpret_cast<float2*>(turn)[i] = make_float2(a.amplitude * c, a.amplitude * s);
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int u = 0; u < kItems; ++u) {
+      const bool stored = first + u * kThreadsR + tid < items;
+      if (piece[u] >= turned) {
+        if (stored)
+          __builtin_nontemporal_store(u32x4{lo[u][0], lo[u][1], hi[u][0], hi[u][1]},
+                                      reinterpret_cast<u32x4*>(dst[u] + 8 * piece[u]));
+        continue;
+      }
+      float v[8], o[8];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        v[2 * i] = bf16lo_to_f32(lo[u][i]);
+        v[2 * i + 1] = bf16hi_to_f32(lo[u][i]);
+        v[4 + 2 * i] = bf16lo_to_f32(hi[u][i]);
+        v[5 + 2 * i] = bf16hi_to_f32(hi[u][i]);
+      }
+      const float2* f = reinterpret_cast<const float2*>(turn) + tok[u] * half + 4 * piece[u];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int x = INTER ? 2 * i : i, y = INTER ? 2 * i + 1 : 4 + i;
+        const float2 cs = f[i];
+        o[x] = v[x] * cs.x - v[y] * cs.y;
+        o[y] = v[y] * cs.x + v[x] * cs.y;
+      }
+      if (!stored) continue;
+      const u32x2 w0 = {pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
+      const u32x2 w1 = {pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])};
+      if (INTER) {
+        __builtin_nontemporal_store(u32x4{w0[0], w0[1], w1[0], w1[1]}, reinterpret_cast<u32x4*>(dst[u] + 8 * piece[u]));
+      } else {
+        __builtin_nontemporal_store(w0, reinterpret_cast<u32x2*>(dst[u] + 4 * piece[u]));
+        __builtin_nontemporal_store(w1, reinterpret_cast<u32x2*>(dst[u] + half + 4 * piece[u]));
+      }
+    }
+  }
+}
+
 }  // namespace
+
+hipError_t launch_rope_scaled(const RopeScaledArgs& a, bool interleaved, hipStream_t stream) {
+  const int heads = a.H[0] + a.H[1], pieces = a.copy ? a.D / 8 : a.R / 8;
+  const int64_t full = kItems * kThreadsR / ((int64_t)heads * pieces);
+  int64_t per = full < 1 ? 1 : full > kMaxTokens ? kMaxTokens : full;
+  while (per > 1 && (a.T + per - 1) / per < 1024) per /= 2;
+  const dim3 grid((unsigned)((a.T + per - 1) / per)), block(kThreadsR);
+  auto by = [](int n) { return (uint32_t)(((uint64_t(1) << 32) + n - 1) / n); };
+  const unsigned lds = (unsigned)(per * a.R * 4);   // at most 16 KB
+  if (interleaved)
+    hipLaunchKernelGGL(rope_scaled_kernel<true>, grid, block, lds, stream, a, (int)per, by(heads), by(pieces));
+  else
+    hipLaunchKernelGGL(rope_scaled_kernel<false>, grid, block, lds, stream, a, (int)per, by(heads), by(pieces));
+  return hipGetLastError();
+}
 
 hipError_t launch_rope(const RopeArgs& a, int D, bool interleaved, hipStream_t stream) {
   if (D == 64) {

@@ -975,3 +975,268 @@ def attention_packed(q, k, v, cu_seqlens=None, causal=False, scale=None, out=Non
     _launch("svdq_attention_packed", q.device, *qa, *ka, *va, _p(cu_seqlens), B, T, H, Hk, D, 1 if causal else 0,
             scale if scale is not None else D ** -0.5 if D > 0 else 1.0, *oa)   # D = 0 is refused there
     return out
+
+
+def _blocks128(n):
+    return -(-n // 128)
+
+
+def _quantize_fp8(name, entry, x, smooth, codes, scales, weight):
+    _need(x, name, torch.bfloat16, 2)
+    M, K = x.shape
+    _k_ok(K)
+    if smooth is not None:
+        _need(smooth, "smooth", torch.bfloat16, shape=(K,))
+    shape = (_blocks128(M), _blocks128(K)) if weight else (_blocks128(K), M)
+    if codes is None:
+        codes = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    else:
+        _need(codes, "codes", torch.float8_e4m3fn, shape=(M, K))
+    if scales is None:
+        scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+    else:
+        _need(scales, "scales", torch.float32, shape=shape)
+    _on_one_device(x.get_device(), smooth=smooth, codes=codes, scales=scales, **{name: x})
+    _launch(entry, x.device, _p(x), _p(smooth), M, K, _p(codes), _p(scales))
+    return codes, scales
+
+
+def quantize_fp8(x, smooth=None, codes=None, scales=None):
+    """e4m3 codes of activations with a scale per 128 channels of a token: v = x * smooth, the scale the
+    least power of two 2^e (e >= -100) with max |v| <= 448 * 2^e, codes = v / scale to nearest even. x [M, K] bf16,
+    smooth [K] bf16 or None. Returns (codes float8_e4m3fn [M, K], scales float32 [ceil(K / 128), M])."""
+    return _quantize_fp8("x", "svdq_quantize_fp8", x, smooth, codes, scales, False)
+
+
+def quantize_weight_fp8(w, smooth=None, codes=None, scales=None):
+    """The same for a weight w [N, K] bf16, with a scale per block of 128 x 128 (smooth = 1 / the layer's
+    smooth). Returns (codes float8_e4m3fn [N, K], scales float32 [ceil(N / 128), ceil(K / 128)])."""
+    return _quantize_fp8("w", "svdq_quantize_weight_fp8", w, smooth, codes, scales, True)
+
+
+def _check_fp8_weight(weight, wscales, bias, K):
+    _need(weight, "weight", torch.float8_e4m3fn, 2)
+    N = weight.shape[0]
+    if weight.shape[1] != K:
+        raise ValueError(f"the activations have K={K}, weight has K={weight.shape[1]}")
+    _need(wscales, "wscales", torch.float32, shape=(_blocks128(N), _blocks128(K)))
+    if bias is not None:
+        _need(bias, "bias", torch.bfloat16, shape=(N,))
+    return N
+
+
+def gemm_fp8_workspace_bytes(M, N, K):
+    """Scratch bytes gemm_fp8 needs."""
+    return _lib.lib().svdq_gemm_fp8_workspace_bytes(M, N, K)
+
+
+def gemm_fp8_plan(M, N, K):
+    """How gemm_fp8 runs a size (tests and tuning): (tile, ways k is split), tile as in svdq.h or -1 for the
+    kernel for few tokens."""
+    tile, splits = ctypes.c_int(0), ctypes.c_int(0)
+    _lib.check("svdq_gemm_fp8_plan", _lib.lib().svdq_gemm_fp8_plan(M, N, K, ctypes.byref(tile), ctypes.byref(splits)))
+    return tile.value, splits.value
+
+
+def linear_fp8_workspace_bytes(M, N, K):
+    """Scratch bytes linear_fp8 needs."""
+    return _lib.lib().svdq_linear_fp8_workspace_bytes(M, N, K)
+
+
+def gemm_fp8(codes, ascales, weight, wscales, bias=None, y=None, workspace=None):
+    """y [M, N] bf16 = codes @ weight^T, each block of 128 channels p times ascales[p, m] *
+    wscales[n // 128, p], + bias: codes float8_e4m3fn [M, K] and ascales float32 [ceil(K / 128), M] (quantize_fp8),
+    weight float8_e4m3fn [N, K] and wscales float32 [ceil(N / 128), ceil(K / 128)] (quantize_weight_fp8, or any
+    others), bias bf16 [N] or None."""
+    _need(codes, "codes", torch.float8_e4m3fn, 2)
+    M, K = codes.shape
+    _k_ok(K)
+    _need(ascales, "ascales", torch.float32, shape=(_blocks128(K), M))
+    N = _check_fp8_weight(weight, wscales, bias, K)
+    dev = codes.device
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(y, "y", torch.bfloat16, shape=(M, N))
+    workspace, ws_bytes = _workspace(workspace, gemm_fp8_workspace_bytes(M, N, K), dev)
+    _on_one_device(codes.get_device(), codes=codes, ascales=ascales, weight=weight, wscales=wscales, bias=bias, y=y,
+                   workspace=workspace)
+    _launch("svdq_gemm_fp8", dev, _p(codes), _p(ascales), _p(weight), _p(wscales), _p(bias), M, N, K, _p(y),
+            _p(workspace), ws_bytes)
+    return y
+
+
+def linear_fp8(x, weight, wscales, bias=None, smooth=None, y=None, workspace=None):
+    """The whole linear in 8-bit floating point: quantize_fp8(x, smooth), then gemm_fp8. x [M, K] bf16,
+    weight float8_e4m3fn [N, K], wscales float32 [ceil(N / 128), ceil(K / 128)]; returns y [M, N] bf16."""
+    _need(x, "x", torch.bfloat16, 2)
+    M, K = x.shape
+    _k_ok(K)
+    N = _check_fp8_weight(weight, wscales, bias, K)
+    if smooth is not None:
+        _need(smooth, "smooth", torch.bfloat16, shape=(K,))
+    dev = x.device
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(y, "y", torch.bfloat16, shape=(M, N))
+    workspace, ws_bytes = _workspace(workspace, linear_fp8_workspace_bytes(M, N, K), dev)
+    _on_one_device(x.get_device(), x=x, smooth=smooth, weight=weight, wscales=wscales, bias=bias, y=y,
+                   workspace=workspace)
+    _launch("svdq_linear_fp8", dev, _p(x), _p(smooth), _p(weight), _p(wscales), _p(bias), M, N, K, _p(y),
+            _p(workspace), ws_bytes)
+    return y
+
+
+def rope_scaled(q, k, positions, rotary_dim=None, theta=10000.0, interleaved=False, factor=1.0, original_length=0,
+                low_rotations=1.0, high_rotations=32.0, amplitude=1.0, q_out=None, k_out=None):
+    """Rotary positions on the first rotary_dim elements of each head (default: all), with frequencies scaled
+    for contexts longer than trained on, for q [T, H, D] and k [T, Hk, D] (bf16 views with any token and head strides;
+    either may be None); positions int32 [T]. Frequencies f_i = theta^(-2i / rotary_dim): with original_length 0
+    all of them divided by `factor`; else by parts: those that turn at most low_rotations times within
+    original_length are divided by it, those that turn high_rotations times or more are kept, between them a
+    linear mix. cos and sin are taken times `amplitude`. interleaved: pairs are neighbours, else
+    halves of the rotary_dim. D and rotary_dim multiples of 8, D <= 256. q_out / k_out may be q / k themselves (in
+    place); new ones are laid out like their input. Returns (q_out, k_out)."""
+    if q is None and k is None:
+        raise ValueError("q or k is required")
+    given = q if q is not None else k
+    qa, ka, qoa, koa, H, Hk = _NO_HEADS, _NO_HEADS, _NO_HEADS, _NO_HEADS, 0, 0
+    if q is not None:
+        qa = _need_heads(q, "q")
+        H = q.shape[1]
+    if k is not None:
+        ka = _need_heads(k, "k")
+        Hk = k.shape[1]
+    T, _, D = given.shape
+    if q is not None and k is not None and (k.shape[0] != T or k.shape[2] != D):
+        raise ValueError(f"k must have shape {[T, Hk, D]}, got {list(k.shape)}")
+    _need(positions, "positions", torch.int32, shape=(T,))
+    if q is not None:
+        q_out = torch.empty_like(q) if q_out is None else q_out
+        qoa = _need_heads(q_out, "q_out", q.shape)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    if k is not None:
+        k_out = torch.empty_like(k) if k_out is None else k_out
+        koa = _need_heads(k_out, "k_out", k.shape)
+    elif k_out is not None:
+        raise ValueError("k_out needs k")
+    _on_one_device(given.get_device(), q=q, k=k, positions=positions, q_out=q_out, k_out=k_out)
+    _launch("svdq_rope_scaled", given.device, *qa, H, *ka, Hk, positions.data_ptr(),
+            D if rotary_dim is None else rotary_dim, theta, factor, original_length, low_rotations, high_rotations,
+            amplitude, 1 if interleaved else 0, T, D, *qoa, *koa)
+    return q_out, k_out
+
+
+@dataclass
+class Fp8Cache:
+    """Keys and values in pages, in e4m3 with a power-of-two scale per page and head: k_codes
+    [pages, Hk, page, D] and v_codes [pages, Hk, D, page] (elements first: a page's tokens are contiguous
+    there) float8_e4m3fn, k_scales and v_scales uint8 [pages, Hk], value = code * 2^(scale - 127), 255 NaN.
+    page: 16, 32, 64 or 128 tokens; D: 64 or 128. A sequence's pages are listed in a block table, int32
+    [B, width]: token t is in page table[b, t // page], slot t % page. What a slot holds that no token was
+    appended to is never used."""
+    k_codes: torch.Tensor
+    v_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_scales: torch.Tensor
+
+
+def new_cache_fp8(pages, heads, head_dim, page=64, device="cuda"):
+    """An empty Fp8Cache of `pages` pages of `page` tokens for `heads` key heads (its contents are not initialised)."""
+    return Fp8Cache(torch.empty((pages, heads, page, head_dim), dtype=torch.float8_e4m3fn, device=device),
+                    torch.empty((pages, heads, head_dim, page), dtype=torch.float8_e4m3fn, device=device),
+                    torch.empty((pages, heads), dtype=torch.uint8, device=device),
+                    torch.empty((pages, heads), dtype=torch.uint8, device=device))
+
+
+def _check_cache(cache, block_table, lengths, lengths_name, cu_seqlens):
+    """The checked cache, tables and sequence count as the C ABI takes them: (cache arguments ..., D),
+    (table, width, lengths, cu_seqlens, B), and the cache's shape (pages, Hk, page, D)."""
+    kc, vc, ks, vs = cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales
+    _need(kc, "k_codes", torch.float8_e4m3fn, 4)
+    shape = kc.shape
+    pages, Hk, page, D = shape
+    _need(vc, "v_codes", torch.float8_e4m3fn, shape=(pages, Hk, D, page))
+    _need(ks, "k_scales", torch.uint8, shape=(pages, Hk))
+    _need(vs, "v_scales", torch.uint8, shape=(pages, Hk))
+    _need(block_table, "block_table", torch.int32, 2)
+    B, width = block_table.shape
+    _need(lengths, lengths_name, torch.int32, shape=(B,))
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, shape=(B + 1,))
+    _on_one_device(kc.get_device(), k_codes=kc, v_codes=vc, k_scales=ks, v_scales=vs, block_table=block_table,
+                   cu_seqlens=cu_seqlens, **{lengths_name: lengths})
+    return ((kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, Hk, page, D, block_table.data_ptr(),
+             width, lengths.data_ptr(), _p(cu_seqlens), B), shape)
+
+
+def cache_append_fp8(k, v, cache: Fp8Cache, block_table, lengths, cu_seqlens=None):
+    """Write packed tokens' keys and values k, v [T, Hk, D] (bf16 views with any token and head strides) into the
+    cache: sequence b's tokens, cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (None: one token each), become its tokens
+    lengths[b], lengths[b] + 1, ... (int32 [B]: what each held before). A page's scale is set by the call that
+    writes its first slot and grows when later tokens need it, with what is there rescaled. Tokens
+    whose page the table does not have are left out. A page that is written must belong to one sequence."""
+    ka = _need_heads(k, "k")
+    args, (_, Hk, _, D) = _check_cache(cache, block_table, lengths, "lengths", cu_seqlens)
+    T = k.shape[0]
+    if k.shape != (T, Hk, D):
+        raise ValueError(f"k must have shape {[T, Hk, D]}, got {list(k.shape)}")
+    va = _need_heads(v, "v", k.shape)
+    _on_one_device(cache.k_codes.get_device(), k_codes=cache.k_codes, k=k, v=v)
+    _launch("svdq_cache_append_fp8", cache.k_codes.device, *ka, *va, *args, T)
+
+
+def cache_read_fp8(cache: Fp8Cache, block_table, starts, cu_seqlens=None, tokens=None, k=None, v=None):
+    """Keys and values out of the cache in bf16 (exact), packed: of sequence b its tokens starts[b], ... as many as
+    cu_seqlens[b + 1] - cu_seqlens[b] (None: one each), `tokens` in all. Zeros where the table has no page. Returns
+    (k, v) [tokens, Hk, D]; rows of given ones outside cu_seqlens are left as they were."""
+    args, (_, Hk, _, D) = _check_cache(cache, block_table, starts, "starts", cu_seqlens)
+    if tokens is None:
+        if cu_seqlens is not None and k is None:
+            raise ValueError("tokens or k is required with cu_seqlens")
+        tokens = args[-1] if cu_seqlens is None else k.shape[0]
+    shape = (tokens, Hk, D)
+    dev = cache.k_codes.device
+    k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else _need(k, "k", torch.bfloat16, shape=shape)
+    v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else _need(v, "v", torch.bfloat16, shape=shape)
+    _on_one_device(cache.k_codes.get_device(), k_codes=cache.k_codes, k=k, v=v)
+    _launch("svdq_cache_read_fp8", dev, *args, tokens, _p(k), _p(v))
+    return k, v
+
+
+def attention_cache_fp8_workspace_bytes(T, B, H, Hk, D, max_length, packed):
+    """Scratch bytes attention_cache_fp8 needs for T queries of B sequences (packed: with cu_seqlens)."""
+    return _lib.lib().svdq_attention_cache_fp8_workspace_bytes(T, B, H, Hk, D, max_length, 1 if packed else 0)
+
+
+def attention_cache_fp8(q, cache: Fp8Cache, block_table, lengths, cu_seqlens=None, causal=True, scale=None,
+                        max_length=None, out=None, workspace=None):
+    """softmax(scale * q k^T) v with k and v out of the cache. q [T, H, D] bf16 (a view with any token and head strides;
+    H a multiple of the cache's heads): sequence b's queries are cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (None: one
+    each), its keys the first lengths[b] (int32 [B]) of its pages. causal: the queries are the sequence's last
+    tokens, and each sees the keys up to its own; else all. scale defaults to D ** -0.5. max_length: the longest
+    length, where the caller knows it (it only helps to share the work out; default: what the table can hold).
+    A row without keys is zero; a page that the table does not have counts as zero keys and values. Rows of a given
+    `out` outside cu_seqlens are left as they were. Returns out [T, H, D]."""
+    qa = _need_heads(q, "q")
+    args, (_, Hk, page, D) = _check_cache(cache, block_table, lengths, "lengths", cu_seqlens)
+    T, H, _ = q.shape
+    if q.shape[2] != D:
+        raise ValueError(f"q must have shape {[T, H, D]}, got {list(q.shape)}")
+    if Hk == 0 or H == 0 or H % Hk != 0:
+        raise ValueError(f"q has {H} heads, no positive multiple of the cache's {Hk}")
+    if out is None:
+        out = torch.empty_like(q)
+    oa = _need_heads(out, "out", q.shape)
+    B, width = block_table.shape
+    most = width * page
+    max_length = most if max_length is None else max(1, min(max_length, most))
+    dev = q.device
+    workspace, ws_bytes = _workspace(
+        workspace, attention_cache_fp8_workspace_bytes(T, B, H, Hk, D, max_length, cu_seqlens is not None), dev)
+    _on_one_device(cache.k_codes.get_device(), k_codes=cache.k_codes, q=q, out=out, workspace=workspace)
+    _launch("svdq_attention_cache_fp8", dev, *qa, *args, T, H, max_length, 1 if causal else 0,
+            scale if scale is not None else D ** -0.5, *oa, _p(workspace), ws_bytes)
+    return out

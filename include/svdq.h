@@ -563,6 +563,135 @@ int svdq_attention_packed(const void* q, int64_t q_stride_t, int64_t q_stride_h,
                           void* stream);
 
 /*
+ * Linear in 8-bit floating point (OCP e4m3) with a scale per block of 128 input
+ * channels: per token for the activations, per 128 output channels for the weight.
+ *
+ *   v = x * smooth (fp32, exact; smooth NULL = 1); per token and block p of 128 channels
+ *     e = the least integer >= -100 with max |v| <= 448 * 2^e,
+ *     codes = e4m3(v * 2^-e) to nearest even, ascales[p, m] = 2^e   (bit-exact functions of x
+ *     and smooth). A block with an infinity or NaN has scale NaN and zero codes, and so NaN in all of
+ *     its token's y.
+ *   y = bf16( sum_p ascales[p, m] * wscales[n / 128, p] * sum_{k in p} codes[m, k] * weight[n, k]
+ *             + bias[n] ),   sums in fp32
+ *
+ *   x [M, K] bf16, smooth [K] bf16 or NULL, codes [M, K] e4m3fn, ascales [ceil(K/128), M]
+ *   fp32, weight [N, K] e4m3fn, wscales [ceil(N/128), ceil(K/128)] fp32, bias [N] bf16 or NULL,
+ *   y [M, N] bf16. The last blocks may be smaller. The product takes any fp32 scales (powers of two or not)
+ *   and any codes (NaN codes give NaN).
+ * svdq_quantize_weight_fp8: a bf16 weight w [N, K] by the same rule, over blocks of 128 x 128 (smooth =
+ *   1 / the layer's smooth, or NULL). N at most 2^23 - 128.
+ * svdq_gemm_fp8: from codes; svdq_linear_fp8: the whole layer from x.
+ * K: a positive multiple of 16, at most 2^20. M, N: at most 2^24, M * N at most 2^38,
+ *   M * ceil(K/128) below 2^31 for the quantisation.
+ * workspace: svdq_gemm_fp8_workspace_bytes(M, N, K) and svdq_linear_fp8_workspace_bytes(M, N, K)
+ *   bytes (0 for some sizes: then it may be NULL); no initialisation needed, contents
+ *   unspecified afterwards.
+ */
+int svdq_quantize_fp8(const void* x, const void* smooth, int64_t M, int64_t K, void* codes, void* ascales,
+                      void* stream);
+int svdq_quantize_weight_fp8(const void* w, const void* smooth, int64_t N, int64_t K, void* codes, void* wscales,
+                             void* stream);
+size_t svdq_gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int svdq_gemm_fp8(const void* codes, const void* ascales, const void* weight, const void* wscales,
+                  const void* bias, int64_t M, int64_t N, int64_t K, void* y, void* workspace,
+                  size_t workspace_bytes, void* stream);
+/* How svdq_gemm_fp8 runs (M, N, K), host only (tests and tuning): the tile's number and the ways k is split, or
+ * tile -1 (the kernel for few tokens) and 1. */
+int svdq_gemm_fp8_plan(int64_t M, int64_t N, int64_t K, int* tile, int* splits);
+size_t svdq_linear_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int svdq_linear_fp8(const void* x, const void* smooth, const void* weight, const void* wscales, const void* bias,
+                    int64_t M, int64_t N, int64_t K, void* y, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Rotary positions on the first R elements of each head, with frequencies scaled for contexts
+ * longer than those trained on, for q and k in one call. Pair i of the R / 2 turns by
+ * positions[t] * f_i, its cos and sin taken times `amplitude`:
+ *
+ *   u' = amplitude * (u cos - w sin),  w' = amplitude * (w cos + u sin)
+ *   g_i = theta^(-2 i / R)
+ *   original_length 0: f_i = g_i / factor (positions interpolated);
+ *   else by parts: r = original_length * g_i / (2 pi) turns within the original length,
+ *     s = clamp((r - low_rotations) / (high_rotations - low_rotations), 0, 1),
+ *     f_i = g_i * (s + (1 - s) / factor)
+ *   interleaved != 0: pair i is (z[2i], z[2i+1]); 0: (z[i], z[i + R/2]). z[R..D-1] are copied.
+ *
+ *   q [T, H, D], k [T, Hk, D] bf16, q_out, k_out, their strides, in-place use and overlaps as
+ *     for svdq_rope_axes (with R < D, in place leaves the rest of a head alone); positions [T] int32
+ *     on the device (negative ones are allowed).
+ * Angles are reduced in fp64; the rotation runs in fp32 with one rounding to bf16. D: a multiple of 8, at
+ * most 256; R: a multiple of 8 in 8..D; T below 2^24; (H + Hk) D at most 524280; theta in [1, 1e9], factor in
+ * [1, 1e6], original_length in [0, 1e9], with it 0 <= low_rotations < high_rotations <= 1e9, amplitude in (0, 1e6].
+ */
+int svdq_rope_scaled(const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t H, const void* k,
+                     int64_t k_stride_t, int64_t k_stride_h, int64_t Hk, const void* positions, int64_t R, double theta,
+                     double factor, double original_length, double low_rotations, double high_rotations,
+                     float amplitude, int interleaved, int64_t T, int64_t D, void* q_out, int64_t qo_stride_t,
+                     int64_t qo_stride_h, void* k_out, int64_t ko_stride_t, int64_t ko_stride_h, void* stream);
+
+/*
+ * A cache of keys and values in pages of `page` tokens (16, 32, 64 or 128), in e4m3 with a power-of-two
+ * scale per page and key head:
+ *
+ *   k_codes [pages, Hk, page, D], v_codes [pages, Hk, D, page] e4m3fn (a page's values are stored element by
+ *     element, so that the tokens are contiguous); k_scales, v_scales [pages, Hk] bytes:
+ *     value = code * 2^(scale - 127), 255 = NaN. All contiguous, on the device.
+ *   block_table [B, width] int32 on the device: token t of sequence b is in page
+ *     block_table[b, t / page], slot t % page. Entries outside 0..pages - 1, and tokens past the
+ *     table's width, are pages that it does not have: nothing outside the tensors is accessed.
+ *   Packed tokens: sequence b's are cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (B + 1 int32 offsets on the
+ *     device, not decreasing; offsets outside 0..T, or decreasing ones, cause no access outside the
+ *     tensors), or with cu_seqlens NULL one each (T = B).
+ *   int32 tensors need 4-byte alignment, the scales none.
+ *
+ * svdq_cache_append_fp8: k, v [T, Hk, D] bf16 (token and head strides as in svdq_rope_axes) become tokens
+ *   lengths[b], lengths[b] + 1, ... of their sequence (lengths: B int32 on the device, what each holds
+ *   before; negative ones count as 0). A page's scale is the least 2^e, e >= -100, with max |.| <= 448 * 2^e
+ *   over the tokens of the call that writes its slot 0; a call that adds to a page raises the scale if its tokens
+ *   need more, and rescales what is there (exactly, but for codes that become subnormal). Codes are rounded
+ *   to nearest even. A page that gets an infinity or NaN has scale 255 until its slot 0 is written again. Slots
+ *   that no token of the call goes to, other than those rescaled, are left as they were. Tokens whose page the
+ *   table does not have are left out. A page that is written must not be in use by another sequence of the call.
+ * svdq_cache_read_fp8: k_out, v_out [T, Hk, D] bf16, the values of tokens starts[b], starts[b] + 1, ... (exact for
+ *   scales from 27, which is 2^-100, to 246); zeros where the table has no page. Rows outside the offsets are
+ *   left as they were.
+ * svdq_attention_cache_fp8:
+ *
+ *   o[t, h] = sum_j softmax_j( scale * q[t, h] . k[j, h / (H / Hk)] ) v[j, h / (H / Hk)]
+ *
+ *   over the first lengths[b] tokens j of t's sequence (at most what the table's width holds); causal: the
+ *   n queries of a sequence are its last tokens, and query i sees j <= lengths[b] - n + i. A row that sees no
+ *   key is zero. A page that the table does not have counts as zero keys and values. q, o [T, H, D] bf16
+ *   with token and head strides as in svdq_rope_axes; o must not overlap an input. Rows of o outside the
+ *   offsets are left as they were. What pages hold past a sequence's length, NaN included, has no effect. As
+ *   in svdq_attention_packed, within a causal sequence a non-finite v may reach rows before it; a scale
+ *   of 255 makes every key (value) of its page NaN.
+ *   Scores and softmax statistics are fp32, the codes are taken exactly; the probabilities are rounded to bf16 for
+ *   the second product (their sum is taken before that), o once to bf16.
+ *   max_length: a bound of the lengths, where the caller knows one (else width * page): it only decides how
+ *   the keys are shared out, a greater length is computed as well.
+ *   workspace: svdq_attention_cache_fp8_workspace_bytes(T, B, H, Hk, D, min(max_length, width * page), packed =
+ *   cu_seqlens given) bytes, as for svdq_gemm_fp8.
+ * D: 64 or 128; H a multiple of Hk; T below 2^24; B, H, Hk at most 65535; width at most 2^24; pages below 2^31;
+ * scale in (0, 2^20]; 16 T H / Hk + 512 B below 2^32 - 65536.
+ */
+int svdq_cache_append_fp8(const void* k, int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                          int64_t v_stride_h, void* k_codes, void* v_codes, void* k_scales, void* v_scales,
+                          int64_t pages, int64_t Hk, int64_t page, int64_t D, const void* block_table, int64_t width,
+                          const void* lengths, const void* cu_seqlens, int64_t B, int64_t T, void* stream);
+int svdq_cache_read_fp8(const void* k_codes, const void* v_codes, const void* k_scales, const void* v_scales,
+                        int64_t pages, int64_t Hk, int64_t page, int64_t D, const void* block_table, int64_t width,
+                        const void* starts, const void* cu_seqlens, int64_t B, int64_t T, void* k_out, void* v_out,
+                        void* stream);
+size_t svdq_attention_cache_fp8_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D,
+                                                int64_t max_length, int packed);
+int svdq_attention_cache_fp8(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_codes,
+                             const void* v_codes, const void* k_scales, const void* v_scales, int64_t pages,
+                             int64_t Hk, int64_t page, int64_t D, const void* block_table, int64_t width,
+                             const void* lengths, const void* cu_seqlens, int64_t B, int64_t T, int64_t H,
+                             int64_t max_length, int causal, float scale, void* o, int64_t o_stride_t,
+                             int64_t o_stride_h, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Measurement helpers. Not part of the layer and not from the pages: they
  * calibrate the roofline figures reported beside AMD's published MI355X peaks.
  *
