@@ -1151,6 +1151,13 @@ def new_cache_fp8(pages, heads, head_dim, page=64, device="cuda"):
                     torch.empty((pages, heads), dtype=torch.uint8, device=device))
 
 
+def _cache_device(cache, block_table, lengths, lengths_name, cu_seqlens, **others):
+    """Every tensor of the call is on the cache's GPU; called after the checks of sizes."""
+    _on_one_device(cache.k_codes.get_device(), k_codes=cache.k_codes, v_codes=cache.v_codes, k_scales=cache.k_scales,
+                   v_scales=cache.v_scales, block_table=block_table, cu_seqlens=cu_seqlens, **{lengths_name: lengths},
+                   **others)
+
+
 def _check_cache(cache, block_table, lengths, lengths_name, cu_seqlens):
     """The checked cache, tables and sequence count as the C ABI takes them: (cache arguments ..., D),
     (table, width, lengths, cu_seqlens, B), and the cache's shape (pages, Hk, page, D)."""
@@ -1166,8 +1173,6 @@ def _check_cache(cache, block_table, lengths, lengths_name, cu_seqlens):
     _need(lengths, lengths_name, torch.int32, shape=(B,))
     if cu_seqlens is not None:
         _need(cu_seqlens, "cu_seqlens", torch.int32, shape=(B + 1,))
-    _on_one_device(kc.get_device(), k_codes=kc, v_codes=vc, k_scales=ks, v_scales=vs, block_table=block_table,
-                   cu_seqlens=cu_seqlens, **{lengths_name: lengths})
     return ((kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, Hk, page, D, block_table.data_ptr(),
              width, lengths.data_ptr(), _p(cu_seqlens), B), shape)
 
@@ -1184,7 +1189,7 @@ def cache_append_fp8(k, v, cache: Fp8Cache, block_table, lengths, cu_seqlens=Non
     if k.shape != (T, Hk, D):
         raise ValueError(f"k must have shape {[T, Hk, D]}, got {list(k.shape)}")
     va = _need_heads(v, "v", k.shape)
-    _on_one_device(cache.k_codes.get_device(), k_codes=cache.k_codes, k=k, v=v)
+    _cache_device(cache, block_table, lengths, "lengths", cu_seqlens, k=k, v=v)
     _launch("svdq_cache_append_fp8", cache.k_codes.device, *ka, *va, *args, T)
 
 
@@ -1201,7 +1206,7 @@ def cache_read_fp8(cache: Fp8Cache, block_table, starts, cu_seqlens=None, tokens
     dev = cache.k_codes.device
     k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else _need(k, "k", torch.bfloat16, shape=shape)
     v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else _need(v, "v", torch.bfloat16, shape=shape)
-    _on_one_device(cache.k_codes.get_device(), k_codes=cache.k_codes, k=k, v=v)
+    _cache_device(cache, block_table, starts, "starts", cu_seqlens, k=k, v=v)
     _launch("svdq_cache_read_fp8", dev, *args, tokens, _p(k), _p(v))
     return k, v
 
@@ -1236,7 +1241,7 @@ def attention_cache_fp8(q, cache: Fp8Cache, block_table, lengths, cu_seqlens=Non
     dev = q.device
     workspace, ws_bytes = _workspace(
         workspace, attention_cache_fp8_workspace_bytes(T, B, H, Hk, D, max_length, cu_seqlens is not None), dev)
-    _on_one_device(cache.k_codes.get_device(), k_codes=cache.k_codes, q=q, out=out, workspace=workspace)
+    _cache_device(cache, block_table, lengths, "lengths", cu_seqlens, q=q, out=out, workspace=workspace)
     _launch("svdq_attention_cache_fp8", dev, *qa, *args, T, H, max_length, 1 if causal else 0,
             scale if scale is not None else D ** -0.5, *oa, _p(workspace), ws_bytes)
     return out

@@ -1,0 +1,234 @@
+"""Refusals of the 8-bit floating-point serving operators, on any host: the C ABI's checks with fake device addresses
+(never dereferenced; every case fails validation or is an empty problem), and the Python binding's checks with CPU
+tensors."""
+
+import ctypes
+
+import pytest
+import torch
+
+from bit_w4a4_quantized_quantize_amd import _lib, ops
+
+no_gpu_only = pytest.mark.skipif(torch.cuda.is_available(),
+                                 reason="fake-pointer validation cases run on CPU-only hosts")
+bf, f32, f8, u8, i32 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.uint8, torch.int32
+
+
+def fake(i):
+    return 0x7F0000000000 + i * 0x1000000000
+
+
+def err():
+    return _lib.lib().svdq_last_error().decode()
+
+
+def call(fn, defaults, kw):
+    a = dict(defaults)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return getattr(_lib.lib(), fn)(*a.values(), None)
+
+
+QUANT = dict(x=fake(1), smooth=fake(2), M=64, K=256, codes=fake(3), scales=fake(4))
+GEMM = dict(codes=fake(1), ascales=fake(2), weight=fake(3), wscales=fake(4), bias=None, M=64, N=128, K=256, y=fake(5),
+            ws=fake(6), ws_bytes=1 << 34)
+ROPE = dict(q=fake(1), qst=1024, qsh=128, H=8, k=fake(2), kst=256, ksh=128, Hk=2, pos=fake(3), R=64, theta=1e4, factor=4.0,
+            original=4096.0, low=1.0, high=32.0, amp=1.0, inter=0, T=10, D=128, qo=fake(4), qost=1024, qosh=128, ko=fake(5),
+            kost=256, kosh=128)
+APPEND = dict(k=fake(1), kst=256, ksh=128, v=fake(2), vst=256, vsh=128, kc=fake(3), vc=fake(4), ks=fake(5), vs=fake(6), pages=10,
+              Hk=2, page=64, D=128, table=fake(7), width=4, lens=fake(8), cu=fake(9), B=3, T=10)
+READ = dict(kc=fake(3), vc=fake(4), ks=fake(5), vs=fake(6), pages=10, Hk=2, page=64, D=128, table=fake(7), width=4,
+            starts=fake(8), cu=fake(9), B=3, T=10, k=fake(1), v=fake(2))
+ATTN = dict(q=fake(1), qst=1024, qsh=128, kc=fake(3), vc=fake(4), ks=fake(5), vs=fake(6), pages=10, Hk=2, page=64, D=128,
+            table=fake(7), width=400, lens=fake(8), cu=fake(9), B=3, T=10, H=8, most=25600, causal=1, scale=0.1, o=fake(2),
+            ost=1024, osh=128, ws=fake(10), ws_bytes=1 << 34)
+
+
+@no_gpu_only
+@pytest.mark.parametrize("fn", ["svdq_quantize_fp8", "svdq_quantize_weight_fp8"])
+@pytest.mark.parametrize("kw,code", [
+    (dict(M=-1), 2), (dict(K=24), 2), (dict(K=0), 2), (dict(K=(1 << 20) + 16), 3), (dict(M=(1 << 24) + 1), 3),
+    (dict(M=1 << 24, K=1 << 20), 3), (dict(x=None), 1), (dict(codes=None), 1), (dict(scales=None), 1), (dict(smooth=fake(2) + 8), 4),
+    (dict(codes=fake(3) + 4), 4), (dict(codes=fake(1)), 6), (dict(scales=fake(3) + 64), 6), (dict(codes=fake(2) + 256), 6),
+])
+def test_quantize(fn, kw, code):
+    assert call(fn, QUANT, kw) == code and err()
+
+
+@no_gpu_only
+def test_quantize_weight_rows():
+    assert call("svdq_quantize_weight_fp8", QUANT, dict(M=65535 * 128 + 1, K=16)) == 3 and err()
+
+
+@no_gpu_only
+@pytest.mark.parametrize("kw,code", [
+    (dict(M=-1), 2), (dict(N=-1), 2), (dict(K=40), 2), (dict(K=(1 << 20) + 16), 3), (dict(N=(1 << 24) + 1), 3),
+    (dict(M=1 << 24, N=1 << 15), 3), (dict(weight=None), 1), (dict(wscales=None), 1), (dict(y=None), 1), (dict(codes=None), 1),
+    (dict(bias=fake(7) + 2), 4), (dict(y=fake(5) + 2), 4), (dict(y=fake(3) + 128), 6), (dict(y=fake(4)), 6), (dict(y=fake(1)), 6),
+    (dict(bias=fake(5)), 6),
+])
+def test_gemm_and_linear(kw, code):
+    assert call("svdq_gemm_fp8", GEMM, kw) == code and err()
+    # the layer takes x and smooth where the product takes codes and scales
+    assert call("svdq_linear_fp8", GEMM, kw) == code and err()
+
+
+@no_gpu_only
+def test_gemm_workspace():
+    L = _lib.lib()
+    big = dict(M=333, N=3840, K=10240)
+    need = L.svdq_linear_fp8_workspace_bytes(333, 3840, 10240)
+    assert need >= 333 * 10240 + 80 * 333 * 4
+    for kw, code in ((dict(ws_bytes=need - 1), 5), (dict(ws=None), 1), (dict(ws=fake(6) + 8), 4), (dict(ws=fake(5)), 6), (dict(ws=fake(1)), 6)):
+        assert call("svdq_linear_fp8", GEMM, dict(big, **kw)) == code, kw
+    assert L.svdq_linear_fp8_workspace_bytes(0, 10, 128) == 0 and L.svdq_gemm_fp8_workspace_bytes(1, 3840, 3840) == 0
+    tile, splits = ctypes.c_int(0), ctypes.c_int(0)
+    assert L.svdq_gemm_fp8_plan(0, 128, 256, ctypes.byref(tile), ctypes.byref(splits)) == 2
+    assert L.svdq_gemm_fp8_plan(1, 128, 256, None, ctypes.byref(splits)) == 1
+    assert L.svdq_gemm_fp8_plan(1, 128, 256, ctypes.byref(tile), ctypes.byref(splits)) == 0 and tile.value == -1 and splits.value == 1
+
+
+@no_gpu_only
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=-1), 2), (dict(T=1 << 24), 3), (dict(D=12), 3), (dict(D=264), 3), (dict(R=0), 2), (dict(R=12), 2), (dict(R=136), 2),
+    (dict(H=-1), 2), (dict(H=0, Hk=0), 2), (dict(H=0), 8), (dict(H=60000), 3), (dict(theta=0.5), 8), (dict(theta=float("nan")), 8),
+    (dict(factor=0.5), 8), (dict(factor=float("inf")), 8), (dict(original=-1.0), 8), (dict(original=float("nan")), 8),
+    (dict(low=4.0, high=4.0), 8), (dict(low=-1.0), 8), (dict(high=float("nan")), 8), (dict(amp=0.0), 8), (dict(amp=float("nan")), 8),
+    (dict(pos=None), 1), (dict(pos=fake(3) + 4), 4), (dict(q=None), 1), (dict(ko=None), 1), (dict(q=fake(1) + 2), 4),
+    (dict(qst=1028), 4), (dict(qst=64), 2), (dict(qosh=64), 2), (dict(qo=fake(2)), 6), (dict(ko=fake(4)), 6), (dict(qo=fake(1) + 256), 6),
+    (dict(ko=fake(3)), 6), (dict(qo=fake(1), qost=2048), 6), (dict(qost=1 << 24), 3),
+])
+def test_rope(kw, code):
+    assert call("svdq_rope_scaled", ROPE, kw) == code and err()
+
+
+CACHE_CASES = [
+    (dict(T=-1), 2), (dict(T=1 << 24), 3), (dict(D=96), 3), (dict(D=0), 3), (dict(page=8), 3), (dict(page=48), 3), (dict(page=256), 3),
+    (dict(pages=0), 2), (dict(pages=1 << 31), 2), (dict(Hk=0), 2), (dict(Hk=65536), 3), (dict(B=-1), 2), (dict(B=65536), 3),
+    (dict(cu=None), 8), (dict(width=0), 2), (dict(width=(1 << 24) + 1), 2), (dict(kc=None), 1), (dict(vc=None), 1), (dict(ks=None), 1),
+    (dict(vs=None), 1), (dict(table=None), 1), (dict(table=fake(7) + 2), 4), (dict(cu=fake(9) + 1), 4), (dict(kc=fake(3) + 8), 4),
+    (dict(kc=fake(4) + 16), 6), (dict(vs=fake(5) + 3), 6), (dict(ks=fake(3) + 64), 6),
+]
+
+
+@no_gpu_only
+@pytest.mark.parametrize("kw,code", CACHE_CASES)
+def test_caches(kw, code):
+    assert call("svdq_cache_append_fp8", APPEND, kw) == code and err()
+    assert call("svdq_cache_read_fp8", READ, kw) == code and err()
+    assert call("svdq_attention_cache_fp8", ATTN, kw) == code and err()
+
+
+@no_gpu_only
+@pytest.mark.parametrize("kw,code", [
+    (dict(k=None), 1), (dict(v=fake(2) + 2), 4), (dict(kst=130), 4), (dict(kst=64), 2), (dict(k=fake(3) + 1024), 6), (dict(v=fake(6)), 6),
+    (dict(lens=None), 1), (dict(lens=fake(8) + 2), 4), (dict(lens=fake(5)), 6), (dict(table=fake(3)), 6), (dict(cu=fake(4)), 6),
+])
+def test_append(kw, code):
+    assert call("svdq_cache_append_fp8", APPEND, kw) == code and err()
+
+
+@no_gpu_only
+@pytest.mark.parametrize("kw,code", [
+    (dict(k=None), 1), (dict(v=fake(2) + 2), 4), (dict(k=fake(2) + 512), 6), (dict(k=fake(3)), 6), (dict(v=fake(6)), 6),
+    (dict(k=fake(7)), 6), (dict(v=fake(9)), 6), (dict(starts=None), 1),
+])
+def test_read(kw, code):
+    assert call("svdq_cache_read_fp8", READ, kw) == code and err()
+
+
+@no_gpu_only
+@pytest.mark.parametrize("kw,code", [
+    (dict(H=0), 2), (dict(H=9), 2), (dict(H=65538), 3), (dict(scale=0.0), 8), (dict(scale=float("nan")), 8), (dict(scale=2.0 ** 21), 8),
+    (dict(most=0), 2), (dict(T=(1 << 24) - 1, H=64), 3), (dict(q=None), 1), (dict(q=fake(1) + 8), 4), (dict(qst=64), 2), (dict(qsh=100), 4),
+    (dict(o=None), 1), (dict(osh=64), 2), (dict(o=fake(1)), 6), (dict(o=fake(3) + 64), 6), (dict(o=fake(9)), 6), (dict(ws_bytes=100), 5),
+    (dict(ws=None), 1), (dict(ws=fake(10) + 8), 4), (dict(ws=fake(2)), 6), (dict(ws=fake(1)), 6), (dict(ws=fake(4)), 6), (dict(lens=None), 1),
+])
+def test_attention(kw, code):
+    assert call("svdq_attention_cache_fp8", ATTN, kw) == code and err()
+
+
+@no_gpu_only
+def test_attention_workspace_sizes():
+    size = _lib.lib().svdq_attention_cache_fp8_workspace_bytes
+    assert size(1, 1, 32, 8, 128, 65536, 0) > 0 and size(1, 1, 32, 8, 128, 64, 0) == 0
+    assert size(0, 1, 32, 8, 128, 65536, 0) == 0 and size(1, 1, 32, 5, 128, 65536, 0) == 0
+
+
+@no_gpu_only
+def test_empty_problems_need_no_tokens():
+    assert call("svdq_quantize_fp8", QUANT, dict(M=0, x=None, codes=None, scales=None)) == 0
+    assert call("svdq_gemm_fp8", GEMM, dict(M=0, codes=None, y=None)) == 0
+    assert call("svdq_linear_fp8", GEMM, dict(N=0, weight=None, y=None)) == 0
+    assert call("svdq_rope_scaled", ROPE, dict(T=0, q=None, k=None, pos=None, qo=None, ko=None)) == 0
+    assert call("svdq_cache_append_fp8", APPEND, dict(T=0, k=None, v=None)) == 0
+    assert call("svdq_cache_read_fp8", READ, dict(T=0, k=None, v=None)) == 0
+    assert call("svdq_attention_cache_fp8", ATTN, dict(T=0, q=None, o=None, ws=None, ws_bytes=0)) == 0
+    assert call("svdq_cache_append_fp8", APPEND, dict(T=0, B=0, table=None, lens=None, cu=None)) == 0
+
+
+# ---- the binding ----
+
+def cpu_cache(pages=4, Hk=2, D=64, page=16):
+    return ops.new_cache_fp8(pages, Hk, D, page, device="cpu")
+
+
+def z(*shape, dtype=bf):
+    return torch.zeros(shape, dtype=dtype)
+
+
+def raises(part, fn, *args, **kw):
+    with pytest.raises(ValueError, match=part):
+        fn(*args, **kw)
+
+
+def test_binding_linear():
+    w, ws = z(40, 256, dtype=f8), z(1, 2, dtype=f32)
+    raises("bfloat16", ops.linear_fp8, z(3, 256, dtype=f32), w, ws)
+    raises("multiple of 16", ops.linear_fp8, z(3, 250), w, ws)
+    raises("K=128", ops.linear_fp8, z(3, 128), w, ws)
+    raises("wscales must have shape", ops.linear_fp8, z(3, 256), w, z(40, 2, dtype=f32))
+    raises("weight must be", ops.linear_fp8, z(3, 256), z(40, 256, dtype=torch.int8), ws)
+    raises("bias must have shape", ops.linear_fp8, z(3, 256), w, ws, bias=z(41))
+    raises("smooth must have shape", ops.linear_fp8, z(3, 256), w, ws, smooth=z(255))
+    raises("contiguous", ops.linear_fp8, z(256, 3).t(), w, ws)
+    raises("ascales must have shape", ops.gemm_fp8, z(3, 256, dtype=f8), z(3, 2, dtype=f32), w, ws)
+    raises("y must have shape", ops.gemm_fp8, z(3, 256, dtype=f8), z(2, 3, dtype=f32), w, ws, y=z(3, 41))
+    raises("GPU tensor", ops.linear_fp8, z(3, 256), w, ws, workspace=z(1 << 20, dtype=u8))
+    raises("scales must have shape", ops.quantize_fp8, z(3, 256), scales=z(3, 2, dtype=f32))
+    raises("scales must have shape", ops.quantize_weight_fp8, z(300, 256), scales=z(2, 3, dtype=f32))
+    raises("GPU tensor", ops.quantize_weight_fp8, z(300, 256))
+
+
+def test_binding_rope():
+    q, k, pos = z(5, 4, 64), z(5, 2, 64), z(5, dtype=i32)
+    raises("q or k", ops.rope_scaled, None, None, pos)
+    raises("positions must be", ops.rope_scaled, q, k, z(5, dtype=torch.int64))
+    raises("positions must have shape", ops.rope_scaled, q, k, z(5, 1, dtype=i32))
+    raises("k must have shape", ops.rope_scaled, q, z(4, 2, 64), pos)
+    raises("q_out needs q", ops.rope_scaled, None, k, pos, q_out=q)
+    raises("k_out must have shape", ops.rope_scaled, q, k, pos, k_out=q)
+    raises("GPU tensor", ops.rope_scaled, q, k, pos)
+
+
+def test_binding_cache():
+    c, k, table, lens = cpu_cache(), z(3, 2, 64), z(3, 2, dtype=i32), z(3, dtype=i32)
+    cu = z(4, dtype=i32)
+    raises("k must have shape", ops.cache_append_fp8, z(3, 4, 64), k, c, table, lens)
+    raises("v must have shape", ops.cache_append_fp8, k, z(2, 2, 64), c, table, lens)
+    raises("lengths must have shape", ops.cache_append_fp8, k, k, c, table, z(2, dtype=i32))
+    raises("block_table must be", ops.cache_append_fp8, k, k, c, table.long(), lens)
+    raises("cu_seqlens must have shape", ops.cache_append_fp8, k, k, c, table, lens, z(3, dtype=i32))
+    raises("v_codes must have shape", ops.cache_append_fp8, k, k,
+           ops.Fp8Cache(c.k_codes, z(4, 2, 16, 64, dtype=f8), c.k_scales, c.v_scales), table, lens)
+    raises("k_scales must be", ops.cache_append_fp8, k, k,
+           ops.Fp8Cache(c.k_codes, c.v_codes, c.k_scales.float(), c.v_scales), table, lens)
+    raises("contiguous", ops.cache_append_fp8, k, k,
+           ops.Fp8Cache(z(8, 2, 16, 64, dtype=f8)[::2], c.v_codes, c.k_scales, c.v_scales), table, lens)
+    raises("GPU tensor", ops.cache_append_fp8, k, k, c, table, lens)
+    raises("GPU tensor", ops.cache_read_fp8, c, table, lens, cu, 3)
+    q = z(3, 4, 64)
+    raises("q must have shape", ops.attention_cache_fp8, z(3, 4, 128), c, table, lens)
+    raises("no positive multiple", ops.attention_cache_fp8, z(3, 3, 64), c, table, lens)
+    raises("out must have shape", ops.attention_cache_fp8, q, c, table, lens, out=k)
+    raises("GPU tensor", ops.attention_cache_fp8, q, c, table, lens)
