@@ -277,6 +277,370 @@ __global__ __launch_bounds__(64 * kWavesF) void attention_few_kernel(AttnCacheAr
   }
 }
 
+// Many rows. A workgroup of NW waves takes 32 NW rows, 32 a wave, and tiles of 64 keys in LDS: codes travel
+// to registers a step ahead, become bf16 and are written to LDS before the next step's barrier. K^T's tile is
+// [64][D]; V^T's is [D][64] with each 16 keys in the order of P^T's operand (0-3, 8-11 for the lower half of the
+// wave, 4-7, 12-15 for the upper), so that both products read whole 16-byte pieces. Products,
+// exponentials and the lazy maximum are arranged as in attention.hip.
+constexpr int kAheadC = 2;   // operand reads in flight ahead of a product
+
+template <int D, bool CAUSAL, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArgs a) {
+  constexpr int kRowBytes = 2 * D;
+  constexpr int kTileBytes = kTile * kRowBytes;     // of K, and of V
+  constexpr int KD = D / 16;                        // 16-element steps of the first product
+  constexpr int JD = D / 32;                        // 32-element blocks of the output
+  constexpr int kCP = D / 16;                       // 16-byte pieces of a key's codes
+  constexpr int kPieces = kTile * kCP / (64 * NW);  // of a tile, per thread; as many of V
+  constexpr int kLgRows = NW == 8 ? 8 : 7;
+  static_assert(NW * 32 == 1 << kLgRows && kPieces >= 1, "waves");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * kTileBytes];
+
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = tid & 63;
+  const int h = lane >> 5, l32 = lane & 31;
+  const int G = a.H / a.c.Hk, lg_page = a.c.lg_page, P = 1 << lg_page;
+
+  // row blocks of one head stay on one XCD (its L2 holds their keys)
+  const int per_xcd = (int)(gridDim.x / 8);
+  const int id = (int)(blockIdx.x % 8) * per_xcd + (int)(blockIdx.x / 8);
+  const int blocks = (int)((a.T * G) >> kLgRows) + a.B;
+  if (id >= blocks * a.splits * a.c.Hk) return;
+  const int hk = id / (blocks * a.splits);
+  const int split = id % (blocks * a.splits) / blocks;
+  RowBlock rb;
+  if (!find_rows(a, G, kLgRows, id % blocks, rb)) return;
+  const int n_rows = rb.n * G;
+  if (CAUSAL) {   // those with the most keys first
+    const int last_block = (n_rows - 1) >> kLgRows;
+    rb.row0 = (last_block << kLgRows) - rb.row0;
+  }
+  const int L = (int)keys_of(a, rb.b);
+  const int per = tiles_per_split(a, L);
+  const bool only = (L + kTile - 1) / kTile <= per;
+  if (split > 0 && (int64_t)split * per * kTile >= L) return;
+
+  // this wave's rows, this lane's row (past the end: the last) and the keys it sees
+  const int row0 = rb.row0 + 32 * wave;
+  const int row = min(row0 + l32, n_rows - 1);
+  const int query = row / G, head = hk * G + row - query * G;
+  const int off = L - rb.n;                                  // causal: query i sees keys up to off + i
+  const int last = CAUSAL ? off + query : L - 1;
+  // keys up to `low` are seen by every row of the wave, none past `high` by any
+  const int low = CAUSAL ? off + min(row0, n_rows - 1) / G : L - 1;
+  const int high = CAUSAL ? off + min(row0 + 31, n_rows - 1) / G : L - 1;
+  const int wg_high = CAUSAL ? off + min(rb.row0 + 32 * NW - 1, n_rows - 1) / G : L - 1;
+  const int kt0 = split * per;
+  const int nt = max(min((wg_high >> 6) + 1, kt0 + per) - kt0, 0);              // tiles of the workgroup (>> of -1 is -1)
+  const int ntw = row0 < n_rows ? max(min((high >> 6) + 1, kt0 + per) - kt0, 0) : 0;   // and of this wave
+
+  bf16x8 fq[KD];
+  {
+    const uint16_t* qp = a.q.p + (int64_t)(rb.tok0 + query) * a.q.st + head * a.q.sh + 8 * h;
+#pragma unroll
+    for (int t = 0; t < KD; ++t) fq[t] = *reinterpret_cast<const bf16x8*>(qp + 16 * t);
+  }
+
+  // Pieces of 16 codes: of K, key kr and elements 16 ks ..; of V, element vd and keys 16 vk ..
+  auto swz_k = [](int r) { return D == 128 ? (r & 15) : ((r >> 1) & 7); };
+  auto swz_v = [](int r) { return (r ^ (r >> 3)) & 7; };
+  const int32_t* table = a.table + (int64_t)rb.b * a.width;
+  const int64_t page_bytes = (int64_t)P * D;
+  auto page_at = [&](int key) {   // the page of a key; -1: none
+    const int at = key >> lg_page;
+    const int p = at < a.width && key < L ? table[at] : -1;
+    return (uint32_t)p < (uint32_t)a.c.pages ? p : -1;
+  };
+  int pk[kPieces], pv[kPieces];          // pages of the pieces to be requested next
+  u32x4 wk[kPieces], wv[kPieces];        // codes on their way
+  uint32_t sk[kPieces], sv[kPieces];     // and their scales
+  auto k_pages = [&](int kt) {
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c) pk[c] = page_at((kt0 + kt) * kTile + (tid + 64 * NW * c) / kCP);
+  };
+  auto v_pages = [&](int kt) {
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c) pv[c] = page_at((kt0 + kt) * kTile + 16 * (tid & 3));
+  };
+  auto request_k = [&](int kt) {
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c) {
+      const int i = tid + 64 * NW * c, key = (kt0 + kt) * kTile + i / kCP;
+      const int64_t at = (int64_t)max(pk[c], 0) * a.c.Hk + hk;
+      wk[c] = *reinterpret_cast<const u32x4*>(a.c.k + at * page_bytes + (key & (P - 1)) * D + 16 * (i % kCP));
+      sk[c] = a.c.ks[at];
+      if (pk[c] < 0) sk[c] = 256;        // no codes
+    }
+  };
+  auto request_v = [&](int kt) {
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c) {
+      const int i = tid + 64 * NW * c, key = (kt0 + kt) * kTile + 16 * (i & 3);
+      const int64_t at = (int64_t)max(pv[c], 0) * a.c.Hk + hk;
+      wv[c] = *reinterpret_cast<const u32x4*>(a.c.v + at * page_bytes + (i >> 2) * P + (key & (P - 1)));
+      sv[c] = a.c.vs[at];
+      if (pv[c] < 0) sv[c] = 256;
+    }
+  };
+  auto store_k = [&](int kt) {
+    uint8_t* st = smem + (kt & 1) * (2 * kTileBytes);
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c) {
+      const int i = tid + 64 * NW * c, r = i / kCP, s = 2 * (i % kCP);
+      const float sc = cache_scale(sk[c] & 255u);
+      const u32x4 w = sk[c] > 255u ? zero4() : wk[c];
+      uint8_t* at = st + r * kRowBytes;
+      *reinterpret_cast<bf16x8*>(at + ((s ^ swz_k(r)) * 16)) = bf16_operand(w[0], w[1], sc);
+      *reinterpret_cast<bf16x8*>(at + (((s + 1) ^ swz_k(r)) * 16)) = bf16_operand(w[2], w[3], sc);
+    }
+  };
+  auto store_v = [&](int kt) {
+    uint8_t* st = smem + (kt & 1) * (2 * kTileBytes) + kTileBytes;
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c) {
+      const int i = tid + 64 * NW * c, d = i >> 2, s = 2 * (i & 3);
+      const float sc = cache_scale(sv[c] & 255u);
+      u32x4 w = sv[c] > 255u ? zero4() : wv[c];
+      const int left = L - (kt0 + kt) * kTile - 8 * s;   // values past the sequence are zero, whatever the page holds
+      if (left < 16) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int n = max(min(left - 4 * e, 4), 0);
+          w[e] &= n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
+        }
+      }
+      uint8_t* at = st + d * 128;
+      *reinterpret_cast<bf16x8*>(at + ((s ^ swz_v(d)) * 16)) = bf16_operand(w[0], w[2], sc);
+      *reinterpret_cast<bf16x8*>(at + (((s + 1) ^ swz_v(d)) * 16)) = bf16_operand(w[1], w[3], sc);
+    }
+  };
+
+  // operand u of the first product (keys 32 (u % 2) of the tile, elements 16 (u / 2) of the head), and of the second
+  // (keys 16 (u / JD), elements 32 (u % JD))
+  // pieces 2 t + h, permuted by an exclusive or: that of t applies to the address of t = 0. Row 32 j + l32 of V^T is
+  // permuted like row l32, with 4 j more
+  int kfrag = l32 * kRowBytes + ((h ^ swz_k(l32)) * 16), vfrag = l32 * 128 + ((h ^ swz_v(l32)) * 16);
+  auto read_k = [&](const uint8_t* sk_, int u) {
+    return *reinterpret_cast<const bf16x8*>(sk_ + 32 * (u & 1) * kRowBytes + (kfrag ^ (32 * (u >> 1))));
+  };
+  auto read_v = [&](const uint8_t* sv_, int u) {
+    return *reinterpret_cast<const bf16x8*>(sv_ + 32 * (u % JD) * 128 + (vfrag ^ (32 * (u / JD)) ^ (((u % JD) & 1) * 64)));
+  };
+  constexpr int NK = 2 * KD, NV = 4 * JD;   // products of a tile
+
+  f32x16 acc[JD];
+#pragma unroll
+  for (int j = 0; j < JD; ++j) acc[j] = f32x16{};
+  const float c = a.scale * 1.4426950408889634f;   // exponents in base 2
+  float m = kLowest / fmaxf(c, 1.0f);              // below every finite score whose exponent is finite
+  const float slack = kSlackC / c;
+  // a tile's probabilities first, then l with what its last addition lost, as in attention.hip
+  float l = 0.0f, lost = 0.0f, tile_sum = 0.0f;
+  auto add_tile = [&] {
+    const float y = tile_sum - lost, t = l + y;
+    lost = (t - l) - y;
+    l = t;
+    tile_sum = 0.0f;
+  };
+  auto pair = [&](const f32x16 (&x)[2], uint32_t (&p)[16], int r) {
+    const float p0 = __builtin_amdgcn_exp2f((x[r >> 3][2 * (r & 7)] - m) * c);
+    const float p1 = __builtin_amdgcn_exp2f((x[r >> 3][2 * (r & 7) + 1] - m) * c);
+    p[r] = pack_bf16x2(p0, p1);
+    tile_sum += p0 + p1;
+    asm volatile("" : "+v"(p[r]), "+v"(tile_sum));   // made here: not moved to their use
+  };
+  auto prob_operand = [&](const uint32_t (&p)[16], int t) {
+    return __builtin_bit_cast(bf16x8, u32x4{p[4 * t], p[4 * t + 1], p[4 * t + 2], p[4 * t + 3]});
+  };
+  auto mask = [&](f32x16 (&x)[2], int kt) {
+    const int k0 = (kt0 + kt) * kTile;
+    if (k0 + kTile - 1 > low) {
+      const int lim = last - k0 - 4 * h;
+#pragma unroll
+      for (int r = 0; r < 32; ++r) {
+        if (32 * (r >> 4) + 8 * ((r & 15) >> 2) + (r & 3) > lim) x[r >> 4][r & 15] = -__builtin_inff();
+        if (r % 8 == 7) __builtin_amdgcn_sched_barrier(0);   // few condition registers at a time
+      }
+    }
+  };
+  auto raise = [&](float mx) {
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    const float mn = fmaxf(m, mx);
+    const float alpha = __builtin_amdgcn_exp2f((m - mn) * c);
+    m = mn;
+    l *= alpha;
+    lost *= alpha;
+    return alpha;
+  };
+
+  // Start of step kt: one barrier frees K(kt) and V(kt - 1) and publishes K(kt + 1) and V(kt); the codes of the next
+  // two tiles are requested, their pages were a step ago
+  auto begin_step = [&](int kt) {
+    __syncthreads();
+    if (kt + 2 < nt) {
+      request_k(kt + 2);
+      k_pages(kt + 3);
+    }
+    if (kt + 1 < nt) {
+      request_v(kt + 1);
+      v_pages(kt + 2);
+    }
+  };
+  auto end_step = [&](int kt) {
+    if (kt + 2 < nt) store_k(kt + 2);
+    if (kt + 1 < nt) store_v(kt + 1);
+  };
+  auto step = [&](f32x16 (&cur)[2], uint32_t (&pc)[16], f32x16 (&nxt)[2], uint32_t (&pn)[16], int kt) {
+    begin_step(kt);
+    asm volatile("" : "+v"(kfrag), "+v"(vfrag));   // the addresses of each read are made anew: 10 registers
+    const uint8_t* sk_ = smem + ((kt + 1) & 1) * (2 * kTileBytes);
+    const uint8_t* sv_ = smem + (kt & 1) * (2 * kTileBytes) + kTileBytes;
+    bf16x8 fk[NK], fv[NV];
+#pragma unroll
+    for (int u = 0; u < kAheadC; ++u) fk[u] = read_k(sk_, u);
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int u = 0; u < NK; ++u) {
+      if (u + kAheadC < NK) fk[u + kAheadC] = read_k(sk_, u + kAheadC);
+      else fv[u + kAheadC - NK] = read_v(sv_, u + kAheadC - NK);
+      nxt[u & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fk[u], fq[u >> 1], u < 2 ? f32x16{} : nxt[u & 1], 0, 0, 0);
+#pragma unroll
+      for (int r = 8 + 8 * u / NK; r < 8 + 8 * (u + 1) / NK; ++r) pair(cur, pc, r);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    __builtin_amdgcn_s_setprio(0);
+    add_tile();
+    mask(nxt, kt + 1);
+    constexpr int kMax = NV / 4;   // products that cover the maximum
+    auto value = [&](int u) {
+      if (u + kAheadC < NV) fv[u + kAheadC] = read_v(sv_, u + kAheadC);
+      acc[u % JD] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fv[u], prob_operand(pc, u / JD), acc[u % JD], 0, 0, 0);
+    };
+    float mx = -__builtin_inff(), alpha = 1.0f;
+#pragma unroll
+    for (int u = 0; u < kMax; ++u) {
+      value(u);
+#pragma unroll
+      for (int r = 32 * u / kMax; r < 32 * (u + 1) / kMax; ++r) mx = fmaxf(mx, nxt[r >> 4][r & 15]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    const bool up = __ballot(mx > m + slack) != 0;
+    if (up) alpha = raise(mx);
+#pragma unroll
+    for (int u = kMax; u < NV; ++u) {
+      value(u);
+#pragma unroll
+      for (int r = 8 * (u - kMax) / (NV - kMax); r < 8 * (u + 1 - kMax) / (NV - kMax); ++r) pair(nxt, pn, r);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (up) {
+#pragma unroll
+      for (int j = 0; j < JD; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[j][r] *= alpha;
+    }
+    end_step(kt);
+  };
+
+  if (nt > 0) {
+    k_pages(0);
+    v_pages(0);
+    request_k(0);
+    request_v(0);
+    store_k(0);
+    store_v(0);
+    if (nt > 1) {
+      k_pages(1);
+      request_k(1);
+      store_k(1);
+      k_pages(2);
+      v_pages(1);
+    }
+    __syncthreads();
+  }
+  int kt = 0;
+  if (ntw > 0) {
+    f32x16 s0[2], s1[2];
+    uint32_t p0[16], p1[16];
+#pragma unroll
+    for (int u = 0; u < NK; ++u)
+      s0[u & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_k(smem, u), fq[u >> 1], u < 2 ? f32x16{} : s0[u & 1], 0, 0, 0);
+    mask(s0, 0);
+    float mx = s0[0][0];
+#pragma unroll
+    for (int r = 1; r < 32; ++r) mx = fmaxf(mx, s0[r >> 4][r & 15]);
+    raise(mx);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) pair(s0, p0, r);
+    for (; kt + 2 < ntw; kt += 2) {
+      step(s0, p0, s1, p1, kt);
+      step(s1, p1, s0, p0, kt + 1);
+    }
+    if (kt + 1 < ntw) {
+      step(s0, p0, s1, p1, kt);
+      s0[1] = s1[1];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) p0[r] = p1[r];
+      ++kt;
+    }
+    begin_step(kt);   // the last tile
+    const uint8_t* sv_ = smem + (kt & 1) * (2 * kTileBytes) + kTileBytes;
+#pragma unroll
+    for (int r = 8; r < 16; ++r) pair(s0, p0, r);
+    add_tile();
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+      acc[u % JD] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_v(sv_, u), prob_operand(p0, u / JD), acc[u % JD], 0, 0, 0);
+    end_step(kt);
+    ++kt;
+  }
+  for (; kt < nt; ++kt) {   // tiles that only other waves need
+    begin_step(kt);
+    end_step(kt);
+  }
+
+  l += __shfl_xor(l, 32);
+  if (!only) {   // this lane holds elements 32 j + 8 (r / 4) + 4 h + r % 4 of its row
+    if (row0 + l32 >= n_rows) return;
+    const int64_t at = ((int64_t)split * a.T + rb.tok0 + query) * a.H + head;
+    float* dst = a.partial + at * D + 4 * h;
+#pragma unroll
+    for (int j = 0; j < JD; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; r += 4)
+        *reinterpret_cast<f32x4*>(dst + 32 * j + 2 * r) = f32x4{acc[j][r], acc[j][r + 1], acc[j][r + 2], acc[j][r + 3]};
+    if (h == 0) {
+      float* st = a.partial + (int64_t)a.splits * a.T * a.H * D + 2 * at;
+      st[0] = m;
+      st[1] = l;
+    }
+    return;
+  }
+  // O^T through LDS (the tiles' space): each wave turns its block into rows and stores whole
+  // 16-byte pieces. Row r's pieces are permuted by piece ^ (r % pieces).
+  __syncthreads();
+  constexpr int kOP = D / 8, kRowsPerCopy = 64 / kOP;
+  uint8_t* out = smem + wave * (32 * kRowBytes);
+  static_assert(NW * 32 * kRowBytes <= 4 * kTileBytes, "output staging");
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int j = 0; j < JD; ++j)
+#pragma unroll
+    for (int r = 0; r < 16; r += 4)
+      *reinterpret_cast<u32x2*>(out + l32 * kRowBytes + (((4 * j + r / 4) ^ (l32 & (kOP - 1))) * 16) + 8 * h) =
+          u32x2{pack_bf16x2(acc[j][r] * inv, acc[j][r + 1] * inv), pack_bf16x2(acc[j][r + 2] * inv, acc[j][r + 3] * inv)};
+  __syncthreads();
+  uint16_t* op = a.o + hk * G * a.o_sh;
+#pragma unroll
+  for (int u = 0; u < 32 / kRowsPerCopy; ++u) {
+    const int r = u * kRowsPerCopy + lane / kOP, piece = lane % kOP;
+    const u32x4 w = *reinterpret_cast<const u32x4*>(out + r * kRowBytes + ((piece ^ (r & (kOP - 1))) * 16));
+    const int tq = __shfl(query, r), th = __shfl(head, r) - hk * G;
+    if (row0 + r < n_rows) *reinterpret_cast<u32x4*>(op + (int64_t)(rb.tok0 + tq) * a.o_st + th * a.o_sh + 8 * piece) = w;
+  }
+}
+
 // The splits of a row (a query's head) together, a wave each.
 template <int D>
 __global__ __launch_bounds__(256) void join_kernel(AttnCacheArgs a) {
@@ -312,21 +676,45 @@ __global__ __launch_bounds__(256) void join_kernel(AttnCacheArgs a) {
   else *dst = (uint16_t)f32_to_bf16_rne(o[0] * inv);
 }
 
-int plan_splits(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t max_length, bool packed) {
+// Rows of a sequence and key head on average, and the kernel for them: 0 few, 1 tiles by four waves, 2 by eight.
+struct AttnPlan {
+  int kernel, splits, least;
+};
+AttnPlan plan_attention(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_length, bool packed) {
   const int64_t G = H / Hk;
-  const int64_t blocks = packed ? (T * G + 15) / 16 : B * ((G + 15) / 16);
   const int64_t tiles = (max_length + kTile - 1) / kTile;
-  int64_t s = (1024 + blocks * Hk - 1) / (blocks * Hk);
-  if (s > (tiles + 3) / 4) s = (tiles + 3) / 4;
-  return (int)(s < 1 ? 1 : s);
+  AttnPlan p;
+  p.kernel = T * G <= 32 * B ? 0 : D == 128 && T * G >= 4096 * B ? 2 : 1;
+  const int rows = p.kernel == 0 ? 16 : p.kernel == 1 ? 128 : 256;
+  const int64_t blocks = (packed ? (T * G + rows - 1) / rows : B * ((G + rows - 1) / rows)) * Hk;
+  const int64_t want = p.kernel == 0 ? 1024 : 512;
+  p.least = 4;
+  int64_t s = blocks >= want ? 1 : want / blocks;
+  if (s > (tiles + p.least - 1) / p.least) s = (tiles + p.least - 1) / p.least;
+  p.splits = (int)(s < 1 ? 1 : s);
+  return p;
+}
+
+template <int D, int NW>
+void launch_tiles(const AttnCacheArgs& a, hipStream_t stream) {
+  const int64_t total = ((a.T * (a.H / a.c.Hk) >> (NW == 8 ? 8 : 7)) + a.B) * a.splits * a.c.Hk;
+  const dim3 grid((unsigned)((total + 7) / 8 * 8)), block(64 * NW);
+  if (a.causal) hipLaunchKernelGGL((attention_tile_kernel<D, true, NW>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((attention_tile_kernel<D, false, NW>), grid, block, 0, stream, a);
 }
 
 template <int D>
-hipError_t launch_d(const AttnCacheArgs& a, hipStream_t stream) {
+hipError_t launch_d(const AttnCacheArgs& a, int kernel, hipStream_t stream) {
   const int64_t G = a.H / a.c.Hk;
-  const int64_t blocks = a.cu == nullptr ? a.B * ((G + 15) / 16) : (a.T * G >> 4) + a.B;
-  hipLaunchKernelGGL(attention_few_kernel<D>, dim3((unsigned)(blocks * a.splits), (unsigned)a.c.Hk), dim3(64 * kWavesF),
-                     0, stream, a);
+  if (kernel == 0) {
+    const int64_t blocks = a.cu == nullptr ? a.B * ((G + 15) / 16) : (a.T * G >> 4) + a.B;
+    hipLaunchKernelGGL(attention_few_kernel<D>, dim3((unsigned)(blocks * a.splits), (unsigned)a.c.Hk), dim3(64 * kWavesF),
+                       0, stream, a);
+  } else if (kernel == 2) {
+    if constexpr (D == 128) launch_tiles<D, 8>(a, stream);
+  } else {
+    launch_tiles<D, 4>(a, stream);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   hipLaunchKernelGGL(join_kernel<D>, dim3((unsigned)((a.T * a.H + 3) / 4)), dim3(256), 0, stream, a);
@@ -337,14 +725,15 @@ hipError_t launch_d(const AttnCacheArgs& a, hipStream_t stream) {
 
 size_t attention_cache_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_length,
                                        bool packed) {
-  const int s = plan_splits(T, B, H, Hk, max_length, packed);
-  return s > 1 ? (size_t)s * (size_t)T * (size_t)H * (size_t)(D + 2) * 4 : 0;
+  const AttnPlan p = plan_attention(T, B, H, Hk, D, max_length, packed);
+  return p.splits > 1 ? (size_t)p.splits * (size_t)T * (size_t)H * (size_t)(D + 2) * 4 : 0;
 }
 
 hipError_t launch_attention_cache(AttnCacheArgs a, int64_t max_length, hipStream_t stream) {
-  a.splits = plan_splits(a.T, a.B, a.H, a.c.Hk, max_length, a.cu != nullptr);
-  a.least = 4;
-  return a.c.D == 64 ? launch_d<64>(a, stream) : launch_d<128>(a, stream);
+  const AttnPlan p = plan_attention(a.T, a.B, a.H, a.c.Hk, a.c.D, max_length, a.cu != nullptr);
+  a.splits = p.splits;
+  a.least = p.least;
+  return a.c.D == 64 ? launch_d<64>(a, p.kernel, stream) : launch_d<128>(a, p.kernel, stream);
 }
 
 }  // namespace svdq
