@@ -96,7 +96,7 @@ __device__ __forceinline__ float across_rows(float v) {
 constexpr int kWavesF = 4;
 
 template <int D>
-__global__ __launch_bounds__(64 * kWavesF) void attention_few_kernel(AttnCacheArgs a) {
+__global__ __launch_bounds__(64 * kWavesF, D == 64 ? 4 : 2) void attention_few_kernel(AttnCacheArgs a) {
   constexpr int KP = D / 64;      // 16-byte pieces of a key per lane
   constexpr int JD = D / 16;      // 16-element blocks of the output
   __shared__ float sm[kWavesF][2][16];
@@ -145,51 +145,63 @@ __global__ __launch_bounds__(64 * kWavesF) void attention_few_kernel(AttnCacheAr
   const float slack = kSlackC / c;
   bool first = true;
 
-  for (int64_t k0 = k_begin + kTile * wave; k0 < k_end; k0 += kTile * kWavesF) {
-    // keys: this lane loads pieces of keys kk + 4 t; values: of keys kv .. kv + 15
-    const int64_t kk = k0 + 16 * (l16 >> 2) + (l16 & 3), kv = k0 + 16 * q;
-    const int pk = page_of(kk), pv = page_of(kv);
-    const int64_t pk_at = (int64_t)max(pk, 0) * a.c.Hk + hk, pv_at = (int64_t)max(pv, 0) * a.c.Hk + hk;
-    const uint8_t* kp = a.c.k + pk_at * page_bytes + (kk & (P - 1)) * D + 16 * q;
-    const uint8_t* vp = a.c.v + pv_at * page_bytes + l16 * P + (kv & (P - 1));
-    float ks = cache_scale(a.c.ks[pk_at]), vs = cache_scale(a.c.vs[pv_at]);
-    u32x4 wk[4][KP], wv[JD];
+  // A step's codes are requested while the step before is computed (keys as soon as its scores are there, values after
+  // its second product), their pages a step earlier still.
+  // This lane's pieces: keys kk + 4 t of the step, values of its keys kv .. kv + 15
+  const int kk = 16 * (l16 >> 2) + (l16 & 3), kv = 16 * q;
+  const int64_t k_first = k_begin + kTile * wave;
+  constexpr int kStride = kTile * kWavesF;
+  u32x4 wk[4][KP], wv[JD];
+  uint32_t ks, vs;               // scales; 256: no page
+  int pk = page_of(k_first + kk), pv = page_of(k_first + kv);
+  auto request_k = [&](int64_t k0) {
+    const int64_t at = (int64_t)max(pk, 0) * a.c.Hk + hk;
+    const uint8_t* p = a.c.k + at * page_bytes + (((int)k0 + kk) & (P - 1)) * D + 16 * q;
+    ks = a.c.ks[at];
+    if (pk < 0) ks = 256;
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int u = 0; u < KP; ++u) wk[t][u] = *reinterpret_cast<const u32x4*>(kp + 4 * t * D + 64 * u);
+      for (int u = 0; u < KP; ++u) wk[t][u] = *reinterpret_cast<const u32x4*>(p + 4 * t * D + 64 * u);
+  };
+  auto request_v = [&](int64_t k0) {
+    const int64_t at = (int64_t)max(pv, 0) * a.c.Hk + hk;
+    const uint8_t* p = a.c.v + at * page_bytes + l16 * P + (((int)k0 + kv) & (P - 1));
+    vs = a.c.vs[at];
+    if (pv < 0) vs = 256;
 #pragma unroll
-    for (int j = 0; j < JD; ++j) wv[j] = *reinterpret_cast<const u32x4*>(vp + 16 * j * P);
-    if (pk < 0) {
-      ks = 1.0f;
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int u = 0; u < KP; ++u) wk[t][u] = zero4();
-    }
-    // values past the sequence, or without a page, are zero: their probabilities are, but what
-    // the page holds there may be NaN
-    const int64_t left = pv < 0 ? 0 : L - kv;
-    if (left < 16) {
-      if (left <= 0) vs = 1.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int n = (int)max(min(left - 4 * i, (int64_t)4), (int64_t)0);
-        const uint32_t keep = n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
-#pragma unroll
-        for (int j = 0; j < JD; ++j) wv[j][i] &= keep;
-      }
-    }
-
+    for (int j = 0; j < JD; ++j) wv[j] = *reinterpret_cast<const u32x4*>(p + 16 * j * P);
+  };
+  if (k_first < k_end) {
+    request_k(k_first);
+    request_v(k_first);
+    pk = page_of(k_first + kStride + kk);
+    pv = page_of(k_first + kStride + kv);
+  }
+  for (int64_t k0 = k_first; k0 < k_end; k0 += kStride) {
     f32x4 x[4];
+    {
+      if (ks > 255u) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      x[t] = f32x4{};
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int u = 0; u < KP; ++u) {
-        x[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16_operand(wk[t][u][0], wk[t][u][1], ks), fq[2 * u], x[t], 0, 0, 0);
-        x[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16_operand(wk[t][u][2], wk[t][u][3], ks), fq[2 * u + 1], x[t], 0, 0, 0);
+          for (int u = 0; u < KP; ++u) wk[t][u] = zero4();
       }
+      const float sc = cache_scale(ks & 255u);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        x[t] = f32x4{};
+#pragma unroll
+        for (int u = 0; u < KP; ++u) {
+          x[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16_operand(wk[t][u][0], wk[t][u][1], sc), fq[2 * u], x[t], 0, 0, 0);
+          x[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16_operand(wk[t][u][2], wk[t][u][3], sc), fq[2 * u + 1], x[t], 0, 0, 0);
+        }
+      }
+    }
+    const bool more = k0 + kStride < k_end;
+    if (more) {
+      request_k(k0 + kStride);
+      pk = page_of(k0 + 2 * kStride + kk);
     }
     float mx = -__builtin_inff();
     if (k0 + kTile > last + 1) {
@@ -197,7 +209,7 @@ __global__ __launch_bounds__(64 * kWavesF) void attention_few_kernel(AttnCacheAr
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (kv + 4 * t + r > last) x[t][r] = -__builtin_inff();
+          if (k0 + kv + 4 * t + r > last) x[t][r] = -__builtin_inff();
     }
 #pragma unroll
     for (int t = 0; t < 4; ++t)
@@ -225,10 +237,27 @@ __global__ __launch_bounds__(64 * kWavesF) void attention_few_kernel(AttnCacheAr
     l += sum;
     const bf16x8 fp0 = __builtin_bit_cast(bf16x8, u32x4{p[0], p[1], p[2], p[3]});
     const bf16x8 fp1 = __builtin_bit_cast(bf16x8, u32x4{p[4], p[5], p[6], p[7]});
+    // values past the sequence, or without a page, are zero: their probabilities are, but what
+    // the page holds there may be NaN
+    const int64_t left = vs > 255u ? 0 : L - k0 - kv;
+    const float sc = cache_scale(left <= 0 ? 0u : vs & 255u);
+    if (left < 16) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = (int)max(min(left - 4 * i, (int64_t)4), (int64_t)0);
+        const uint32_t keep = n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
+#pragma unroll
+        for (int j = 0; j < JD; ++j) wv[j][i] &= keep;
+      }
+    }
 #pragma unroll
     for (int j = 0; j < JD; ++j) {
-      acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16_operand(wv[j][0], wv[j][1], vs), fp0, acc[j], 0, 0, 0);
-      acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16_operand(wv[j][2], wv[j][3], vs), fp1, acc[j], 0, 0, 0);
+      acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16_operand(wv[j][0], wv[j][1], sc), fp0, acc[j], 0, 0, 0);
+      acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16_operand(wv[j][2], wv[j][3], sc), fp1, acc[j], 0, 0, 0);
+    }
+    if (more) {
+      request_v(k0 + kStride);
+      pv = page_of(k0 + 2 * kStride + kv);
     }
   }
 
@@ -641,13 +670,18 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
   }
 }
 
-// The splits of a row (a query's head) together, a wave each.
+// The splits of a row (a query's head) together, a workgroup each: the splits' weights in LDS, then groups of D / 4
+// threads take every kGroups-th split, four elements a thread. (A wave per row that walked through its splits
+// took longer than the attention from 64 splits on.)
+constexpr int kMaxSplits = 256;
+
 template <int D>
 __global__ __launch_bounds__(256) void join_kernel(AttnCacheArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int64_t rows = a.T * a.H;
-  if (row >= rows) return;
+  constexpr int kGroups = 256 / (D / 4);
+  __shared__ float weight[kMaxSplits];
+  __shared__ float part[4];
+  __shared__ f32x4 sums[kGroups][D / 4];
+  const int64_t row = blockIdx.x, rows = a.T * a.H;
   const int64_t tok = row / a.H;
   int b = (int)tok;
   if (a.cu != nullptr) {
@@ -658,22 +692,42 @@ __global__ __launch_bounds__(256) void join_kernel(AttnCacheArgs a) {
   const int per = tiles_per_split(a, L);
   const int n = (int)(((L + kTile - 1) / kTile + per - 1) / per);   // splits with keys
   if (n <= 1) return;                                              // written whole
+  const int tid = threadIdx.x, e = tid % (D / 4), g = tid / (D / 4);
   const float c = a.scale * 1.4426950408889634f;
   const float* st = a.partial + (int64_t)a.splits * rows * D;
-  float M = kLowest;
-  for (int s = 0; s < n; ++s) M = fmaxf(M, st[2 * (s * rows + row)]);
-  float total = 0.0f, o[D / 64] = {};
-  for (int s = 0; s < n; ++s) {
-    const int64_t at = s * rows + row;
-    const float f = __builtin_amdgcn_exp2f((st[2 * at] - M) * c);
-    total += st[2 * at + 1] * f;
-#pragma unroll
-    for (int e = 0; e < D / 64; ++e) o[e] += a.partial[at * D + lane * (D / 64) + e] * f;
+  float m = kLowest, l = 0.0f;
+  if (tid < n) {
+    const float2 v = *reinterpret_cast<const float2*>(st + 2 * (tid * rows + row));
+    m = v.x;
+    l = v.y;
   }
+  f32x4 o = {};
+  const float top = wave_reduce<true>(m);   // NaN where one is
+  if ((tid & 63) == 0) part[tid >> 6] = top;
+  __syncthreads();
+  const float M = max_or_nan(max_or_nan(part[0], part[1]), max_or_nan(part[2], part[3]));
+  const float f = tid < n ? __builtin_amdgcn_exp2f((m - M) * c) : 0.0f;
+  if (tid < n) weight[tid] = f;
+  const float share = wave_reduce<false>(l * f);
+  __syncthreads();   // everyone has the maxima
+  if ((tid & 63) == 0) part[tid >> 6] = share;
+  const float* src = a.partial + row * D + 4 * e;
+#pragma unroll 4
+  for (int s = g; s < n; s += kGroups) {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(src + s * rows * D);
+    const float w = weight[s];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(v[i], w, o[i]);
+  }
+  sums[g][e] = o;
+  __syncthreads();
+  if (g > 0) return;
+#pragma unroll
+  for (int i = 1; i < kGroups; ++i) o += sums[i][e];
+  const float total = part[0] + part[1] + part[2] + part[3];
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-  uint16_t* dst = a.o + tok * a.o_st + (row - tok * a.H) * a.o_sh + lane * (D / 64);
-  if constexpr (D == 128) *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(o[0] * inv, o[1] * inv);
-  else *dst = (uint16_t)f32_to_bf16_rne(o[0] * inv);
+  *reinterpret_cast<u32x2*>(a.o + tok * a.o_st + (row - tok * a.H) * a.o_sh + 4 * e) =
+      u32x2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
 }
 
 // Rows of a sequence and key head on average, and the kernel for them: 0 few, 1 tiles by four waves, 2 by eight.
@@ -691,6 +745,7 @@ AttnPlan plan_attention(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, 
   p.least = 4;
   int64_t s = blocks >= want ? 1 : want / blocks;
   if (s > (tiles + p.least - 1) / p.least) s = (tiles + p.least - 1) / p.least;
+  if (s > kMaxSplits) s = kMaxSplits;
   p.splits = (int)(s < 1 ? 1 : s);
   return p;
 }
@@ -717,7 +772,7 @@ hipError_t launch_d(const AttnCacheArgs& a, int kernel, hipStream_t stream) {
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL(join_kernel<D>, dim3((unsigned)((a.T * a.H + 3) / 4)), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL(join_kernel<D>, dim3((unsigned)(a.T * a.H)), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
