@@ -134,6 +134,14 @@ __global__ __launch_bounds__(256) void quant_weight_fp8_kernel(const uint16_t* _
 __device__ __forceinline__ void f8_to_lds(__amdgpu_buffer_rsrc_t r, void* lds, int voff, int soff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, F8_LDS_PTR(lds), 16, voff, soff, 0, 0);
 }
+__device__ __forceinline__ void f8_to_lds4(__amdgpu_buffer_rsrc_t r, void* lds, int voff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, F8_LDS_PTR(lds), 4, voff, 0, 0, 0);
+}
+template <int N>
+__device__ __forceinline__ void f8_wait_copies() {   // vmcnt(N), lgkmcnt(0)
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
+}
 __device__ __forceinline__ f32x16 f8_mfma32(i32x8 a, i32x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);   // e4m3 both, unscaled
 }
@@ -148,7 +156,7 @@ __device__ __forceinline__ void f8_barrier() {   // as in gemm_bf16.hip: the wai
 }
 
 // Tile of a workgroup: WM x WN waves of TM x TN blocks of 32 tokens x 32 channels. A panel is the 128 codes of a
-// scale block: chunks of 32 rows x 128 bytes, row r at r * 128 with its eight 16-byte pieces
+// scale block and its scales: chunks of 32 rows x 128 bytes, row r at r * 128 with its eight 16-byte pieces
 // permuted by piece ^ swz(r), so that an operand read (32 rows, one piece each) meets every LDS
 // bank evenly and a copy reads whole 128-byte row segments.
 template <int WM, int WN, int TM, int TN, int S>
@@ -157,11 +165,12 @@ struct F8Cfg {
   static constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN;
   static constexpr int kChunksA = BM / 32, kChunks = (BM + BN) / 32;
   static constexpr int kChunkBytes = 4096;
-  static constexpr int kStageBytes = kChunks * kChunkBytes;
+  static constexpr int kScalesA = kChunks * kChunkBytes;         // the tokens' scales
+  static constexpr int kStageBytes = kScalesA + BM * 4;
   static constexpr int kCopies = kChunks * 4;                    // 1 KB copies of a panel
   static constexpr int kPerWave = kCopies / kWaves;
   static constexpr int kOutBytes = kWaves * 32 * (32 * TN + 8) * 2;   // output staging
-  static constexpr int kLdsBytes = S * kStageBytes > kOutBytes ? S * kStageBytes : kOutBytes;
+  static constexpr int kLdsBytes = S * kStageBytes + 512 > kOutBytes ? S * kStageBytes + 512 : kOutBytes;
   static_assert(kCopies % kWaves == 0, "copies per wave");
 };
 
@@ -174,7 +183,7 @@ struct F8Split {
 template <int WM, int WN, int TM, int TN, int S>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_kernel(Fp8GemmArgs a, F8Split sp) {
   using C = F8Cfg<WM, WN, TM, TN, S>;
-  static_assert(S == 2, "two stages");
+  static_assert(S >= 2 && S <= 4, "stages");
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -205,40 +214,44 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_kernel(Fp8GemmArgs a, F
   const int p1 = min(p0 + sp.panels, KB);
 
   auto swz = [](int r) { return (r ^ (r >> 3)) & 7; };
-  // copy c of a panel: chunk c / 4, rows 8 (c % 4) .. + 7; an offset past the buffer reads
-  // zero (rows past the tensor, and pieces past K in the last panel)
+  // Copy u of a wave: its 8 rows are 8 kWaves further on with each u, at the same pieces. Rows past the tensor are past
+  // the buffer and read zero; so do pieces past K in the last panel, at an offset that is.
   constexpr int kPast = 0x7FFFFFF0;
-  int off[C::kPerWave];
-#pragma unroll
-  for (int u = 0; u < C::kPerWave; ++u) {
-    const int c = wave + C::kWaves * u;
-    const int r32 = 8 * (c & 3) + (lane >> 3);
-    const bool is_a = c / 4 < C::kChunksA;
-    const int row = 32 * (is_a ? c / 4 : c / 4 - C::kChunksA) + r32;
-    off[u] = row < (is_a ? rows_a : rows_b) ? row * K + 16 * ((lane & 7) ^ swz(r32)) : kPast;
-  }
-  auto load_panel = [&](int kp) {
+  static_assert(C::kWaves % 4 == 0 && C::kChunksA * 4 % C::kWaves == 0, "a wave's copies are of the tokens, then of the weight");
+  constexpr int kCopiesA = C::kChunksA * 4 / C::kWaves;
+  const int piece = 16 * ((lane & 7) ^ swz(8 * (wave & 3) + (lane >> 3)));
+  int copy_at = (8 * wave + (lane >> 3)) * K + piece;
+  const int copy_step = 8 * C::kWaves * K;
+  // The scales of a panel: 64 tokens' by each of the first waves; the tile's channels' for 16 panels at a time, by the last
+  // wave, panel i of block b in lane 16 b + i (two places in turn).
+  const int as_off = 4 * (m0 + 64 * wave + lane);
+  const int nb0 = n0 / 128, n_blocks = min((N + 127) / 128 - nb0, 4);
+  const __amdgpu_buffer_rsrc_t rws = make_rsrc(a.wscales + (size_t)nb0 * KB, (uint32_t)n_blocks * (uint32_t)KB * 4u);
+  const int ws_off = 4 * ((lane >> 4) * KB + (lane & 15));
+  static_assert(C::BN <= 384, "at most 4 blocks of 128 channels, aligned to 64");
+  // Panel kp's copies, part `part` of kParts (all but the first go out between the next panel's products); panels past
+  // the last land as zeros: no branch.
+  constexpr int kParts = TN >= 3 ? 3 : TN;
+  auto load_panel = [&](int kp, int part) {
     uint8_t* st = smem + ((kp - p0) % S) * C::kStageBytes;
     const int k0 = kp * 128;
-    const bool tail = k0 + 128 > K;
+    const bool none = kp >= p1;
+    const bool past = none || k0 + piece >= K;
+    asm volatile("" : "+v"(copy_at));   // the copies' offsets are made here, not kept
 #pragma unroll
     for (int u = 0; u < C::kPerWave; ++u) {
-      const int c = wave + C::kWaves * u;
-      int v = off[u];
-      if (tail && k0 + 16 * ((lane & 7) ^ swz(8 * (c & 3) + (lane >> 3))) >= K) v = kPast;
-      if (c / 4 < C::kChunksA) f8_to_lds(ra, st + c * 1024, v, k0);
-      else f8_to_lds(rb, st + c * 1024, v, k0);
+      if (u * kParts / C::kPerWave != part) continue;
+      const bool is_a = u < kCopiesA;
+      const int v = past ? kPast : copy_at + (is_a ? u : u - kCopiesA) * copy_step;
+      f8_to_lds(is_a ? ra : rb, st + (wave + C::kWaves * u) * 1024, v, k0);
+    }
+    if (part == 0) {
+      if (wave < C::BM / 64)
+        f8_to_lds4(make_rsrc(a.ascales + (size_t)(none ? 0 : kp) * M, (uint32_t)M * 4u), st + C::kScalesA + 256 * wave, as_off);
+      if (wave == C::kWaves - 1 && (kp - p0) % 16 == 0)
+        f8_to_lds4(rws, smem + S * C::kStageBytes + ((kp - p0) & 16) * 16, ws_off + 4 * (none ? 0 : kp));
     }
   };
-
-  // a panel's scales: this lane's token of each block of 32, and the wave's channels' (one block of 128
-  // holds whole blocks of 32)
-  const float* as_at[TM];
-  const float* ws_at[TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i) as_at[i] = a.ascales + min(m_w + 32 * i + l32, M - 1);
-#pragma unroll
-  for (int j = 0; j < TN; ++j) ws_at[j] = a.wscales + (size_t)(min(n_w + 32 * j, N - 1) / 128) * KB;
 
   f32x16 acc[TM][TN];
 #pragma unroll
@@ -246,42 +259,110 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_kernel(Fp8GemmArgs a, F
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = f32x16{};
 
-  int frag[4];   // this lane's operand pieces (row l32, piece 2 t + h) within a chunk
-#pragma unroll
-  for (int t = 0; t < 4; ++t) frag[t] = l32 * 128 + (((2 * t + h) ^ swz(l32)) * 16);
+  // this lane's operand pieces (row l32, piece 2 t + h) within a chunk: 32 t by exclusive or from t = 0
+  int frag = l32 * 128 + ((h ^ swz(l32)) * 16);
   auto operand = [&](const uint8_t* chunk, int s) {
-    return join8(*reinterpret_cast<const i32x4*>(chunk + frag[2 * s]),
-                 *reinterpret_cast<const i32x4*>(chunk + frag[2 * s + 1]));
+    return join8(*reinterpret_cast<const i32x4*>(chunk + (frag ^ (64 * s))),
+                 *reinterpret_cast<const i32x4*>(chunk + (frag ^ (64 * s + 32))));
   };
+  const int chunk_m = wave_m * TM * C::kChunkBytes, chunk_n = (C::kChunksA + wave_n * TN) * C::kChunkBytes;
 
-  if (p0 < p1) load_panel(p0);
-  for (int kp = p0; kp < p1; ++kp) {
-    float as[TM], ws[TN];
+  // Block j of channels: the products of both halves of the panel with each block of tokens, then the sums times their
+  // scales. A sum is added while another's matrix instruction runs (the first one's beside the last one's second
+  // half, the others' beside the next block's first halves), and each operand is read for the next
+  // block (or the next panel) as soon as its last product is issued. One barrier a panel, before its last block: it frees
+  // the panel, which is read to its end, and publishes the next one.
+  i32x8 ft[TM][2], fw[2];
+  f32x16 sum[TM];
+  float as[TM], ws;
+  const int as_lane = C::kScalesA + 4 * (wave_m * TM * 32 + l32);
+  auto read_as = [&](const uint8_t* st, int i) { return *reinterpret_cast<const float*>(st + as_lane + 128 * i); };
+  auto read_ws = [&](int kp, int j) {   // a block of 128 holds whole blocks of 32
+    const int at = kp - p0;
+    return *reinterpret_cast<const float*>(smem + S * C::kStageBytes + (at & 16) * 16 + 64 * ((n_w + 32 * j) / 128 - nb0) +
+                                           4 * (at & 15));
+  };
+  auto add_sum = [&](int i, int j, float s) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) as[i] = as_at[i][(size_t)kp * M];
+    for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_fmaf(sum[i][r], s, acc[i][j][r]);
+    asm volatile("" : "+v"(acc[i][j]));   // added here: the sums' registers are free
+  };
+  constexpr int kFirst = (C::kPerWave + kParts - 1) / kParts;   // copies of a panel's first part
+  if (p0 < p1) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) ws[j] = ws_at[j][kp];
-    __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0), lgkmcnt(0)
-    f8_barrier();   // panel kp visible to every wave, the other stage is read to its end
-    if (kp + 1 < p1) load_panel(kp + 1);
-    const uint8_t* st = smem + ((kp - p0) & 1) * C::kStageBytes;
-    i32x8 ft[TM][2];
+    for (int u = 0; u < S; ++u)
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+      for (int part = 0; part < (u < S - 1 ? kParts : 1); ++part) load_panel(p0 + u, part);
+    // (waves with copies of scales wait for a little more than panel p0)
+    f8_wait_copies<(S - 2) * C::kPerWave + kFirst>();
+    f8_barrier();
 #pragma unroll
-      for (int s = 0; s < 2; ++s) ft[i][s] = operand(st + (wave_m * TM + i) * C::kChunkBytes, s);
+    for (int s = 0; s < 2; ++s) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const uint8_t* chunk = st + (C::kChunksA + wave_n * TN + j) * C::kChunkBytes;
-      const i32x8 fw0 = operand(chunk, 0), fw1 = operand(chunk, 1);
+      for (int i = 0; i < TM; ++i) ft[i][s] = operand(smem + chunk_m + i * C::kChunkBytes, s);
+      fw[s] = operand(smem + chunk_n, s);
+    }
 #pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const f32x16 sum = f8_mfma32(fw1, ft[i][1], f8_mfma32(fw0, ft[i][0], f32x16{}));
-        const float s = as[i] * ws[j];
+    for (int i = 0; i < TM; ++i) as[i] = read_as(smem, i);
+    ws = read_ws(p0, 0);
+    float scale[TM];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_fmaf(sum[r], s, acc[i][j][r]);
+    for (int i = 0; i < TM; ++i) {
+      sum[i] = f32x16{};
+      scale[i] = 0.0f;
+    }
+    for (int kp = p0; kp < p1; ++kp) {
+      const uint8_t* cur = smem + ((kp - p0) % S) * C::kStageBytes;
+      const uint8_t* nxt = smem + ((kp - p0 + 1) % S) * C::kStageBytes;
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const bool last = j == TN - 1;
+        if (last) {
+          f8_wait_copies<(S - 2) * C::kPerWave>();   // panel kp + 1 has landed, panel kp is read
+          f8_barrier();
+          load_panel(kp + S, 0);
+        } else if (j + 1 < kParts) {
+          load_panel(kp + S - 1, j + 1);
+        }
+        // (after the last panel: whatever its stage holds, not used)
+        const uint8_t* next_w = last ? nxt + chunk_n : cur + chunk_n + (j + 1) * C::kChunkBytes;
+        asm volatile("" : "+v"(frag));
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          if (i > 0) add_sum(i, (j + TN - 1) % TN, scale[i]);
+          scale[i] = as[i] * ws;
+          sum[i] = f8_mfma32(fw[0], ft[i][0], f32x16{});
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        fw[0] = operand(next_w, 0);
+        if (last) {
+#pragma unroll
+          for (int i = 0; i < TM; ++i) ft[i][0] = operand(nxt + chunk_m + i * C::kChunkBytes, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          sum[i] = f8_mfma32(fw[1], ft[i][1], sum[i]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        fw[1] = operand(next_w, 1);
+        if (last) {
+#pragma unroll
+          for (int i = 0; i < TM; ++i) ft[i][1] = operand(nxt + chunk_m + i * C::kChunkBytes, 1);
+        }
+        ws = read_ws(last ? kp + 1 : kp, last ? 0 : j + 1);
+        if (last) {
+#pragma unroll
+          for (int i = 0; i < TM; ++i) as[i] = read_as(nxt, i);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        add_sum(0, j, scale[0]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
+#pragma unroll
+    for (int i = 1; i < TM; ++i) add_sum(i, TN - 1, scale[i]);
+    f8_wait_copies<0>();   // nothing lands in LDS from here on
   }
 
   // this lane holds channels n_w + 32 j + 8 (r / 4) + 4 h + r % 4 of token m_w + 32 i + l32
@@ -522,10 +603,11 @@ struct F8Plan {
 };
 
 F8Plan plan_fp8(int64_t M, int64_t N, int64_t K) {
+  static const struct { int bm, bn; } shapes[] = {
+      {256, 320}, {256, 256}, {256, 128}, {192, 128}, {128, 128}, {128, 64}, {64, 64}};
   const int64_t panels = (K + 127) / 128;
-  const int shape = M > 1024 ? 0 : M > 64 ? 1 : 2;
-  static const int bm[] = {256, 128, 64}, bn[] = {256, 128, 64};
-  const int64_t tiles = ((M + bm[shape] - 1) / bm[shape]) * ((N + bn[shape] - 1) / bn[shape]);
+  const int shape = M > 1024 ? 1 : M > 64 ? 4 : 6;
+  const int64_t tiles = ((M + shapes[shape].bm - 1) / shapes[shape].bm) * ((N + shapes[shape].bn - 1) / shapes[shape].bn);
   int64_t sp = 1;
   while (sp < 8 && tiles * sp * 2 <= 512 && panels >= 4 * sp) sp *= 2;
   const int64_t per = (panels + sp - 1) / sp;
@@ -586,9 +668,13 @@ hipError_t launch_gemm_fp8(const Fp8GemmArgs& a, void* workspace, hipStream_t st
   if (few_tokens(a.M, a.N, a.K)) return launch_few(a, nullptr, nullptr, stream);
   const F8Plan p = plan_fp8(a.M, a.N, a.K);
   const F8Split sp{p.panels, p.splits, static_cast<float*>(workspace)};
-  hipError_t e = p.shape == 0   ? launch_fp8_cfg<4, 2, 2, 4, 2>(a, sp, stream)
-                 : p.shape == 1 ? launch_fp8_cfg<2, 2, 2, 2, 2>(a, sp, stream)
-                                : launch_fp8_cfg<2, 2, 1, 1, 2>(a, sp, stream);
+  hipError_t e = p.shape == 0   ? launch_fp8_cfg<4, 2, 2, 5, 2>(a, sp, stream)
+                 : p.shape == 1 ? launch_fp8_cfg<4, 2, 2, 4, 2>(a, sp, stream)
+                 : p.shape == 2 ? launch_fp8_cfg<4, 2, 2, 2, 3>(a, sp, stream)
+                 : p.shape == 3 ? launch_fp8_cfg<2, 2, 3, 2, 2>(a, sp, stream)
+                 : p.shape == 4 ? launch_fp8_cfg<2, 2, 2, 2, 2>(a, sp, stream)
+                 : p.shape == 5 ? launch_fp8_cfg<2, 2, 2, 1, 3>(a, sp, stream)
+                                : launch_fp8_cfg<2, 2, 1, 1, 4>(a, sp, stream);
   if (e != hipSuccess || p.splits == 1) return e;
   const int w = a.N % 4 == 0 ? 4 : 1;
   const dim3 grid((unsigned)((a.M * (a.N / w) + 255) / 256));
