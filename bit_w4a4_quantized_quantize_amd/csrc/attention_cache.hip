@@ -82,10 +82,10 @@ __device__ __forceinline__ int tiles_per_split(const AttnCacheArgs& a, int64_t L
 // sum or maximum over the four lanes l16, l16 + 16, .. of a row
 template <bool MAX>
 __device__ __forceinline__ float across_rows(float v) {
-  const float u = __shfl_xor(v, 16);
-  v = MAX ? fmaxf(v, u) : v + u;
-  const float w = __shfl_xor(v, 32);
-  return MAX ? fmaxf(v, w) : v + w;
+  const Pair p = halves16(v);
+  v = MAX ? fmaxf(p.a, p.b) : p.a + p.b;
+  const Pair r = halves32(v);
+  return MAX ? fmaxf(r.a, r.b) : r.a + r.b;
 }
 
 // Few rows. The four waves of a workgroup take 16 rows together, steps of 64 keys in turn; a step's operands
@@ -494,8 +494,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
     }
   };
   auto raise = [&](float mx) {
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
-    const float mn = fmaxf(m, mx);
+    const Pair both = halves32(mx);
+    const float mn = fmaxf(m, fmaxf(both.a, both.b));
     const float alpha = __builtin_amdgcn_exp2f((m - mn) * c);
     m = mn;
     l *= alpha;
@@ -629,7 +629,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
     end_step(kt);
   }
 
-  l += __shfl_xor(l, 32);
+  const Pair sums = halves32(l);
+  l = sums.a + sums.b;
   if (!only) {   // this lane holds elements 32 j + 8 (r / 4) + 4 h + r % 4 of its row
     if (row0 + l32 >= n_rows) return;
     const int64_t at = ((int64_t)split * a.T + rb.tok0 + query) * a.H + head;

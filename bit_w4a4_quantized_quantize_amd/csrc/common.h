@@ -213,6 +213,19 @@ __device__ __forceinline__ float wave_reduce(float v) {
   return both(both(r0, r1), both(r2, r3));
 }
 
+// The two values that the lanes l and l ^ 32 (l and l ^ 16) hold, in both of them, without a trip through LDS.
+struct Pair {
+  float a, b;
+};
+__device__ __forceinline__ Pair halves32(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return Pair{__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+__device__ __forceinline__ Pair halves16(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return Pair{__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+
 // Position of `x` among not decreasing device offsets cu[0 .. n - 1]: the number of them
 // that are <= x. The wave's 64 lanes probe together, so up to 64 offsets cost one load.
 // Offsets out of order give some number in 0..n.

@@ -226,8 +226,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_kernel(Fp8GemmArgs a, F
   // wave, panel i of block b in lane 16 b + i (two places in turn).
   const int as_off = 4 * (m0 + 64 * wave + lane);
   const int nb0 = n0 / 128, n_blocks = min((N + 127) / 128 - nb0, 4);
-  const __amdgpu_buffer_rsrc_t rws = make_rsrc(a.wscales + (size_t)nb0 * KB, (uint32_t)n_blocks * (uint32_t)KB * 4u);
   const int ws_off = 4 * ((lane >> 4) * KB + (lane & 15));
+  const __amdgpu_buffer_rsrc_t rws = make_rsrc(a.wscales + (size_t)nb0 * KB, (uint32_t)n_blocks * (uint32_t)KB * 4u);
   static_assert(C::BN <= 384, "at most 4 blocks of 128 channels, aligned to 64");
   // Panel kp's copies, part `part` of kParts (all but the first go out between the next panel's products); panels past
   // the last land as zeros: no branch.
@@ -405,11 +405,19 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_kernel(Fp8GemmArgs a, F
 #pragma unroll
       for (int r = 0; r < 16; r += 4) {
         const int c = 32 * j + 2 * r + 4 * h;
-        float v[4];
+        float v[4] = {acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]};
+        if (a.bias != nullptr) {
+          const int n = n_w + c;
+          if (N % 4 == 0) {
+            const u32x2 b = n < N ? *reinterpret_cast<const u32x2*>(a.bias + n) : u32x2{0u, 0u};
+            v[0] += bf16lo_to_f32(b[0]);
+            v[1] += bf16hi_to_f32(b[0]);
+            v[2] += bf16lo_to_f32(b[1]);
+            v[3] += bf16hi_to_f32(b[1]);
+          } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = acc[i][j][r + e];
-          if (a.bias != nullptr) v[e] += n_w + c + e < N ? bf16lo_to_f32(a.bias[n_w + c + e]) : 0.0f;
+            for (int e = 0; e < 4; ++e) v[e] += n + e < N ? bf16lo_to_f32(a.bias[n + e]) : 0.0f;
+          }
         }
         uint16_t* dst = stage + l32 * kPitch + shift + c;
         const uint32_t w0 = pack_bf16x2(v[0], v[1]), w1 = pack_bf16x2(v[2], v[3]);
@@ -481,14 +489,20 @@ __global__ __launch_bounds__(256) void fp8_reduce_kernel(Fp8GemmArgs a, const fl
 // Few tokens (M <= 16 MT): bound by the weight's bytes, which stream past the tokens once, straight
 // from memory. A workgroup takes 16 output channels, its eight waves share k in blocks of 128;
 // v_mfma_f32_16x16x128_f8f6f4 with the weight rows as A and the tokens as B, and the waves' sums
-// meet in LDS. FROM_X: the activations come as x; a block's maximum lies within the 32 channels of
-// four lanes, so every wave makes its own operands in registers.
+// meet in LDS. QUANT: the activations come as x, and each workgroup first makes all the tokens' codes
+// for itself in LDS (small M * K: cheaper than a launch of its own), with the first weight blocks already on their way.
+// LEAD: weight blocks in flight per wave.
 constexpr int kFewWaves = 8;
 
-template <int MT, int LEAD, bool FROM_X, bool SMOOTH>
+__host__ __device__ constexpr int few_pitch(int K) { return (K + 255) / 256 * 256 + 16; }   // LDS bytes of a token
+// codes, then scales [ceil(K / 128), M]
+__host__ __device__ constexpr int few_lds(int M, int K) { return M * (few_pitch(K) + 4 * ((K + 127) / 128)); }
+
+template <int MT, int LEAD, bool QUANT, bool SMOOTH>
 __global__ __launch_bounds__(64 * kFewWaves) void gemm_fp8_few_kernel(Fp8GemmArgs a, const uint16_t* __restrict__ x,
                                                                      const uint16_t* __restrict__ smooth) {
   __shared__ f32x4 part[kFewWaves][MT][64];
+  extern __shared__ __attribute__((aligned(16))) uint8_t tok[];
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lane = tid & 63;
@@ -498,62 +512,96 @@ __global__ __launch_bounds__(64 * kFewWaves) void gemm_fp8_few_kernel(Fp8GemmArg
   const int n0 = (int)blockIdx.x * 16;
   // a lane's operand: pieces q and q + 4 of the row's eight 16-byte pieces; K % 16 == 0, so a piece is
   // entirely before or past K, and zero past it
-  const uint8_t* pw = a.weight + (size_t)min(n0 + l16, N - 1) * K + 16 * q;
   auto codes_at = [&](const uint8_t* row, int p) {
     const i32x4 zero = {};
     const int k = 128 * p + 16 * q;
     return join8(k < K ? *reinterpret_cast<const i32x4*>(row + 128 * p) : zero,
                  k + 64 < K ? *reinterpret_cast<const i32x4*>(row + 128 * p + 64) : zero);
   };
-  const float* ws = a.wscales + (size_t)(n0 / 128) * KB;
+  const uint8_t* pw = a.weight + (size_t)min(n0 + l16, N - 1) * K + 16 * q;
+  const float* ws_at = a.wscales + (size_t)(n0 / 128) * KB;
+  constexpr int kStep = kFewWaves * LEAD;
   i32x8 fw[LEAD];
+  float ws[LEAD];
+  auto request = [&](int u, int p) {
+    if (p < KB) {
+      fw[u] = codes_at(pw, p);
+      ws[u] = ws_at[p];
+    }
+  };
 #pragma unroll
-  for (int u = 0; u < LEAD; ++u) fw[u] = codes_at(pw, wave + kFewWaves * u);
+  for (int u = 0; u < LEAD; ++u) request(u, wave + kFewWaves * u);
 
+  const uint8_t* pt[MT];
+  const float* as_at = a.ascales;
+  if constexpr (QUANT) {
+    // 16 lanes a block, 8 channels each; zeros up to the end of a row's last block
+    const int pitch = few_pitch(K), items = M * KB;
+    float* scales = reinterpret_cast<float*>(tok + M * pitch);
+    constexpr int kGroups = 4 * kFewWaves, U = 4;   // U blocks of a thread with their loads in flight together
+    for (int g0 = 4 * wave; g0 < items; g0 += U * kGroups) {   // the wave's four
+      u32x4 xw[U], sw[U];
+      int at[U], to[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (g0 + u * kGroups >= items) break;
+        const int g = min(g0 + u * kGroups + q, items - 1);   // (past the end: the last one again)
+        const int m = M == 1 ? 0 : g / KB, p = g - m * KB, k = 128 * p + 8 * (tid & 15);
+        to[u] = m * pitch + k;
+        at[u] = p * M + m;
+        xw[u] = k < K ? *reinterpret_cast<const u32x4*>(x + (size_t)m * K + k) : zero4();
+        sw[u] = SMOOTH && k < K ? *reinterpret_cast<const u32x4*>(smooth + k) : zero4();
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (g0 + u * kGroups >= items) break;
+        float v[8], amax = 0.0f;
+        f8_scaled8<SMOOTH>(xw[u], sw[u], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = max_or_nan(amax, fabsf(v[e]));
+        const Fp8Scale s = fp8_scale(max_row16(amax));
+        *reinterpret_cast<u32x2*>(tok + to[u]) = fp8_codes8(v, s.inv);
+        if ((tid & 15) == 0) scales[at[u]] = s.scale;
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t) pt[t] = tok + min(16 * t + l16, M - 1) * pitch + 16 * q;
+    as_at = scales;
+    __syncthreads();
+  } else {
+#pragma unroll
+    for (int t = 0; t < MT; ++t) pt[t] = a.codes + (size_t)min(16 * t + l16, M - 1) * K + 16 * q;
+  }
   f32x4 acc[MT] = {};
-  for (int p = wave; p < KB; p += kFewWaves * LEAD) {
+  for (int p = wave; p < KB; p += kStep) {
+    i32x8 ft[LEAD][MT];
+    float as[LEAD][MT];
 #pragma unroll
     for (int u = 0; u < LEAD; ++u) {
       const int pu = p + kFewWaves * u;
-      const float wsu = ws[min(pu, KB - 1)];
+      if (pu < KB) {
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const int m = min(16 * t + l16, M - 1);
-        i32x8 ft;
-        float as;
-        if constexpr (FROM_X) {
-          float v[4][8], amax = 0.0f;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int k = 128 * pu + 64 * (c >> 1) + 16 * q + 8 * (c & 1);
-            const bool in = k < K;
-            f8_scaled8<SMOOTH>(in ? *reinterpret_cast<const u32x4*>(x + (size_t)m * K + k) : zero4(),
-                               SMOOTH && in ? *reinterpret_cast<const u32x4*>(smooth + k) : zero4(), v[c]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) amax = max_or_nan(amax, fabsf(v[c][e]));
-          }
-          amax = max_or_nan(amax, __shfl_xor(amax, 16));
-          amax = max_or_nan(amax, __shfl_xor(amax, 32));
-          const Fp8Scale s = fp8_scale(amax);
-          as = s.scale;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const u32x2 w = fp8_codes8(v[c], s.inv);
-            ft[2 * c] = (int)w[0];
-            ft[2 * c + 1] = (int)w[1];
-          }
-        } else {
-          ft = codes_at(a.codes + (size_t)m * K + 16 * q, pu);
-          as = a.ascales[(size_t)min(pu, KB - 1) * M + m];
+        for (int t = 0; t < MT; ++t) {
+          ft[u][t] = QUANT ? join8(*reinterpret_cast<const i32x4*>(pt[t] + 128 * pu),
+                                   *reinterpret_cast<const i32x4*>(pt[t] + 128 * pu + 64))
+                           : codes_at(pt[t], pu);
+          as[u][t] = as_at[(size_t)pu * M + min(16 * t + l16, M - 1)];
         }
-        const f32x4 sum = f8_mfma16(fw[u], ft, f32x4{});
-        const float s = pu < KB ? as * wsu : 0.0f;
-        if (pu < KB) {
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < LEAD; ++u) {
+      const int pu = p + kFewWaves * u;
+      if (pu < KB) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          const f32x4 sum = f8_mfma16(fw[u], ft[u][t], f32x4{});
+          const float s = as[u][t] * ws[u];
 #pragma unroll
           for (int r = 0; r < 4; ++r) acc[t][r] = __builtin_fmaf(sum[r], s, acc[t][r]);
         }
+        request(u, pu + kStep);
       }
-      fw[u] = codes_at(pw, pu + kFewWaves * LEAD);
     }
   }
 #pragma unroll
@@ -583,35 +631,75 @@ hipError_t launch_few_cfg(const Fp8GemmArgs& a, const uint16_t* x, const uint16_
   const dim3 grid((unsigned)((a.N + 15) / 16)), block(64 * kFewWaves);
   if (x == nullptr)
     hipLaunchKernelGGL((gemm_fp8_few_kernel<MT, LEAD, false, false>), grid, block, 0, stream, a, x, smooth);
-  else if (smooth == nullptr)
-    hipLaunchKernelGGL((gemm_fp8_few_kernel<MT, LEAD, true, false>), grid, block, 0, stream, a, x, smooth);
-  else
-    hipLaunchKernelGGL((gemm_fp8_few_kernel<MT, LEAD, true, true>), grid, block, 0, stream, a, x, smooth);
+  if constexpr (MT == 1) {   // few_from_x: at most 16 tokens
+    const unsigned lds = (unsigned)few_lds((int)a.M, (int)a.K);
+    if (x != nullptr && smooth == nullptr)
+      hipLaunchKernelGGL((gemm_fp8_few_kernel<MT, LEAD, true, false>), grid, block, lds, stream, a, x, smooth);
+    else if (x != nullptr)
+      hipLaunchKernelGGL((gemm_fp8_few_kernel<MT, LEAD, true, true>), grid, block, lds, stream, a, x, smooth);
+  }
   return hipGetLastError();
 }
 
 hipError_t launch_few(const Fp8GemmArgs& a, const uint16_t* x, const uint16_t* smooth, hipStream_t stream) {
-  return launch_few_cfg<1, 4>(a, x, smooth, stream);
+  return a.M <= 16   ? launch_few_cfg<1, 4>(a, x, smooth, stream)
+         : a.M <= 32 ? launch_few_cfg<2, 2>(a, x, smooth, stream)
+         : a.M <= 48 ? launch_few_cfg<3, 2>(a, x, smooth, stream)
+                     : launch_few_cfg<4, 2>(a, x, smooth, stream);
 }
 
-bool few_tokens(int64_t M, int64_t, int64_t) { return M <= 16; }
-bool few_from_x(int64_t M, int64_t N, int64_t K) { return few_tokens(M, N, K); }
+// Every workgroup reads all the tokens' codes, and one of 16 channels works through all of k: above 8 tokens
+// only while both are few (with the quantisation, here and in tiles: 32 x 3840 for 3840 channels 12.4 and 13.7 us, 64 x
+// 3840 16.5 and 15.1, 64 x 2064 for 1300 8.3 and 11.2, 16 x 10240 for 3840 18.1 and 19.4, 16 x 3840 for 10240 18.7
+// and 18.3). With up to 8 the tiles gain nothing (8 x 3840 for 10240: 16.3 and 17.9).
+bool few_tokens(int64_t M, int64_t N, int64_t K) {
+  return M <= 8 || (M <= 64 && M * K <= 163840 && N * K <= (int64_t(1) << 24));
+}
+
+// The layer from x in one launch: every workgroup makes the tokens' codes again, so only while they are few.
+// Against two launches (on the device): 6.0 and 8.2 us for 1 x 3840 (3840 channels), 12.5 and 14.1 for 1 x 10240, 8.6 and 9.5
+// for 8 x 3840, 16.3 and 16.0 for 4 x 10240; another 3 us of the caller's time where the calls are not in a graph.
+bool few_from_x(int64_t M, int64_t N, int64_t K) {
+  // codes, scales and sums together stay inside 64 KB of LDS
+  return M <= 16 && few_tokens(M, N, K) && M * K <= 32768 && few_lds((int)M, (int)K) <= 56 * 1024;
+}
 
 struct F8Plan {
   int shape;     // index into the table
   int splits, panels;
 };
 
+// Tile shape and split of k by an estimate in microseconds, fitted to times with weights from memory (M from 20 to
+// 6000; eight weights from 1300 x 2064 to 10240 x 3840 and 3840 x 10240; every shape with k split 1 to 8
+// ways: profiles/gemm_fp8_tile_grid.txt). A panel takes a workgroup at least `least`, and each of the
+// ceil(workgroups / 256) rounds `share` + `full` times the share of the CUs that work (the more do, the slower
+// each: power and the L2s); 4.2 us start and end a product; a split adds 0.9 us and the partial sums' traffic.
+// As for the 8-bit integers, a call that is not in a graph takes its caller about 10 us and 3 more for a split's
+// launch, so a split pays only where the device takes longer than that. On the device alone the choice is within
+// 0.3% of the best on average and 6% at worst. The estimate without `full` was 4% off on average.
 F8Plan plan_fp8(int64_t M, int64_t N, int64_t K) {
-  static const struct { int bm, bn; } shapes[] = {
-      {256, 320}, {256, 256}, {256, 128}, {192, 128}, {128, 128}, {128, 64}, {64, 64}};
+  static const struct { int bm, bn; double least, share, full; } shapes[] = {
+      {256, 320, 1.56, 1.33, 0.64}, {256, 256, 1.45, 1.30, 0.49}, {256, 128, 0.86, 0.90, 0.31},
+      {128, 128, 0.46, 0.49, 0.27}, {64, 128, 0.33, 0.41, 0.10},  {64, 64, 0.35, 0.29, 0.0}};
   const int64_t panels = (K + 127) / 128;
-  const int shape = M > 1024 ? 1 : M > 64 ? 4 : 6;
-  const int64_t tiles = ((M + shapes[shape].bm - 1) / shapes[shape].bm) * ((N + shapes[shape].bn - 1) / shapes[shape].bn);
-  int64_t sp = 1;
-  while (sp < 8 && tiles * sp * 2 <= 512 && panels >= 4 * sp) sp *= 2;
-  const int64_t per = (panels + sp - 1) / sp;
-  return F8Plan{shape, (int)((panels + per - 1) / per), (int)per};
+  F8Plan best{0, 1, (int)panels};
+  double best_t = 1e300;
+  for (int s = 0; s < 6; ++s) {
+    const int64_t tiles = ((M + shapes[s].bm - 1) / shapes[s].bm) * ((N + shapes[s].bn - 1) / shapes[s].bn);
+    for (int sp = 1; sp <= 8; ++sp) {
+      if (sp > 1 && (panels < 2 * sp || tiles * sp > 1024)) break;
+      const int64_t per = (panels + sp - 1) / sp, rounds = (tiles * sp + 255) / 256;
+      const double fill = (double)(tiles * sp) / (256.0 * (double)rounds);
+      const double device = 4.2 + (double)per * fmax(shapes[s].least, (double)rounds * (shapes[s].share + shapes[s].full * fill)) +
+                            (sp > 1 ? 0.9 + 2.0e-6 * (double)(M * N) * sp : 0.0);
+      const double t = fmax(device, sp > 1 ? 13.0 : 10.0) + 0.01 * device;
+      if (t < best_t) {
+        best_t = t;
+        best = F8Plan{s, (int)((panels + per - 1) / per), (int)per};
+      }
+    }
+  }
+  return best;
 }
 
 template <int WM, int WN, int TM, int TN, int S>
@@ -671,10 +759,9 @@ hipError_t launch_gemm_fp8(const Fp8GemmArgs& a, void* workspace, hipStream_t st
   hipError_t e = p.shape == 0   ? launch_fp8_cfg<4, 2, 2, 5, 2>(a, sp, stream)
                  : p.shape == 1 ? launch_fp8_cfg<4, 2, 2, 4, 2>(a, sp, stream)
                  : p.shape == 2 ? launch_fp8_cfg<4, 2, 2, 2, 3>(a, sp, stream)
-                 : p.shape == 3 ? launch_fp8_cfg<2, 2, 3, 2, 2>(a, sp, stream)
-                 : p.shape == 4 ? launch_fp8_cfg<2, 2, 2, 2, 2>(a, sp, stream)
-                 : p.shape == 5 ? launch_fp8_cfg<2, 2, 2, 1, 3>(a, sp, stream)
-                                : launch_fp8_cfg<2, 2, 1, 1, 4>(a, sp, stream);
+                 : p.shape == 3 ? launch_fp8_cfg<4, 2, 1, 2, 4>(a, sp, stream)
+                 : p.shape == 4 ? launch_fp8_cfg<2, 4, 1, 1, 3>(a, sp, stream)
+                                : launch_fp8_cfg<2, 2, 1, 1, 3>(a, sp, stream);
   if (e != hipSuccess || p.splits == 1) return e;
   const int w = a.N % 4 == 0 ? 4 : 1;
   const dim3 grid((unsigned)((a.M * (a.N / w) + 255) / 256));
