@@ -311,9 +311,15 @@ __global__ __launch_bounds__(64 * kWavesF, D == 64 ? 4 : 2) void attention_few_k
 // [64][D]; V^T's is [D][64] with each 16 keys in the order of P^T's operand (0-3, 8-11 for the lower half of the
 // wave, 4-7, 12-15 for the upper), so that both products read whole 16-byte pieces. Products,
 // exponentials and the lazy maximum are arranged as in attention.hip.
+// WHOLE: pages of 64 or 128 tokens, so that a tile lies in one page: its address and scale are scalar, and a page that the
+// table does not have is a buffer of no bytes, which reads zero.
 constexpr int kAheadC = 2;   // operand reads in flight ahead of a product
 
-template <int D, bool CAUSAL, int NW>
+__device__ __forceinline__ u32x4 load_codes(__amdgpu_buffer_rsrc_t r, int voff, int soff) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0));
+}
+
+template <int D, bool CAUSAL, int NW, bool WHOLE>
 __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArgs a) {
   constexpr int kRowBytes = 2 * D;
   constexpr int kTileBytes = kTile * kRowBytes;     // of K, and of V
@@ -345,7 +351,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
     const int last_block = (n_rows - 1) >> kLgRows;
     rb.row0 = (last_block << kLgRows) - rb.row0;
   }
-  const int L = (int)keys_of(a, rb.b);
+  const int L = __builtin_amdgcn_readfirstlane((int)keys_of(a, rb.b));
   const int per = tiles_per_split(a, L);
   const bool only = (L + kTile - 1) / kTile <= per;
   if (split > 0 && (int64_t)split * per * kTile >= L) return;
@@ -371,77 +377,106 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
     for (int t = 0; t < KD; ++t) fq[t] = *reinterpret_cast<const bf16x8*>(qp + 16 * t);
   }
 
-  // Pieces of 16 codes: of K, key kr and elements 16 ks ..; of V, element vd and keys 16 vk ..
+  // Pieces of 16 codes: of K, key kr and elements 16 ks .. (piece c: 64 NW / kCP keys further on); of V, element vd
+  // and keys 16 vk .. (16 NW elements further on). The LDS swizzles repeat with those steps.
   auto swz_k = [](int r) { return D == 128 ? (r & 15) : ((r >> 1) & 7); };
   auto swz_v = [](int r) { return (r ^ (r >> 3)) & 7; };
+  constexpr int kStepK = 64 * NW / kCP, kStepV = 16 * NW;
+  static_assert(kStepK % 16 == 0 && kStepV % 64 == 0, "swizzles");
+  const int kr = tid / kCP, ks = tid % kCP, vd = tid >> 2, vk = tid & 3;
+  const int k_src = kr * D + 16 * ks;                 // within a tile's page
+  const int k_dst = kr * kRowBytes + (((2 * ks) ^ swz_k(kr)) * 16), v_dst = vd * 128 + (((2 * vk) ^ swz_v(vd)) * 16);
   const int32_t* table = a.table + (int64_t)rb.b * a.width;
-  const int64_t page_bytes = (int64_t)P * D;
+  const uint32_t page_bytes = (uint32_t)(P * D);
   auto page_at = [&](int key) {   // the page of a key; -1: none
     const int at = key >> lg_page;
     const int p = at < a.width && key < L ? table[at] : -1;
     return (uint32_t)p < (uint32_t)a.c.pages ? p : -1;
   };
-  int pk[kPieces], pv[kPieces];          // pages of the pieces to be requested next
   u32x4 wk[kPieces], wv[kPieces];        // codes on their way
-  uint32_t sk[kPieces], sv[kPieces];     // and their scales
+  // pages of the pieces to be requested next, and the scales of those on their way (256 or more: no page); scalar if WHOLE
+  constexpr int kOwn = WHOLE ? 1 : kPieces;
+  int pk[kOwn], pv[kOwn];
+  uint32_t sk[kOwn], sv[kOwn];
   auto k_pages = [&](int kt) {
 #pragma unroll
-    for (int c = 0; c < kPieces; ++c) pk[c] = page_at((kt0 + kt) * kTile + (tid + 64 * NW * c) / kCP);
+    for (int c = 0; c < kOwn; ++c)
+      pk[c] = WHOLE ? __builtin_amdgcn_readfirstlane(page_at((kt0 + kt) * kTile)) : page_at((kt0 + kt) * kTile + kr + kStepK * c);
   };
   auto v_pages = [&](int kt) {
 #pragma unroll
-    for (int c = 0; c < kPieces; ++c) pv[c] = page_at((kt0 + kt) * kTile + 16 * (tid & 3));
+    for (int c = 0; c < kOwn; ++c)
+      pv[c] = WHOLE ? __builtin_amdgcn_readfirstlane(page_at((kt0 + kt) * kTile)) : page_at((kt0 + kt) * kTile + 16 * vk);
   };
   auto request_k = [&](int kt) {
+    if constexpr (WHOLE) {
+      const int64_t at = (int64_t)max(pk[0], 0) * a.c.Hk + hk;
+      const __amdgpu_buffer_rsrc_t r = make_rsrc(a.c.k + at * page_bytes, pk[0] < 0 ? 0u : page_bytes);
+      const int soff = (((kt0 + kt) * kTile) & (P - 1)) * D;
 #pragma unroll
-    for (int c = 0; c < kPieces; ++c) {
-      const int i = tid + 64 * NW * c, key = (kt0 + kt) * kTile + i / kCP;
-      const int64_t at = (int64_t)max(pk[c], 0) * a.c.Hk + hk;
-      wk[c] = *reinterpret_cast<const u32x4*>(a.c.k + at * page_bytes + (key & (P - 1)) * D + 16 * (i % kCP));
-      sk[c] = a.c.ks[at];
-      if (pk[c] < 0) sk[c] = 256;        // no codes
+      for (int c = 0; c < kPieces; ++c) wk[c] = load_codes(r, k_src, soff + kStepK * D * c);
+      sk[0] = pk[0] < 0 ? 256u : a.c.ks[at];
+    } else {
+#pragma unroll
+      for (int c = 0; c < kPieces; ++c) {
+        const int key = (kt0 + kt) * kTile + kr + kStepK * c;
+        const uint32_t p = (uint32_t)max(pk[c], 0);
+        wk[c] = *reinterpret_cast<const u32x4*>(a.c.k + (uint64_t)p * (a.c.Hk * page_bytes) + hk * page_bytes +
+                                                (uint32_t)((key & (P - 1)) * D + 16 * ks));
+        sk[c] = a.c.ks[(int64_t)p * a.c.Hk + hk];
+        if (pk[c] < 0) sk[c] = 256;
+      }
     }
   };
   auto request_v = [&](int kt) {
+    if constexpr (WHOLE) {
+      const int64_t at = (int64_t)max(pv[0], 0) * a.c.Hk + hk;
+      const __amdgpu_buffer_rsrc_t r = make_rsrc(a.c.v + at * page_bytes, pv[0] < 0 ? 0u : page_bytes);
+      const int soff = ((kt0 + kt) * kTile) & (P - 1);
 #pragma unroll
-    for (int c = 0; c < kPieces; ++c) {
-      const int i = tid + 64 * NW * c, key = (kt0 + kt) * kTile + 16 * (i & 3);
-      const int64_t at = (int64_t)max(pv[c], 0) * a.c.Hk + hk;
-      wv[c] = *reinterpret_cast<const u32x4*>(a.c.v + at * page_bytes + (i >> 2) * P + (key & (P - 1)));
-      sv[c] = a.c.vs[at];
-      if (pv[c] < 0) sv[c] = 256;
+      for (int c = 0; c < kPieces; ++c) wv[c] = load_codes(r, vd * P + 16 * vk, soff + kStepV * P * c);
+      sv[0] = pv[0] < 0 ? 256u : a.c.vs[at];
+    } else {
+      const int key = (kt0 + kt) * kTile + 16 * vk;
+      const uint32_t p = (uint32_t)max(pv[0], 0);   // the same keys in each piece
+#pragma unroll
+      for (int c = 0; c < kPieces; ++c)
+        wv[c] = *reinterpret_cast<const u32x4*>(a.c.v + (uint64_t)p * (a.c.Hk * page_bytes) + hk * page_bytes +
+                                                (uint32_t)((vd + kStepV * c) * P + (key & (P - 1))));
+      sv[0] = a.c.vs[(int64_t)p * a.c.Hk + hk];
+      if (pv[0] < 0) sv[0] = 256;
     }
   };
   auto store_k = [&](int kt) {
     uint8_t* st = smem + (kt & 1) * (2 * kTileBytes);
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) {
-      const int i = tid + 64 * NW * c, r = i / kCP, s = 2 * (i % kCP);
-      const float sc = cache_scale(sk[c] & 255u);
-      const u32x4 w = sk[c] > 255u ? zero4() : wk[c];
-      uint8_t* at = st + r * kRowBytes;
-      *reinterpret_cast<bf16x8*>(at + ((s ^ swz_k(r)) * 16)) = bf16_operand(w[0], w[1], sc);
-      *reinterpret_cast<bf16x8*>(at + (((s + 1) ^ swz_k(r)) * 16)) = bf16_operand(w[2], w[3], sc);
+      const uint32_t s = WHOLE ? (uint32_t)__builtin_amdgcn_readfirstlane((int)sk[0]) : sk[c];
+      const float sc = cache_scale(s & 255u);
+      const u32x4 w = !WHOLE && s > 255u ? zero4() : wk[c];
+      *reinterpret_cast<bf16x8*>(st + k_dst + kStepK * kRowBytes * c) = bf16_operand(w[0], w[1], sc);
+      *reinterpret_cast<bf16x8*>(st + (k_dst ^ 16) + kStepK * kRowBytes * c) = bf16_operand(w[2], w[3], sc);
     }
   };
   auto store_v = [&](int kt) {
     uint8_t* st = smem + (kt & 1) * (2 * kTileBytes) + kTileBytes;
+    const int end = L - (kt0 + kt) * kTile;            // keys of the tile: values past the sequence are zero,
+    if (end < kTile) {                                 // whatever the page holds
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int n = max(min(end - 16 * vk - 4 * e, 4), 0);
+        const uint32_t keep = n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
+#pragma unroll
+        for (int c = 0; c < kPieces; ++c) wv[c][e] &= keep;
+      }
+    }
+    const uint32_t s = WHOLE ? (uint32_t)__builtin_amdgcn_readfirstlane((int)sv[0]) : sv[0];
+    const float sc = cache_scale(s & 255u);
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) {
-      const int i = tid + 64 * NW * c, d = i >> 2, s = 2 * (i & 3);
-      const float sc = cache_scale(sv[c] & 255u);
-      u32x4 w = sv[c] > 255u ? zero4() : wv[c];
-      const int left = L - (kt0 + kt) * kTile - 8 * s;   // values past the sequence are zero, whatever the page holds
-      if (left < 16) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int n = max(min(left - 4 * e, 4), 0);
-          w[e] &= n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
-        }
-      }
-      uint8_t* at = st + d * 128;
-      *reinterpret_cast<bf16x8*>(at + ((s ^ swz_v(d)) * 16)) = bf16_operand(w[0], w[2], sc);
-      *reinterpret_cast<bf16x8*>(at + (((s + 1) ^ swz_v(d)) * 16)) = bf16_operand(w[1], w[3], sc);
+      const u32x4 w = !WHOLE && s > 255u ? zero4() : wv[c];
+      *reinterpret_cast<bf16x8*>(st + v_dst + kStepV * 128 * c) = bf16_operand(w[0], w[2], sc);
+      *reinterpret_cast<bf16x8*>(st + (v_dst ^ 16) + kStepV * 128 * c) = bf16_operand(w[1], w[3], sc);
     }
   };
 
@@ -449,7 +484,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
   // (keys 16 (u / JD), elements 32 (u % JD))
   // pieces 2 t + h, permuted by an exclusive or: that of t applies to the address of t = 0. Row 32 j + l32 of V^T is
   // permuted like row l32, with 4 j more
-  int kfrag = l32 * kRowBytes + ((h ^ swz_k(l32)) * 16), vfrag = l32 * 128 + ((h ^ swz_v(l32)) * 16);
+  const int kfrag = l32 * kRowBytes + ((h ^ swz_k(l32)) * 16), vfrag = l32 * 128 + ((h ^ swz_v(l32)) * 16);
   auto read_k = [&](const uint8_t* sk_, int u) {
     return *reinterpret_cast<const bf16x8*>(sk_ + 32 * (u & 1) * kRowBytes + (kfrag ^ (32 * (u >> 1))));
   };
@@ -461,8 +496,10 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
   f32x16 acc[JD];
 #pragma unroll
   for (int j = 0; j < JD; ++j) acc[j] = f32x16{};
-  const float c = a.scale * 1.4426950408889634f;   // exponents in base 2
-  float m = kLowest / fmaxf(c, 1.0f);              // below every finite score whose exponent is finite
+  // exponents in base 2, x c - mc, and scores far from zero, as in attention.hip
+  const float c = a.scale * 1.4426950408889634f;
+  float m = kLowest / fmaxf(c, 1.0f), mc = 0.0f;
+  bool far = true;   // the same in every lane
   const float slack = kSlackC / c;
   // a tile's probabilities first, then l with what its last addition lost, as in attention.hip
   float l = 0.0f, lost = 0.0f, tile_sum = 0.0f;
@@ -473,8 +510,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
     tile_sum = 0.0f;
   };
   auto pair = [&](const f32x16 (&x)[2], uint32_t (&p)[16], int r) {
-    const float p0 = __builtin_amdgcn_exp2f((x[r >> 3][2 * (r & 7)] - m) * c);
-    const float p1 = __builtin_amdgcn_exp2f((x[r >> 3][2 * (r & 7) + 1] - m) * c);
+    const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r >> 3][2 * (r & 7)], c, -mc));
+    const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r >> 3][2 * (r & 7) + 1], c, -mc));
     p[r] = pack_bf16x2(p0, p1);
     tile_sum += p0 + p1;
     asm volatile("" : "+v"(p[r]), "+v"(tile_sum));   // made here: not moved to their use
@@ -496,11 +533,22 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
   auto raise = [&](float mx) {
     const Pair both = halves32(mx);
     const float mn = fmaxf(m, fmaxf(both.a, both.b));
-    const float alpha = __builtin_amdgcn_exp2f((m - mn) * c);
+    float mcn = mn * c;
+    const bool far_n = __ballot(fabsf(mcn) > 1048576.0f) != 0;
+    if (far_n) mcn = 0.0f;
+    const float alpha = __builtin_amdgcn_exp2f(__builtin_fmaf((far ? m : 0.0f) - (far_n ? mn : 0.0f), c, mc - mcn));
     m = mn;
+    mc = mcn;
+    far = far_n;
     l *= alpha;
     lost *= alpha;
     return alpha;
+  };
+  auto from_max = [&](f32x16 (&x)[2]) {
+    if (far) {
+#pragma unroll
+      for (int r = 0; r < 32; ++r) x[r >> 4][r & 15] -= m;
+    }
   };
 
   // Start of step kt: one barrier frees K(kt) and V(kt - 1) and publishes K(kt + 1) and V(kt); the codes of the next
@@ -522,7 +570,6 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
   };
   auto step = [&](f32x16 (&cur)[2], uint32_t (&pc)[16], f32x16 (&nxt)[2], uint32_t (&pn)[16], int kt) {
     begin_step(kt);
-    asm volatile("" : "+v"(kfrag), "+v"(vfrag));   // the addresses of each read are made anew: 10 registers
     const uint8_t* sk_ = smem + ((kt + 1) & 1) * (2 * kTileBytes);
     const uint8_t* sv_ = smem + (kt & 1) * (2 * kTileBytes) + kTileBytes;
     bf16x8 fk[NK], fv[NV];
@@ -556,6 +603,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
     }
     const bool up = __ballot(mx > m + slack) != 0;
     if (up) alpha = raise(mx);
+    from_max(nxt);
 #pragma unroll
     for (int u = kMax; u < NV; ++u) {
       value(u);
@@ -577,14 +625,14 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
     v_pages(0);
     request_k(0);
     request_v(0);
+    k_pages(1);
     store_k(0);
     store_v(0);
     if (nt > 1) {
-      k_pages(1);
       request_k(1);
-      store_k(1);
       k_pages(2);
       v_pages(1);
+      store_k(1);
     }
     __syncthreads();
   }
@@ -600,6 +648,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
 #pragma unroll
     for (int r = 1; r < 32; ++r) mx = fmaxf(mx, s0[r >> 4][r & 15]);
     raise(mx);
+    from_max(s0);
 #pragma unroll
     for (int r = 0; r < 8; ++r) pair(s0, p0, r);
     for (; kt + 2 < ntw; kt += 2) {
@@ -633,17 +682,19 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
   l = sums.a + sums.b;
   if (!only) {   // this lane holds elements 32 j + 8 (r / 4) + 4 h + r % 4 of its row
     if (row0 + l32 >= n_rows) return;
+    // relative to the maximum itself, not to its rounded product
+    const float f = far ? 1.0f : __builtin_amdgcn_exp2f(__builtin_fmaf(-m, c, mc));
     const int64_t at = ((int64_t)split * a.T + rb.tok0 + query) * a.H + head;
     float* dst = a.partial + at * D + 4 * h;
 #pragma unroll
     for (int j = 0; j < JD; ++j)
 #pragma unroll
       for (int r = 0; r < 16; r += 4)
-        *reinterpret_cast<f32x4*>(dst + 32 * j + 2 * r) = f32x4{acc[j][r], acc[j][r + 1], acc[j][r + 2], acc[j][r + 3]};
+        *reinterpret_cast<f32x4*>(dst + 32 * j + 2 * r) = f32x4{acc[j][r] * f, acc[j][r + 1] * f, acc[j][r + 2] * f, acc[j][r + 3] * f};
     if (h == 0) {
       float* st = a.partial + (int64_t)a.splits * a.T * a.H * D + 2 * at;
       st[0] = m;
-      st[1] = l;
+      st[1] = l * f;
     }
     return;
   }
@@ -755,8 +806,11 @@ template <int D, int NW>
 void launch_tiles(const AttnCacheArgs& a, hipStream_t stream) {
   const int64_t total = ((a.T * (a.H / a.c.Hk) >> (NW == 8 ? 8 : 7)) + a.B) * a.splits * a.c.Hk;
   const dim3 grid((unsigned)((total + 7) / 8 * 8)), block(64 * NW);
-  if (a.causal) hipLaunchKernelGGL((attention_tile_kernel<D, true, NW>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((attention_tile_kernel<D, false, NW>), grid, block, 0, stream, a);
+  const bool whole = a.c.lg_page >= 6;
+  if (a.causal && whole) hipLaunchKernelGGL((attention_tile_kernel<D, true, NW, true>), grid, block, 0, stream, a);
+  else if (a.causal) hipLaunchKernelGGL((attention_tile_kernel<D, true, NW, false>), grid, block, 0, stream, a);
+  else if (whole) hipLaunchKernelGGL((attention_tile_kernel<D, false, NW, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((attention_tile_kernel<D, false, NW, false>), grid, block, 0, stream, a);
 }
 
 template <int D>
