@@ -388,34 +388,40 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
   const int k_dst = kr * kRowBytes + (((2 * ks) ^ swz_k(kr)) * 16), v_dst = vd * 128 + (((2 * vk) ^ swz_v(vd)) * 16);
   const int32_t* table = a.table + (int64_t)rb.b * a.width;
   const uint32_t page_bytes = (uint32_t)(P * D);
-  auto page_at = [&](int key) {   // the page of a key; -1: none
+  auto entry_of = [&](int key) {   // the table's entry for a key, looked at when it is used: not waited for here
     const int at = key >> lg_page;
-    const int p = at < a.width && key < L ? table[at] : -1;
-    return (uint32_t)p < (uint32_t)a.c.pages ? p : -1;
+    return at < a.width && key < L ? table[at] : -1;
+  };
+  auto page_of = [&](int entry) {   // -1: none
+    if (WHOLE) entry = __builtin_amdgcn_readfirstlane(entry);
+    return (uint32_t)entry < (uint32_t)a.c.pages ? entry : -1;
   };
   u32x4 wk[kPieces], wv[kPieces];        // codes on their way
-  // pages of the pieces to be requested next, and the scales of those on their way (256 or more: no page); scalar if WHOLE
+  // Table entries of the pieces to be requested next; the scales of those on their way and which have no page (bit c of
+  // `gone`). What a load brings is looked at a step later, not where it is requested.
   constexpr int kOwn = WHOLE ? 1 : kPieces;
-  int pk[kOwn], pv[kOwn];
-  uint32_t sk[kOwn], sv[kOwn];
+  int ek[kOwn], ev, gone_k = 0, gone_v = 0;
+  uint32_t sk[kOwn], sv;
   auto k_pages = [&](int kt) {
 #pragma unroll
-    for (int c = 0; c < kOwn; ++c)
-      pk[c] = WHOLE ? __builtin_amdgcn_readfirstlane(page_at((kt0 + kt) * kTile)) : page_at((kt0 + kt) * kTile + kr + kStepK * c);
+    for (int c = 0; c < kOwn; ++c) ek[c] = entry_of((kt0 + kt) * kTile + (WHOLE ? 0 : kr + kStepK * c));
   };
-  auto v_pages = [&](int kt) {
+  auto v_pages = [&](int kt) { ev = entry_of((kt0 + kt) * kTile + (WHOLE ? 0 : 16 * vk)); };
+  auto request_k = [&](int kt, u32x4 (&wk)[kPieces], uint32_t (&sk)[kOwn], int& gone_k) {
+    int pk[kOwn];
+    gone_k = 0;
 #pragma unroll
-    for (int c = 0; c < kOwn; ++c)
-      pv[c] = WHOLE ? __builtin_amdgcn_readfirstlane(page_at((kt0 + kt) * kTile)) : page_at((kt0 + kt) * kTile + 16 * vk);
-  };
-  auto request_k = [&](int kt) {
+    for (int c = 0; c < kOwn; ++c) {
+      pk[c] = page_of(ek[c]);
+      gone_k |= (pk[c] < 0 ? 1 : 0) << c;
+    }
     if constexpr (WHOLE) {
       const int64_t at = (int64_t)max(pk[0], 0) * a.c.Hk + hk;
       const __amdgpu_buffer_rsrc_t r = make_rsrc(a.c.k + at * page_bytes, pk[0] < 0 ? 0u : page_bytes);
       const int soff = (((kt0 + kt) * kTile) & (P - 1)) * D;
 #pragma unroll
       for (int c = 0; c < kPieces; ++c) wk[c] = load_codes(r, k_src, soff + kStepK * D * c);
-      sk[0] = pk[0] < 0 ? 256u : a.c.ks[at];
+      sk[0] = a.c.ks[at];
     } else {
 #pragma unroll
       for (int c = 0; c < kPieces; ++c) {
@@ -424,36 +430,37 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
         wk[c] = *reinterpret_cast<const u32x4*>(a.c.k + (uint64_t)p * (a.c.Hk * page_bytes) + hk * page_bytes +
                                                 (uint32_t)((key & (P - 1)) * D + 16 * ks));
         sk[c] = a.c.ks[(int64_t)p * a.c.Hk + hk];
-        if (pk[c] < 0) sk[c] = 256;
       }
     }
   };
   auto request_v = [&](int kt) {
+    const int pv = page_of(ev);
+    gone_v = pv < 0;
     if constexpr (WHOLE) {
-      const int64_t at = (int64_t)max(pv[0], 0) * a.c.Hk + hk;
-      const __amdgpu_buffer_rsrc_t r = make_rsrc(a.c.v + at * page_bytes, pv[0] < 0 ? 0u : page_bytes);
+      const int64_t at = (int64_t)max(pv, 0) * a.c.Hk + hk;
+      const __amdgpu_buffer_rsrc_t r = make_rsrc(a.c.v + at * page_bytes, pv < 0 ? 0u : page_bytes);
       const int soff = ((kt0 + kt) * kTile) & (P - 1);
 #pragma unroll
       for (int c = 0; c < kPieces; ++c) wv[c] = load_codes(r, vd * P + 16 * vk, soff + kStepV * P * c);
-      sv[0] = pv[0] < 0 ? 256u : a.c.vs[at];
+      sv = a.c.vs[at];
     } else {
       const int key = (kt0 + kt) * kTile + 16 * vk;
-      const uint32_t p = (uint32_t)max(pv[0], 0);   // the same keys in each piece
+      const uint32_t p = (uint32_t)max(pv, 0);   // the same keys in each piece
 #pragma unroll
       for (int c = 0; c < kPieces; ++c)
         wv[c] = *reinterpret_cast<const u32x4*>(a.c.v + (uint64_t)p * (a.c.Hk * page_bytes) + hk * page_bytes +
                                                 (uint32_t)((vd + kStepV * c) * P + (key & (P - 1))));
-      sv[0] = a.c.vs[(int64_t)p * a.c.Hk + hk];
-      if (pv[0] < 0) sv[0] = 256;
+      sv = a.c.vs[(int64_t)p * a.c.Hk + hk];
     }
   };
-  auto store_k = [&](int kt) {
+  auto store_k = [&](int kt, const u32x4 (&wk)[kPieces], const uint32_t (&sk)[kOwn], int gone_k) {
     uint8_t* st = smem + (kt & 1) * (2 * kTileBytes);
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) {
       const uint32_t s = WHOLE ? (uint32_t)__builtin_amdgcn_readfirstlane((int)sk[0]) : sk[c];
-      const float sc = cache_scale(s & 255u);
-      const u32x4 w = !WHOLE && s > 255u ? zero4() : wk[c];
+      const bool gone = (gone_k >> (WHOLE ? 0 : c)) & 1;
+      const float sc = gone ? 1.0f : cache_scale(s);
+      const u32x4 w = !WHOLE && gone ? zero4() : wk[c];
       *reinterpret_cast<bf16x8*>(st + k_dst + kStepK * kRowBytes * c) = bf16_operand(w[0], w[1], sc);
       *reinterpret_cast<bf16x8*>(st + (k_dst ^ 16) + kStepK * kRowBytes * c) = bf16_operand(w[2], w[3], sc);
     }
@@ -470,11 +477,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
         for (int c = 0; c < kPieces; ++c) wv[c][e] &= keep;
       }
     }
-    const uint32_t s = WHOLE ? (uint32_t)__builtin_amdgcn_readfirstlane((int)sv[0]) : sv[0];
-    const float sc = cache_scale(s & 255u);
+    const uint32_t s = WHOLE ? (uint32_t)__builtin_amdgcn_readfirstlane((int)sv) : sv;
+    const float sc = gone_v ? 1.0f : cache_scale(s);
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) {
-      const u32x4 w = !WHOLE && s > 255u ? zero4() : wv[c];
+      const u32x4 w = !WHOLE && gone_v ? zero4() : wv[c];
       *reinterpret_cast<bf16x8*>(st + v_dst + kStepV * 128 * c) = bf16_operand(w[0], w[2], sc);
       *reinterpret_cast<bf16x8*>(st + (v_dst ^ 16) + kStepV * 128 * c) = bf16_operand(w[1], w[3], sc);
     }
@@ -556,7 +563,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
   auto begin_step = [&](int kt) {
     __syncthreads();
     if (kt + 2 < nt) {
-      request_k(kt + 2);
+      request_k(kt + 2, wk, sk, gone_k);
       k_pages(kt + 3);
     }
     if (kt + 1 < nt) {
@@ -565,7 +572,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
     }
   };
   auto end_step = [&](int kt) {
-    if (kt + 2 < nt) store_k(kt + 2);
+    if (kt + 2 < nt) store_k(kt + 2, wk, sk, gone_k);
     if (kt + 1 < nt) store_v(kt + 1);
   };
   auto step = [&](f32x16 (&cur)[2], uint32_t (&pc)[16], f32x16 (&nxt)[2], uint32_t (&pn)[16], int kt) {
@@ -620,20 +627,25 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
     end_step(kt);
   };
 
-  if (nt > 0) {
+  if (nt > 0) {   // the first two tiles of K and the first of V, all requested before any is waited for
+    u32x4 wk1[kPieces];
+    uint32_t sk1[kOwn];
+    int next[kOwn], gone1;
+    k_pages(1);
+#pragma unroll
+    for (int c = 0; c < kOwn; ++c) next[c] = ek[c];
     k_pages(0);
     v_pages(0);
-    request_k(0);
+    request_k(0, wk, sk, gone_k);
     request_v(0);
-    k_pages(1);
-    store_k(0);
+#pragma unroll
+    for (int c = 0; c < kOwn; ++c) ek[c] = next[c];
+    request_k(1, wk1, sk1, gone1);   // (without a second tile: a page that is not there)
+    k_pages(2);
+    v_pages(1);
+    store_k(0, wk, sk, gone_k);
     store_v(0);
-    if (nt > 1) {
-      request_k(1);
-      k_pages(2);
-      v_pages(1);
-      store_k(1);
-    }
+    store_k(1, wk1, sk1, gone1);
     __syncthreads();
   }
   int kt = 0;
