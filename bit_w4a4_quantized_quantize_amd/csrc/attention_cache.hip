@@ -131,11 +131,11 @@ __global__ __launch_bounds__(64 * kWavesF, D == 64 ? 4 : 2) void attention_few_k
 
   const int32_t* table = a.table + (int64_t)rb.b * a.width;
   const int64_t page_bytes = (int64_t)P * D;
-  auto page_of = [&](int64_t key) {   // -1: none
+  auto entry_of = [&](int64_t key) {   // the table's entry for a key, looked at when it is used: not waited for here
     const int64_t at = key >> a.c.lg_page;
-    const int p = at < a.width ? table[at] : -1;
-    return (uint32_t)p < (uint32_t)a.c.pages ? p : -1;
+    return at < a.width ? table[at] : -1;
   };
+  auto page_of = [&](int entry) { return (uint32_t)entry < (uint32_t)a.c.pages ? entry : -1; };   // -1: none
 
   f32x4 acc[JD];
 #pragma unroll
@@ -152,42 +152,46 @@ __global__ __launch_bounds__(64 * kWavesF, D == 64 ? 4 : 2) void attention_few_k
   const int64_t k_first = k_begin + kTile * wave;
   constexpr int kStride = kTile * kWavesF;
   u32x4 wk[4][KP], wv[JD];
-  uint32_t ks, vs;               // scales; 256: no page
-  int pk = page_of(k_first + kk), pv = page_of(k_first + kv);
+  uint32_t ks, vs;                          // scales
+  bool k_gone = false, v_gone = false;      // no page
+  int ek = entry_of(k_first + kk), ev = entry_of(k_first + kv);
   auto request_k = [&](int64_t k0) {
+    const int pk = page_of(ek);
+    k_gone = pk < 0;
     const int64_t at = (int64_t)max(pk, 0) * a.c.Hk + hk;
     const uint8_t* p = a.c.k + at * page_bytes + (((int)k0 + kk) & (P - 1)) * D + 16 * q;
-    ks = a.c.ks[at];
-    if (pk < 0) ks = 256;
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int u = 0; u < KP; ++u) wk[t][u] = *reinterpret_cast<const u32x4*>(p + 4 * t * D + 64 * u);
+    ks = a.c.ks[at];
   };
   auto request_v = [&](int64_t k0) {
+    const int pv = page_of(ev);
+    v_gone = pv < 0;
     const int64_t at = (int64_t)max(pv, 0) * a.c.Hk + hk;
     const uint8_t* p = a.c.v + at * page_bytes + l16 * P + (((int)k0 + kv) & (P - 1));
-    vs = a.c.vs[at];
-    if (pv < 0) vs = 256;
 #pragma unroll
     for (int j = 0; j < JD; ++j) wv[j] = *reinterpret_cast<const u32x4*>(p + 16 * j * P);
+    vs = a.c.vs[at];
   };
   if (k_first < k_end) {
+    const int ek1 = entry_of(k_first + kStride + kk), ev1 = entry_of(k_first + kStride + kv);
     request_k(k_first);
     request_v(k_first);
-    pk = page_of(k_first + kStride + kk);
-    pv = page_of(k_first + kStride + kv);
+    ek = ek1;
+    ev = ev1;
   }
   for (int64_t k0 = k_first; k0 < k_end; k0 += kStride) {
     f32x4 x[4];
     {
-      if (ks > 255u) {
+      if (k_gone) {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
           for (int u = 0; u < KP; ++u) wk[t][u] = zero4();
       }
-      const float sc = cache_scale(ks & 255u);
+      const float sc = k_gone ? 1.0f : cache_scale(ks);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         x[t] = f32x4{};
@@ -201,7 +205,7 @@ __global__ __launch_bounds__(64 * kWavesF, D == 64 ? 4 : 2) void attention_few_k
     const bool more = k0 + kStride < k_end;
     if (more) {
       request_k(k0 + kStride);
-      pk = page_of(k0 + 2 * kStride + kk);
+      ek = entry_of(k0 + 2 * kStride + kk);
     }
     float mx = -__builtin_inff();
     if (k0 + kTile > last + 1) {
@@ -239,8 +243,8 @@ __global__ __launch_bounds__(64 * kWavesF, D == 64 ? 4 : 2) void attention_few_k
     const bf16x8 fp1 = __builtin_bit_cast(bf16x8, u32x4{p[4], p[5], p[6], p[7]});
     // values past the sequence, or without a page, are zero: their probabilities are, but what
     // the page holds there may be NaN
-    const int64_t left = vs > 255u ? 0 : L - k0 - kv;
-    const float sc = cache_scale(left <= 0 ? 0u : vs & 255u);
+    const int64_t left = v_gone ? 0 : L - k0 - kv;
+    const float sc = left <= 0 ? 1.0f : cache_scale(vs);
     if (left < 16) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -257,7 +261,7 @@ __global__ __launch_bounds__(64 * kWavesF, D == 64 ? 4 : 2) void attention_few_k
     }
     if (more) {
       request_v(k0 + kStride);
-      pv = page_of(k0 + 2 * kStride + kv);
+      ev = entry_of(k0 + 2 * kStride + kv);
     }
   }
 
@@ -734,84 +738,144 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
   }
 }
 
-// The splits of a row (a query's head) together, a workgroup each: the splits' weights in LDS, then groups of D / 4
-// threads take every kGroups-th split, four elements a thread. (A wave per row that walked through its splits
-// took longer than the attention from 64 splits on.)
-constexpr int kMaxSplits = 256;
+// The splits of a row (a query's head) together, four elements a thread. WIDE: a workgroup a row, its groups of D / 4
+// threads take the splits in turn; else a group a row, for up to 8 splits, all requested at once. (A wave per row
+// that walked through its splits took longer than the attention from 64 splits on.)
+constexpr int kMaxSplits = 256, kFewSplits = 8;
 
-template <int D>
+template <int D, bool WIDE>
 __global__ __launch_bounds__(256) void join_kernel(AttnCacheArgs a) {
   constexpr int kGroups = 256 / (D / 4);
-  __shared__ float weight[kMaxSplits];
+  __shared__ float weight[WIDE ? kMaxSplits : 1];
   __shared__ float part[4];
-  __shared__ f32x4 sums[kGroups][D / 4];
-  const int64_t row = blockIdx.x, rows = a.T * a.H;
+  __shared__ f32x4 sums[WIDE ? kGroups : 1][D / 4];
+  const int tid = threadIdx.x, e = tid % (D / 4), g = tid / (D / 4);
+  const int64_t rows = a.T * a.H;
+  const int64_t row = WIDE ? (int64_t)blockIdx.x : min((int64_t)blockIdx.x * kGroups + g, rows - 1);
   const int64_t tok = row / a.H;
   int b = (int)tok;
-  if (a.cu != nullptr) {
-    b = wave_count_le(a.cu, a.B + 1, tok) - 1;
-    if (b < 0 || b >= a.B) return;   // outside the sequences
+  if (a.cu != nullptr) {   // the sequence of a token: of the wave's rows, those of the same token together
+    b = 0;
+    if (WIDE) {
+      b = wave_count_le(a.cu, a.B + 1, tok) - 1;
+    } else {
+      int lo = 0, hi = a.B + 1;
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (a.cu[mid] <= tok) lo = mid + 1;
+        else hi = mid;
+      }
+      b = lo - 1;
+    }
   }
-  const int64_t L = keys_of(a, b);
+  const bool in = b >= 0 && b < a.B;   // else outside the sequences
+  const int64_t L = in ? keys_of(a, b) : 0;
   const int per = tiles_per_split(a, L);
-  const int n = (int)(((L + kTile - 1) / kTile + per - 1) / per);   // splits with keys
-  if (n <= 1) return;                                              // written whole
-  const int tid = threadIdx.x, e = tid % (D / 4), g = tid / (D / 4);
+  const int n = (int)(((L + kTile - 1) / kTile + per - 1) / per);   // splits with keys; 0 or 1: written whole
+  if (WIDE && n <= 1) return;
   const float c = a.scale * 1.4426950408889634f;
   const float* st = a.partial + (int64_t)a.splits * rows * D;
-  float m = kLowest, l = 0.0f;
-  if (tid < n) {
-    const float2 v = *reinterpret_cast<const float2*>(st + 2 * (tid * rows + row));
-    m = v.x;
-    l = v.y;
-  }
-  f32x4 o = {};
-  const float top = wave_reduce<true>(m);   // NaN where one is
-  if ((tid & 63) == 0) part[tid >> 6] = top;
-  __syncthreads();
-  const float M = max_or_nan(max_or_nan(part[0], part[1]), max_or_nan(part[2], part[3]));
-  const float f = tid < n ? __builtin_amdgcn_exp2f((m - M) * c) : 0.0f;
-  if (tid < n) weight[tid] = f;
-  const float share = wave_reduce<false>(l * f);
-  __syncthreads();   // everyone has the maxima
-  if ((tid & 63) == 0) part[tid >> 6] = share;
   const float* src = a.partial + row * D + 4 * e;
+  f32x4 o = {};
+  float total = 0.0f;
+  if constexpr (WIDE) {
+    float m = kLowest, l = 0.0f;
+    if (tid < n) {
+      const float2 v = *reinterpret_cast<const float2*>(st + 2 * (tid * rows + row));
+      m = v.x;
+      l = v.y;
+    }
+    const float top = wave_reduce<true>(m);
+    if ((tid & 63) == 0) part[tid >> 6] = top;
+    __syncthreads();
+    const float M = max_or_nan(max_or_nan(part[0], part[1]), max_or_nan(part[2], part[3]));
+    const float f = tid < n ? __builtin_amdgcn_exp2f((m - M) * c) : 0.0f;
+    if (tid < n) weight[tid] = f;
+    const float share = wave_reduce<false>(l * f);
+    __syncthreads();   // everyone has the maxima
+    if ((tid & 63) == 0) part[tid >> 6] = share;
 #pragma unroll 4
-  for (int s = g; s < n; s += kGroups) {
-    const f32x4 v = *reinterpret_cast<const f32x4*>(src + s * rows * D);
-    const float w = weight[s];
+    for (int s = g; s < n; s += kGroups) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(src + s * rows * D);
+      const float w = weight[s];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(v[i], w, o[i]);
+      for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(v[i], w, o[i]);
+    }
+    sums[g][e] = o;
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) o += sums[i][e];
+    total = part[0] + part[1] + part[2] + part[3];
+  } else {
+    f32x4 v[kFewSplits];
+    float2 s[kFewSplits];
+    float M = kLowest;
+#pragma unroll
+    for (int i = 0; i < kFewSplits; ++i) {
+      if (i < n) {
+        s[i] = *reinterpret_cast<const float2*>(st + 2 * (i * rows + row));
+        v[i] = *reinterpret_cast<const f32x4*>(src + i * rows * D);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kFewSplits; ++i)
+      if (i < n) M = fmaxf(M, s[i].x);
+#pragma unroll
+    for (int i = 0; i < kFewSplits; ++i) {
+      if (i < n) {
+        const float f = __builtin_amdgcn_exp2f((s[i].x - M) * c);
+        total += s[i].y * f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(v[i][r], f, o[r]);
+      }
+    }
+    if (n <= 1 || (int64_t)blockIdx.x * kGroups + g >= rows) return;
   }
-  sums[g][e] = o;
-  __syncthreads();
-  if (g > 0) return;
-#pragma unroll
-  for (int i = 1; i < kGroups; ++i) o += sums[i][e];
-  const float total = part[0] + part[1] + part[2] + part[3];
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   *reinterpret_cast<u32x2*>(a.o + tok * a.o_st + (row - tok * a.H) * a.o_sh + 4 * e) =
       u32x2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
 }
 
-// Rows of a sequence and key head on average, and the kernel for them: 0 few, 1 tiles by four waves, 2 by eight.
+// Which kernel (0 few rows, 1 tiles) and how many ways the keys are split, by an estimate in microseconds from what the host
+// knows: T, B and a bound of the lengths (with several sequences taken to average 0.6 of it). A workgroup walks through
+// its share in steps (64 keys a wave of few rows, a tile), each at least `least` long; all of them together
+// take `full` a step for each workgroup on a CU, and `tail` a step for the longest one's end; `base` starts and ends
+// the call, a split adds a launch and its partial results. Fitted to both kernels at 160 sizes (1 to 64 sequences of 1
+// to 1024 queries on 150 to 22000 keys, groups of 1, 4 and 8, keys split up to 64 ways:
+// profiles/attention_cache_grid.txt): within 2.3% of the best on average and 28% at worst. One token on 65537
+// keys, 32 heads on 8: 29 us split 32 ways, 51 16 ways, 32 128 ways. 40 tokens on 540 keys: 9.7 us by few rows, 19 by tiles;
+// 512 on 8704: 192 and 105.
 struct AttnPlan {
   int kernel, splits, least;
 };
+constexpr int64_t kMostPartial = int64_t(1) << 28;   // bytes
+
 AttnPlan plan_attention(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_length, bool packed) {
-  const int64_t G = H / Hk;
-  const int64_t tiles = (max_length + kTile - 1) / kTile;
-  AttnPlan p;
-  p.kernel = T * G <= 32 * B ? 0 : D == 128 && T * G >= 4096 * B ? 2 : 1;
-  const int rows = p.kernel == 0 ? 16 : p.kernel == 1 ? 128 : 256;
-  const int64_t blocks = (packed ? (T * G + rows - 1) / rows : B * ((G + rows - 1) / rows)) * Hk;
-  const int64_t want = p.kernel == 0 ? 1024 : 512;
-  p.least = 4;
-  int64_t s = blocks >= want ? 1 : want / blocks;
-  if (s > (tiles + p.least - 1) / p.least) s = (tiles + p.least - 1) / p.least;
-  if (s > kMaxSplits) s = kMaxSplits;
-  p.splits = (int)(s < 1 ? 1 : s);
-  return p;
+  static const struct { int rows, keys; double base, least, full, tail; } kernels[] = {
+      {16, 4 * kTile, 5.6, 1.10, 1.42, 0.93}, {128, kTile, 6.3, 1.34, 0.96, 0.96}};
+  static const int ways[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128};
+  const int64_t G = H / Hk, tiles = (max_length + kTile - 1) / kTile;
+  AttnPlan best{0, 1, 2};
+  double best_t = 1e300;
+  for (int k = 0; k < 2; ++k) {
+    const int rows = kernels[k].rows;
+    int64_t blocks = packed ? (T * G + rows - 1) / rows : B * ((G + rows - 1) / rows);
+    blocks = (blocks < B ? B : blocks) * Hk;
+    const double wide = k == 0 ? (double)D / 128.0 : 0.3 + 0.7 * (double)D / 128.0;
+    for (int s : ways) {
+      if (s > 1 && (tiles < 2 * s || (int64_t)s * T * H * (D + 2) * 4 > kMostPartial)) break;
+      const double steps = (double)(((tiles + s - 1) / s * kTile + kernels[k].keys - 1) / kernels[k].keys);
+      const double all = (double)(blocks * s) / 256.0 * steps * (B > 1 ? 0.6 : 1.0) * kernels[k].full * wide;
+      const double t = kernels[k].base + fmax(steps * kernels[k].least, all + steps * kernels[k].tail) +
+                       (s > 1 ? 3.5 + 2.1e-6 * (double)(T * H * D) * s : 0.0);
+      if (t < best_t) {
+        best_t = t;
+        best = AttnPlan{k, s, 2};
+      }
+    }
+  }
+  return best;
 }
 
 template <int D, int NW>
@@ -832,14 +896,14 @@ hipError_t launch_d(const AttnCacheArgs& a, int kernel, hipStream_t stream) {
     const int64_t blocks = a.cu == nullptr ? a.B * ((G + 15) / 16) : (a.T * G >> 4) + a.B;
     hipLaunchKernelGGL(attention_few_kernel<D>, dim3((unsigned)(blocks * a.splits), (unsigned)a.c.Hk), dim3(64 * kWavesF),
                        0, stream, a);
-  } else if (kernel == 2) {
-    if constexpr (D == 128) launch_tiles<D, 8>(a, stream);
   } else {
     launch_tiles<D, 4>(a, stream);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL(join_kernel<D>, dim3((unsigned)(a.T * a.H)), dim3(256), 0, stream, a);
+  const int64_t rows = a.T * a.H;
+  if (a.splits > kFewSplits) hipLaunchKernelGGL((join_kernel<D, true>), dim3((unsigned)rows), dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((join_kernel<D, false>), dim3((unsigned)((rows + 1024 / D - 1) / (1024 / D))), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 

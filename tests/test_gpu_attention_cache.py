@@ -281,11 +281,11 @@ def test_views_strides_streams_and_guards(gpu_lib):
 def test_rows_outside_the_offsets_are_left_alone(gpu_lib):
     for lens in ([100, 300], [100, 30000]):
         c = Case(gpu_lib, [3, 4], lens, 4, 2, 64, 64, 18)
-        ref = c.run()
         q = torch.cat([c.q[:2], c.q, c.q[:5]])
         out = torch.full_like(q, 7.0)
         c.lib.attention_cache_fp8(q, c.cache, i32(c.table), i32(c.lens), cu_seqlens=i32([2, 5, 9]), max_length=max(lens), out=out)
-        assert torch.equal(out[2:9], ref) and bool((out[:2] == 7).all()) and bool((out[9:] == 7).all())
+        c.check(out[2:9])   # (not bit for bit a call without the other rows: keys may be shared out differently)
+        assert bool((out[:2] == 7).all()) and bool((out[9:] == 7).all())
 
 
 @pytest.mark.parametrize("cu", [[0, 40, 20, 60], [-5, 10, 30, 60], [0, 10, 30, 1000], [60, 40, 20, 0], [50, 50, 50, 60]])
