@@ -112,6 +112,8 @@ SIGNATURES = {
     "svdq_cache_read_fp8": (_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, _i64, _c_void_p, _i64,
                                    _c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p, _c_void_p]),
     "svdq_attention_cache_fp8_workspace_bytes": (_size, [_i64, _i64, _i64, _i64, _i64, _i64, _int]),
+    "svdq_attention_cache_fp8_plan": (_int, [_i64, _i64, _i64, _i64, _i64, _i64, _int, ctypes.POINTER(_int),
+                                             ctypes.POINTER(_int)]),
     "svdq_attention_cache_fp8": (_int, [_c_void_p, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i64,
                                         _i64, _i64, _c_void_p, _i64, _c_void_p, _c_void_p, _i64, _i64, _i64, _i64, _int,
                                         _f32, _c_void_p, _i64, _i64, _c_void_p, _size, _c_void_p]),

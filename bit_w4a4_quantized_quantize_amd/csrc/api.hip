@@ -2038,6 +2038,16 @@ size_t svdq_attention_cache_fp8_workspace_bytes(int64_t T, int64_t B, int64_t H,
   return svdq::attention_cache_workspace_bytes(T, B, H, Hk, D, max_length, packed != 0);
 }
 
+int svdq_attention_cache_fp8_plan(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_length,
+                                  int packed, int* kernel, int* splits) {
+  if (T < 1 || B < 1 || Hk < 1 || H < Hk || H % Hk != 0 || max_length < 1)
+    return fail(SVDQ_ERR_SHAPE, "T, B, H, Hk, max_length must be positive, H a multiple of Hk");
+  if (D != 64 && D != 128) return fail(SVDQ_ERR_UNSUPPORTED, "head size D = %lld is not 64 or 128", (long long)D);
+  if (kernel == nullptr || splits == nullptr) return fail(SVDQ_ERR_NULL, "%s is NULL", kernel == nullptr ? "kernel" : "splits");
+  svdq::attention_cache_plan(T, B, H, Hk, D, max_length, packed != 0, kernel, splits);
+  return ok();
+}
+
 int svdq_attention_cache_fp8(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_codes,
                              const void* v_codes, const void* k_scales, const void* v_scales, int64_t pages,
                              int64_t Hk, int64_t page, int64_t D, const void* block_table, int64_t width,

@@ -838,14 +838,14 @@ __global__ __launch_bounds__(256) void join_kernel(AttnCacheArgs a) {
 }
 
 // Which kernel (0 few rows, 1 tiles) and how many ways the keys are split, by an estimate in microseconds from what the host
-// knows: T, B and a bound of the lengths (with several sequences taken to average 0.6 of it). A workgroup walks through
-// its share in steps (64 keys a wave of few rows, a tile), each at least `least` long; all of them together
-// take `full` a step for each workgroup on a CU, and `tail` a step for the longest one's end; `base` starts and ends
-// the call, a split adds a launch and its partial results. Fitted to both kernels at 160 sizes (1 to 64 sequences of 1
-// to 1024 queries on 150 to 22000 keys, groups of 1, 4 and 8, keys split up to 64 ways:
-// profiles/attention_cache_grid.txt): within 2.3% of the best on average and 28% at worst. One token on 65537
-// keys, 32 heads on 8: 29 us split 32 ways, 51 16 ways, 32 128 ways. 40 tokens on 540 keys: 9.7 us by few rows, 19 by tiles;
-// 512 on 8704: 192 and 105.
+// knows: T, B and a bound of the lengths. A workgroup walks through its share in steps (64 keys for each wave of few rows, a
+// tile of 64); a step takes at least `least`, and `full` for each workgroup on a CU: those there together up to two, else
+// all that come by, and `tail` for the last ones' end. Of several sequences the longest counts 1.34 of a step's share while all
+// are there, and they average 0.8 of it else. `base` starts and ends the call, a split adds a launch and its partial results.
+// Fitted to both kernels at 330 sizes (1 to 64 sequences of 1 to 4096 queries on 150 to 30000 keys, groups of 1, 4 and
+// 8, keys split up to 64 ways: profiles/attention_cache_grid.txt): within 2% of the best on average and 35% at
+// worst. One token on 65537 keys, 32 heads on 8: 29 us split 32 ways, 51 16 ways, 32 128 ways. 40 tokens on 540 keys: 9.7 us by
+// few rows, 19 by tiles; 512 on 8704: 192 and 105.
 struct AttnPlan {
   int kernel, splits, least;
 };
@@ -853,7 +853,7 @@ constexpr int64_t kMostPartial = int64_t(1) << 28;   // bytes
 
 AttnPlan plan_attention(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_length, bool packed) {
   static const struct { int rows, keys; double base, least, full, tail; } kernels[] = {
-      {16, 4 * kTile, 5.6, 1.10, 1.42, 0.93}, {128, kTile, 6.3, 1.34, 0.96, 0.96}};
+      {16, 4 * kTile, 3.9, 1.39, 1.81, 0.55}, {128, kTile, 6.2, 1.60, 0.83, 0.86}};
   static const int ways[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128};
   const int64_t G = H / Hk, tiles = (max_length + kTile - 1) / kTile;
   AttnPlan best{0, 1, 2};
@@ -866,9 +866,10 @@ AttnPlan plan_attention(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, 
     for (int s : ways) {
       if (s > 1 && (tiles < 2 * s || (int64_t)s * T * H * (D + 2) * 4 > kMostPartial)) break;
       const double steps = (double)(((tiles + s - 1) / s * kTile + kernels[k].keys - 1) / kernels[k].keys);
-      const double all = (double)(blocks * s) / 256.0 * steps * (B > 1 ? 0.6 : 1.0) * kernels[k].full * wide;
-      const double t = kernels[k].base + fmax(steps * kernels[k].least, all + steps * kernels[k].tail) +
-                       (s > 1 ? 3.5 + 2.1e-6 * (double)(T * H * D) * s : 0.0);
+      const double on_cu = (double)(blocks * s) / 256.0;
+      const double share = on_cu <= 2.0 ? on_cu * (B > 1 ? 1.34 : 1.0) : on_cu * (B > 1 ? 0.8 : 1.0) + kernels[k].tail;
+      const double t = kernels[k].base + steps * fmax(kernels[k].least, share * kernels[k].full * wide) +
+                       (s > 1 ? 5.0 + 2.2e-6 * (double)(T * H * D) * s : 0.0);
       if (t < best_t) {
         best_t = t;
         best = AttnPlan{k, s, 2};
@@ -913,6 +914,13 @@ size_t attention_cache_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t 
                                        bool packed) {
   const AttnPlan p = plan_attention(T, B, H, Hk, D, max_length, packed);
   return p.splits > 1 ? (size_t)p.splits * (size_t)T * (size_t)H * (size_t)(D + 2) * 4 : 0;
+}
+
+void attention_cache_plan(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_length, bool packed,
+                          int* kernel, int* splits) {
+  const AttnPlan p = plan_attention(T, B, H, Hk, D, max_length, packed);
+  *kernel = p.kernel;
+  *splits = p.splits;
 }
 
 hipError_t launch_attention_cache(AttnCacheArgs a, int64_t max_length, hipStream_t stream) {

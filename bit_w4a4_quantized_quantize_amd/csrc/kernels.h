@@ -316,6 +316,8 @@ struct AttnCacheArgs {
 };
 size_t attention_cache_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_length,
                                        bool packed);
+void attention_cache_plan(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_length, bool packed,
+                          int* kernel, int* splits);
 hipError_t launch_attention_cache(AttnCacheArgs a, int64_t max_length, hipStream_t stream);
 
 // Measurement helpers (not part of the layer): sustained f16 matrix-instruction

@@ -1216,6 +1216,15 @@ def attention_cache_fp8_workspace_bytes(T, B, H, Hk, D, max_length, packed):
     return _lib.lib().svdq_attention_cache_fp8_workspace_bytes(T, B, H, Hk, D, max_length, 1 if packed else 0)
 
 
+def attention_cache_fp8_plan(T, B, H, Hk, D, max_length, packed):
+    """How attention_cache_fp8 runs these sizes (tests and tuning): (kernel, ways the keys are split), kernel 0 for few rows
+    or 1 for tiles."""
+    kernel, splits = ctypes.c_int(0), ctypes.c_int(0)
+    _lib.check("svdq_attention_cache_fp8_plan", _lib.lib().svdq_attention_cache_fp8_plan(
+        T, B, H, Hk, D, max_length, 1 if packed else 0, ctypes.byref(kernel), ctypes.byref(splits)))
+    return kernel.value, splits.value
+
+
 def attention_cache_fp8(q, cache: Fp8Cache, block_table, lengths, cu_seqlens=None, causal=True, scale=None,
                         max_length=None, out=None, workspace=None):
     """softmax(scale * q k^T) v with k and v out of the cache. q [T, H, D] bf16 (a view with any token and head strides;

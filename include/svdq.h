@@ -688,6 +688,10 @@ int svdq_cache_read_fp8(const void* k_codes, const void* v_codes, const void* k_
                         void* stream);
 size_t svdq_attention_cache_fp8_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D,
                                                 int64_t max_length, int packed);
+/* How svdq_attention_cache_fp8 runs these sizes, host only (tests and tuning): kernel 0 (few rows) or 1 (tiles of 128
+ * rows) and the ways the keys are split. */
+int svdq_attention_cache_fp8_plan(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_length,
+                                  int packed, int* kernel, int* splits);
 int svdq_attention_cache_fp8(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_codes,
                              const void* v_codes, const void* k_scales, const void* v_scales, int64_t pages,
                              int64_t Hk, int64_t page, int64_t D, const void* block_table, int64_t width,
