@@ -1679,8 +1679,8 @@ static int quantize_fp8_impl(const void* x, const void* smooth, int64_t M, int64
                              bool weight, void* stream) {
   int st = check_fp8_mnk(M, 0, K);
   if (st) return st;
-  if (M * blocks128(K) >= (int64_t(1) << 31))
-    return fail(SVDQ_ERR_UNSUPPORTED, "2^31 blocks of 128 or more (rows=%lld K=%lld)", (long long)M, (long long)K);
+  if (M * blocks128(K) >= (int64_t(1) << 30))   // four threads of the grid each
+    return fail(SVDQ_ERR_UNSUPPORTED, "2^30 blocks of 128 or more (rows=%lld K=%lld)", (long long)M, (long long)K);
   if (weight && blocks128(M) > 65535)
     return fail(SVDQ_ERR_UNSUPPORTED, "N = %lld is above %d", (long long)M, 65535 * 128);
   if (M == 0) return ok();
@@ -1802,8 +1802,8 @@ int svdq_linear_fp8(const void* x, const void* smooth, const void* weight, const
                     int64_t M, int64_t N, int64_t K, void* y, void* workspace, size_t workspace_bytes, void* stream) {
   int st = check_fp8_mnk(M, N, K);
   if (st) return st;
-  if (M * blocks128(K) >= (int64_t(1) << 31))
-    return fail(SVDQ_ERR_UNSUPPORTED, "2^31 blocks of 128 or more (M=%lld K=%lld)", (long long)M, (long long)K);
+  if (M * blocks128(K) >= (int64_t(1) << 30))   // four threads of the grid each
+    return fail(SVDQ_ERR_UNSUPPORTED, "2^30 blocks of 128 or more (M=%lld K=%lld)", (long long)M, (long long)K);
   if (M == 0 || N == 0) return ok();
   const char* names[] = {"x"};
   const void* ptrs[] = {x};
@@ -1939,6 +1939,9 @@ static int check_cache(const void* k_codes, const void* v_codes, const void* k_s
     return fail(SVDQ_ERR_INVALID, "without cu_seqlens each of the B = %lld sequences has one token, but T = %lld",
                 (long long)B, (long long)T);
   if (width < 1 || width > kMaxDim) return fail(SVDQ_ERR_SHAPE, "table width %lld is not in 1..2^24", (long long)width);
+  if (width * page > (int64_t(1) << 30))
+    return fail(SVDQ_ERR_UNSUPPORTED, "a table of %lld pages of %lld tokens: at most 2^30 tokens are supported",
+                (long long)width, (long long)page);
   const char* names[] = {"k_codes", "v_codes"};
   const void* ptrs[] = {k_codes, v_codes};
   if ((st = check_ptrs(names, ptrs, 2))) return st;
@@ -2064,9 +2067,11 @@ int svdq_attention_cache_fp8(const void* q, int64_t q_stride_t, int64_t q_stride
   if (H > 65535) return fail(SVDQ_ERR_UNSUPPORTED, "H = %lld may be at most 65535", (long long)H);
   if (!(scale > 0.0f && scale <= 1048576.0f)) return fail(SVDQ_ERR_INVALID, "scale = %g is not in (0, 2^20]", scale);
   if (max_length < 1) return fail(SVDQ_ERR_SHAPE, "max_length = %lld must be positive", (long long)max_length);
-  // work items of the grid, 256 for 16 rows
-  if (16 * T * (H / Hk) + 512 * B >= (int64_t(1) << 32) - 65536)
-    return fail(SVDQ_ERR_UNSUPPORTED, "16 T H / Hk + 512 B must be below 2^32 - 65536 (T=%lld B=%lld H=%lld Hk=%lld)",
+  // work items of the grids, 256 for 16 rows of a head or 128 of any
+  const int64_t most = (int64_t(1) << 32) - 65536;
+  if (16 * T * (H / Hk) + 512 * B >= most || 2 * T * H + 256 * B * Hk >= most)
+    return fail(SVDQ_ERR_UNSUPPORTED,
+                "16 T H / Hk + 512 B and 2 T H + 256 B Hk must be below 2^32 - 65536 (T=%lld B=%lld H=%lld Hk=%lld)",
                 (long long)T, (long long)B, (long long)H, (long long)Hk);
   if (T == 0 || B == 0) return ok();
   Heads hq, ho;

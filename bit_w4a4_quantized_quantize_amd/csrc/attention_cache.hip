@@ -26,6 +26,7 @@ namespace {
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kTile = 64;             // keys of a step
+constexpr int kLeastTiles = 2;        // of a split
 constexpr float kSlackC = 8.0f;       // powers of two that a score may pass the running maximum by
 constexpr float kLowest = -3.4028234663852886e38f;
 
@@ -76,7 +77,7 @@ __device__ __forceinline__ int64_t keys_of(const AttnCacheArgs& a, int b) {
 // tiles of 64 keys that a split takes, and how many splits have any
 __device__ __forceinline__ int tiles_per_split(const AttnCacheArgs& a, int64_t L) {
   const int tiles = (int)((L + kTile - 1) / kTile);
-  return max((tiles + a.splits - 1) / a.splits, a.least);
+  return max((tiles + a.splits - 1) / a.splits, kLeastTiles);
 }
 
 // sum or maximum over the four lanes l16, l16 + 16, .. of a row
@@ -310,29 +311,29 @@ __global__ __launch_bounds__(64 * kWavesF, D == 64 ? 4 : 2) void attention_few_k
   }
 }
 
-// Many rows. A workgroup of NW waves takes 32 NW rows, 32 a wave, and tiles of 64 keys in LDS: codes travel
+// Many rows. A workgroup of four waves takes 128 rows, 32 a wave, and tiles of 64 keys in LDS: codes travel
 // to registers a step ahead, become bf16 and are written to LDS before the next step's barrier. K^T's tile is
 // [64][D]; V^T's is [D][64] with each 16 keys in the order of P^T's operand (0-3, 8-11 for the lower half of the
 // wave, 4-7, 12-15 for the upper), so that both products read whole 16-byte pieces. Products,
 // exponentials and the lazy maximum are arranged as in attention.hip.
 // WHOLE: pages of 64 or 128 tokens, so that a tile lies in one page: its address and scale are scalar, and a page that the
 // table does not have is a buffer of no bytes, which reads zero.
+constexpr int kWavesT = 4, kLgRows = 7;
+static_assert(kWavesT * 32 == 1 << kLgRows, "32 rows a wave");
 constexpr int kAheadC = 2;   // operand reads in flight ahead of a product
 
 __device__ __forceinline__ u32x4 load_codes(__amdgpu_buffer_rsrc_t r, int voff, int soff) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0));
 }
 
-template <int D, bool CAUSAL, int NW, bool WHOLE>
-__global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArgs a) {
+template <int D, bool CAUSAL, bool WHOLE>
+__global__ __launch_bounds__(64 * kWavesT, 2) void attention_tile_kernel(AttnCacheArgs a) {
   constexpr int kRowBytes = 2 * D;
   constexpr int kTileBytes = kTile * kRowBytes;     // of K, and of V
   constexpr int KD = D / 16;                        // 16-element steps of the first product
   constexpr int JD = D / 32;                        // 32-element blocks of the output
   constexpr int kCP = D / 16;                       // 16-byte pieces of a key's codes
-  constexpr int kPieces = kTile * kCP / (64 * NW);  // of a tile, per thread; as many of V
-  constexpr int kLgRows = NW == 8 ? 8 : 7;
-  static_assert(NW * 32 == 1 << kLgRows && kPieces >= 1, "waves");
+  constexpr int kPieces = kTile * kCP / (64 * kWavesT);  // of a tile, per thread; as many of V
   __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * kTileBytes];
 
   const int tid = threadIdx.x;
@@ -369,7 +370,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
   // keys up to `low` are seen by every row of the wave, none past `high` by any
   const int low = CAUSAL ? off + min(row0, n_rows - 1) / G : L - 1;
   const int high = CAUSAL ? off + min(row0 + 31, n_rows - 1) / G : L - 1;
-  const int wg_high = CAUSAL ? off + min(rb.row0 + 32 * NW - 1, n_rows - 1) / G : L - 1;
+  const int wg_high = CAUSAL ? off + min(rb.row0 + 32 * kWavesT - 1, n_rows - 1) / G : L - 1;
   const int kt0 = split * per;
   const int nt = max(min((wg_high >> 6) + 1, kt0 + per) - kt0, 0);              // tiles of the workgroup (>> of -1 is -1)
   const int ntw = row0 < n_rows ? max(min((high >> 6) + 1, kt0 + per) - kt0, 0) : 0;   // and of this wave
@@ -381,11 +382,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
     for (int t = 0; t < KD; ++t) fq[t] = *reinterpret_cast<const bf16x8*>(qp + 16 * t);
   }
 
-  // Pieces of 16 codes: of K, key kr and elements 16 ks .. (piece c: 64 NW / kCP keys further on); of V, element vd
-  // and keys 16 vk .. (16 NW elements further on). The LDS swizzles repeat with those steps.
+  // Pieces of 16 codes: of K, key kr and elements 16 ks .. (piece c: 256 / kCP keys further on); of V, element vd
+  // and keys 16 vk .. (64 elements further on). The LDS swizzles repeat with those steps.
   auto swz_k = [](int r) { return D == 128 ? (r & 15) : ((r >> 1) & 7); };
   auto swz_v = [](int r) { return (r ^ (r >> 3)) & 7; };
-  constexpr int kStepK = 64 * NW / kCP, kStepV = 16 * NW;
+  constexpr int kStepK = 64 * kWavesT / kCP, kStepV = 16 * kWavesT;
   static_assert(kStepK % 16 == 0 && kStepV % 64 == 0, "swizzles");
   const int kr = tid / kCP, ks = tid % kCP, vd = tid >> 2, vk = tid & 3;
   const int k_src = kr * D + 16 * ks;                 // within a tile's page
@@ -719,7 +720,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_tile_kernel(AttnCacheArg
   __syncthreads();
   constexpr int kOP = D / 8, kRowsPerCopy = 64 / kOP;
   uint8_t* out = smem + wave * (32 * kRowBytes);
-  static_assert(NW * 32 * kRowBytes <= 4 * kTileBytes, "output staging");
+  static_assert(kWavesT * 32 * kRowBytes <= 4 * kTileBytes, "output staging");
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
   for (int j = 0; j < JD; ++j)
@@ -847,7 +848,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnCacheArgs a) {
 // worst. One token on 65537 keys, 32 heads on 8: 29 us split 32 ways, 51 16 ways, 32 128 ways. 40 tokens on 540 keys: 9.7 us by
 // few rows, 19 by tiles; 512 on 8704: 192 and 105.
 struct AttnPlan {
-  int kernel, splits, least;
+  int kernel, splits;
 };
 constexpr int64_t kMostPartial = int64_t(1) << 28;   // bytes
 
@@ -856,7 +857,7 @@ AttnPlan plan_attention(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, 
       {16, 4 * kTile, 3.9, 1.39, 1.81, 0.55}, {128, kTile, 6.2, 1.60, 0.83, 0.86}};
   static const int ways[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128};
   const int64_t G = H / Hk, tiles = (max_length + kTile - 1) / kTile;
-  AttnPlan best{0, 1, 2};
+  AttnPlan best{0, 1};
   double best_t = 1e300;
   for (int k = 0; k < 2; ++k) {
     const int rows = kernels[k].rows;
@@ -864,7 +865,7 @@ AttnPlan plan_attention(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, 
     blocks = (blocks < B ? B : blocks) * Hk;
     const double wide = k == 0 ? (double)D / 128.0 : 0.3 + 0.7 * (double)D / 128.0;
     for (int s : ways) {
-      if (s > 1 && (tiles < 2 * s || (int64_t)s * T * H * (D + 2) * 4 > kMostPartial)) break;
+      if (s > 1 && (tiles < kLeastTiles * s || (int64_t)s * T * H * (D + 2) * 4 > kMostPartial)) break;
       const double steps = (double)(((tiles + s - 1) / s * kTile + kernels[k].keys - 1) / kernels[k].keys);
       const double on_cu = (double)(blocks * s) / 256.0;
       const double share = on_cu <= 2.0 ? on_cu * (B > 1 ? 1.34 : 1.0) : on_cu * (B > 1 ? 0.8 : 1.0) + kernels[k].tail;
@@ -872,22 +873,22 @@ AttnPlan plan_attention(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, 
                        (s > 1 ? 5.0 + 2.2e-6 * (double)(T * H * D) * s : 0.0);
       if (t < best_t) {
         best_t = t;
-        best = AttnPlan{k, s, 2};
+        best = AttnPlan{k, s};
       }
     }
   }
   return best;
 }
 
-template <int D, int NW>
+template <int D>
 void launch_tiles(const AttnCacheArgs& a, hipStream_t stream) {
-  const int64_t total = ((a.T * (a.H / a.c.Hk) >> (NW == 8 ? 8 : 7)) + a.B) * a.splits * a.c.Hk;
-  const dim3 grid((unsigned)((total + 7) / 8 * 8)), block(64 * NW);
+  const int64_t total = ((a.T * (a.H / a.c.Hk) >> kLgRows) + a.B) * a.splits * a.c.Hk;
+  const dim3 grid((unsigned)((total + 7) / 8 * 8)), block(64 * kWavesT);
   const bool whole = a.c.lg_page >= 6;
-  if (a.causal && whole) hipLaunchKernelGGL((attention_tile_kernel<D, true, NW, true>), grid, block, 0, stream, a);
-  else if (a.causal) hipLaunchKernelGGL((attention_tile_kernel<D, true, NW, false>), grid, block, 0, stream, a);
-  else if (whole) hipLaunchKernelGGL((attention_tile_kernel<D, false, NW, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((attention_tile_kernel<D, false, NW, false>), grid, block, 0, stream, a);
+  if (a.causal && whole) hipLaunchKernelGGL((attention_tile_kernel<D, true, true>), grid, block, 0, stream, a);
+  else if (a.causal) hipLaunchKernelGGL((attention_tile_kernel<D, true, false>), grid, block, 0, stream, a);
+  else if (whole) hipLaunchKernelGGL((attention_tile_kernel<D, false, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((attention_tile_kernel<D, false, false>), grid, block, 0, stream, a);
 }
 
 template <int D>
@@ -898,7 +899,7 @@ hipError_t launch_d(const AttnCacheArgs& a, int kernel, hipStream_t stream) {
     hipLaunchKernelGGL(attention_few_kernel<D>, dim3((unsigned)(blocks * a.splits), (unsigned)a.c.Hk), dim3(64 * kWavesF),
                        0, stream, a);
   } else {
-    launch_tiles<D, 4>(a, stream);
+    launch_tiles<D>(a, stream);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
@@ -926,7 +927,6 @@ void attention_cache_plan(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D
 hipError_t launch_attention_cache(AttnCacheArgs a, int64_t max_length, hipStream_t stream) {
   const AttnPlan p = plan_attention(a.T, a.B, a.H, a.c.Hk, a.c.D, max_length, a.cu != nullptr);
   a.splits = p.splits;
-  a.least = p.least;
   return a.c.D == 64 ? launch_d<64>(a, p.kernel, stream) : launch_d<128>(a, p.kernel, stream);
 }
 

@@ -310,8 +310,8 @@ struct AttnCacheArgs {
   int64_t T, width;
   int B, H, causal;
   float scale;
-  // the keys of a sequence are shared among `splits` workgroups, whole tiles of 64 each, at least `least`
-  int splits, least;
+  // the keys of a sequence are shared among `splits` workgroups, whole tiles of 64 each
+  int splits;
   float* partial;          // [splits, T * H, D], then [splits, T * H, 2]: maximum and sum
 };
 size_t attention_cache_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_length,

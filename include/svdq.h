@@ -586,7 +586,7 @@ int svdq_attention_packed(const void* q, int64_t q_stride_t, int64_t q_stride_h,
  *   1 / the layer's smooth, or NULL). N at most 2^23 - 128.
  * svdq_gemm_fp8: from codes; svdq_linear_fp8: the whole layer from x.
  * K: a positive multiple of 16, at most 2^20. M, N: at most 2^24, M * N at most 2^38,
- *   M * ceil(K/128) below 2^31 for the quantisation.
+ *   M * ceil(K/128) below 2^30 for the quantisation.
  * workspace: svdq_gemm_fp8_workspace_bytes(M, N, K) and svdq_linear_fp8_workspace_bytes(M, N, K)
  *   bytes (0 for some sizes: then it may be NULL); no initialisation needed, contents
  *   unspecified afterwards.
@@ -675,8 +675,8 @@ int svdq_rope_scaled(const void* q, int64_t q_stride_t, int64_t q_stride_h, int6
  *   the keys are shared out, a greater length is computed as well.
  *   workspace: svdq_attention_cache_fp8_workspace_bytes(T, B, H, Hk, D, min(max_length, width * page), packed =
  *   cu_seqlens given) bytes, as for svdq_gemm_fp8.
- * D: 64 or 128; H a multiple of Hk; T below 2^24; B, H, Hk at most 65535; width at most 2^24; pages below 2^31;
- * scale in (0, 2^20]; 16 T H / Hk + 512 B below 2^32 - 65536.
+ * D: 64 or 128; H a multiple of Hk; T below 2^24; B, H, Hk at most 65535; width at most 2^24 and
+ * width * page at most 2^30; pages below 2^31; scale in (0, 2^20]; 16 T H / Hk + 512 B and 2 T H + 256 B Hk below 2^32 - 65536.
  */
 int svdq_cache_append_fp8(const void* k, int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
                           int64_t v_stride_h, void* k_codes, void* v_codes, void* k_scales, void* v_scales,

@@ -48,7 +48,7 @@ ATTN = dict(q=fake(1), qst=1024, qsh=128, kc=fake(3), vc=fake(4), ks=fake(5), vs
 @pytest.mark.parametrize("fn", ["svdq_quantize_fp8", "svdq_quantize_weight_fp8"])
 @pytest.mark.parametrize("kw,code", [
     (dict(M=-1), 2), (dict(K=24), 2), (dict(K=0), 2), (dict(K=(1 << 20) + 16), 3), (dict(M=(1 << 24) + 1), 3),
-    (dict(M=1 << 24, K=1 << 20), 3), (dict(x=None), 1), (dict(codes=None), 1), (dict(scales=None), 1), (dict(smooth=fake(2) + 8), 4),
+    (dict(M=1 << 24, K=1 << 20), 3), (dict(M=1 << 23, K=1 << 14), 3), (dict(x=None), 1), (dict(codes=None), 1), (dict(scales=None), 1), (dict(smooth=fake(2) + 8), 4),
     (dict(codes=fake(3) + 4), 4), (dict(codes=fake(1)), 6), (dict(scales=fake(3) + 64), 6), (dict(codes=fake(2) + 256), 6),
 ])
 def test_quantize(fn, kw, code):
@@ -105,7 +105,8 @@ def test_rope(kw, code):
 CACHE_CASES = [
     (dict(T=-1), 2), (dict(T=1 << 24), 3), (dict(D=96), 3), (dict(D=0), 3), (dict(page=8), 3), (dict(page=48), 3), (dict(page=256), 3),
     (dict(pages=0), 2), (dict(pages=1 << 31), 2), (dict(Hk=0), 2), (dict(Hk=65536), 3), (dict(B=-1), 2), (dict(B=65536), 3),
-    (dict(cu=None), 8), (dict(width=0), 2), (dict(width=(1 << 24) + 1), 2), (dict(kc=None), 1), (dict(vc=None), 1), (dict(ks=None), 1),
+    (dict(cu=None), 8), (dict(width=0), 2), (dict(width=(1 << 24) + 1), 2), (dict(width=(1 << 23) + 1, page=128), 3),
+    (dict(kc=None), 1), (dict(vc=None), 1), (dict(ks=None), 1),
     (dict(vs=None), 1), (dict(table=None), 1), (dict(table=fake(7) + 2), 4), (dict(cu=fake(9) + 1), 4), (dict(kc=fake(3) + 8), 4),
     (dict(kc=fake(4) + 16), 6), (dict(vs=fake(5) + 3), 6), (dict(ks=fake(3) + 64), 6),
 ]
@@ -140,7 +141,7 @@ def test_read(kw, code):
 @no_gpu_only
 @pytest.mark.parametrize("kw,code", [
     (dict(H=0), 2), (dict(H=9), 2), (dict(H=65538), 3), (dict(scale=0.0), 8), (dict(scale=float("nan")), 8), (dict(scale=2.0 ** 21), 8),
-    (dict(most=0), 2), (dict(T=(1 << 24) - 1, H=64), 3), (dict(q=None), 1), (dict(q=fake(1) + 8), 4), (dict(qst=64), 2), (dict(qsh=100), 4),
+    (dict(most=0), 2), (dict(T=(1 << 24) - 1, H=64), 3), (dict(B=65535, Hk=512, H=512), 3), (dict(q=None), 1), (dict(q=fake(1) + 8), 4), (dict(qst=64), 2), (dict(qsh=100), 4),
     (dict(o=None), 1), (dict(osh=64), 2), (dict(o=fake(1)), 6), (dict(o=fake(3) + 64), 6), (dict(o=fake(9)), 6), (dict(ws_bytes=100), 5),
     (dict(ws=None), 1), (dict(ws=fake(10) + 8), 4), (dict(ws=fake(2)), 6), (dict(ws=fake(1)), 6), (dict(ws=fake(4)), 6), (dict(lens=None), 1),
 ])
