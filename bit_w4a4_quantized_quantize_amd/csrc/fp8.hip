@@ -676,15 +676,18 @@ struct F8Plan {
 // each: power and the L2s); 4.2 us start and end a product; a split adds 0.9 us and the partial sums' traffic.
 // As for the 8-bit integers, a call that is not in a graph takes its caller about 10 us and 3 more for a split's
 // launch, so a split pays only where the device takes longer than that. On the device alone the choice is within
-// 0.3% of the best on average and 6% at worst. The estimate without `full` was 4% off on average.
+// 0.2% of the best on average and 6% at worst. The estimate without `full` was 4% off on average. Tiles of 192 x 128 take
+// 8 to 14% off where rows fill them and 128's or 256's leave CUs idle (333 x 3840, K = 10240: 36 -> 33; 1500 x 3840, K = 3840:
+// 37 -> 32.5).
 F8Plan plan_fp8(int64_t M, int64_t N, int64_t K) {
   static const struct { int bm, bn; double least, share, full; } shapes[] = {
       {256, 320, 1.56, 1.33, 0.64}, {256, 256, 1.45, 1.30, 0.49}, {256, 128, 0.86, 0.90, 0.31},
-      {128, 128, 0.46, 0.49, 0.27}, {64, 128, 0.33, 0.41, 0.10},  {64, 64, 0.35, 0.29, 0.0}};
+      {128, 128, 0.46, 0.49, 0.27}, {64, 128, 0.33, 0.41, 0.10},  {64, 64, 0.35, 0.29, 0.0},
+      {192, 128, 1.03, 0.97, 0.0}};
   const int64_t panels = (K + 127) / 128;
   F8Plan best{0, 1, (int)panels};
   double best_t = 1e300;
-  for (int s = 0; s < 6; ++s) {
+  for (int s = 0; s < 7; ++s) {
     const int64_t tiles = ((M + shapes[s].bm - 1) / shapes[s].bm) * ((N + shapes[s].bn - 1) / shapes[s].bn);
     for (int sp = 1; sp <= 8; ++sp) {
       if (sp > 1 && (panels < 2 * sp || tiles * sp > 1024)) break;
@@ -761,7 +764,8 @@ hipError_t launch_gemm_fp8(const Fp8GemmArgs& a, void* workspace, hipStream_t st
                  : p.shape == 2 ? launch_fp8_cfg<4, 2, 2, 2, 3>(a, sp, stream)
                  : p.shape == 3 ? launch_fp8_cfg<4, 2, 1, 2, 4>(a, sp, stream)
                  : p.shape == 4 ? launch_fp8_cfg<2, 4, 1, 1, 3>(a, sp, stream)
-                                : launch_fp8_cfg<2, 2, 1, 1, 3>(a, sp, stream);
+                 : p.shape == 5 ? launch_fp8_cfg<2, 2, 1, 1, 3>(a, sp, stream)
+                                : launch_fp8_cfg<2, 4, 3, 1, 3>(a, sp, stream);
   if (e != hipSuccess || p.splits == 1) return e;
   const int w = a.N % 4 == 0 ? 4 : 1;
   const dim3 grid((unsigned)((a.M * (a.N / w) + 255) / 256));

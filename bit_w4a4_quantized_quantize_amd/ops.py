@@ -977,6 +977,21 @@ def attention_packed(q, k, v, cu_seqlens=None, causal=False, scale=None, out=Non
     return out
 
 
+def _heads_of(t):
+    """A new [tokens, heads, D] tensor as the C ABI takes it."""
+    strides = t.stride()
+    return t.data_ptr(), strides[0], strides[1]
+
+
+def _all_on(index, *tensors):
+    """Every given tensor (None skipped) is on GPU `index`. Where not, _devices has the error: the calls that a decoded
+    token waits for name their tensors only then."""
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            return False
+    return index >= 0
+
+
 def _blocks128(n):
     return -(-n // 128)
 
@@ -1081,8 +1096,8 @@ def linear_fp8(x, weight, wscales, bias=None, smooth=None, y=None, workspace=Non
     else:
         _need(y, "y", torch.bfloat16, shape=(M, N))
     workspace, ws_bytes = _workspace(workspace, linear_fp8_workspace_bytes(M, N, K), dev)
-    _on_one_device(x.get_device(), x=x, smooth=smooth, weight=weight, wscales=wscales, bias=bias, y=y,
-                   workspace=workspace)
+    if not _all_on(x.get_device(), smooth, weight, wscales, bias, y, workspace):
+        _devices(x=x, smooth=smooth, weight=weight, wscales=wscales, bias=bias, y=y, workspace=workspace)
     _launch("svdq_linear_fp8", dev, _p(x), _p(smooth), _p(weight), _p(wscales), _p(bias), M, N, K, _p(y),
             _p(workspace), ws_bytes)
     return y
@@ -1104,25 +1119,33 @@ def rope_scaled(q, k, positions, rotary_dim=None, theta=10000.0, interleaved=Fal
     qa, ka, qoa, koa, H, Hk = _NO_HEADS, _NO_HEADS, _NO_HEADS, _NO_HEADS, 0, 0
     if q is not None:
         qa = _need_heads(q, "q")
-        H = q.shape[1]
+        T, H, D = q.shape
     if k is not None:
         ka = _need_heads(k, "k")
-        Hk = k.shape[1]
-    T, _, D = given.shape
-    if q is not None and k is not None and (k.shape[0] != T or k.shape[2] != D):
-        raise ValueError(f"k must have shape {[T, Hk, D]}, got {list(k.shape)}")
+        have, Hk, size = k.shape
+        if q is None:
+            T, D = have, size
+        elif have != T or size != D:
+            raise ValueError(f"k must have shape {[T, Hk, D]}, got {list(k.shape)}")
     _need(positions, "positions", torch.int32, shape=(T,))
     if q is not None:
-        q_out = torch.empty_like(q) if q_out is None else q_out
-        qoa = _need_heads(q_out, "q_out", q.shape)
+        if q_out is None:
+            q_out = torch.empty_like(q)
+            qoa = _heads_of(q_out)
+        else:
+            qoa = _need_heads(q_out, "q_out", q.shape)
     elif q_out is not None:
         raise ValueError("q_out needs q")
     if k is not None:
-        k_out = torch.empty_like(k) if k_out is None else k_out
-        koa = _need_heads(k_out, "k_out", k.shape)
+        if k_out is None:
+            k_out = torch.empty_like(k)
+            koa = _heads_of(k_out)
+        else:
+            koa = _need_heads(k_out, "k_out", k.shape)
     elif k_out is not None:
         raise ValueError("k_out needs k")
-    _on_one_device(given.get_device(), q=q, k=k, positions=positions, q_out=q_out, k_out=k_out)
+    if not _all_on(given.get_device(), q, k, positions, q_out, k_out):
+        _devices(q=q, k=k, positions=positions, q_out=q_out, k_out=k_out)
     _launch("svdq_rope_scaled", given.device, *qa, H, *ka, Hk, positions.data_ptr(),
             D if rotary_dim is None else rotary_dim, theta, factor, original_length, low_rotations, high_rotations,
             amplitude, 1 if interleaved else 0, T, D, *qoa, *koa)
@@ -1151,11 +1174,12 @@ def new_cache_fp8(pages, heads, head_dim, page=64, device="cuda"):
                     torch.empty((pages, heads), dtype=torch.uint8, device=device))
 
 
-def _cache_device(cache, block_table, lengths, lengths_name, cu_seqlens, **others):
-    """Every tensor of the call is on the cache's GPU; called after the checks of sizes."""
-    _on_one_device(cache.k_codes.get_device(), k_codes=cache.k_codes, v_codes=cache.v_codes, k_scales=cache.k_scales,
-                   v_scales=cache.v_scales, block_table=block_table, cu_seqlens=cu_seqlens, **{lengths_name: lengths},
-                   **others)
+def _cache_device(cache, block_table, lengths, lengths_name, cu_seqlens, a, b, names, workspace=None):
+    """Every tensor of the call, `names` those of a and b, is on the cache's GPU; called after the checks of sizes."""
+    kc, vc, ks, vs = cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales
+    if not _all_on(kc.get_device(), vc, ks, vs, block_table, lengths, cu_seqlens, a, b, workspace):
+        _devices(k_codes=kc, v_codes=vc, k_scales=ks, v_scales=vs, block_table=block_table, cu_seqlens=cu_seqlens,
+                 workspace=workspace, **{lengths_name: lengths, names[0]: a, names[1]: b})
 
 
 def _check_cache(cache, block_table, lengths, lengths_name, cu_seqlens):
@@ -1189,7 +1213,7 @@ def cache_append_fp8(k, v, cache: Fp8Cache, block_table, lengths, cu_seqlens=Non
     if k.shape != (T, Hk, D):
         raise ValueError(f"k must have shape {[T, Hk, D]}, got {list(k.shape)}")
     va = _need_heads(v, "v", k.shape)
-    _cache_device(cache, block_table, lengths, "lengths", cu_seqlens, k=k, v=v)
+    _cache_device(cache, block_table, lengths, "lengths", cu_seqlens, k, v, "kv")
     _launch("svdq_cache_append_fp8", cache.k_codes.device, *ka, *va, *args, T)
 
 
@@ -1205,8 +1229,8 @@ def cache_read_fp8(cache: Fp8Cache, block_table, starts, cu_seqlens=None, tokens
     shape = (tokens, Hk, D)
     dev = cache.k_codes.device
     k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else _need(k, "k", torch.bfloat16, shape=shape)
-    v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else _need(v, "v", torch.bfloat16, shape=shape)
-    _cache_device(cache, block_table, starts, "starts", cu_seqlens, k=k, v=v)
+    v = torch.empty_like(k) if v is None else _need(v, "v", torch.bfloat16, shape=shape)
+    _cache_device(cache, block_table, starts, "starts", cu_seqlens, k, v, "kv")
     _launch("svdq_cache_read_fp8", dev, *args, tokens, _p(k), _p(v))
     return k, v
 
@@ -1243,14 +1267,16 @@ def attention_cache_fp8(q, cache: Fp8Cache, block_table, lengths, cu_seqlens=Non
         raise ValueError(f"q has {H} heads, no positive multiple of the cache's {Hk}")
     if out is None:
         out = torch.empty_like(q)
-    oa = _need_heads(out, "out", q.shape)
-    B, width = block_table.shape
+        oa = _heads_of(out)
+    else:
+        oa = _need_heads(out, "out", q.shape)
+    B, width = args[-1], args[9]
     most = width * page
     max_length = most if max_length is None else max(1, min(max_length, most))
     dev = q.device
     workspace, ws_bytes = _workspace(
         workspace, attention_cache_fp8_workspace_bytes(T, B, H, Hk, D, max_length, cu_seqlens is not None), dev)
-    _cache_device(cache, block_table, lengths, "lengths", cu_seqlens, q=q, out=out, workspace=workspace)
+    _cache_device(cache, block_table, lengths, "lengths", cu_seqlens, q, out, ("q", "out"), workspace)
     _launch("svdq_attention_cache_fp8", dev, *qa, *args, T, H, max_length, 1 if causal else 0,
             scale if scale is not None else D ** -0.5, *oa, _p(workspace), ws_bytes)
     return out

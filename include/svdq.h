@@ -599,8 +599,8 @@ size_t svdq_gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int svdq_gemm_fp8(const void* codes, const void* ascales, const void* weight, const void* wscales,
                   const void* bias, int64_t M, int64_t N, int64_t K, void* y, void* workspace,
                   size_t workspace_bytes, void* stream);
-/* How svdq_gemm_fp8 runs (M, N, K), host only (tests and tuning): tile 0..5 for 256 x 320, 256 x 256, 256 x 128,
- * 128 x 128, 64 x 128 and 64 x 64 outputs and the ways k is split, or tile -1 (the kernel for few tokens) and 1. */
+/* How svdq_gemm_fp8 runs (M, N, K), host only (tests and tuning): tile 0..6 for 256 x 320, 256 x 256, 256 x 128,
+ * 128 x 128, 64 x 128, 64 x 64 and 192 x 128 outputs and the ways k is split, or tile -1 (the kernel for few tokens) and 1. */
 int svdq_gemm_fp8_plan(int64_t M, int64_t N, int64_t K, int* tile, int* splits);
 size_t svdq_linear_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int svdq_linear_fp8(const void* x, const void* smooth, const void* weight, const void* wscales, const void* bias,
