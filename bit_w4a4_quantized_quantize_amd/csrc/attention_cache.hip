@@ -70,6 +70,26 @@ __device__ __forceinline__ bool find_rows(const AttnCacheArgs& a, int G, int lg,
   return true;
 }
 
+// The same for at most 64 sequences, those with the most keys first, so that the longest do not start last: a lane has a
+// sequence, whose blocks follow those of longer ones (of equal ones before it).
+__device__ __forceinline__ bool find_rows_longest_first(const AttnCacheArgs& a, int G, int lg, int t, RowBlock& o) {
+  const int lane = threadIdx.x & 63, b = min(lane, a.B - 1);
+  const int c0 = min(max(a.cu[b], 0), (int)a.T), c1 = min(max(a.cu[b + 1], 0), (int)a.T);
+  const int keys = a.lengths[b], n = max(c1 - c0, 0);
+  const int blocks = lane < a.B ? (int)(((int64_t)n * G + (1 << lg) - 1) >> lg) : 0;
+  int at = 0;
+  for (int i = 0; i < a.B; ++i) {
+    const int other = __builtin_amdgcn_readlane(keys, i);
+    if (other > keys || (other == keys && i < lane)) at += __builtin_amdgcn_readlane(blocks, i);
+  }
+  const uint64_t mine = __ballot(t >= at && t - at < blocks);
+  if (mine == 0) return false;
+  const int l = __builtin_ctzll(mine);
+  o = RowBlock{l, __builtin_amdgcn_readlane(c0, l), __builtin_amdgcn_readlane(n, l),
+               (t - __builtin_amdgcn_readlane(at, l)) << lg};
+  return true;
+}
+
 // keys of a sequence: what its table can hold at most
 __device__ __forceinline__ int64_t keys_of(const AttnCacheArgs& a, int b) {
   return min((int64_t)max(a.lengths[b], 0), a.width << a.c.lg_page);
@@ -316,8 +336,10 @@ __global__ __launch_bounds__(64 * kWavesF, D == 64 ? 4 : 2) void attention_few_k
 // [64][D]; V^T's is [D][64] with each 16 keys in the order of P^T's operand (0-3, 8-11 for the lower half of the
 // wave, 4-7, 12-15 for the upper), so that both products read whole 16-byte pieces. Products,
 // exponentials and the lazy maximum are arranged as in attention.hip.
-// WHOLE: pages of 64 or 128 tokens, so that a tile lies in one page: its address and scale are scalar, and a page that the
-// table does not have is a buffer of no bytes, which reads zero.
+// A wave's piece of K is 8 or 16 keys, all in one page; its piece of V is 16 keys of 64 elements (pages of 16 or 32), or with
+// WHOLE (pages of 64 or 128: a tile lies in one page) 64 keys of 16 elements, whose rows are read 64 bytes at a time. So
+// a page's address and scale are scalar throughout, and a page that the table does not have is a buffer of no bytes,
+// which reads zero. Per lane instead: 97 us for 4099 packed queries on 16-token pages, 85 on 64-token ones.
 constexpr int kWavesT = 4, kLgRows = 7;
 static_assert(kWavesT * 32 == 1 << kLgRows, "32 rows a wave");
 constexpr int kAheadC = 2;   // operand reads in flight ahead of a product
@@ -350,7 +372,9 @@ __global__ __launch_bounds__(64 * kWavesT, 2) void attention_tile_kernel(AttnCac
   const int hk = id / (blocks * a.splits);
   const int split = id % (blocks * a.splits) / blocks;
   RowBlock rb;
-  if (!find_rows(a, G, kLgRows, id % blocks, rb)) return;
+  const int block = id % blocks;
+  if (a.cu != nullptr && a.B <= 64 ? !find_rows_longest_first(a, G, kLgRows, block, rb) : !find_rows(a, G, kLgRows, block, rb))
+    return;
   const int n_rows = rb.n * G;
   if (CAUSAL) {   // those with the most keys first
     const int last_block = (n_rows - 1) >> kLgRows;
@@ -382,14 +406,17 @@ __global__ __launch_bounds__(64 * kWavesT, 2) void attention_tile_kernel(AttnCac
     for (int t = 0; t < KD; ++t) fq[t] = *reinterpret_cast<const bf16x8*>(qp + 16 * t);
   }
 
-  // Pieces of 16 codes: of K, key kr and elements 16 ks .. (piece c: 256 / kCP keys further on); of V, element vd
-  // and keys 16 vk .. (64 elements further on). The LDS swizzles repeat with those steps.
+  // Pieces of 16 codes: of K, key kr and elements 16 ks .. (piece c: kStepK keys further on); of V, element vd and keys
+  // 16 vk .. (kStepV elements further on). The LDS swizzles repeat with those steps.
   auto swz_k = [](int r) { return D == 128 ? (r & 15) : ((r >> 1) & 7); };
   auto swz_v = [](int r) { return (r ^ (r >> 3)) & 7; };
   constexpr int kStepK = 64 * kWavesT / kCP, kStepV = 16 * kWavesT;
   static_assert(kStepK % 16 == 0 && kStepV % 64 == 0, "swizzles");
-  const int kr = tid / kCP, ks = tid % kCP, vd = tid >> 2, vk = tid & 3;
-  const int k_src = kr * D + 16 * ks;                 // within a tile's page
+  constexpr int kRowsK = 64 / kCP;                    // keys of a wave's piece
+  const int kr = tid / kCP, ks = tid % kCP;
+  const int vd = WHOLE ? tid >> 2 : lane, vk = WHOLE ? tid & 3 : wave;
+  const int k_src = (lane / kCP) * D + 16 * ks;       // from the wave's first key
+  const int v_src = vd * P + (WHOLE ? 16 * vk : 0);   // from the tile's (WHOLE) or the wave's first key
   const int k_dst = kr * kRowBytes + (((2 * ks) ^ swz_k(kr)) * 16), v_dst = vd * 128 + (((2 * vk) ^ swz_v(vd)) * 16);
   const int32_t* table = a.table + (int64_t)rb.b * a.width;
   const uint32_t page_bytes = (uint32_t)(P * D);
@@ -398,7 +425,7 @@ __global__ __launch_bounds__(64 * kWavesT, 2) void attention_tile_kernel(AttnCac
     return at < a.width && key < L ? table[at] : -1;
   };
   auto page_of = [&](int entry) {   // -1: none
-    if (WHOLE) entry = __builtin_amdgcn_readfirstlane(entry);
+    entry = __builtin_amdgcn_readfirstlane(entry);
     return (uint32_t)entry < (uint32_t)a.c.pages ? entry : -1;
   };
   u32x4 wk[kPieces], wv[kPieces];        // codes on their way
@@ -407,65 +434,43 @@ __global__ __launch_bounds__(64 * kWavesT, 2) void attention_tile_kernel(AttnCac
   constexpr int kOwn = WHOLE ? 1 : kPieces;
   int ek[kOwn], ev, gone_k = 0, gone_v = 0;
   uint32_t sk[kOwn], sv;
+  auto first_k = [&](int kt, int c) { return (kt0 + kt) * kTile + kRowsK * wave + kStepK * c; };
+  auto first_v = [&](int kt) { return (kt0 + kt) * kTile + (WHOLE ? 0 : 16 * wave); };
   auto k_pages = [&](int kt) {
 #pragma unroll
-    for (int c = 0; c < kOwn; ++c) ek[c] = entry_of((kt0 + kt) * kTile + (WHOLE ? 0 : kr + kStepK * c));
+    for (int c = 0; c < kOwn; ++c) ek[c] = entry_of(WHOLE ? (kt0 + kt) * kTile : first_k(kt, c));
   };
-  auto v_pages = [&](int kt) { ev = entry_of((kt0 + kt) * kTile + (WHOLE ? 0 : 16 * vk)); };
+  auto v_pages = [&](int kt) { ev = entry_of(first_v(kt)); };
   auto request_k = [&](int kt, u32x4 (&wk)[kPieces], uint32_t (&sk)[kOwn], int& gone_k) {
-    int pk[kOwn];
     gone_k = 0;
 #pragma unroll
-    for (int c = 0; c < kOwn; ++c) {
-      pk[c] = page_of(ek[c]);
-      gone_k |= (pk[c] < 0 ? 1 : 0) << c;
-    }
-    if constexpr (WHOLE) {
-      const int64_t at = (int64_t)max(pk[0], 0) * a.c.Hk + hk;
-      const __amdgpu_buffer_rsrc_t r = make_rsrc(a.c.k + at * page_bytes, pk[0] < 0 ? 0u : page_bytes);
-      const int soff = (((kt0 + kt) * kTile) & (P - 1)) * D;
+    for (int o = 0; o < kOwn; ++o) {
+      const int page = page_of(ek[o]);
+      const int64_t at = (int64_t)max(page, 0) * a.c.Hk + hk;
+      const __amdgpu_buffer_rsrc_t r = make_rsrc(a.c.k + at * page_bytes, page < 0 ? 0u : page_bytes);
 #pragma unroll
-      for (int c = 0; c < kPieces; ++c) wk[c] = load_codes(r, k_src, soff + kStepK * D * c);
-      sk[0] = a.c.ks[at];
-    } else {
-#pragma unroll
-      for (int c = 0; c < kPieces; ++c) {
-        const int key = (kt0 + kt) * kTile + kr + kStepK * c;
-        const uint32_t p = (uint32_t)max(pk[c], 0);
-        wk[c] = *reinterpret_cast<const u32x4*>(a.c.k + (uint64_t)p * (a.c.Hk * page_bytes) + hk * page_bytes +
-                                                (uint32_t)((key & (P - 1)) * D + 16 * ks));
-        sk[c] = a.c.ks[(int64_t)p * a.c.Hk + hk];
-      }
+      for (int c = WHOLE ? 0 : o; c < (WHOLE ? kPieces : o + 1); ++c)
+        wk[c] = load_codes(r, k_src, (first_k(kt, c) & (P - 1)) * D);
+      sk[o] = a.c.ks[at];
+      gone_k |= (page < 0 ? 1 : 0) << o;
     }
   };
   auto request_v = [&](int kt) {
-    const int pv = page_of(ev);
-    gone_v = pv < 0;
-    if constexpr (WHOLE) {
-      const int64_t at = (int64_t)max(pv, 0) * a.c.Hk + hk;
-      const __amdgpu_buffer_rsrc_t r = make_rsrc(a.c.v + at * page_bytes, pv < 0 ? 0u : page_bytes);
-      const int soff = ((kt0 + kt) * kTile) & (P - 1);
+    const int page = page_of(ev);
+    const int64_t at = (int64_t)max(page, 0) * a.c.Hk + hk;
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(a.c.v + at * page_bytes, page < 0 ? 0u : page_bytes);
 #pragma unroll
-      for (int c = 0; c < kPieces; ++c) wv[c] = load_codes(r, vd * P + 16 * vk, soff + kStepV * P * c);
-      sv = a.c.vs[at];
-    } else {
-      const int key = (kt0 + kt) * kTile + 16 * vk;
-      const uint32_t p = (uint32_t)max(pv, 0);   // the same keys in each piece
-#pragma unroll
-      for (int c = 0; c < kPieces; ++c)
-        wv[c] = *reinterpret_cast<const u32x4*>(a.c.v + (uint64_t)p * (a.c.Hk * page_bytes) + hk * page_bytes +
-                                                (uint32_t)((vd + kStepV * c) * P + (key & (P - 1))));
-      sv = a.c.vs[(int64_t)p * a.c.Hk + hk];
-    }
+    for (int c = 0; c < kPieces; ++c) wv[c] = load_codes(r, v_src, (first_v(kt) & (P - 1)) + kStepV * P * c);
+    sv = a.c.vs[at];
+    gone_v = page < 0;
   };
   auto store_k = [&](int kt, const u32x4 (&wk)[kPieces], const uint32_t (&sk)[kOwn], int gone_k) {
     uint8_t* st = smem + (kt & 1) * (2 * kTileBytes);
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) {
-      const uint32_t s = WHOLE ? (uint32_t)__builtin_amdgcn_readfirstlane((int)sk[0]) : sk[c];
-      const bool gone = (gone_k >> (WHOLE ? 0 : c)) & 1;
-      const float sc = gone ? 1.0f : cache_scale(s);
-      const u32x4 w = !WHOLE && gone ? zero4() : wk[c];
+      const int o = WHOLE ? 0 : c;
+      const float sc = (gone_k >> o) & 1 ? 1.0f : cache_scale((uint32_t)__builtin_amdgcn_readfirstlane((int)sk[o]));
+      const u32x4 w = wk[c];
       *reinterpret_cast<bf16x8*>(st + k_dst + kStepK * kRowBytes * c) = bf16_operand(w[0], w[1], sc);
       *reinterpret_cast<bf16x8*>(st + (k_dst ^ 16) + kStepK * kRowBytes * c) = bf16_operand(w[2], w[3], sc);
     }
@@ -482,11 +487,10 @@ __global__ __launch_bounds__(64 * kWavesT, 2) void attention_tile_kernel(AttnCac
         for (int c = 0; c < kPieces; ++c) wv[c][e] &= keep;
       }
     }
-    const uint32_t s = WHOLE ? (uint32_t)__builtin_amdgcn_readfirstlane((int)sv) : sv;
-    const float sc = gone_v ? 1.0f : cache_scale(s);
+    const float sc = gone_v ? 1.0f : cache_scale((uint32_t)__builtin_amdgcn_readfirstlane((int)sv));
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) {
-      const u32x4 w = !WHOLE && gone_v ? zero4() : wv[c];
+      const u32x4 w = wv[c];
       *reinterpret_cast<bf16x8*>(st + v_dst + kStepV * 128 * c) = bf16_operand(w[0], w[2], sc);
       *reinterpret_cast<bf16x8*>(st + (v_dst ^ 16) + kStepV * 128 * c) = bf16_operand(w[1], w[3], sc);
     }

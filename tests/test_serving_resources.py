@@ -1,6 +1,6 @@
 """Build check: the kernels of 8-bit floating-point serving compile for gfx950 without scratch memory or spills of vector
 registers. Scalar registers that do not fit are held in lanes of vector registers, without a memory access: the cached
-attention's tiles, whose loop keeps the tensors' addresses, the table's and the masks' bounds there, hold up to 44 so,
+attention's tiles, whose loop keeps the tensors' addresses, the table's and the masks' bounds there, hold up to 56 so,
 and nothing else any."""
 
 import os
@@ -14,7 +14,7 @@ from tests.test_kernel_resources import HIPCC
 
 
 @pytest.mark.skipif(not os.path.exists(HIPCC), reason="hipcc not available")
-@pytest.mark.parametrize("src,scalars", [("fp8.hip", 0), ("cache.hip", 0), ("attention_cache.hip", 44), ("rope.hip", 0)])
+@pytest.mark.parametrize("src,scalars", [("fp8.hip", 0), ("cache.hip", 0), ("attention_cache.hip", 56), ("rope.hip", 0)])
 def test_no_scratch_no_spills(src, scalars, tmp_path):
     cmd = [HIPCC, *build.COMMON_FLAGS, "-I", build.INCLUDE, "-I", build.CSRC, "--cuda-device-only", "-c",
            os.path.join(build.CSRC, src), "-o", str(tmp_path / "k.o"), "-Rpass-analysis=kernel-resource-usage"]
