@@ -848,7 +848,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnCacheArgs a) {
 // all that come by, and `tail` for the last ones' end. Of several sequences the longest counts 1.34 of a step's share while all
 // are there, and they average 0.8 of it else. `base` starts and ends the call, a split adds a launch and its partial results.
 // Fitted to both kernels at 330 sizes (1 to 64 sequences of 1 to 4096 queries on 150 to 30000 keys, groups of 1, 4 and
-// 8, keys split up to 64 ways: profiles/attention_cache_grid.txt): within 2% of the best on average and 35% at
+// 8, keys split up to 64 ways: profiles/attention_cache_grid.txt): within 3% of the best on average and 40% at
 // worst. One token on 65537 keys, 32 heads on 8: 29 us split 32 ways, 51 16 ways, 32 128 ways. 40 tokens on 540 keys: 9.7 us by
 // few rows, 19 by tiles; 512 on 8704: 192 and 105.
 struct AttnPlan {
