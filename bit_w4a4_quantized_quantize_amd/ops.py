@@ -1206,7 +1206,8 @@ def cache_append_fp8(k, v, cache: Fp8Cache, block_table, lengths, cu_seqlens=Non
     cache: sequence b's tokens, cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (None: one token each), become its tokens
     lengths[b], lengths[b] + 1, ... (int32 [B]: what each held before). A page's scale is set by the call that
     writes its first slot and grows when later tokens need it, with what is there rescaled. Tokens
-    whose page the table does not have are left out. A page that is written must belong to one sequence."""
+    whose page the table does not have are left out. A page that is written must be listed once only among those that
+    the tokens go to."""
     ka = _need_heads(k, "k")
     args, (_, Hk, _, D) = _check_cache(cache, block_table, lengths, "lengths", cu_seqlens)
     T = k.shape[0]

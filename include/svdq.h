@@ -576,7 +576,8 @@ int svdq_attention_packed(const void* q, int64_t q_stride_t, int64_t q_stride_h,
  *   The matrix instruction adds products in groups of 8 neighbouring channels, aligned to the largest exponent
  *   in the group, and drops what lies below 2^-13 of it: a product loses less than 2^-13 of its group's largest,
  *   nothing where the group's products stay within 2^7 of each other. For activations and weights of normal
- *   distribution that is about 1e-4 of y's norm, against 1.7e-3 of its rounding to bf16.
+ *   distribution that is about 2e-5 of y's norm (5e-5 where one channel in a hundred is 20 times larger), against
+ *   1.7e-3 of its rounding to bf16.
  *
  *   x [M, K] bf16, smooth [K] bf16 or NULL, codes [M, K] e4m3fn, ascales [ceil(K/128), M]
  *   fp32, weight [N, K] e4m3fn, wscales [ceil(N/128), ceil(K/128)] fp32, bias [N] bf16 or NULL,
@@ -654,7 +655,8 @@ int svdq_rope_scaled(const void* q, int64_t q_stride_t, int64_t q_stride_h, int6
  *   need more, and rescales what is there (exactly, but for codes that become subnormal). Codes are rounded
  *   to nearest even. A page that gets an infinity or NaN has scale 255 until its slot 0 is written again. Slots
  *   that no token of the call goes to, other than those rescaled, are left as they were. Tokens whose page the
- *   table does not have are left out. A page that is written must not be in use by another sequence of the call.
+ *   table does not have are left out. A page that is written must be listed once only among the pages that the call's
+ *   tokens go to (else its contents are undefined; nothing else is written).
  * svdq_cache_read_fp8: k_out, v_out [T, Hk, D] bf16, the values of tokens starts[b], starts[b] + 1, ... (exact for
  *   scales from 27, which is 2^-100, to 246); zeros where the table has no page. Rows outside the offsets are
  *   left as they were.
