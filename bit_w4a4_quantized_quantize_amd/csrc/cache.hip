@@ -13,7 +13,9 @@ namespace svdq {
 
 namespace {
 
-constexpr int kThreadsC = 256;
+// Threads of a page's workgroup: four tokens of 8 elements each, up to 256 (a page of 128 tokens of 128: two fours each)
+template <int D, int P>
+constexpr int kThreadsC = P * D / 32 < 64 ? 64 : P * D / 32 > 256 ? 256 : P * D / 32;
 
 // The pages that a sequence of n tokens touches from any start are at most floor((n - 2) / P) + 2, so blocks
 // of P packed tokens are numbered with two more per sequence: sequence b starts at floor(cu[b] / P) + 2 b.
@@ -46,21 +48,22 @@ __device__ __forceinline__ bool touched_block(const CacheTokens& a, int lg, int6
 }
 
 // The page of a block and the tokens in it: packed tokens tok0 .. tok0 + (s1 - s0) - 1 go to slots s0 .. s1 - 1.
-// page is -1 where the table has none.
+// `entry` is the table's, to be looked at where it is needed: the tokens are requested meanwhile.
 struct Block {
-  int64_t page;
-  int tok0, s0, s1;
+  int entry, tok0, s0, s1;
 };
-__device__ __forceinline__ bool find_block(const CacheTokens& a, const CacheShape& c, Block& o) {
+template <int P>
+__device__ __forceinline__ bool find_block(const CacheTokens& a, Block& o) {
+  constexpr int kLg = __builtin_ctz(P);
   Touched t;
-  if (!touched_block(a, c.lg_page, (int64_t)blockIdx.x, t) || t.count <= 0) return false;
+  if (!touched_block(a, kLg, (int64_t)blockIdx.x, t) || t.count <= 0) return false;
   const int64_t start = max(a.starts[t.b], 0), end = start + t.count;
-  const int64_t block = (start >> c.lg_page) + t.local;
-  const int64_t p0 = block << c.lg_page;
+  const int64_t block = (start >> kLg) + t.local;
+  const int64_t p0 = block << kLg;
   if (p0 >= end) return false;
-  const int64_t from = max(start, p0), to = min(end, p0 + (1 << c.lg_page));
-  const int page = block < a.width ? a.table[(int64_t)t.b * a.width + block] : -1;
-  o = Block{(uint32_t)page < (uint32_t)c.pages ? page : -1, t.first + (int)(from - start), (int)(from - p0), (int)(to - p0)};
+  const int64_t from = max(start, p0), to = min(end, p0 + P);
+  o = Block{block < a.width ? a.table[(int64_t)t.b * a.width + block] : -1, t.first + (int)(from - start),
+            (int)(from - p0), (int)(to - p0)};
   return true;
 }
 
@@ -88,16 +91,14 @@ __device__ __forceinline__ void store_bytes(uint8_t* dst, u32x4 w, int lo, int h
 
 // An image of a page of values in LDS: row d of P slots, its 16-byte pieces permuted by the rows' eights, so that
 // lanes that write (or read) the same slots of every eighth row meet different banks.
+template <int D, int P>
 struct Image {
+  static constexpr int kBytes = D * (P + 16);
   uint8_t* at;
-  int lg_page;
   __device__ __forceinline__ uint8_t* slot(int d, int s) const {
-    const int pieces = (1 << (lg_page - 4)) - 1;
-    return at + d * ((1 << lg_page) + 16) + ((((s >> 4) ^ ((d >> 3) & pieces)) << 4) | (s & 15));
+    return at + d * (P + 16) + ((((s >> 4) ^ ((d >> 3) & (P / 16 - 1))) << 4) | (s & 15));
   }
 };
-template <int D>
-constexpr int kImageBytes = D * (kMaxPage + 16);
 
 // bytes i of four dwords -> dword i (the transpose of 4 x 4 bytes)
 __device__ __forceinline__ u32x4 transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -107,17 +108,20 @@ __device__ __forceinline__ u32x4 transpose4(uint32_t a, uint32_t b, uint32_t c, 
                __builtin_amdgcn_perm(cd1, ab1, 0x05040100u), __builtin_amdgcn_perm(cd1, ab1, 0x07060302u)};
 }
 
-// Packed prompts of 16411 tokens, 8 heads of 128 (101 MB): 22 us; 32 single tokens 5.5, the chain of loads that finds the page.
-template <int D>
-__global__ __launch_bounds__(kThreadsC) void append_kernel(CacheTokens a, CacheShape c, HeadView k, HeadView v) {
+// Memory bound: packed prompts of 16411 tokens, 8 heads of 128 on pages of 64 (101 MB, from memory) 24.8 us. 32 single
+// tokens take 5.2, the chain of loads that finds the page. Kernels made for their page's size have as many threads as it
+// has work (written and read back: pages of 16 tokens 80 -> 46 us, of 32 54 -> 46).
+template <int D, int P>
+__global__ __launch_bounds__((kThreadsC<D, P>)) void append_kernel(CacheTokens a, CacheShape c, HeadView k, HeadView v) {
+  constexpr int kThreads = kThreadsC<D, P>;
   constexpr int kLanes = D / 8;                       // lanes of a token, 8 elements each
-  constexpr int kRows = kThreadsC / kLanes;           // fours of tokens of a pass
-  constexpr int kPasses = kMaxPage / (4 * kRows);
-  __shared__ __attribute__((aligned(16))) uint8_t smem[kImageBytes<D>];
-  __shared__ float part[kThreadsC / 64];
+  constexpr int kRows = kThreads / kLanes;            // fours of tokens of a pass
+  constexpr int kPasses = (P + 4 * kRows - 1) / (4 * kRows);
+  __shared__ __attribute__((aligned(16))) uint8_t smem[Image<D, P>::kBytes];
+  __shared__ float part[kThreads / 64];
   Block blk;
-  if (!find_block(a, c, blk) || blk.page < 0) return;
-  const int tid = threadIdx.x, P = 1 << c.lg_page;
+  if (!find_block<P>(a, blk)) return;
+  const int tid = threadIdx.x;
   const int head = (int)blockIdx.y;
   const bool is_v = blockIdx.z != 0;
   const HeadView in = is_v ? v : k;
@@ -133,7 +137,9 @@ __global__ __launch_bounds__(kThreadsC) void append_kernel(CacheTokens a, CacheS
       const int r = row + 4 * kRows * u + i;
       w[u][i] = r < n ? *reinterpret_cast<const u32x4*>(in.p + (int64_t)(blk.tok0 + r) * in.st + head * in.sh + e0) : zero4();
     }
-  uint8_t* scale_at = (is_v ? c.vs : c.ks) + blk.page * c.Hk + head;
+  const int64_t at_page = (int64_t)blk.entry * c.Hk + head;
+  if ((uint32_t)blk.entry >= (uint32_t)c.pages) return;   // the table has no page: left out
+  uint8_t* scale_at = (is_v ? c.vs : c.ks) + at_page;
   const int old = blk.s0 > 0 ? *scale_at : 0;         // below every scale that is written
 #pragma unroll
   for (int u = 0; u < kPasses; ++u)
@@ -146,7 +152,7 @@ __global__ __launch_bounds__(kThreadsC) void append_kernel(CacheTokens a, CacheS
   if ((tid & 63) == 0) part[tid >> 6] = amax;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kThreadsC / 64; ++i) amax = max_or_nan(amax, part[i]);
+  for (int i = 0; i < kThreads / 64; ++i) amax = max_or_nan(amax, part[i]);
   const bool fine = amax <= 3.4028234663852886e38f;
   const int now = fine ? max(fp8_exponent(amax) + 127, old) : 255;
   if (tid == 0 && now != old) *scale_at = (uint8_t)now;
@@ -165,10 +171,10 @@ __global__ __launch_bounds__(kThreadsC) void append_kernel(CacheTokens a, CacheS
     return fp8_codes8(f, inv);
   };
 
-  uint8_t* page = (is_v ? c.v : c.k) + (blk.page * c.Hk + head) * ((int64_t)P * D);
+  uint8_t* page = (is_v ? c.v : c.k) + at_page * (P * D);
   if (!is_v) {
     if (grown) {
-      for (int i = tid; i < blk.s0 * (D / 16); i += kThreadsC) {
+      for (int i = tid; i < blk.s0 * (D / 16); i += kThreads) {
         u32x4* at = reinterpret_cast<u32x4*>(page) + i;
         *at = rescale16(*at, by);
       }
@@ -183,10 +189,10 @@ __global__ __launch_bounds__(kThreadsC) void append_kernel(CacheTokens a, CacheS
     return;
   }
   // values: the page's image [D][P] is put together in LDS and leaves by rows
-  const Image image{smem, c.lg_page};
+  const Image<D, P> image{smem};
   if (grown) {
-    for (int i = tid; i < D * (P / 16); i += kThreadsC) {
-      const int d = i >> (c.lg_page - 4), s = 16 * (i & (P / 16 - 1));
+    for (int i = tid; i < D * (P / 16); i += kThreads) {
+      const int d = i / (P / 16), s = 16 * (i % (P / 16));
       if (s < blk.s0)
         *reinterpret_cast<u32x4*>(image.slot(d, s)) = rescale16(*reinterpret_cast<const u32x4*>(page + d * P + s), by);
     }
@@ -217,8 +223,8 @@ __global__ __launch_bounds__(kThreadsC) void append_kernel(CacheTokens a, CacheS
   }
   __syncthreads();
   const int from = grown ? 0 : blk.s0;
-  for (int i = tid; i < D * (P / 16); i += kThreadsC) {
-    const int d = i >> (c.lg_page - 4), s = 16 * (i & (P / 16 - 1));
+  for (int i = tid; i < D * (P / 16); i += kThreads) {
+    const int d = i / (P / 16), s = 16 * (i % (P / 16));
     if (s + 16 > from && s < blk.s1)
       store_bytes(page + d * P + s, *reinterpret_cast<const u32x4*>(image.slot(d, s)), from - s, blk.s1 - s);
   }
@@ -234,25 +240,28 @@ __device__ __forceinline__ void widen16(u32x4 w, float scale, u32x4 (&o)[2]) {
 }
 
 // Packed tokens' keys and values back in bf16; zeros where the table has no page.
-template <int D>
-__global__ __launch_bounds__(kThreadsC) void read_kernel(CacheTokens a, CacheShape c, uint16_t* k_out, uint16_t* v_out) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[kImageBytes<D>];
+// Memory bound: the same prompts 19.6 us (5.1 TB/s).
+template <int D, int P>
+__global__ __launch_bounds__((kThreadsC<D, P>)) void read_kernel(CacheTokens a, CacheShape c, uint16_t* k_out,
+                                                                 uint16_t* v_out) {
+  constexpr int kThreads = kThreadsC<D, P>;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[Image<D, P>::kBytes];
   Block blk;
-  if (!find_block(a, c, blk)) return;
-  const int tid = threadIdx.x, P = 1 << c.lg_page;
+  if (!find_block<P>(a, blk)) return;
+  const int tid = threadIdx.x;
   const int head = (int)blockIdx.y;
   const bool is_v = blockIdx.z != 0;
   const int n = blk.s1 - blk.s0;
-  const int64_t page_at = max(blk.page, (int64_t)0);
-  const uint8_t* page = (is_v ? c.v : c.k) + (page_at * c.Hk + head) * ((int64_t)P * D);
-  const uint32_t scale_byte = (is_v ? c.vs : c.ks)[page_at * c.Hk + head];
-  const bool none = blk.page < 0;
+  const bool none = (uint32_t)blk.entry >= (uint32_t)c.pages;
+  const int64_t at_page = (none ? 0 : (int64_t)blk.entry) * c.Hk + head;
+  const uint8_t* page = (is_v ? c.v : c.k) + at_page * (P * D);
+  const uint32_t scale_byte = (is_v ? c.vs : c.ks)[at_page];
   const int64_t out_st = (int64_t)c.Hk * D;
   uint16_t* out = (is_v ? v_out : k_out) + blk.tok0 * out_st + head * D;
   if (is_v) {
-    const Image image{smem, c.lg_page};
-    for (int i = tid; i < D * (P / 16); i += kThreadsC) {
-      const int d = i >> (c.lg_page - 4), s = 16 * (i & (P / 16 - 1));
+    const Image<D, P> image{smem};
+    for (int i = tid; i < D * (P / 16); i += kThreads) {
+      const int d = i / (P / 16), s = 16 * (i % (P / 16));
       if (s + 16 > blk.s0 && s < blk.s1)
         *reinterpret_cast<u32x4*>(image.slot(d, s)) = *reinterpret_cast<const u32x4*>(page + d * P + s);
     }
@@ -260,7 +269,7 @@ __global__ __launch_bounds__(kThreadsC) void read_kernel(CacheTokens a, CacheSha
     const float scale = cache_scale(scale_byte);
     // 8 elements of four slots an item
     const int first = blk.s0 / 4, fours = (blk.s1 + 3) / 4 - first;
-    for (int i = tid; i < fours * (D / 8); i += kThreadsC) {
+    for (int i = tid; i < fours * (D / 8); i += kThreads) {
       const int s = 4 * (first + i / (D / 8)), e = 8 * (i % (D / 8));
       u32x4 z[2];
 #pragma unroll
@@ -280,7 +289,7 @@ __global__ __launch_bounds__(kThreadsC) void read_kernel(CacheTokens a, CacheSha
     }
   } else {
     const float scale = cache_scale(scale_byte);
-    for (int i = tid; i < n * (D / 16); i += kThreadsC) {
+    for (int i = tid; i < n * (D / 16); i += kThreads) {
       const int r = i / (D / 16), e = 16 * (i % (D / 16));
       u32x4 o[2];
       widen16(*reinterpret_cast<const u32x4*>(page + (blk.s0 + r) * D + e), scale, o);
@@ -295,21 +304,31 @@ unsigned touched_blocks(const CacheTokens& a, int lg) {
   return (unsigned)(a.cu == nullptr ? a.B : (a.T >> lg) + 2 * (int64_t)a.B);
 }
 
+// (kernel of D and the page's tokens, grid of pages touched x heads x keys and values)
+#define SVDQ_CACHE_LAUNCH(kernel, d, p, ...)                                                                       \
+  hipLaunchKernelGGL((kernel<d, p>), dim3(touched_blocks(a, c.lg_page), (unsigned)c.Hk, 2), dim3(kThreadsC<d, p>), 0, \
+                     stream, a, c, __VA_ARGS__)
+#define SVDQ_CACHE_PAGES(kernel, d, ...)                                     \
+  do {                                                                       \
+    if (c.lg_page == 4) SVDQ_CACHE_LAUNCH(kernel, d, 16, __VA_ARGS__);       \
+    else if (c.lg_page == 5) SVDQ_CACHE_LAUNCH(kernel, d, 32, __VA_ARGS__);  \
+    else if (c.lg_page == 6) SVDQ_CACHE_LAUNCH(kernel, d, 64, __VA_ARGS__);  \
+    else SVDQ_CACHE_LAUNCH(kernel, d, 128, __VA_ARGS__);                     \
+  } while (0)
+
 }  // namespace
 
 hipError_t launch_cache_append(const CacheTokens& a, const CacheShape& c, const HeadView& k, const HeadView& v,
                                hipStream_t stream) {
-  const dim3 grid(touched_blocks(a, c.lg_page), (unsigned)c.Hk, 2), block(kThreadsC);
-  if (c.D == 64) hipLaunchKernelGGL(append_kernel<64>, grid, block, 0, stream, a, c, k, v);
-  else hipLaunchKernelGGL(append_kernel<128>, grid, block, 0, stream, a, c, k, v);
+  if (c.D == 64) SVDQ_CACHE_PAGES(append_kernel, 64, k, v);
+  else SVDQ_CACHE_PAGES(append_kernel, 128, k, v);
   return hipGetLastError();
 }
 
 hipError_t launch_cache_read(const CacheTokens& a, const CacheShape& c, uint16_t* k_out, uint16_t* v_out,
                              hipStream_t stream) {
-  const dim3 grid(touched_blocks(a, c.lg_page), (unsigned)c.Hk, 2), block(kThreadsC);
-  if (c.D == 64) hipLaunchKernelGGL(read_kernel<64>, grid, block, 0, stream, a, c, k_out, v_out);
-  else hipLaunchKernelGGL(read_kernel<128>, grid, block, 0, stream, a, c, k_out, v_out);
+  if (c.D == 64) SVDQ_CACHE_PAGES(read_kernel, 64, k_out, v_out);
+  else SVDQ_CACHE_PAGES(read_kernel, 128, k_out, v_out);
   return hipGetLastError();
 }
 

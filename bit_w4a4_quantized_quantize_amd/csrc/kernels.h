@@ -277,7 +277,6 @@ hipError_t launch_attention(const AttnArgs& a, int D, hipStream_t stream);
 
 // A cache of keys [pages, Hk, P, D] and values [pages, Hk, D, P] in e4m3 with an exponent byte per page and head
 // (cache.hip), P = 1 << lg_page tokens.
-constexpr int kMaxPage = 128;
 struct CacheShape {
   uint8_t *k, *v, *ks, *vs;
   int64_t pages;
