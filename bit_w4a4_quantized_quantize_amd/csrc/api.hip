@@ -1870,13 +1870,16 @@ int svdq_rope_scaled(const void* q, int64_t q_stride_t, int64_t q_stride_h, int6
     if ((st = make_heads(&out[i], out_name[i], op[i], os[i][0], os[i][1], T, n[i], D))) return st;
     if (!heads_distinct(out[i])) return fail(SVDQ_ERR_SHAPE, "%s: heads overlap under its strides", out_name[i]);
   }
-  bool all_in_place = true;
+  bool all_in_place = true, any_in_place = false;
   for (int o = 0; o < 2; ++o) {
     if (n[o] == 0) continue;
     for (int i = 0; i < 2; ++i) {
       if (n[i] == 0) continue;
       const bool in_place = i == o && in[i].p == out[o].p && in[i].st == out[o].st && in[i].sh == out[o].sh;
-      if (i == o && !in_place) all_in_place = false;
+      if (i == o) {
+        all_in_place = all_in_place && in_place;
+        any_in_place = any_in_place || in_place;
+      }
       if (!in_place && !heads_disjoint(in[i], out[o]))
         return fail(SVDQ_ERR_ALIAS, "output %s overlaps input %s", out[o].name, in[i].name);
     }
@@ -1913,7 +1916,7 @@ int svdq_rope_scaled(const void* q, int64_t q_stride_t, int64_t q_stride_h, int6
     a.turns[i] = (double)(f * (kept + (1.0L - kept) / (long double)factor));
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t e = svdq::launch_rope_scaled(a, interleaved != 0, s);
+  hipError_t e = svdq::launch_rope_scaled(a, interleaved != 0, any_in_place, s);
   if (int st_ = launched(e, "rotary positions", s)) return st_;
   return ok();
 }

@@ -261,7 +261,7 @@ struct RopeScaledArgs {
   float amplitude;
   double turns[128];         // per pair: its frequency in turns
 };
-hipError_t launch_rope_scaled(const RopeScaledArgs& a, bool interleaved, hipStream_t stream);
+hipError_t launch_rope_scaled(const RopeScaledArgs& a, bool interleaved, bool in_place, hipStream_t stream);
 
 // Attention over packed sequences.
 struct AttnArgs {

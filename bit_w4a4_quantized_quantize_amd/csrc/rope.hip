@@ -193,13 +193,19 @@ void launch_rope_cfg(const RopeArgs& a, hipStream_t s) {
 
 // Rotary positions on the first R elements of any head size, one position per token. A workgroup takes `per` whole
 // tokens (one token in several passes, where that has more than 512 pieces): loads first, then the tokens' angles
-// in LDS, once for all heads. A piece is 8 elements: of the turned part, 8 consecutive ones
-// (interleaved) or 4 of each half; then, out of place, the rest 8 at a time. Memory bound: 16896 tokens, 30 + 30 heads of
-// 128 (519 MB) 93 us; 4099 tokens, 24 + 8 heads of 64 (34 MB) 13, one round of workgroups that read, then write.
+// in LDS, once for all heads. A piece is 8 elements of a head; out of place, those past R are copied. Of the turned part
+//   INTER: 8 consecutive ones, four pairs;
+//   WIDE: 8 of one half, with 8 of the other read beside them (so not in place; 16 divides R): whole lines are written
+//     where a head is turned in part;
+//   else: 4 of each half; PART: a head is turned in part.
+// Memory bound: 16896 tokens, 30 + 30 heads of 128 (519 MB) 93 us. Stores past the cache pay where a wave writes whole
+// lines (R = 64 of 64 elements, 4099 tokens, 24 + 8 heads: 7.8 and 8.5 us without; the long one 93 and 101), and cost where
+// it does not (R = 16, 4 of each half: 12.9 and 11.2 without; WIDE, with them, 8.0).
 // by_heads, by_pieces: 2^32 / heads and / pieces of a head, rounded up (exact quotients below 2^16).
-template <bool INTER>
+template <bool INTER, bool WIDE, bool PART>
 __global__ __launch_bounds__(kThreadsR) void rope_scaled_kernel(RopeScaledArgs a, int per, uint32_t by_heads,
                                                                 uint32_t by_pieces) {
+  static_assert(!INTER || !WIDE, "neighbours are in one piece");
   extern __shared__ __attribute__((aligned(16))) float turn[];   // per token and pair: cos and sin
   const int tid = threadIdx.x;
   const int64_t t0 = (int64_t)blockIdx.x * per;
@@ -209,7 +215,7 @@ __global__ __launch_bounds__(kThreadsR) void rope_scaled_kernel(RopeScaledArgs a
   const int token_items = heads * pieces, items = here * token_items;
 
   for (int first = 0; first < items; first += kItems * kThreadsR) {
-    u32x2 lo[kItems], hi[kItems];
+    u32x4 w[kItems], other[kItems];   // 8 elements (4 + 4: w only), WIDE: those of the other half
     int tok[kItems], piece[kItems];
     uint16_t* dst[kItems];
 #pragma unroll
@@ -226,13 +232,14 @@ __global__ __launch_bounds__(kThreadsR) void rope_scaled_kernel(RopeScaledArgs a
       const uint16_t* src = in.p + t * in.st + head * in.sh;
       dst[u] = (is_k ? a.out[1] : a.out[0]) + t * (is_k ? a.out_st[1] : a.out_st[0]) +
                head * (is_k ? a.out_sh[1] : a.out_sh[0]);
-      if (INTER || piece[u] >= turned) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(src + 8 * piece[u]);
-        lo[u] = u32x2{w[0], w[1]};
-        hi[u] = u32x2{w[2], w[3]};
+      if (INTER || WIDE || piece[u] >= turned) {
+        w[u] = *reinterpret_cast<const u32x4*>(src + 8 * piece[u]);
+        if (WIDE && piece[u] < turned)
+          other[u] = *reinterpret_cast<const u32x4*>(src + 8 * piece[u] + (8 * piece[u] < half ? half : -half));
       } else {
-        lo[u] = *reinterpret_cast<const u32x2*>(src + 4 * piece[u]);
-        hi[u] = *reinterpret_cast<const u32x2*>(src + half + 4 * piece[u]);
+        const u32x2 lo = *reinterpret_cast<const u32x2*>(src + 4 * piece[u]);
+        const u32x2 hi = *reinterpret_cast<const u32x2*>(src + half + 4 * piece[u]);
+        w[u] = u32x4{lo[0], lo[1], hi[0], hi[1]};
       }
     }
     if (first == 0) {
@@ -249,35 +256,49 @@ __global__ __launch_bounds__(kThreadsR) void rope_scaled_kernel(RopeScaledArgs a
     for (int u = 0; u < kItems; ++u) {
       const bool stored = first + u * kThreadsR + tid < items;
       if (piece[u] >= turned) {
-        if (stored)
-          __builtin_nontemporal_store(u32x4{lo[u][0], lo[u][1], hi[u][0], hi[u][1]},
-                                      reinterpret_cast<u32x4*>(dst[u] + 8 * piece[u]));
+        if (stored) __builtin_nontemporal_store(w[u], reinterpret_cast<u32x4*>(dst[u] + 8 * piece[u]));
         continue;
       }
       float v[8], o[8];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        v[2 * i] = bf16lo_to_f32(lo[u][i]);
-        v[2 * i + 1] = bf16hi_to_f32(lo[u][i]);
-        v[4 + 2 * i] = bf16lo_to_f32(hi[u][i]);
-        v[5 + 2 * i] = bf16hi_to_f32(hi[u][i]);
-      }
-      const float2* f = reinterpret_cast<const float2*>(turn) + tok[u] * half + 4 * piece[u];
-#pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int x = INTER ? 2 * i : i, y = INTER ? 2 * i + 1 : 4 + i;
-        const float2 cs = f[i];
-        o[x] = v[x] * cs.x - v[y] * cs.y;
-        o[y] = v[y] * cs.x + v[x] * cs.y;
+        v[2 * i] = bf16lo_to_f32(w[u][i]);
+        v[2 * i + 1] = bf16hi_to_f32(w[u][i]);
+      }
+      const bool lower = 8 * piece[u] < half;   // WIDE
+      const float2* f = reinterpret_cast<const float2*>(turn) + tok[u] * half +
+                        (WIDE ? 8 * piece[u] - (lower ? 0 : half) : 4 * piece[u]);
+      if (WIDE) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float z = i % 2 ? bf16hi_to_f32(other[u][i / 2]) : bf16lo_to_f32(other[u][i / 2]);
+          const float2 cs = f[i];
+          const float s = lower ? -cs.y : cs.y;
+          o[i] = v[i] * cs.x + z * s;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int x = INTER ? 2 * i : i, y = INTER ? 2 * i + 1 : 4 + i;
+          const float2 cs = f[i];
+          o[x] = v[x] * cs.x - v[y] * cs.y;
+          o[y] = v[y] * cs.x + v[x] * cs.y;
+        }
       }
       if (!stored) continue;
-      const u32x2 w0 = {pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
-      const u32x2 w1 = {pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])};
-      if (INTER) {
-        __builtin_nontemporal_store(u32x4{w0[0], w0[1], w1[0], w1[1]}, reinterpret_cast<u32x4*>(dst[u] + 8 * piece[u]));
+      const u32x4 r = {pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])};
+      if (INTER || WIDE) {
+        __builtin_nontemporal_store(r, reinterpret_cast<u32x4*>(dst[u] + 8 * piece[u]));
       } else {
-        __builtin_nontemporal_store(w0, reinterpret_cast<u32x2*>(dst[u] + 4 * piece[u]));
-        __builtin_nontemporal_store(w1, reinterpret_cast<u32x2*>(dst[u] + half + 4 * piece[u]));
+        u32x2* at = reinterpret_cast<u32x2*>(dst[u] + 4 * piece[u]);
+        u32x2* high = reinterpret_cast<u32x2*>(dst[u] + half + 4 * piece[u]);
+        if (PART) {
+          *at = u32x2{r[0], r[1]};
+          *high = u32x2{r[2], r[3]};
+        } else {
+          __builtin_nontemporal_store(u32x2{r[0], r[1]}, at);
+          __builtin_nontemporal_store(u32x2{r[2], r[3]}, high);
+        }
       }
     }
   }
@@ -285,7 +306,7 @@ __global__ __launch_bounds__(kThreadsR) void rope_scaled_kernel(RopeScaledArgs a
 
 }  // namespace
 
-hipError_t launch_rope_scaled(const RopeScaledArgs& a, bool interleaved, hipStream_t stream) {
+hipError_t launch_rope_scaled(const RopeScaledArgs& a, bool interleaved, bool in_place, hipStream_t stream) {
   const int heads = a.H[0] + a.H[1], pieces = a.copy ? a.D / 8 : a.R / 8;
   const int64_t full = kItems * kThreadsR / ((int64_t)heads * pieces);
   int64_t per = full < 1 ? 1 : full > kMaxTokens ? kMaxTokens : full;
@@ -293,10 +314,15 @@ hipError_t launch_rope_scaled(const RopeScaledArgs& a, bool interleaved, hipStre
   const dim3 grid((unsigned)((a.T + per - 1) / per)), block(kThreadsR);
   auto by = [](int n) { return (uint32_t)(((uint64_t(1) << 32) + n - 1) / n); };
   const unsigned lds = (unsigned)(per * a.R * 4);   // at most 16 KB
+  const bool part = a.R < a.D;
   if (interleaved)
-    hipLaunchKernelGGL(rope_scaled_kernel<true>, grid, block, lds, stream, a, (int)per, by(heads), by(pieces));
+    hipLaunchKernelGGL((rope_scaled_kernel<true, false, false>), grid, block, lds, stream, a, (int)per, by(heads), by(pieces));
+  else if (part && !in_place && a.R % 16 == 0)
+    hipLaunchKernelGGL((rope_scaled_kernel<false, true, false>), grid, block, lds, stream, a, (int)per, by(heads), by(pieces));
+  else if (part)
+    hipLaunchKernelGGL((rope_scaled_kernel<false, false, true>), grid, block, lds, stream, a, (int)per, by(heads), by(pieces));
   else
-    hipLaunchKernelGGL(rope_scaled_kernel<false>, grid, block, lds, stream, a, (int)per, by(heads), by(pieces));
+    hipLaunchKernelGGL((rope_scaled_kernel<false, false, false>), grid, block, lds, stream, a, (int)per, by(heads), by(pieces));
   return hipGetLastError();
 }
 
