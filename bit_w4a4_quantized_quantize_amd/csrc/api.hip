@@ -1679,8 +1679,8 @@ static int quantize_fp8_impl(const void* x, const void* smooth, int64_t M, int64
                              bool weight, void* stream) {
   int st = check_fp8_mnk(M, 0, K);
   if (st) return st;
-  if (M * blocks128(K) >= (int64_t(1) << 30))   // four threads of the grid each
-    return fail(SVDQ_ERR_UNSUPPORTED, "2^30 blocks of 128 or more (rows=%lld K=%lld)", (long long)M, (long long)K);
+  if ((M + 31) / 32 * blocks128(K) >= (int64_t(1) << 24))   // workgroups of 256
+    return fail(SVDQ_ERR_UNSUPPORTED, "2^24 blocks of 32 rows and 128 channels or more (rows=%lld K=%lld)", (long long)M, (long long)K);
   if (weight && blocks128(M) > 65535)
     return fail(SVDQ_ERR_UNSUPPORTED, "N = %lld is above %d", (long long)M, 65535 * 128);
   if (M == 0) return ok();
@@ -1802,8 +1802,8 @@ int svdq_linear_fp8(const void* x, const void* smooth, const void* weight, const
                     int64_t M, int64_t N, int64_t K, void* y, void* workspace, size_t workspace_bytes, void* stream) {
   int st = check_fp8_mnk(M, N, K);
   if (st) return st;
-  if (M * blocks128(K) >= (int64_t(1) << 30))   // four threads of the grid each
-    return fail(SVDQ_ERR_UNSUPPORTED, "2^30 blocks of 128 or more (M=%lld K=%lld)", (long long)M, (long long)K);
+  if ((M + 31) / 32 * blocks128(K) >= (int64_t(1) << 24))
+    return fail(SVDQ_ERR_UNSUPPORTED, "2^24 blocks of 32 tokens and 128 channels or more (M=%lld K=%lld)", (long long)M, (long long)K);
   if (M == 0 || N == 0) return ok();
   const char* names[] = {"x"};
   const void* ptrs[] = {x};

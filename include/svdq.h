@@ -587,7 +587,7 @@ int svdq_attention_packed(const void* q, int64_t q_stride_t, int64_t q_stride_h,
  *   1 / the layer's smooth, or NULL). N at most 2^23 - 128.
  * svdq_gemm_fp8: from codes; svdq_linear_fp8: the whole layer from x.
  * K: a positive multiple of 16, at most 2^20. M, N: at most 2^24, M * N at most 2^38,
- *   M * ceil(K/128) below 2^30 for the quantisation.
+ *   ceil(M/32) * ceil(K/128) below 2^24 for the quantisation.
  * workspace: svdq_gemm_fp8_workspace_bytes(M, N, K) and svdq_linear_fp8_workspace_bytes(M, N, K)
  *   bytes (0 for some sizes: then it may be NULL); no initialisation needed, contents
  *   unspecified afterwards.
