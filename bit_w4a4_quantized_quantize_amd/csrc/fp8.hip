@@ -157,7 +157,7 @@ __device__ __forceinline__ void f8_barrier() {   // as in gemm_bf16.hip: the wai
 // scale block and its scales: chunks of 32 rows x 128 bytes, row r at r * 128 with its eight 16-byte pieces
 // permuted by piece ^ swz(r), so that an operand read (32 rows, one piece each) meets every LDS
 // bank evenly and a copy reads whole 128-byte row segments.
-// 4096 x 10240, K = 3840: 152 us (2.1 PFLOP/s; a library's product with one scale a tensor reaches 3.2). The matrix units
+// 4096 x 10240, K = 3840: 150 us (2.15 PFLOP/s; a library's product with one scale a tensor reaches 3.2). The matrix units
 // are busy 55% of the time and the vector units, most of it adding the scaled sums, 48%; without those additions it takes
 // 27 us less, without the copies 24. 333 x 3840, K = 10240: 27 us and 5 to add four partial sums; operand traffic
 // (190 MB through the L2s, 7 TB/s) and the latency of one workgroup a CU.
