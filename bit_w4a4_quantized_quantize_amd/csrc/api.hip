@@ -2041,7 +2041,9 @@ int svdq_cache_read_fp8(const void* k_codes, const void* v_codes, const void* k_
 size_t svdq_attention_cache_fp8_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D,
                                                 int64_t max_length, int packed) {
   if (T <= 0 || B <= 0 || Hk <= 0 || H < Hk || H % Hk != 0 || max_length <= 0) return 0;
-  return svdq::attention_cache_workspace_bytes(T, B, H, Hk, D, max_length, packed != 0);
+  int kernel, splits;
+  svdq::attention_cache_plan(T, B, H, Hk, D, max_length, packed != 0, &kernel, &splits);
+  return svdq::attention_cache_partial_bytes(T, H, D, splits);
 }
 
 int svdq_attention_cache_fp8_plan(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_length,
@@ -2083,7 +2085,9 @@ int svdq_attention_cache_fp8(const void* q, int64_t q_stride_t, int64_t q_stride
   if (!heads_distinct(ho)) return fail(SVDQ_ERR_SHAPE, "o: heads overlap under its strides");
   if (!heads_disjoint(hq, ho)) return fail(SVDQ_ERR_ALIAS, "output o overlaps input q");
   max_length = max_length < width * page ? max_length : width * page;
-  const size_t need = svdq::attention_cache_workspace_bytes(T, B, H, Hk, D, max_length, cu_seqlens != nullptr);
+  int kernel, splits;
+  svdq::attention_cache_plan(T, B, H, Hk, D, max_length, cu_seqlens != nullptr, &kernel, &splits);
+  const size_t need = svdq::attention_cache_partial_bytes(T, H, D, splits);
   if (need > 0) {
     if (workspace_bytes < need)
       return fail(SVDQ_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
@@ -2109,9 +2113,10 @@ int svdq_attention_cache_fp8(const void* q, int64_t q_stride_t, int64_t q_stride
   a.H = (int)H;
   a.causal = causal != 0;
   a.scale = scale;
+  a.splits = splits;
   a.partial = static_cast<float*>(need > 0 ? workspace : nullptr);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t e = svdq::launch_attention_cache(a, max_length, s);
+  hipError_t e = svdq::launch_attention_cache(a, kernel, s);
   if (int st_ = launched(e, "attention over a cache", s)) return st_;
   return ok();
 }

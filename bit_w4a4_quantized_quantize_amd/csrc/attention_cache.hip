@@ -851,21 +851,25 @@ __global__ __launch_bounds__(256) void join_kernel(AttnCacheArgs a) {
 // Which kernel (0 few rows, 1 tiles) and how many ways the keys are split, by an estimate in microseconds from what the host
 // knows: T, B and a bound of the lengths. A workgroup walks through its share in steps (64 keys for each wave of few rows, a
 // tile of 64); a step takes at least `least`, and `full` for each workgroup on a CU: those there together up to two, else
-// all that come by, and `tail` for the last ones' end. Of several sequences the longest counts 1.34 of a step's share while all
-// are there, and they average 0.8 of it else. `base` starts and ends the call, a split adds a launch and its partial results.
-// Fitted to both kernels at 330 sizes (1 to 64 sequences of 1 to 4096 queries on 150 to 30000 keys, groups of 1, 4 and
-// 8, keys split up to 64 ways: profiles/attention_cache_grid.txt): within 3% of the best on average and 40% at
-// worst. One token on 65537 keys, 32 heads on 8: 29 us split 32 ways, 51 16 ways, 32 128 ways. 40 tokens on 540 keys: 9.7 us by
-// few rows, 19 by tiles; 512 on 8704: 192 and 105.
+// all that come by, and `tail` for the last ones' end. Of several sequences the longest counts `longest` of a step's share
+// while all are there, and they average `mean` of it else; one sequence's shares are equal, so the CU with the most counts.
+// All steps together take no less than the codes at 7 TB/s. `base` starts and ends the call, a split adds a launch and
+// its partial results. As for the linears, a call that is not in a graph takes its caller 10.3 us, and with a workspace and a
+// second launch 14, so a split pays only where the device takes longer than that.
+// Fitted to both kernels at 345 sizes (1 to 64 sequences of 1 to 4096 queries on 150 to 65000 keys, groups of 1, 4 and
+// 8, keys split up to 64 ways, those on the longest 128, from memory: profiles/attention_cache_grid.txt). Where the device takes 14 us or more it is
+// within 4% of the best on average and 28% at worst. One token on 65537 keys, 32 heads on 8: 31.6 us split 32 ways, 40 16
+// ways, 33 64 ways. 40 tokens on 540 keys: 9.7 us by few rows, 19 by tiles; 512 on 8704: 192 and 105.
 struct AttnPlan {
   int kernel, splits;
 };
 constexpr int64_t kMostPartial = int64_t(1) << 28;   // bytes
 
 AttnPlan plan_attention(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_length, bool packed) {
-  static const struct { int rows, keys; double base, least, full, tail; } kernels[] = {
-      {16, 4 * kTile, 3.9, 1.39, 1.81, 0.55}, {128, kTile, 6.2, 1.60, 0.83, 0.86}};
+  static const struct { int rows, keys; double base, least, full, tail, longest, mean; } kernels[] = {
+      {16, 4 * kTile, 3.14, 2.01, 1.38, 0.53, 1.15, 0.84}, {128, kTile, 5.35, 1.64, 0.83, 1.06, 1.34, 0.8}};
   static const int ways[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128};
+  const double memory = 2.0 * (double)(Hk * D) * (double)max_length * (B > 1 ? 0.6 * (double)B : 1.0) / 7e6;
   const int64_t G = H / Hk, tiles = (max_length + kTile - 1) / kTile;
   AttnPlan best{0, 1};
   double best_t = 1e300;
@@ -877,10 +881,12 @@ AttnPlan plan_attention(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, 
     for (int s : ways) {
       if (s > 1 && (tiles < kLeastTiles * s || (int64_t)s * T * H * (D + 2) * 4 > kMostPartial)) break;
       const double steps = (double)(((tiles + s - 1) / s * kTile + kernels[k].keys - 1) / kernels[k].keys);
-      const double on_cu = (double)(blocks * s) / 256.0;
-      const double share = on_cu <= 2.0 ? on_cu * (B > 1 ? 1.34 : 1.0) : on_cu * (B > 1 ? 0.8 : 1.0) + kernels[k].tail;
-      const double t = kernels[k].base + steps * fmax(kernels[k].least, share * kernels[k].full * wide) +
-                       (s > 1 ? 5.0 + 2.2e-6 * (double)(T * H * D) * s : 0.0);
+      const double on_cu = B > 1 ? (double)(blocks * s) / 256.0 : (double)((blocks * s + 255) / 256);
+      const double share = on_cu <= 2.0 ? on_cu * (B > 1 ? kernels[k].longest : 1.0)
+                                        : on_cu * (B > 1 ? kernels[k].mean : 1.0) + kernels[k].tail;
+      const double device = kernels[k].base + fmax(steps * fmax(kernels[k].least, share * kernels[k].full * wide), memory) +
+                            (s > 1 ? 6.46 + 1.92e-6 * (double)(T * H * D) * s : 0.0);
+      const double t = fmax(device, s > 1 ? 14.0 : 10.3) + 0.01 * device;
       if (t < best_t) {
         best_t = t;
         best = AttnPlan{k, s};
@@ -921,12 +927,6 @@ hipError_t launch_d(const AttnCacheArgs& a, int kernel, hipStream_t stream) {
 
 }  // namespace
 
-size_t attention_cache_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_length,
-                                       bool packed) {
-  const AttnPlan p = plan_attention(T, B, H, Hk, D, max_length, packed);
-  return p.splits > 1 ? (size_t)p.splits * (size_t)T * (size_t)H * (size_t)(D + 2) * 4 : 0;
-}
-
 void attention_cache_plan(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_length, bool packed,
                           int* kernel, int* splits) {
   const AttnPlan p = plan_attention(T, B, H, Hk, D, max_length, packed);
@@ -934,10 +934,12 @@ void attention_cache_plan(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D
   *splits = p.splits;
 }
 
-hipError_t launch_attention_cache(AttnCacheArgs a, int64_t max_length, hipStream_t stream) {
-  const AttnPlan p = plan_attention(a.T, a.B, a.H, a.c.Hk, a.c.D, max_length, a.cu != nullptr);
-  a.splits = p.splits;
-  return a.c.D == 64 ? launch_d<64>(a, p.kernel, stream) : launch_d<128>(a, p.kernel, stream);
+size_t attention_cache_partial_bytes(int64_t T, int64_t H, int64_t D, int splits) {
+  return splits > 1 ? (size_t)splits * (size_t)T * (size_t)H * (size_t)(D + 2) * 4 : 0;
+}
+
+hipError_t launch_attention_cache(const AttnCacheArgs& a, int kernel, hipStream_t stream) {
+  return a.c.D == 64 ? launch_d<64>(a, kernel, stream) : launch_d<128>(a, kernel, stream);
 }
 
 }  // namespace svdq

@@ -313,11 +313,10 @@ struct AttnCacheArgs {
   int splits;
   float* partial;          // [splits, T * H, D], then [splits, T * H, 2]: maximum and sum
 };
-size_t attention_cache_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_length,
-                                       bool packed);
 void attention_cache_plan(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_length, bool packed,
                           int* kernel, int* splits);
-hipError_t launch_attention_cache(AttnCacheArgs a, int64_t max_length, hipStream_t stream);
+size_t attention_cache_partial_bytes(int64_t T, int64_t H, int64_t D, int splits);
+hipError_t launch_attention_cache(const AttnCacheArgs& a, int kernel, hipStream_t stream);   // a.splits of the plan
 
 // Measurement helpers (not part of the layer): sustained f16 matrix-instruction
 // rate on a caller-filled operand table of calib_table_bytes() bytes, with the

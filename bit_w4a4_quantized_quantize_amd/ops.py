@@ -710,7 +710,7 @@ def _workspace(workspace, need, dev):
     if workspace is None:
         if need == 0:
             return None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        return torch.empty(need, dtype=torch.uint8, device=dev), need
     return workspace, _need(workspace, "workspace", torch.uint8, 1, min_numel=need).numel()
 
 
@@ -1092,7 +1092,7 @@ def linear_fp8(x, weight, wscales, bias=None, smooth=None, y=None, workspace=Non
         _need(smooth, "smooth", torch.bfloat16, shape=(K,))
     dev = x.device
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        y = x.new_empty((M, N))
     else:
         _need(y, "y", torch.bfloat16, shape=(M, N))
     workspace, ws_bytes = _workspace(workspace, linear_fp8_workspace_bytes(M, N, K), dev)
@@ -1229,7 +1229,7 @@ def cache_read_fp8(cache: Fp8Cache, block_table, starts, cu_seqlens=None, tokens
         tokens = args[-1] if cu_seqlens is None else k.shape[0]
     shape = (tokens, Hk, D)
     dev = cache.k_codes.device
-    k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else _need(k, "k", torch.bfloat16, shape=shape)
+    k = cache.k_codes.new_empty(shape, dtype=torch.bfloat16) if k is None else _need(k, "k", torch.bfloat16, shape=shape)
     v = torch.empty_like(k) if v is None else _need(v, "v", torch.bfloat16, shape=shape)
     _cache_device(cache, block_table, starts, "starts", cu_seqlens, k, v, "kv")
     _launch("svdq_cache_read_fp8", dev, *args, tokens, _p(k), _p(v))

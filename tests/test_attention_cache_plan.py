@@ -18,10 +18,10 @@ MIDDLE = [(700, 2838), (1001, 2500), (0, 5), (600, 599), (1, 2838), (700, 703), 
 # kernel, ways the keys are split, (queries, keys) of each sequence, H, Hk, D: both joins (up to eight ways, and more)
 SIZES = [
     (0, 1, [(1, 92), (3, 40)], 4, 2, 64), (0, 1, [(5, 64), (1, 9)], 6, 2, 128),
-    (0, 6, [(1, 1027)], 2, 1, 64), (0, 6, [(1, 1045)], 3, 1, 128),
+    (0, 8, [(1, 1811)], 2, 1, 64), (0, 8, [(1, 1845), (1, 3)], 3, 1, 128),
     (0, 12, [(1, 2074), (2, 70)], 2, 1, 64), (0, 12, [(2, 2072)], 5, 1, 128),
-    (1, 1, RAGGED, 24, 3, 64), (1, 1, RAGGED, 16, 2, 128), (1, 8, MIDDLE, 2, 1, 64), (1, 6, MIDDLE, 2, 1, 128),
-    (1, 16, LONG, 6, 2, 64), (1, 16, LONG, 3, 1, 128)]
+    (1, 1, RAGGED, 24, 3, 64), (1, 1, RAGGED, 16, 2, 128), (1, 4, MIDDLE, 6, 2, 64), (1, 6, MIDDLE, 2, 1, 128),
+    (1, 12, LONG, 12, 2, 64), (1, 16, LONG, 4, 1, 128)]
 
 
 def plan(seqs, H, Hk, D):
@@ -51,16 +51,18 @@ def measured_grid():
 
 
 def test_choice_against_the_measured_grid():
-    """The chosen kernel and split, by the times measured for all of them."""
-    loss = {}
+    """The chosen kernel and split, by the times measured for all of them: what a refit may lose, by the device's time, and
+    where that is less than a call takes its caller."""
+    loss, short = [], []
     for (H, Hk, D, B, n, before, longest), times in measured_grid():
         got = ops.attention_cache_fp8_plan(B * n, B, H, Hk, D, longest, n > 1)
         if got not in times:     # more ways than were measured at its size
             assert max(s for k, s in times if k == got[0]) < got[1], (H, Hk, D, B, n, before, got)
             continue
-        loss[H, Hk, D, B, n, before] = times[got] / min(times.values())
-    assert len(loss) > 300
-    assert np.mean(list(loss.values())) <= 1.04 and max(loss.values()) <= 1.45, max(loss.items(), key=lambda x: x[1])
+        best = min(times.values())
+        (short if best < 14 else loss).append(times[got] / best)
+    assert len(loss) > 150 and len(short) > 100
+    assert np.mean(loss) <= 1.05 and max(loss) <= 1.35 and np.mean(short) <= 1.02 and max(short) <= 1.25
 
 
 @pytest.mark.parametrize("sizes", [(0, 1, 4, 2, 128, 100), (1, 0, 4, 2, 128, 100), (1, 1, 5, 2, 128, 100), (1, 1, 4, 0, 128, 100),

@@ -12,7 +12,7 @@ from tests.test_gpu_attention_cache import Case, i32
 pytestmark = pytest.mark.gpu
 
 # sequences, H, Hk, D: keys whole, and split
-WHOLE, SPLIT = (RAGGED, 16, 2, 128), (LONG, 3, 1, 128)
+WHOLE, SPLIT = (RAGGED, 16, 2, 128), (LONG, 4, 1, 128)
 NARROW = (RAGGED, 24, 3, 64)
 
 
@@ -127,7 +127,7 @@ def test_equal_keys_far_from_zero(gpu_lib, batch):
 
 def test_old_keys_keep_their_weight(gpu_lib):
     """Scores that climb from key to key move the maximum often."""
-    L, page, H, Hk, D = 2048, 64, 16, 2, 128
+    L, page, H, Hk, D = 2048, 64, 24, 3, 128
     c = tiles(gpu_lib, ([(512, L), (300, L), (1, 64)], H, Hk, D), page, 37)
     k = torch.zeros(L, D)
     k[:, 0] = torch.arange(L) // 16                                  # rounded below
@@ -198,7 +198,7 @@ def test_bad_offsets_stay_inside(gpu_lib, batch, how):
 def test_graphs_sharing_a_workspace(gpu_lib):
     """Two captured calls with one workspace, replayed in turn between eager work; lengths change in between."""
     cases = [tiles(gpu_lib, SPLIT, 64, 41), tiles(gpu_lib, SPLIT, 16, 42)]
-    need = gpu_lib.attention_cache_fp8_workspace_bytes(cases[0].q.shape[0], len(LONG), 3, 1, 128, 6000, True)
+    need = gpu_lib.attention_cache_fp8_workspace_bytes(cases[0].q.shape[0], len(LONG), *SPLIT[1:], 6000, True)
     work = torch.empty(need, dtype=torch.uint8, device="cuda")
     graphs = []
     for c in cases:
