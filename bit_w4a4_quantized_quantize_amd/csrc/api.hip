@@ -1906,17 +1906,20 @@ int svdq_rope_scaled(const void* q, int64_t q_stride_t, int64_t q_stride_h, int6
   // theta^(-2 i / R) / 2 pi by products of the ratio: the long double's 64 bits leave 127 of them at
   // half a unit of a double or below
   const long double ratio = powl((long double)theta, -2.0L / (long double)R);
+  const long double by_factor = 1.0L / factor;
+  const long double by_span = original_length > 0.0 ? 1.0L / ((long double)high_rotations - low_rotations) : 0.0L;
   long double f = 0.159154943091895335768883763372514362L;
+  double frequencies[128];
   for (int i = 0; i < (int)R / 2; ++i, f *= ratio) {
     long double kept = 0.0L;
     if (original_length > 0.0) {
-      kept = ((long double)original_length * f - low_rotations) / ((long double)high_rotations - low_rotations);
+      kept = ((long double)original_length * f - low_rotations) * by_span;
       kept = kept < 0.0L ? 0.0L : kept > 1.0L ? 1.0L : kept;
     }
-    a.turns[i] = (double)(f * (kept + (1.0L - kept) / (long double)factor));
+    frequencies[i] = (double)(f * (kept + (1.0L - kept) * by_factor));
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t e = svdq::launch_rope_scaled(a, interleaved != 0, any_in_place, s);
+  hipError_t e = svdq::launch_rope_scaled(a, frequencies, interleaved != 0, any_in_place, s);
   if (int st_ = launched(e, "rotary positions", s)) return st_;
   return ok();
 }

@@ -259,9 +259,10 @@ struct RopeScaledArgs {
   int64_t T;
   int D, R, copy;
   float amplitude;
-  double turns[128];         // per pair: its frequency in turns
 };
-hipError_t launch_rope_scaled(const RopeScaledArgs& a, bool interleaved, bool in_place, hipStream_t stream);
+// frequencies: R / 2, in turns
+hipError_t launch_rope_scaled(const RopeScaledArgs& a, const double* frequencies, bool interleaved, bool in_place,
+                              hipStream_t stream);
 
 // Attention over packed sequences.
 struct AttnArgs {

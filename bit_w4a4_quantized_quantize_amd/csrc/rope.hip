@@ -202,9 +202,13 @@ void launch_rope_cfg(const RopeArgs& a, hipStream_t s) {
 // lines (R = 64 of 64 elements, 4099 tokens, 24 + 8 heads: 7.8 and 8.5 us without; the long one 93 and 101), and cost where
 // it does not (R = 16, 4 of each half: 12.9 and 11.2 without; WIDE, with them, 8.0).
 // by_heads, by_pieces: 2^32 / heads and / pieces of a head, rounded up (exact quotients below 2^16).
-template <bool INTER, bool WIDE, bool PART>
-__global__ __launch_bounds__(kThreadsR) void rope_scaled_kernel(RopeScaledArgs a, int per, uint32_t by_heads,
-                                                                uint32_t by_pieces) {
+template <int PAIRS>
+struct Turns {
+  double at[PAIRS];   // per pair: its frequency in turns
+};
+template <bool INTER, bool WIDE, bool PART, int PAIRS>
+__global__ __launch_bounds__(kThreadsR) void rope_scaled_kernel(RopeScaledArgs a, Turns<PAIRS> turns, int per,
+                                                                uint32_t by_heads, uint32_t by_pieces) {
   static_assert(!INTER || !WIDE, "neighbours are in one piece");
   extern __shared__ __attribute__((aligned(16))) float turn[];   // per token and pair: cos and sin
   const int tid = threadIdx.x;
@@ -245,7 +249,7 @@ __global__ __launch_bounds__(kThreadsR) void rope_scaled_kernel(RopeScaledArgs a
     if (first == 0) {
       for (int i = tid; i < here * half; i += kThreadsR) {
         const int k = i / half, p = i - k * half;
-        const double x = (double)a.positions[t0 + k] * a.turns[p];
+        const double x = (double)a.positions[t0 + k] * turns.at[p];
         float s, c;
         sincospif(2.0f * (float)(x - __builtin_rint(x)), &s, &c);
         reinterpret_cast<float2*>(turn)[i] = make_float2(a.amplitude * c, a.amplitude * s);
@@ -304,9 +308,8 @@ __global__ __launch_bounds__(kThreadsR) void rope_scaled_kernel(RopeScaledArgs a
   }
 }
 
-}  // namespace
-
-hipError_t launch_rope_scaled(const RopeScaledArgs& a, bool interleaved, bool in_place, hipStream_t stream) {
+template <int PAIRS>
+void launch_scaled(const RopeScaledArgs& a, const double* frequencies, bool interleaved, bool in_place, hipStream_t stream) {
   const int heads = a.H[0] + a.H[1], pieces = a.copy ? a.D / 8 : a.R / 8;
   const int64_t full = kItems * kThreadsR / ((int64_t)heads * pieces);
   int64_t per = full < 1 ? 1 : full > kMaxTokens ? kMaxTokens : full;
@@ -314,15 +317,30 @@ hipError_t launch_rope_scaled(const RopeScaledArgs& a, bool interleaved, bool in
   const dim3 grid((unsigned)((a.T + per - 1) / per)), block(kThreadsR);
   auto by = [](int n) { return (uint32_t)(((uint64_t(1) << 32) + n - 1) / n); };
   const unsigned lds = (unsigned)(per * a.R * 4);   // at most 16 KB
+  Turns<PAIRS> turns;
+  for (int i = 0; i < PAIRS; ++i) turns.at[i] = i < a.R / 2 ? frequencies[i] : 0.0;
   const bool part = a.R < a.D;
   if (interleaved)
-    hipLaunchKernelGGL((rope_scaled_kernel<true, false, false>), grid, block, lds, stream, a, (int)per, by(heads), by(pieces));
+    hipLaunchKernelGGL((rope_scaled_kernel<true, false, false, PAIRS>), grid, block, lds, stream, a, turns, (int)per, by(heads),
+                       by(pieces));
   else if (part && !in_place && a.R % 16 == 0)
-    hipLaunchKernelGGL((rope_scaled_kernel<false, true, false>), grid, block, lds, stream, a, (int)per, by(heads), by(pieces));
+    hipLaunchKernelGGL((rope_scaled_kernel<false, true, false, PAIRS>), grid, block, lds, stream, a, turns, (int)per, by(heads),
+                       by(pieces));
   else if (part)
-    hipLaunchKernelGGL((rope_scaled_kernel<false, false, true>), grid, block, lds, stream, a, (int)per, by(heads), by(pieces));
+    hipLaunchKernelGGL((rope_scaled_kernel<false, false, true, PAIRS>), grid, block, lds, stream, a, turns, (int)per, by(heads),
+                       by(pieces));
   else
-    hipLaunchKernelGGL((rope_scaled_kernel<false, false, false>), grid, block, lds, stream, a, (int)per, by(heads), by(pieces));
+    hipLaunchKernelGGL((rope_scaled_kernel<false, false, false, PAIRS>), grid, block, lds, stream, a, turns, (int)per, by(heads),
+                       by(pieces));
+}
+
+}  // namespace
+
+hipError_t launch_rope_scaled(const RopeScaledArgs& a, const double* frequencies, bool interleaved, bool in_place,
+                              hipStream_t stream) {
+  // (a kernel's arguments of 1.2 KB take the caller 0.5 us more than those of 0.4)
+  if (a.R <= 64) launch_scaled<32>(a, frequencies, interleaved, in_place, stream);
+  else launch_scaled<128>(a, frequencies, interleaved, in_place, stream);
   return hipGetLastError();
 }
 
