@@ -164,7 +164,9 @@ __global__ __launch_bounds__(64 * kWavesF, D == 64 ? 4 : 2) void attention_few_k
 #pragma unroll
   for (int j = 0; j < JD; ++j) acc[j] = f32x4{};
   const float c = a.scale * 1.4426950408889634f;   // exponents in base 2
-  float m = kLowest / fmaxf(c, 1.0f), l = 0.0f;
+  // The maximum starts at the least finite score, not the least whose power of two is finite: only differences are
+  // taken times c, and a row whose scores all lie below -2^128 / c has its best key too
+  float m = kLowest, l = 0.0f;
   const float slack = kSlackC / c;
   bool first = true;
 
@@ -518,9 +520,10 @@ __global__ __launch_bounds__(64 * kWavesT, 2) void attention_tile_kernel(AttnCac
   f32x16 acc[JD];
 #pragma unroll
   for (int j = 0; j < JD; ++j) acc[j] = f32x16{};
-  // exponents in base 2, x c - mc, and scores far from zero, as in attention.hip
+  // exponents in base 2, x c - mc, and scores far from zero, as in attention.hip; the maximum starts as for few rows
+  // (its product with c may be infinite, which is `far`)
   const float c = a.scale * 1.4426950408889634f;
-  float m = kLowest / fmaxf(c, 1.0f), mc = 0.0f;
+  float m = kLowest, mc = 0.0f;
   bool far = true;   // the same in every lane
   const float slack = kSlackC / c;
   // a tile's probabilities first, then l with what its last addition lost, as in attention.hip

@@ -671,8 +671,9 @@ int svdq_rope_scaled(const void* q, int64_t q_stride_t, int64_t q_stride_h, int6
  *   offsets are left as they were. What pages hold past a sequence's length, NaN included, has no effect. As
  *   in svdq_attention_packed, within a causal sequence a non-finite v may reach rows before it; a scale
  *   of 255 makes every key (value) of its page NaN.
- *   Scores and softmax statistics are fp32, the codes are taken exactly; the probabilities are rounded to bf16 for
- *   the second product (their sum is taken before that), o once to bf16.
+ *   Scores and softmax statistics are fp32 (a score q . k that overflows to minus infinity counts like a key that
+ *   is not seen), the codes are taken exactly; the probabilities are rounded to bf16 for the second product (their
+ *   sum is taken before that), o once to bf16.
  *   max_length: a bound of the lengths, where the caller knows one (else width * page): it only decides how
  *   the keys are shared out, a greater length is computed as well.
  *   workspace: svdq_attention_cache_fp8_workspace_bytes(T, B, H, Hk, D, min(max_length, width * page), packed =
