@@ -189,10 +189,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a, int l
 #pragma unroll
   for (int j = 0; j < JD; ++j) acc[j] = f32x16{};
   const float c = a.scale * 1.4426950408889634f;   // exponents in base 2
-  // The maximum starts below every finite score whose exponent is finite. Exponents are x c - mc,
+  // The maximum starts at the least finite score. Exponents are x c - mc,
   // mc = m c: its rounding is a factor common to the row (raise() carries it over), unless it is so
-  // large (`far`) that the factor leaves fp32: then m is taken off the scores first and mc is 0.
-  float m = -3.4028234663852886e38f / fmaxf(c, 1.0f), mc = 0.0f;
+  // large (`far`; it may be infinite) that the factor leaves fp32: then m is taken off the scores
+  // first and mc is 0.
+  float m = -3.4028234663852886e38f, mc = 0.0f;
   bool far = true;   // the same in every lane
   const float slack = kSlack / c;
 
