@@ -157,7 +157,8 @@ __global__ __launch_bounds__((kThreadsC<D, P>)) void append_kernel(CacheTokens a
   const int now = fine ? max(fp8_exponent(amax) + 127, old) : 255;
   if (tid == 0 && now != old) *scale_at = (uint8_t)now;
   // a NaN scale says it all: codes are left as they are, new ones are zero
-  const float inv = now < 255 ? __uint_as_float((uint32_t)(254 - now) << 23) : 0.0f;
+  // (2^(127 - now); for 254, which only a page filled elsewhere can have, that is 2^-127, a subnormal)
+  const float inv = now < 254 ? __uint_as_float((uint32_t)(254 - now) << 23) : now == 254 ? 0x1p-127f : 0.0f;
   const bool grown = blk.s0 > 0 && now > old && now < 255;
   // 2^(old - now); below 2^-126 every code becomes zero
   const float by = now - old < 127 ? __uint_as_float((uint32_t)(127 + old - now) << 23) : 0.0f;
