@@ -46,3 +46,35 @@ def test_append_behind_a_scale_from_elsewhere(gpu_lib, byte, page, D):
         gpu_lib.cache_append_fp8(one[:, :Hk], one[:, Hk:], cache, i32([[1]]), i32([held + new]))
         oracle.append({"k": f64(one[:, :Hk]), "v": f64(one[:, Hk:])}, [[1]], [held + new], [0, 1])
         check_held(gpu_lib, cache, oracle, [[1]], [held + new + 1])
+
+
+def to_bf16(v):
+    """Nearest bf16 in float64, subnormals and the overflow to infinity included."""
+    _, e = np.frexp(np.maximum(np.abs(v), 2.0 ** -126))
+    step = np.ldexp(1.0, e - 8)
+    z = np.rint(v / step) * step
+    return np.where(np.abs(z) >= 2.0 ** 128, np.copysign(np.inf, z), z)
+
+
+def test_every_scale_byte(gpu_lib):
+    """A head for each byte, every code: what is read back, and what a row answers that sees one key."""
+    Hk, page, D = 256, 16, 128
+    codes = torch.arange(256, dtype=torch.uint8)
+    codes[0x7F] = codes[0xFF] = 0                                    # the NaN codes
+    k = torch.zeros(1, Hk, page, D, dtype=torch.uint8)
+    k[:, :, :2] = codes.view(1, 1, 2, D)
+    scales = torch.arange(256, dtype=torch.uint8)[None].cuda()
+    held = gpu_lib.Fp8Cache(k.view(torch.float8_e4m3fn).cuda(), k.transpose(2, 3).contiguous().view(torch.float8_e4m3fn).cuda(),
+                            scales, scales.clone())
+    value = codes.view(torch.float8_e4m3fn).double().view(2, 1, D) * 2.0 ** (torch.arange(256).double() - 127).view(1, 256, 1)
+    want = to_bf16(value.numpy())[:, :255]
+    for got in gpu_lib.cache_read_fp8(held, i32([[0]]), i32([0]), i32([0, 2]), 2):
+        assert np.array_equal(f64(got)[:, :255], want) and np.isnan(f64(got)[:, 255]).all()
+    held.k_codes.view(torch.uint8).zero_()
+    held.k_scales.fill_(127)
+    for T, H in ((1, 256), (1, 512), (200, 256)):
+        q = torch.ones(T, H, D, device="cuda").bfloat16()
+        o = f64(gpu_lib.attention_cache_fp8(q, held, i32([[0]]), i32([1]), cu_seqlens=i32([0, T]), causal=False))
+        o = o.reshape(T, 256, H // 256, D)
+        assert np.array_equal(o[:, :255], np.broadcast_to(want[0][None, :, None], o[:, :255].shape))
+        assert np.isnan(o[:, 255]).all()
