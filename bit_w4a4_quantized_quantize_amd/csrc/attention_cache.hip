@@ -755,7 +755,9 @@ __global__ __launch_bounds__(64 * kWavesT, 2) void attention_tile_kernel(AttnCac
 // The splits of a row (a query's head) together, four elements a thread. WIDE: a workgroup a row, its groups of D / 4
 // threads take the splits in turn; else a group a row, for up to 8 splits, all requested at once. (A wave per row
 // that walked through its splits took longer than the attention from 64 splits on.)
-constexpr int kMaxSplits = 256, kFewSplits = 8;
+constexpr int kWays[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128};   // that keys are split
+constexpr int kMaxSplits = kWays[sizeof(kWays) / sizeof(kWays[0]) - 1], kFewSplits = 8;
+static_assert(kMaxSplits <= 256, "a thread of join_kernel a split");
 
 template <int D, bool WIDE>
 __global__ __launch_bounds__(256) void join_kernel(AttnCacheArgs a) {
@@ -871,7 +873,6 @@ constexpr int64_t kMostPartial = int64_t(1) << 28;   // bytes
 AttnPlan plan_attention(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_length, bool packed) {
   static const struct { int rows, keys; double base, least, full, tail, longest, mean; } kernels[] = {
       {16, 4 * kTile, 3.14, 2.01, 1.38, 0.53, 1.15, 0.84}, {128, kTile, 5.35, 1.64, 0.83, 1.06, 1.34, 0.8}};
-  static const int ways[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128};
   const double memory = 2.0 * (double)(Hk * D) * (double)max_length * (B > 1 ? 0.6 * (double)B : 1.0) / 7e6;
   const int64_t G = H / Hk, tiles = (max_length + kTile - 1) / kTile;
   AttnPlan best{0, 1};
@@ -881,7 +882,7 @@ AttnPlan plan_attention(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t D, 
     int64_t blocks = packed ? (T * G + rows - 1) / rows : B * ((G + rows - 1) / rows);
     blocks = (blocks < B ? B : blocks) * Hk;
     const double wide = k == 0 ? (double)D / 128.0 : 0.3 + 0.7 * (double)D / 128.0;
-    for (int s : ways) {
+    for (int s : kWays) {
       if (s > 1 && (tiles < kLeastTiles * s || (int64_t)s * T * H * (D + 2) * 4 > kMostPartial)) break;
       const double steps = (double)(((tiles + s - 1) / s * kTile + kernels[k].keys - 1) / kernels[k].keys);
       const double on_cu = B > 1 ? (double)(blocks * s) / 256.0 : (double)((blocks * s + 255) / 256);

@@ -180,7 +180,7 @@ hipError_t launch_linear_int8(const Int8GemmArgs& a, const uint16_t* x, const ui
 
 // Linear in 8-bit floating point: e4m3 codes and fp32 scales of x * smooth per 128 channels, and
 // y = bf16(sum_p ascales[p, m] * wscales[n / 128, p] * (codes @ weight^T over block p) + bias).
-// K % 16 == 0, K <= kFp8MaxK; M * ceil(K / 128) < 2^31 for the quantisation.
+// K % 16 == 0, K <= kFp8MaxK; ceil(M / 32) * ceil(K / 128) < 2^24 for the quantisation's grid (workgroups of 256).
 constexpr int64_t kFp8MaxK = int64_t(1) << 20;
 hipError_t launch_quant_fp8(const uint16_t* x, const uint16_t* smooth, int64_t M, int64_t K, uint8_t* codes,
                             float* ascales, hipStream_t stream);
@@ -298,7 +298,7 @@ hipError_t launch_cache_read(const CacheTokens& a, const CacheShape& c, uint16_t
                              hipStream_t stream);
 
 // Attention over such a cache: queries packed as in AttnArgs (cu NULL: one each), keys 0 .. lengths[b] - 1 of
-// sequence b; causal: its queries are the last of them. partial: attention_cache_workspace_bytes(...).
+// sequence b; causal: its queries are the last of them. partial: attention_cache_partial_bytes(...).
 struct AttnCacheArgs {
   HeadView q;
   uint16_t* o;
