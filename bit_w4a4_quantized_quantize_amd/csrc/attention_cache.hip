@@ -862,8 +862,9 @@ __global__ __launch_bounds__(256) void join_kernel(AttnCacheArgs a) {
 // its partial results. As for the linears, a call that is not in a graph takes its caller 10.3 us, and with a workspace and a
 // second launch 14, so a split pays only where the device takes longer than that.
 // Fitted to both kernels at 345 sizes (1 to 64 sequences of 1 to 4096 queries on 150 to 65000 keys, groups of 1, 4 and
-// 8, keys split up to 64 ways, those on the longest 128, from memory: profiles/attention_cache_grid.txt). Where the device takes 14 us or more it is
-// within 4% of the best on average and 28% at worst. One token on 65537 keys, 32 heads on 8: 31.6 us split 32 ways, 40 16
+// 8, keys split up to 64 ways, those on the longest 128, from memory: profiles/attention_cache_grid.txt). Where the best takes the device 14 us or more
+// the choice is within 4% of it on average and 28% at worst; below, 1.3% and 18% (64 queries on 3064 keys, 8 heads on one:
+// 14.1 us split 12 ways, 12.0 split 8). The caller is taken to be eager: a call captured in a graph chooses alike. One token on 65537 keys, 32 heads on 8: 31.6 us split 32 ways, 40 16
 // ways, 33 64 ways. 40 tokens on 540 keys: 9.7 us by few rows, 19 by tiles; 512 on 8704: 192 and 105.
 struct AttnPlan {
   int kernel, splits;

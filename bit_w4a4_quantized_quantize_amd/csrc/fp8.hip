@@ -678,8 +678,10 @@ struct F8Plan {
 // ceil(workgroups / 256) rounds `share` + `full` times the share of the CUs that work (the more do, the slower
 // each: power and the L2s); 4.2 us start and end a product; a split adds 0.9 us and the partial sums' traffic.
 // As for the 8-bit integers, a call that is not in a graph takes its caller about 10 us and 3 more for a split's
-// launch, so a split pays only where the device takes longer than that. On the device alone the choice is within
-// 0.2% of the best on average and 6% at worst. The estimate without `full` was 4% off on average. Tiles of 192 x 128 take
+// launch, so a split pays only where the device takes longer than that. The caller is taken to be eager: a call captured
+// in a graph chooses alike. Where the best takes the device 13 us or more, the choice is within 0.2% of it on average and 6%
+// at worst; with the sizes below it is 1.0% and 27% (100 tokens, 1300 channels, K = 2064: 11.2 us unsplit, 8.8 split), which
+// an eager caller does not see and a graph does. The estimate without `full` was 4% off on average. Tiles of 192 x 128 take
 // 8 to 14% off where rows fill them and 128's or 256's leave CUs idle (333 x 3840, K = 10240: 36 -> 33; 1500 x 3840, K = 3840:
 // 37 -> 32.5).
 F8Plan plan_fp8(int64_t M, int64_t N, int64_t K) {

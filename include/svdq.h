@@ -582,7 +582,8 @@ int svdq_attention_packed(const void* q, int64_t q_stride_t, int64_t q_stride_h,
  *   x [M, K] bf16, smooth [K] bf16 or NULL, codes [M, K] e4m3fn, ascales [ceil(K/128), M]
  *   fp32, weight [N, K] e4m3fn, wscales [ceil(N/128), ceil(K/128)] fp32, bias [N] bf16 or NULL,
  *   y [M, N] bf16. The last blocks may be smaller. The product takes any fp32 scales (powers of two or not)
- *   and any codes (NaN codes give NaN).
+ *   and any codes (NaN codes give NaN). A block's two scales are multiplied first, in fp32: their product has to be in
+ *   its range.
  * svdq_quantize_weight_fp8: a bf16 weight w [N, K] by the same rule, over blocks of 128 x 128 (smooth =
  *   1 / the layer's smooth, or NULL). N at most 2^23 - 128.
  * svdq_gemm_fp8: from codes; svdq_linear_fp8: the whole layer from x.
