@@ -335,8 +335,8 @@ __global__ __launch_bounds__(64 * kWavesF, D == 64 ? 4 : 2) void attention_few_k
   }
 }
 
-// Many rows: 2048 queries on 16896 keys, 30 heads of 128, 550 to 600 us (0.89 to 0.96 PFLOP/s; a bf16 library product reaches
-// 1.39). Matrix and vector units are busy 43% of the time each; without the conversions it is 6% faster, without the
+// Many rows: 2048 queries on 16896 keys, 30 heads of 128, 550 us in a loop (0.97 PFLOP/s; a bf16 library product reaches
+// 1.39), 600 to 635 in the first calls after an idle time (0.84 to 0.89). Matrix and vector units are busy 43% of the time each; without the conversions it is 6% faster, without the
 // exponentials 5, without the writes to LDS 13, without the loads 14. Measured and not kept: eight waves with 256 rows
 // (slower at every size), conversions between the second product's instructions, three to six reads ahead, other priorities.
 // A workgroup of four waves takes 128 rows, 32 a wave, and tiles of 64 keys in LDS: codes travel
